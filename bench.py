@@ -52,8 +52,8 @@ GRAPH_CHUNK = 50   # steps per captured CUDA graph
 # code it was taken on (kernel_source_sha); reported only while that code is
 # unchanged.
 NCU_TRAFFIC: dict = {
-    "copy": {"src_sha": "012614f4d8ee5b8b", "bytes_per_launch": 536938240 + 485307136},
-    "rowsum": {"src_sha": "012614f4d8ee5b8b", "bytes_per_launch": 1073840384 + 2676736},
+    "copy": {"src_sha": "e102672aaf294d6a", "bytes_per_launch": 536938240 + 485307136},
+    "rowsum": {"src_sha": "e102672aaf294d6a", "bytes_per_launch": 1073840384 + 2676736},
 }
 
 def copy_bytes(c=COPY):
@@ -69,7 +69,7 @@ def kernel_source_sha() -> str:
     comment keeps the key) of the files that hold the copy and row-sum
     kernels (the other kernels live in their own headers)."""
     h = hashlib.sha256()
-    for f in ("mbtile_kernels.cu", "internal.h"):
+    for f in ("mbtile_kernels.cu", "mbtile_ptx.cuh", "internal.h"):
         with open(os.path.join(ROOT, "mbarrier_async_tile_gb300", "csrc", f)) as fh:
             for line in fh:
                 code = line.split("//", 1)[0].rstrip()

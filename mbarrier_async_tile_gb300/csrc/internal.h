@@ -212,7 +212,16 @@ cudaError_t set_kernel_smem_limit(int optin, int *usable);
 // 8 = row sum with a barrier pair per box, 9 = wide row sum, 10 = wide column
 // sum.
 cudaError_t kernel_fit_per_sm(int op, int dtype, int threads, int smem, int *fit);
+// Device address of the current device's status word.
+cudaError_t status_word(int32_t **word);
 // Read the device status word and clear it (synchronous).
 cudaError_t read_and_clear_status(int32_t info[4]);
+
+// (mbtile_host.cpp)  SM count and opt-in shared memory of the current device.
+int device_limits(int *num_sms, int *smem_optin);
+// (mbtile_host.cpp)  At least `bytes` bytes of the partial-sum part of the
+// library's workspace for (current device, stream), 256-byte aligned, contents
+// undefined; the sums' tickets are left as they are.
+int owned_scratch(void *stream, size_t bytes, void **scratch);
 
 }  // namespace mbt

@@ -829,14 +829,12 @@ std::tuple<int, uintptr_t, size_t> owned_key(int dev, void *stream) {
     return std::make_tuple(dev, reinterpret_cast<uintptr_t>(stream), thread);
 }
 
-// Tickets for `groups` reduction groups and `partial_bytes` of partial sums
-// from the library's workspace for (current device, stream).
-int owned_workspace(void *stream, int64_t groups, size_t partial_bytes, int32_t **ticket,
-                    int32_t **clear, int64_t *clear_n, float **partial) {
+// The workspace of (current device, stream), grown to `groups` ticket words a
+// set and `partial_bytes` of partial sums.  The caller holds g_owned_mutex.
+int grow_owned(void *stream, int64_t groups, size_t partial_bytes, OwnedWorkspace **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MBT_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    std::lock_guard<std::mutex> lock(g_owned_mutex);
     OwnedWorkspace &w = g_owned[owned_key(dev, stream)];
     if (w.base == nullptr || w.ticket_cap < groups || w.partial_bytes < partial_bytes) {
         // Allocating inside a stream capture would end the capture with an error.
@@ -864,6 +862,19 @@ int owned_workspace(void *stream, int64_t groups, size_t partial_bytes, int32_t 
         nw.base = static_cast<char *>(p);
         w = nw;
     }
+    *out = &w;
+    return MBT_OK;
+}
+
+// Tickets for `groups` reduction groups and `partial_bytes` of partial sums
+// from the library's workspace for (current device, stream).
+int owned_workspace(void *stream, int64_t groups, size_t partial_bytes, int32_t **ticket,
+                    int32_t **clear, int64_t *clear_n, float **partial) {
+    std::lock_guard<std::mutex> lock(g_owned_mutex);
+    OwnedWorkspace *grown = nullptr;
+    const int rc = grow_owned(stream, groups, partial_bytes, &grown);
+    if (rc != MBT_OK) return rc;
+    OwnedWorkspace &w = *grown;
     const int64_t parity = static_cast<int64_t>(w.uses++ & 1u);
     int32_t *sets = reinterpret_cast<int32_t *>(w.base);
     *ticket = sets + parity * w.ticket_cap;
@@ -1009,6 +1020,28 @@ int workspace_bytes(int op, int64_t M, int64_t N, int tile_m, int tile_n, int st
 }
 
 }  // namespace
+
+namespace mbt {
+
+int device_limits(int *num_sms, int *smem_optin) {
+    DeviceFigures d;
+    const int rc = device_figures(&d);
+    if (rc != MBT_OK) return rc;
+    *num_sms = d.num_sms;
+    *smem_optin = d.smem_optin;
+    return MBT_OK;
+}
+
+int owned_scratch(void *stream, size_t bytes, void **scratch) {
+    std::lock_guard<std::mutex> lock(g_owned_mutex);
+    OwnedWorkspace *w = nullptr;
+    const int rc = grow_owned(stream, 0, bytes, &w);
+    if (rc != MBT_OK) return rc;
+    *scratch = w->base + 2 * w->ticket_cap * 4;
+    return MBT_OK;
+}
+
+}  // namespace mbt
 
 extern "C" {
 

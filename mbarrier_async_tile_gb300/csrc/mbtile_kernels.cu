@@ -1346,6 +1346,10 @@ cudaError_t kernel_fit_per_sm(int op, int dtype, int threads, int smem, int *fit
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(fit, fn, threads, smem);
 }
 
+cudaError_t status_word(int32_t **word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_status);
+}
+
 cudaError_t read_and_clear_status(int32_t info[4]) {
     int32_t host[4] = {0, 0, 0, 0};
     cudaError_t e = cudaMemcpyFromSymbol(host, g_status, sizeof host);
