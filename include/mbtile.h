@@ -89,7 +89,12 @@ extern "C" {
 #endif
 
 /* Element types.  Copies move raw bits; row sums widen exactly to fp32. */
-typedef enum mbt_dtype { MBT_F16 = 0, MBT_BF16 = 1, MBT_F32 = 2 } mbt_dtype;
+typedef enum mbt_dtype {
+    MBT_F16 = 0,
+    MBT_BF16 = 1,
+    MBT_F32 = 2,
+    MBT_E4M3 = 3               /* 8-bit float; layer operators only */
+} mbt_dtype;
 
 typedef enum mbt_status {
     MBT_OK = 0,
@@ -525,6 +530,132 @@ int tile_workspace_release(void *stream);
  * misaligned, src NULL with bytes > 0), MBT_ERR_ALIGN or MBT_ERR_CUDA.
  */
 int tile_read_checksum(const void *src, size_t bytes, uint32_t *out, void *stream);
+
+/*
+ * Layer operators: the streaming steps of a model's layer next to copies and
+ * sums.  Conventions as above (device pointers, row-major, stream, status
+ * codes, argument errors before any launch), with these differences: pointers
+ * need the alignment of their element type only, unless stated (16-byte
+ * aligned bases and pitches run faster); a pitch of 0 selects a dense matrix;
+ * pitches are in elements.  The pages have no counterpart of these entry
+ * points.
+ */
+
+/* Output of tile_rmsnorm: in the input's type, or e4m3 with fp32 scales, one
+ * for a row or one for each 32, 64 or 128 columns (the value itself). */
+enum { MBT_QUANT_NONE = -1, MBT_QUANT_ROW = 0 };
+
+/*
+ * tile_rmsnorm -- root-mean-square norm of each row, with the residual's
+ * addition:
+ *   h[i][j] = x[i][j] + residual[i][j]
+ *   rstd[i] = 1 / sqrt(mean_j h[i][j]^2 + eps)
+ *   out[i][j] = h[i][j] * rstd[i] * (weight[j] + weight_offset)
+ * in fp32, each output rounded once (out does not see residual_out's rounding).
+ *   residual      optional (NULL: h = x), residual_out optional, receives h;
+ *                 both in x's type (dtype).  residual_out may be residual or x
+ *                 itself; no other overlap of outputs with inputs, except
+ *                 that out may be x or residual when it has their type and
+ *                 pitch.
+ *   weight        optional, N elements of weight_dtype.  NULL: factor 1, and
+ *                 weight_offset is not used.
+ *   quant         MBT_QUANT_NONE: out has x's type.  MBT_QUANT_ROW, 32, 64 or
+ *                 128: out is e4m3, scales[i][j / quant] (dense, one per row
+ *                 with MBT_QUANT_ROW, ceil(N / quant) otherwise; the last group
+ *                 may be short) = max(largest |y| of the group / 448, 2^-126),
+ *                 out = y / scale rounded to nearest even.  A group with a NaN
+ *                 has a NaN scale.
+ *   rstd          fp32[M], always written (tile_rmsnorm_backward reads it).
+ * M = 0 does nothing; N = 0 writes rstd = 1 / sqrt(eps) only (and, with
+ * MBT_QUANT_ROW, the smallest scale).
+ */
+int tile_rmsnorm(const void *x, const void *residual, const void *weight, void *out,
+                 void *residual_out, float *scales, float *rstd, int64_t M, int64_t N,
+                 int64_t ld_x, int64_t ld_res, int64_t ld_out, int64_t ld_res_out, int dtype,
+                 int weight_dtype, int quant, float eps, float weight_offset, void *stream);
+
+/*
+ * tile_rmsnorm_backward -- gradient of tile_rmsnorm at h, from dy and the
+ * forward call's rstd.  With xh = h rstd and g = dy (weight + weight_offset):
+ *   dx[i][j] = rstd[i] (g[i][j] - xh[i][j] mean_j(g xh)) + dresidual[i][j]
+ *   dweight[j] = sum_i dy[i][j] xh[i][j]
+ *   dy, h, dx     matrices of type dtype; h is tile_rmsnorm's residual_out (or
+ *                 x without a residual).  dx may be dy or dresidual itself.
+ *                 dx is the gradient of x and of residual alike.
+ *   dresidual     optional: the gradient that reaches h past the norm.
+ *   weight        as in tile_rmsnorm; dweight optional, fp32[N], overwritten.
+ * The sums' order is fixed: equal calls on one device give equal bits.  dweight
+ * takes scratch of the library's workspace for (device, stream), see
+ * tile_rowsum (MBT_ERR_WORKSPACE where it would have to grow in a capture).
+ * M = 0 zeroes dweight; N = 0 does nothing.
+ */
+int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const void *weight,
+                          const void *dresidual, void *dx, float *dweight, int64_t M, int64_t N,
+                          int64_t ld_dy, int64_t ld_h, int64_t ld_dres, int64_t ld_dx, int dtype,
+                          int weight_dtype, float weight_offset, void *stream);
+
+/*
+ * tile_w4_matvec -- products of a few rows with a matrix in 4 bits:
+ *   out[t][n] = sum_k x[t][k] (q[n][k] - zeros[n][k / group]) scales[n][k / group]
+ * in fp32, rounded once to out_dtype.
+ *   x             T x K, fp16, bf16, or e4m3 with x_scales (fp32, dense: T of
+ *                 them with x_group = 0, T x ceil(K / 128) with x_group = 128,
+ *                 as tile_rmsnorm writes them); pitch ld_x.
+ *   q             N rows of K / 2 bytes, column k in the low half of byte k / 2
+ *                 for even k, in the high half for odd; 16-byte aligned, the
+ *                 pitch ld_q (bytes; 0 => K / 2) a multiple of 16.
+ *   scales        N x ceil(K / group), dense, of scale_dtype (fp16, bf16, fp32).
+ *   zeros         optional, uint8 of the same shape, values 0..15; NULL: 8.
+ *   group         32, 64 or 128; K a multiple of 32 (MBT_ERR_UNSUPPORTED).
+ * Made for 1 to 8 rows of x; more are taken eight at a time, each reading q
+ * again.  A NaN or infinity in row t of x makes values of row t of out NaN or
+ * infinite and leaves the other rows alone.  T = 0 or N = 0 does nothing,
+ * K = 0 writes zeros.
+ */
+int tile_w4_matvec(const void *x, const float *x_scales, const uint8_t *q, const void *scales,
+                   const uint8_t *zeros, void *out, int64_t T, int64_t N, int64_t K, int64_t ld_x,
+                   int64_t ld_q, int64_t ld_out, int group, int x_group, int dtype,
+                   int scale_dtype, int out_dtype, void *stream);
+
+/*
+ * tile_adamw -- one AdamW step over many tensors:
+ *   g = grad * *grad_scale
+ *   m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, updating param, exp_avg and exp_avg_sq in place.
+ *   tensors       HOST array of count descriptors, read during the call.  All
+ *                 params have param_dtype, all grads grad_dtype (fp16, bf16 or
+ *                 fp32).  master: for 16-bit params, optional fp32 weights that
+ *                 hold p (the param receives them rounded); all tensors or none.
+ *   state_dtype   MBT_F32: exp_avg and exp_avg_sq are fp32[n], m_scales and
+ *                 v_scales NULL.  MBT_E4M3: 8-bit codes in blocks of
+ *                 MBT_ADAMW_BLOCK elements, scales fp32[ceil(n / block)]:
+ *                 m = code * m_scale, sqrt(v) = code * v_scale; a zero-filled
+ *                 state is a valid first one.  m is rounded to nearest, sqrt(v)
+ *                 up or down at random (so that a change below half a code is
+ *                 not lost every step), by 16 bits of the 32-bit MurmurHash3
+ *                 finaliser of (tensor * 0x9E3779B9 + i / 2) ^ seed, the low
+ *                 half for even i; a sqrt(v) above 0 never becomes 0.
+ *   step          1, 2, ...: the step being taken.
+ *   grad_scale    optional DEVICE pointer to one fp32 factor (clipping, loss
+ *                 scaling).
+ * Tensors must not overlap.  Empty ones are allowed.
+ */
+#define MBT_ADAMW_BLOCK 256
+typedef struct mbt_adamw_tensor {
+    void *param;
+    const void *grad;
+    void *exp_avg;
+    void *exp_avg_sq;
+    float *master;
+    float *m_scales;
+    float *v_scales;
+    int64_t n;                 /* elements */
+} mbt_adamw_tensor;
+int tile_adamw(const mbt_adamw_tensor *tensors, int64_t count, int param_dtype, int grad_dtype,
+               int state_dtype, int64_t step, double lr, double beta1, double beta2, double eps,
+               double weight_decay, const float *grad_scale, uint32_t seed, void *stream);
 
 /* Synchronises `stream`, then reads and clears the current device's status
  * word.  info (may be NULL) receives {code, block, stage, role * 2 + parity}

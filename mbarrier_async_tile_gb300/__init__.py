@@ -28,6 +28,8 @@ __all__ = [
     "tile_workspace_release", "tile_read_checksum",
     "tile_status", "tile_plan", "tile_plan_device", "tile_device_info", "tile_strerror",
     "tile_stage_image",
+    "E4M3", "RmsNorm", "AdamwTensors",
+    "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw",
 ]
 
 MBT_OK = 0
@@ -551,3 +553,7 @@ def tile_read_checksum(buf: torch.Tensor, out: torch.Tensor | None = None,
                                     out.data_ptr(), _stream_handle(stream))
     _check(rc, "tile_read_checksum")
     return out
+
+
+from .layer import (E4M3, AdamwTensors, RmsNorm, tile_adamw, tile_rmsnorm,  # noqa: E402
+                    tile_rmsnorm_backward, tile_w4_matvec)

@@ -1,0 +1,317 @@
+// tile_rmsnorm and tile_rmsnorm_backward: the root-mean-square norm over a
+// matrix's rows, with the residual's addition, and its gradient.
+//
+//   h = x + r    rstd_i = (mean_j h_ij^2 + eps)^(-1/2)    y = h rstd (w + o)
+//   xh = h rstd  g = dy (w + o)  c_i = mean_j(g xh)
+//   dx = rstd (g - xh c) + dres          dw_j = sum_i dy xh
+//
+// Both read and write every matrix once and compute a handful of operations
+// per element: device memory bounds them.  All sums are fp32.
+#include <algorithm>
+
+#include "internal.h"
+#include "mbtile_elem.cuh"
+#include "mbtile_ptx.cuh"
+
+namespace mbt {
+namespace {
+
+struct NormArgs {
+    const void *x, *res, *w;
+    void *out, *res_out;
+    float *scales, *rstd;
+    int64_t M, N, ld_x, ld_res, ld_out, ld_res_out;
+    int64_t groups;          // scales per row
+    int32_t wdt, quant;      // quant: -1 none, 0 a scale per row, else columns per scale
+    float eps, woff;
+};
+
+struct NormGradArgs {
+    const void *dy, *h, *w, *dres;
+    const float *rstd;
+    void *dx;
+    float *dw, *partial;     // partial: [splits][N]
+    int64_t M, N, ld_dy, ld_h, ld_dres, ld_dx;
+    int64_t splits;
+    int32_t wdt;
+    float woff;
+};
+
+constexpr int kRowThreads = 512;
+
+// Sum and largest magnitude over the CTA, the same in every thread.
+template <int THREADS>
+__device__ __forceinline__ void block_reduce(float &sum, uint32_t &amax, float *red) {
+    sum = warp_sum(sum);
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    uint32_t *redm = reinterpret_cast<uint32_t *>(red + THREADS / 32);
+    __syncthreads();   // the last round's reads of red are over
+    if ((threadIdx.x & 31) == 0) {
+        red[threadIdx.x >> 5] = sum;
+        redm[threadIdx.x >> 5] = amax;
+    }
+    __syncthreads();
+    sum = 0.f;
+    amax = 0;
+#pragma unroll
+    for (int k = 0; k < THREADS / 32; ++k) {
+        sum += red[k];
+        amax = max(amax, redm[k]);
+    }
+}
+
+__device__ __forceinline__ float weight_at(const void *w, int wdt, float woff, int64_t j) {
+    return w ? load_any(w, wdt, j) + woff : 1.f;
+}
+
+// Any strides and lengths: a CTA per row, two passes over it (the second one's
+// reads hit the caches), one element per access.
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads) mbt_rmsnorm_rows_kernel(const NormArgs a) {
+    using T = typename Elem<DT>::type;
+    __shared__ float red[2 * kRowThreads / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t i = blockIdx.x; i < a.M; i += gridDim.x) {
+        const T *x = static_cast<const T *>(a.x) + i * a.ld_x;
+        const T *r = a.res ? static_cast<const T *>(a.res) + i * a.ld_res : nullptr;
+        T *ro = a.res_out ? static_cast<T *>(a.res_out) + i * a.ld_res_out : nullptr;
+        auto h_at = [&](int64_t j) {
+            return Elem<DT>::widen(x[j]) + (r ? Elem<DT>::widen(r[j]) : 0.f);
+        };
+        float ss = 0.f;
+        uint32_t amax = 0;
+        for (int64_t j = threadIdx.x; j < a.N; j += kRowThreads) {
+            const float h = h_at(j);
+            ss += h * h;
+            if (a.quant == 0) amax = max(amax, magnitude(h * weight_at(a.w, a.wdt, a.woff, j)));
+        }
+        block_reduce<kRowThreads>(ss, amax, red);
+        const float rstd = 1.f / sqrtf((a.N ? ss / static_cast<float>(a.N) : 0.f) + a.eps);
+        if (threadIdx.x == 0) a.rstd[i] = rstd;
+        if (a.quant <= 0) {
+            const float scale = group_scale(magnitude(__uint_as_float(amax) * rstd));
+            const float inv = 1.f / scale;
+            if (a.quant == 0 && threadIdx.x == 0) a.scales[i] = scale;
+            for (int64_t j = threadIdx.x; j < a.N; j += kRowThreads) {
+                const float h = h_at(j);
+                const float y = h * rstd * weight_at(a.w, a.wdt, a.woff, j);
+                if (a.quant == 0)
+                    static_cast<uint8_t *>(a.out)[i * a.ld_out + j] =
+                        static_cast<uint8_t>(to_e4m3x2(y * inv, 0.f));
+                else
+                    static_cast<T *>(a.out)[i * a.ld_out + j] = Elem<DT>::round(y);
+                if (ro) ro[j] = Elem<DT>::round(h);
+            }
+            continue;
+        }
+        // groups of 32, 64 or 128 columns: a warp takes 128 columns at a time
+        for (int64_t j0 = warp * 128; j0 < a.N; j0 += kRowThreads * 4) {
+            float y[4];
+            uint32_t m[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t j = j0 + 32 * k + lane;
+                y[k] = 0.f;
+                if (j < a.N) {
+                    const float h = h_at(j);
+                    y[k] = h * rstd * weight_at(a.w, a.wdt, a.woff, j);
+                    if (ro) ro[j] = Elem<DT>::round(h);
+                }
+                m[k] = __reduce_max_sync(0xffffffffu, magnitude(y[k]));
+            }
+            if (a.quant >= 64) {
+                m[0] = m[1] = max(m[0], m[1]);
+                m[2] = m[3] = max(m[2], m[3]);
+            }
+            if (a.quant >= 128) m[0] = m[1] = m[2] = m[3] = max(m[0], m[2]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t j = j0 + 32 * k + lane;
+                const float scale = group_scale(m[k]);
+                if (j < a.N) {
+                    static_cast<uint8_t *>(a.out)[i * a.ld_out + j] =
+                        static_cast<uint8_t>(to_e4m3x2(y[k] * (1.f / scale), 0.f));
+                    if (j % a.quant == 0) a.scales[i * a.groups + j / a.quant] = scale;
+                }
+            }
+        }
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads) mbt_rmsnorm_dx_rows_kernel(const NormGradArgs a) {
+    using T = typename Elem<DT>::type;
+    __shared__ float red[2 * kRowThreads / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t i = blockIdx.x; i < a.M; i += gridDim.x) {
+        const T *dy = static_cast<const T *>(a.dy) + i * a.ld_dy;
+        const T *h = static_cast<const T *>(a.h) + i * a.ld_h;
+        const T *dr = a.dres ? static_cast<const T *>(a.dres) + i * a.ld_dres : nullptr;
+        T *dx = static_cast<T *>(a.dx) + i * a.ld_dx;
+        const float rstd = a.rstd[i];
+        float dot = 0.f;
+        uint32_t none = 0;
+        for (int64_t j = threadIdx.x; j < a.N; j += kRowThreads)
+            dot += Elem<DT>::widen(dy[j]) * weight_at(a.w, a.wdt, a.woff, j) *
+                   (Elem<DT>::widen(h[j]) * rstd);
+        block_reduce<kRowThreads>(dot, none, red);
+        const float c = dot / static_cast<float>(a.N);
+        for (int64_t j = threadIdx.x; j < a.N; j += kRowThreads) {
+            const float g = Elem<DT>::widen(dy[j]) * weight_at(a.w, a.wdt, a.woff, j);
+            const float d = rstd * (g - Elem<DT>::widen(h[j]) * rstd * c);
+            dx[j] = Elem<DT>::round(d + (dr ? Elem<DT>::widen(dr[j]) : 0.f));
+        }
+    }
+}
+
+constexpr int kColThreads = 128;
+
+// dw's partial sums: CTA (b, s) takes 128 columns of the rows of split s.
+template <int DT>
+__global__ void __launch_bounds__(kColThreads) mbt_rmsnorm_dw_rows_kernel(const NormGradArgs a) {
+    using T = typename Elem<DT>::type;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t j = static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x;
+    if (j >= a.N) return;
+    const int64_t s = blockIdx.y, lo = s * a.M / a.splits, hi = (s + 1) * a.M / a.splits;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int64_t i = lo; i < hi; ++i)
+        sum += Elem<DT>::widen(static_cast<const T *>(a.dy)[i * a.ld_dy + j]) *
+               (Elem<DT>::widen(static_cast<const T *>(a.h)[i * a.ld_h + j]) * a.rstd[i]);
+    a.partial[s * a.N + j] = sum;
+}
+
+// dw from its partial sums, in split order.
+__global__ void __launch_bounds__(kColThreads) mbt_rmsnorm_dw_finish_kernel(const NormGradArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t j = static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x;
+    if (j >= a.N) return;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int64_t s = 0; s < a.splits; ++s) sum += a.partial[s * a.N + j];
+    a.dw[j] = sum;
+}
+
+template <class K, class A>
+cudaError_t launch(K kernel, dim3 grid, int threads, cudaStream_t stream, const A &a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+int64_t elem_bytes(int dtype) { return dtype == MBT_F32 ? 4 : 2; }
+
+bool float_type(int dtype) { return dtype == MBT_F16 || dtype == MBT_BF16 || dtype == MBT_F32; }
+
+bool aligned_elem(const void *p, int dtype) {
+    return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(elem_bytes(dtype)) == 0;
+}
+
+constexpr int64_t kMaxIndex = int64_t{1} << 46;   // elements an address may be away
+
+// Row pitch (0 => N) and its bounds.
+bool pitch(int64_t *ld, int64_t M, int64_t N) {
+    if (*ld == 0) *ld = N;
+    return *ld >= N && (M == 0 || *ld <= kMaxIndex / M);
+}
+
+}  // namespace
+}  // namespace mbt
+
+extern "C" int tile_rmsnorm(const void *x, const void *residual, const void *weight, void *out,
+                            void *residual_out, float *scales, float *rstd, int64_t M, int64_t N,
+                            int64_t ld_x, int64_t ld_res, int64_t ld_out, int64_t ld_res_out,
+                            int dtype, int weight_dtype, int quant, float eps, float weight_offset,
+                            void *stream) {
+    using namespace mbt;
+    if (M < 0 || N < 0 || N > 0x7fffffff || !float_type(dtype) ||
+        (weight && !float_type(weight_dtype)) || !(eps >= 0.f))
+        return MBT_ERR_ARG;
+    if (quant != MBT_QUANT_NONE && quant != MBT_QUANT_ROW && quant != 32 && quant != 64 && quant != 128)
+        return MBT_ERR_UNSUPPORTED;
+    if (!pitch(&ld_x, M, N) || !pitch(&ld_res, M, N) || !pitch(&ld_out, M, N) ||
+        !pitch(&ld_res_out, M, N))
+        return MBT_ERR_ARG;
+    if (M == 0) return MBT_OK;
+    if (!rstd || (N > 0 && (!x || !out)) || (quant != MBT_QUANT_NONE) != (scales != nullptr) ||
+        (residual_out && !residual))
+        return MBT_ERR_ARG;
+    if (!aligned_elem(x, dtype) || !aligned_elem(residual, dtype) ||
+        !aligned_elem(residual_out, dtype) || (weight && !aligned_elem(weight, weight_dtype)) ||
+        (quant == MBT_QUANT_NONE && !aligned_elem(out, dtype)) || !aligned_elem(rstd, MBT_F32) ||
+        !aligned_elem(scales, MBT_F32))
+        return MBT_ERR_ALIGN;
+    const NormArgs a{x,      residual, weight, out,        residual_out, scales,
+                     rstd,   M,        N,      ld_x,       ld_res,       ld_out,
+                     ld_res_out, quant > 0 ? (N + quant - 1) / quant : 1,
+                     weight_dtype, quant, eps, weight_offset};
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(M, 1 << 20)));
+    const cudaError_t e = dtype == MBT_F16 ? launch(mbt_rmsnorm_rows_kernel<MBT_F16>, grid, kRowThreads, s, a)
+                          : dtype == MBT_BF16
+                              ? launch(mbt_rmsnorm_rows_kernel<MBT_BF16>, grid, kRowThreads, s, a)
+                              : launch(mbt_rmsnorm_rows_kernel<MBT_F32>, grid, kRowThreads, s, a);
+    return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
+}
+
+extern "C" int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd,
+                                     const void *weight, const void *dresidual, void *dx,
+                                     float *dweight, int64_t M, int64_t N, int64_t ld_dy,
+                                     int64_t ld_h, int64_t ld_dres, int64_t ld_dx, int dtype,
+                                     int weight_dtype, float weight_offset, void *stream) {
+    using namespace mbt;
+    if (M < 0 || N < 0 || N > 0x7fffffff || !float_type(dtype) ||
+        (weight && !float_type(weight_dtype)))
+        return MBT_ERR_ARG;
+    if (!pitch(&ld_dy, M, N) || !pitch(&ld_h, M, N) || !pitch(&ld_dres, M, N) || !pitch(&ld_dx, M, N))
+        return MBT_ERR_ARG;
+    if (N == 0) return MBT_OK;
+    if (M > 0 && (!dy || !h || !rstd || !dx)) return MBT_ERR_ARG;
+    if (!aligned_elem(dy, dtype) || !aligned_elem(h, dtype) || !aligned_elem(dresidual, dtype) ||
+        !aligned_elem(dx, dtype) || (weight && !aligned_elem(weight, weight_dtype)) ||
+        !aligned_elem(rstd, MBT_F32) || !aligned_elem(dweight, MBT_F32))
+        return MBT_ERR_ALIGN;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        if (!dweight) return MBT_OK;
+        return cudaMemsetAsync(dweight, 0, static_cast<size_t>(N) * 4, s) == cudaSuccess ? MBT_OK
+                                                                                          : MBT_ERR_CUDA;
+    }
+    int sms = 0, smem = 0;
+    int rc = device_limits(&sms, &smem);
+    if (rc != MBT_OK) return rc;
+    NormGradArgs a{dy, h, weight, dresidual, rstd, dx, dweight, nullptr, M, N, ld_dy, ld_h, ld_dres,
+                   ld_dx, 1, weight_dtype, weight_offset};
+    const unsigned cols = static_cast<unsigned>((N + kColThreads - 1) / kColThreads);
+    cudaError_t e = cudaSuccess;
+    if (dweight) {
+        // enough CTAs of 128 columns to fill the device, at least 32 rows each
+        a.splits = std::max<int64_t>(1, std::min<int64_t>((M + 31) / 32, 16 * sms / cols));
+        a.splits = std::min<int64_t>(a.splits, 65535);
+        void *scratch = nullptr;
+        rc = owned_scratch(stream, static_cast<size_t>(a.splits) * N * 4, &scratch);
+        if (rc != MBT_OK) return rc;
+        a.partial = static_cast<float *>(scratch);
+        const dim3 grid(cols, static_cast<unsigned>(a.splits));
+        // before dx, which may overwrite dy or h
+        e = dtype == MBT_F16    ? launch(mbt_rmsnorm_dw_rows_kernel<MBT_F16>, grid, kColThreads, s, a)
+            : dtype == MBT_BF16 ? launch(mbt_rmsnorm_dw_rows_kernel<MBT_BF16>, grid, kColThreads, s, a)
+                                : launch(mbt_rmsnorm_dw_rows_kernel<MBT_F32>, grid, kColThreads, s, a);
+        if (e == cudaSuccess) e = launch(mbt_rmsnorm_dw_finish_kernel, dim3(cols), kColThreads, s, a);
+        if (e != cudaSuccess) return MBT_ERR_CUDA;
+    }
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(M, 1 << 20)));
+    e = dtype == MBT_F16    ? launch(mbt_rmsnorm_dx_rows_kernel<MBT_F16>, grid, kRowThreads, s, a)
+        : dtype == MBT_BF16 ? launch(mbt_rmsnorm_dx_rows_kernel<MBT_BF16>, grid, kRowThreads, s, a)
+                            : launch(mbt_rmsnorm_dx_rows_kernel<MBT_F32>, grid, kRowThreads, s, a);
+    return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
+}
