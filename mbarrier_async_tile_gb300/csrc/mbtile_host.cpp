@@ -10,6 +10,7 @@
 #include <tuple>
 
 #include "internal.h"
+#include "mbtile_layer.h"
 
 namespace {
 
@@ -1029,6 +1030,33 @@ int device_limits(int *num_sms, int *smem_optin) {
     if (rc != MBT_OK) return rc;
     *num_sms = d.num_sms;
     *smem_optin = d.smem_optin;
+    return MBT_OK;
+}
+
+int encode_bytes_map(CUtensorMap *map, const void *src, int64_t rows, int64_t row_bytes, int64_t ld,
+                     int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    const int rc = encoder(&fn);
+    if (rc != MBT_OK) return rc;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(mbt::kBoxRowBytes),
+                               static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t elem_strides[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(src), dims,
+                          strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MBT_OK : MBT_ERR_DRIVER;
+}
+
+int device_status_word(int32_t **word) {
+    static int32_t *words[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MBT_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (words[dev] == nullptr && mbt::status_word(&words[dev]) != cudaSuccess) return MBT_ERR_CUDA;
+    *word = words[dev];
     return MBT_OK;
 }
 
