@@ -608,7 +608,10 @@ int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd, cons
  *   zeros         optional, uint8 of the same shape, values 0..15; NULL: 8.
  *   group         32, 64 or 128; K a multiple of 32 (MBT_ERR_UNSUPPORTED).
  * Made for 1 to 8 rows of x; more are taken eight at a time, each reading q
- * again.  A NaN or infinity in row t of x makes values of row t of out NaN or
+ * again.  Where K is sliced over CTAs the slices' sums are added in slice order
+ * (equal calls give equal bits), in the library's workspace for (device,
+ * stream), see tile_rowsum: make the first call on a stream, with the largest
+ * shape, before a capture on it.  A NaN or infinity in row t of x makes values of row t of out NaN or
  * infinite and leaves the other rows alone.  T = 0 or N = 0 does nothing,
  * K = 0 writes zeros.
  */

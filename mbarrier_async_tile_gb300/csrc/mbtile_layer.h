@@ -12,4 +12,20 @@ int encode_bytes_map(CUtensorMap *map, const void *src, int64_t rows, int64_t ro
 // (mbtile_host.cpp)  Address of the current device's status word, looked up once per device.
 int device_status_word(int32_t **word);
 
+// Launch of any grid with programmatic stream serialization; the kernel waits for
+// its predecessor itself.
+template <class K, class A>
+cudaError_t launch_grid(K kernel, dim3 grid, int threads, cudaStream_t stream, const A &a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 }  // namespace mbt

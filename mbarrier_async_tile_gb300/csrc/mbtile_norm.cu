@@ -9,8 +9,8 @@
 // per element: device memory bounds them.  All sums are fp32.
 #include <algorithm>
 
-#include "internal.h"
 #include "mbtile_elem.cuh"
+#include "mbtile_layer.h"
 #include "mbtile_ptx.cuh"
 
 namespace mbt {
@@ -194,20 +194,6 @@ __global__ void __launch_bounds__(kColThreads) mbt_rmsnorm_dw_finish_kernel(cons
     a.dw[j] = sum;
 }
 
-template <class K, class A>
-cudaError_t launch(K kernel, dim3 grid, int threads, cudaStream_t stream, const A &a) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
 int64_t elem_bytes(int dtype) { return dtype == MBT_F32 ? 4 : 2; }
 
 bool float_type(int dtype) { return dtype == MBT_F16 || dtype == MBT_BF16 || dtype == MBT_F32; }
@@ -256,10 +242,10 @@ extern "C" int tile_rmsnorm(const void *x, const void *residual, const void *wei
                      weight_dtype, quant, eps, weight_offset};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(M, 1 << 20)));
-    const cudaError_t e = dtype == MBT_F16 ? launch(mbt_rmsnorm_rows_kernel<MBT_F16>, grid, kRowThreads, s, a)
+    const cudaError_t e = dtype == MBT_F16 ? launch_grid(mbt_rmsnorm_rows_kernel<MBT_F16>, grid, kRowThreads, s, a)
                           : dtype == MBT_BF16
-                              ? launch(mbt_rmsnorm_rows_kernel<MBT_BF16>, grid, kRowThreads, s, a)
-                              : launch(mbt_rmsnorm_rows_kernel<MBT_F32>, grid, kRowThreads, s, a);
+                              ? launch_grid(mbt_rmsnorm_rows_kernel<MBT_BF16>, grid, kRowThreads, s, a)
+                              : launch_grid(mbt_rmsnorm_rows_kernel<MBT_F32>, grid, kRowThreads, s, a);
     return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
 }
 
@@ -303,15 +289,15 @@ extern "C" int tile_rmsnorm_backward(const void *dy, const void *h, const float 
         a.partial = static_cast<float *>(scratch);
         const dim3 grid(cols, static_cast<unsigned>(a.splits));
         // before dx, which may overwrite dy or h
-        e = dtype == MBT_F16    ? launch(mbt_rmsnorm_dw_rows_kernel<MBT_F16>, grid, kColThreads, s, a)
-            : dtype == MBT_BF16 ? launch(mbt_rmsnorm_dw_rows_kernel<MBT_BF16>, grid, kColThreads, s, a)
-                                : launch(mbt_rmsnorm_dw_rows_kernel<MBT_F32>, grid, kColThreads, s, a);
-        if (e == cudaSuccess) e = launch(mbt_rmsnorm_dw_finish_kernel, dim3(cols), kColThreads, s, a);
+        e = dtype == MBT_F16    ? launch_grid(mbt_rmsnorm_dw_rows_kernel<MBT_F16>, grid, kColThreads, s, a)
+            : dtype == MBT_BF16 ? launch_grid(mbt_rmsnorm_dw_rows_kernel<MBT_BF16>, grid, kColThreads, s, a)
+                                : launch_grid(mbt_rmsnorm_dw_rows_kernel<MBT_F32>, grid, kColThreads, s, a);
+        if (e == cudaSuccess) e = launch_grid(mbt_rmsnorm_dw_finish_kernel, dim3(cols), kColThreads, s, a);
         if (e != cudaSuccess) return MBT_ERR_CUDA;
     }
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(M, 1 << 20)));
-    e = dtype == MBT_F16    ? launch(mbt_rmsnorm_dx_rows_kernel<MBT_F16>, grid, kRowThreads, s, a)
-        : dtype == MBT_BF16 ? launch(mbt_rmsnorm_dx_rows_kernel<MBT_BF16>, grid, kRowThreads, s, a)
-                            : launch(mbt_rmsnorm_dx_rows_kernel<MBT_F32>, grid, kRowThreads, s, a);
+    e = dtype == MBT_F16    ? launch_grid(mbt_rmsnorm_dx_rows_kernel<MBT_F16>, grid, kRowThreads, s, a)
+        : dtype == MBT_BF16 ? launch_grid(mbt_rmsnorm_dx_rows_kernel<MBT_BF16>, grid, kRowThreads, s, a)
+                            : launch_grid(mbt_rmsnorm_dx_rows_kernel<MBT_F32>, grid, kRowThreads, s, a);
     return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
 }

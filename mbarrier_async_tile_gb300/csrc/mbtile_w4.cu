@@ -4,34 +4,44 @@
 // The matrix is read once and each of its elements used at most eight times:
 // device memory bounds the large products, latency the small ones.
 //
-// A CTA takes 128 rows of q and a slice of K; a cluster of up to eight CTAs
-// takes the slices of one row block and adds them, in rank order, through
-// distributed shared memory.  Warp roles:
-//   8 consumer warps, 16 rows each;
-//   a producer thread: tiles of 128 rows x 256 columns (128 bytes) of q by bulk
-//   tensor copies into a ring of 128-byte-swizzled stages;
-//   2 staging warps: x and the scales in segments of 512 columns, converted
-//   once per CTA, through a second ring.
+// The work is cut into units of 64 rows of q by a slice of K short enough for
+// its part of x to stay in shared memory; slice by slice, the units are dealt out
+// evenly to the CTAs (two per SM), so that a CTA stages x once or twice.  Warp
+// roles:
+//   8 consumer warps: 16 rows each, the two halves of a step's columns;
+//   a producer thread: steps of 64 rows x 512 columns (two boxes of 64 x 128
+//   bytes) of q by bulk tensor copies into a ring of 128-byte-swizzled stages;
+//   2 staging warps: a step's scales and zero points, converted once per CTA
+//   into the same stages, from registers loaded several steps ahead;
+//   a flush warp: takes a finished unit's sums from the consumers and, where K is
+//   sliced, writes them to the workspace, whose slices a second, small kernel adds
+//   up in order.  (With tickets the last slice's CTA did that: its one warp took 8
+//   us for 11 slices and 8 rows of x.)
 //
-// The products are m16n8k16 tensor instructions with 16 rows of q as A and
+// The products are m16n8k16 tensor instructions with 16 rows of q as A and up to
 // eight rows of x as B.  (Tcgen05's smallest tile has 64 rows against 8 columns
-// and takes both operands from shared memory or its own memory, where q would
-// first have to be written back in 16 bits; here q goes from registers.)
-// An A element is a 4-bit value left where it lies in a 16-bit half: bits 0..3
-// are the fp16 subnormal q 2^-24 and bits 4..7 are q 2^-20, both exact, so
-// extracting eight values costs four ANDs and a shift.  B's elements for bits
-// 4..7 are divided by 16 beforehand.  Which k goes where in the instruction is
-// free as long as A and B agree: a 16-byte chunk of a row (32 columns) is read
-// by ldmatrix as if it held 16-bit elements, which gives the lane of column
-// pair j the bytes 4j..4j+3, columns 8j..8j+7; nibbles i and i + 4 share a half
-// pair.
+// and takes its operands from shared memory or its own memory, where q would first
+// have to be written back in 16 bits; here q goes from registers.  The e4m3 form
+// of the instruction, for which a nibble is a code as it stands, is carried out as
+// two fp16 ones with conversions here: measured, 1.4 times the instructions.)
+//
+// An A element is q - z as fp16, exactly: a 4-bit value put into the mantissa of
+// 1024 (bits 0..3) is 1024 + q, from which 1024 + z is subtracted; in bits 4..7
+// it is 1024 + 16 q, which a multiplication by 1/16 and a subtraction of 64 + z
+// take to the same.  Eight values cost four ANDs with ORs, a shift and four
+// packed fp16 operations.  (Left as fp16 subnormals the values would need no
+// arithmetic, but the tensor unit then aligns its products by the subnormals'
+// nominal exponent and loses up to ten bits: measured, errors of 80 u times the
+// sum of magnitudes in rows with outliers, against 0.3 u.)  Which k goes where in
+// the instruction is free as long as A and B agree: a 16-byte chunk of a row (32
+// columns) is read by ldmatrix as if it held 16-bit elements, which gives the
+// lane of column pair j the bytes 4j..4j+3, columns 8j..8j+7; nibbles i and
+// i + 4 share a half pair.
 //
 // x is scaled by a power of two per row and group (16-bit inputs of any range
 // then fit fp16: values below 2^-29 of the group's largest lose bits, less than
-// fp32 sums do), and each group's product is taken back in fp32:
-//   acc += s 2^24 (p 2^-e - z 2^-24 sum x).
-#include <cooperative_groups.h>
-
+// fp32 sums do), and each group's product p is taken back in fp32:
+//   acc += s 2^-e p.
 #include <algorithm>
 #include <atomic>
 
@@ -42,16 +52,16 @@
 namespace mbt {
 namespace {
 
-constexpr int kW4Rows = 128;              // rows of q per CTA
-constexpr int kW4Step = 256;              // columns per stage of q
-constexpr int kW4Seg = 512;               // columns per segment of x
+constexpr int kW4Rows = 64;               // rows of q per unit
+constexpr int kW4Step = 512;              // columns per stage
 constexpr int kW4Consumers = 8;           // warps
-constexpr int kW4Threads = 32 * (kW4Consumers + 1) + 64;
-constexpr int kW4StageBytes = kW4Rows * kW4Step / 2;
-constexpr int kW4Segs = 2;                // segments of x staged ahead
+constexpr int kW4Stagers = 64;            // threads, one per row of q
+constexpr int kW4Threads = 32 * (kW4Consumers + 2) + kW4Stagers;
+constexpr int kW4BoxBytes = kW4Rows * kBoxRowBytes;
+constexpr int kW4QBytes = 2 * kW4BoxBytes;
 constexpr int kW4Tokens = 8;
-constexpr int kW4MaxSlices = 8;           // portable cluster size
-constexpr int kW4MaxSmem = 104 * 1024;    // dynamic; two CTAs fit an SM
+// Bytes of a unit's part of x, which with the stages leave room for two CTAs per SM.
+constexpr int kW4XBytes = 36352;
 
 struct W4Args {
     const void *x;
@@ -63,8 +73,13 @@ struct W4Args {
     int64_t groups, x_groups;   // scales of a row of q, of a row of x
     int32_t xdt, sdt, odt;
     int32_t x_row_scale;        // e4m3: a scale per row of x, else per 128 columns
-    int32_t slices;             // CTAs of a cluster, along K
-    int32_t vec_scales;         // a segment's scales of a row are aligned vectors
+    int32_t slices;             // of K, in whole steps
+    int32_t slice_steps;        // steps of the longest slice
+    int32_t x_rows;             // most rows of x in a unit
+    int64_t blocks;             // of 64 rows of q
+    int64_t units;              // eights of rows of x * slices * blocks
+    float *partial;             // [t][slice][64 blocks], with more than one slice
+    int32_t vec_scales;         // a step's 16-bit scales of a row are aligned vectors
     int32_t vec_zeros;
     int32_t vec_x;              // eight columns of x are one aligned vector
     int32_t *status;
@@ -77,369 +92,493 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
                  : "memory");
 }
 
+// c = a b + (FIRST ? 0 : c)
+template <bool FIRST>
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
-        " {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    const float z = 0.f;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(FIRST ? z : c[0]),
+          "f"(FIRST ? z : c[1]), "f"(FIRST ? z : c[2]), "f"(FIRST ? z : c[3]));
 }
-
-struct W4Rings {
-    uint32_t q, x;              // shared-memory addresses of the rings
-    uint32_t x_bytes;           // x's part of a segment buffer
-    uint32_t seg_bytes;         // x, then {2^-e, 2^-24 sum x} per group and token, then
-                                // {s 2^24, z} per group and row of q
-    uint32_t full_q, empty_q, full_x, empty_x;
-};
 
 template <int G>
-struct W4Seg {
-    static constexpr int kGroups = kW4Seg / G;
-    static constexpr int kMeta = kGroups * kW4Tokens * 8;
-    static constexpr int kScales = kGroups * kW4Rows * 8;
-    // Stages of q: what is left of half an SM's shared memory beside the two
-    // segments (of small groups there are more scales).
-    static constexpr int kStages = G == 32 ? 3 : 4;
+struct W4Step {
+    static constexpr int kGroups = kW4Step / G;
+    static constexpr int kScales = kGroups * kW4Rows * 8;   // {s, fp16 pair 1024 + z} per group and row
+    static constexpr int kStage = kW4QBytes + kScales;      // a multiple of 1024
+    static constexpr int kStages = G == 128 ? 4 : 3;
 };
 
-// Rows r and r + 8 of a warp's 16 are neighbours, so one 16-byte read gives a
-// consumer lane both of its rows.
-__device__ __forceinline__ int scale_slot(int row) {
-    return (row & ~15) | (row & 7) << 1 | (row >> 3 & 1);
+// Code that runs once per CTA, or for unaligned arrays only, is kept out of line
+// or in rolled loops: the first pass over any instruction misses the caches.
+
+// Eight columns of x at any alignment.
+__device__ __noinline__ uint4 load_x_elements(const void *x, int xdt, int64_t at) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (xdt == MBT_E4M3) {
+        const uint8_t *p = static_cast<const uint8_t *>(x) + at;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            v.x |= static_cast<uint32_t>(p[i]) << (8 * i);
+            v.y |= static_cast<uint32_t>(p[4 + i]) << (8 * i);
+        }
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(x) + at;
+        v.x = p[0] | static_cast<uint32_t>(p[1]) << 16;
+        v.y = p[2] | static_cast<uint32_t>(p[3]) << 16;
+        v.z = p[4] | static_cast<uint32_t>(p[5]) << 16;
+        v.w = p[6] | static_cast<uint32_t>(p[7]) << 16;
+    }
+    return v;
 }
 
-// A staging thread's two rows of the scales of segment `seg`.
-template <int G, bool S32>
-__device__ __forceinline__ void stage_scales(const W4Args &a, int64_t seg, int64_t row0, int u,
-                                             uint32_t dst) {
-    constexpr int kGroups = kW4Seg / G;
-    constexpr int kWords = S32 ? kGroups : kGroups / 2;
-    const int64_t g0 = seg * kGroups;
+__device__ __forceinline__ uint4 load_x(const W4Args &a, int64_t at) {
+    if (!a.vec_x) return load_x_elements(a.x, a.xdt, at);
+    if (a.xdt == MBT_E4M3) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.x) + at));
+        return make_uint4(q.x, q.y, 0, 0);
+    }
+    return __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at));
+}
+
+// Eight columns of x (as loaded) as B elements, scaled by 2^e with the e of their
+// group, `lanes` neighbouring lanes, which is returned as 2^-e in *down.
+__device__ __noinline__ uint4 convert_x(uint4 v, int xdt, int lanes, float *down) {
+    float f[8];
+    if (xdt == MBT_E4M3) {
+        uint32_t h[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int local = u + 64 * h;
-        const int64_t row = row0 + local;
-        uint32_t w[kWords] = {};
-        uint32_t z[(kGroups + 3) / 4];
+        for (int j = 0; j < 4; ++j) h[j] = e4m3x2_to_half2((j < 2 ? v.x : v.y) >> (16 * (j & 1)));
+        v = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    // 16-bit magnitudes order as integers, NaN above infinity
+    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                          __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    m = max(m & 0xffffu, m >> 16);
+#pragma unroll 1
+    for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    uint32_t top;                           // bits of the largest magnitude, as fp32
+    if (xdt == MBT_BF16) {
+        unpack<MBT_BF16>(v, f);
+        top = m << 16;
+    } else {
+        unpack<MBT_F16>(v, f);
+        top = __float_as_uint(Elem<MBT_F16>::widen2(m).x);
+    }
+    // 2^e brings the group's largest value into [2^14, 2^15); a group of zeros or
+    // with an infinity or NaN is left as it is
+    const int eb = static_cast<int>(top >> 23);
+    const int e = top == 0 || eb == 255 ? 0 : min(14 - (eb - 127), 126);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
-        for (int i = 0; i < (kGroups + 3) / 4; ++i) z[i] = 0x08080808u;
-        if (row < a.N) {
-            const int64_t at = row * a.groups + g0;
-            const char *s = static_cast<const char *>(a.s) + at * (S32 ? 4 : 2);
-            if (a.vec_scales && g0 + kGroups <= a.groups) {
-                if constexpr (kWords == 2) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(s));
-                    w[0] = v.x, w[1] = v.y;
-                } else {
+    for (int j = 0; j < 8; ++j) f[j] *= up;
+    *down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    return make_uint4(Elem<MBT_F16>::round2(f[0], f[4]), Elem<MBT_F16>::round2(f[1], f[5]),
+                      Elem<MBT_F16>::round2(f[2], f[6]), Elem<MBT_F16>::round2(f[3], f[7]));
+}
+
+// Bytes of a row of x in shared memory: rows lie 64 bytes apart in the banks, so
+// that a warp's reads of 8 rows x 64 bytes do not collide.
+__host__ __device__ constexpr int x_pitch(int columns) { return columns * 2 + 64; }
+
+// Columns [k0, k0 + columns) of up to eight rows of x as B elements at xbuf, and
+// 2^-e of each group at meta, [group][8].  All consumer threads take part; columns
+// is a multiple of kW4Step.
+template <int G>
+__device__ __forceinline__ void stage_x(const W4Args &a, int64_t k0, int columns, int64_t t0,
+                                        int tokens, unsigned char *xbuf, int pitch, float *meta) {
+    constexpr int kBatch = 4, kThreads = 32 * kW4Consumers;   // kBatch loads in flight per thread
+    const int per_row = columns / 8, units = per_row * tokens;
+    for (int i0 = threadIdx.x; i0 < units; i0 += kThreads * kBatch) {
+        uint4 raw[kBatch];
+        float xs[kBatch];
 #pragma unroll
-                    for (int i = 0; i < kWords / 4; ++i) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(s) + i);
-                        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-                    }
-                }
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kThreads;
+            const int t = i / per_row, u = i - t * per_row;
+            const int64_t k = k0 + 8 * u;
+            raw[b] = make_uint4(0, 0, 0, 0);
+            xs[b] = 1.f;
+            if (i >= units || k >= a.K) continue;
+            raw[b] = load_x(a, (t0 + t) * a.ld_x + k);
+            if (a.xs) xs[b] = __ldg(a.xs + (t0 + t) * a.x_groups + (a.x_row_scale ? 0 : k / 128));
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kThreads;
+            if (i >= units) break;          // whole warps: units is a multiple of 64
+            const int t = i / per_row, u = i - t * per_row;
+            float down;
+            const uint4 v = convert_x(raw[b], a.xdt, G / 8, &down);
+            *reinterpret_cast<uint4 *>(xbuf + t * pitch + u * 16) = v;
+            if (u % (G / 8) == 0) meta[u / (G / 8) * kW4Tokens + t] = down * xs[b];
+        }
+    }
+}
+
+// Element i of a row's scales or zero points, any type.
+__device__ __noinline__ uint32_t load_scale_bits(const void *s, int sdt, int64_t at) {
+    return sdt == MBT_F32 ? __ldg(static_cast<const uint32_t *>(s) + at)
+                          : __ldg(static_cast<const uint16_t *>(s) + at);
+}
+
+// A staging thread's row of a step's scales and zero points, as loaded.
+template <int G>
+struct RowScales {
+    static constexpr int kGroups = kW4Step / G;
+    uint32_t s[kGroups / 2];                // 16-bit scales
+    uint32_t z[kGroups / 4];
+
+    __device__ __forceinline__ void load(const W4Args &a, int64_t row, int64_t g0) {
+#pragma unroll
+        for (int i = 0; i < kGroups / 2; ++i) s[i] = 0;
+#pragma unroll
+        for (int i = 0; i < kGroups / 4; ++i) z[i] = 0x08080808u;
+        if (row >= a.N) return;
+        const int64_t at = row * a.groups + g0;
+        const bool whole = g0 + kGroups <= a.groups;
+        if (a.vec_scales && whole) {
+            const uint16_t *p = static_cast<const uint16_t *>(a.s) + at;
+            if constexpr (kGroups == 4) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+                s[0] = v.x, s[1] = v.y;
             } else {
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i) {
-                    if (g0 + i >= a.groups) continue;
-                    if constexpr (S32)
-                        w[i] = __ldg(reinterpret_cast<const uint32_t *>(s) + i);
-                    else
-                        w[i / 2] |=
-                            static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(s) + i))
-                            << (16 * (i & 1));
-                }
-            }
-            if (a.z) {
-                if (a.vec_zeros && g0 + kGroups <= a.groups) {
-#pragma unroll
-                    for (int i = 0; i < kGroups / 4; ++i)
-                        z[i] = __ldg(reinterpret_cast<const uint32_t *>(a.z + at) + i);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kGroups; ++i) {
-                        if (i % 4 == 0) z[i / 4] = 0;
-                        if (g0 + i < a.groups)
-                            z[i / 4] |= static_cast<uint32_t>(__ldg(a.z + at + i)) << (8 * (i % 4));
-                    }
+                for (int i = 0; i < kGroups / 8; ++i) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                    s[4 * i] = v.x, s[4 * i + 1] = v.y, s[4 * i + 2] = v.z, s[4 * i + 3] = v.w;
                 }
             }
         }
-        const uint32_t slot = dst + 8u * static_cast<uint32_t>(scale_slot(local));
+        if (a.z && a.vec_zeros && whole) {
 #pragma unroll
+            for (int i = 0; i < kGroups / 4; ++i)
+                z[i] = __ldg(reinterpret_cast<const uint32_t *>(a.z + at) + i);
+        }
+    }
+
+    // Rows n and n + 8 of a warp's 16 lie side by side, so that one 16-byte read
+    // gives a consumer lane both of its rows.
+    __device__ __forceinline__ void store(const W4Args &a, int64_t row, int64_t g0, int local,
+                                          uint2 *dst) const {
+        const int slot = (local & ~15) | (local & 7) << 1 | (local >> 3 & 1);
+        const bool whole = g0 + kGroups <= a.groups;
+        if (a.vec_scales && whole && (a.z == nullptr || a.vec_zeros)) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const uint32_t b = s[i / 2] >> (16 * (i & 1));
+                const float v = a.sdt == MBT_BF16 ? __uint_as_float(b << 16) : Elem<MBT_F16>::widen2(b).x;
+                const uint32_t zero = (0x6400u | (z[i / 4] >> (8 * (i % 4)) & 15u)) * 0x10001u;
+                dst[i * kW4Rows + slot] = make_uint2(__float_as_uint(v), zero);
+            }
+            return;
+        }
+        // other types and alignments, and a row's end (0 past it): element by element
+#pragma unroll 1
         for (int i = 0; i < kGroups; ++i) {
-            float v;
-            if constexpr (S32) {
-                v = __uint_as_float(w[i]);
-            } else {
-                const uint32_t b = w[i / 2] >> (16 * (i & 1));
-                v = a.sdt == MBT_BF16 ? __uint_as_float(b << 16) : Elem<MBT_F16>::widen2(b).x;
-            }
-            const float zero = static_cast<float>(z[i / 4] >> (8 * (i % 4)) & 0xffu);
-            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(slot + i * (8u * kW4Rows)),
-                         "f"(v * 16777216.f), "f"(zero)
-                         : "memory");
+            const bool in = row < a.N && g0 + i < a.groups;
+            const int64_t at = row * a.groups + g0 + i;
+            const uint32_t b = in ? load_scale_bits(a.s, a.sdt, at) : 0u;
+            const uint32_t zero = in && a.z ? a.z[at] & 15u : 8u;
+            const float v = a.sdt == MBT_F32    ? __uint_as_float(b)
+                            : a.sdt == MBT_BF16 ? __uint_as_float(b << 16)
+                                                : Elem<MBT_F16>::widen2(b).x;
+            dst[i * kW4Rows + slot] = make_uint2(__float_as_uint(v), (0x6400u | zero) * 0x10001u);
         }
+    }
+};
+
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
+__device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+
+// Nibbles 0 and 4 of w, less z (z1024 = 1024 + z), from bits 0..3 of each half.
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t w, __half2 z1024) {
+    return as_bits(__hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), z1024));
+}
+
+// Nibbles 1 and 5 of w, less z (z64 = -(64 + z)), from bits 4..7 of each half.
+__device__ __forceinline__ uint32_t high_nibbles(uint32_t w, __half2 z64) {
+    return as_bits(__hfma2(as_half2((w & 0x00f000f0u) | 0x64006400u), as_half2(0x2c002c00u), z64));
+}
+
+// wait_bounded with its first probe in line.
+__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    return mbar_try_wait(bar, parity) || wait_bounded(bar, parity, w, true);
+}
+
+// Four consecutive outputs of row t, those below N.
+__device__ __noinline__ void store_y(const W4Args &a, int64_t t, int64_t n, float4 y) {
+#pragma unroll 1
+    for (int k = 0; k < 4 && n + k < a.N; ++k) {
+        store_any(a.out, a.odt, t * a.ld_out + n + k, y.x);
+        y.x = y.y, y.y = y.z, y.z = y.w;
     }
 }
 
-// A staging warp's half of segment `seg`: 8 columns a lane, every row of x.
+// A CTA's run of units, and what unit i is.
+struct W4Unit {
+    int64_t t0, block, slice, step0, step1;   // first row of x, block of q, slice, its steps
+    int tokens;
+    __device__ __forceinline__ W4Unit(const W4Args &a, int64_t i) {
+        const int64_t steps = (a.K + kW4Step - 1) / kW4Step;
+        block = i % a.blocks;
+        const int64_t r = i / a.blocks;
+        slice = r % a.slices;
+        t0 = r / a.slices * kW4Tokens;
+        tokens = static_cast<int>(a.T - t0 < kW4Tokens ? a.T - t0 : kW4Tokens);
+        step0 = slice * steps / a.slices;
+        step1 = (slice + 1) * steps / a.slices;
+    }
+};
+
 template <int G>
-__device__ __forceinline__ void stage_x(const W4Args &a, int64_t seg, int64_t t0, int tokens, int u,
-                                        uint32_t xbuf, uint32_t meta) {
-    const int64_t k = seg * kW4Seg + 8 * u;
-    const bool in = k < a.K;
-    uint4 raw[kW4Tokens];
-#pragma unroll
-    for (int t = 0; t < kW4Tokens; ++t) {
-        raw[t] = make_uint4(0, 0, 0, 0);
-        if (t >= tokens || !in) continue;
-        const int64_t at = (t0 + t) * a.ld_x + k;
-        if (a.xdt == MBT_E4M3) {
-            const uint8_t *p = static_cast<const uint8_t *>(a.x) + at;
-            uint2 v;
-            if (a.vec_x) {
-                v = __ldg(reinterpret_cast<const uint2 *>(p));
-            } else {
-                v = make_uint2(0, 0);
-                for (int i = 0; i < 4; ++i) {
-                    v.x |= static_cast<uint32_t>(p[i]) << (8 * i);
-                    v.y |= static_cast<uint32_t>(p[4 + i]) << (8 * i);
-                }
-            }
-            raw[t].x = v.x;
-            raw[t].y = v.y;
-        } else {
-            const uint16_t *p = static_cast<const uint16_t *>(a.x) + at;
-            if (a.vec_x) {
-                raw[t] = __ldg(reinterpret_cast<const uint4 *>(p));
-            } else {
-                raw[t].x = p[0] | static_cast<uint32_t>(p[1]) << 16;
-                raw[t].y = p[2] | static_cast<uint32_t>(p[3]) << 16;
-                raw[t].z = p[4] | static_cast<uint32_t>(p[5]) << 16;
-                raw[t].w = p[6] | static_cast<uint32_t>(p[7]) << 16;
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < kW4Tokens; ++t) {
-        if (t >= tokens) break;
-        float f[8];
-        float factor = 1.f;
-        if (a.xdt == MBT_E4M3) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 h = Elem<MBT_F16>::widen2(
-                    e4m3x2_to_half2((i < 2 ? raw[t].x : raw[t].y) >> (16 * (i & 1))));
-                f[2 * i] = h.x;
-                f[2 * i + 1] = h.y;
-            }
-            if (in) factor = __ldg(a.xs + (t0 + t) * a.x_groups + (a.x_row_scale ? 0 : k / 128));
-        } else if (a.xdt == MBT_BF16) {
-            unpack<MBT_BF16>(raw[t], f);
-        } else {
-            unpack<MBT_F16>(raw[t], f);
-        }
-        uint32_t amax = 0;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            amax = max(amax, magnitude(f[i]));
-            sum += f[i];
-        }
-#pragma unroll
-        for (int o = 1; o < G / 8; o <<= 1) {
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        }
-        // 2^e brings the group's largest value into [2^14, 2^15); a group of
-        // zeros or with an infinity or NaN is left as it is
-        const int eb = static_cast<int>(amax >> 23);
-        const int e = amax == 0 || eb == 255 ? 0 : min(max(14 - (eb - 127), -126), 126);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= up;
-        const uint4 v = make_uint4(Elem<MBT_F16>::round2(f[0], f[4]),
-                                   Elem<MBT_F16>::round2(f[1] * 0.0625f, f[5] * 0.0625f),
-                                   Elem<MBT_F16>::round2(f[2], f[6]),
-                                   Elem<MBT_F16>::round2(f[3] * 0.0625f, f[7] * 0.0625f));
-        const uint32_t dst = xbuf + 16u * static_cast<uint32_t>(((u >> 2) * tokens + t) * 4 + (u & 3));
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y),
-                     "r"(v.z), "r"(v.w)
-                     : "memory");
-        if (u % (G / 8) == 0) {
-            const uint32_t m = meta + 64u * static_cast<uint32_t>(u / (G / 8)) + 8u * t;
-            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(m), "f"(down * factor),
-                         "f"(sum * factor * 5.9604644775390625e-8f)
-                         : "memory");
-        }
-    }
-}
-
-// acc += s 2^24 (p 2^-e - z 2^-24 sum x) of the lane's two rows of q and of x; p = 0.
-__device__ __forceinline__ void flush_group(float (&acc)[4], float (&p)[4], uint32_t scales,
-                                            uint32_t meta) {
-    const uint4 m = lds128(meta), v = lds128(scales);
-    const float f0 = __uint_as_float(m.x), x0 = __uint_as_float(m.y);
-    const float f1 = __uint_as_float(m.z), x1 = __uint_as_float(m.w);
-    const float sl = __uint_as_float(v.x), zl = __uint_as_float(v.y);
-    const float sh = __uint_as_float(v.z), zh = __uint_as_float(v.w);
-    acc[0] += sl * (p[0] * f0 - zl * x0);
-    acc[1] += sl * (p[1] * f1 - zl * x1);
-    acc[2] += sh * (p[2] * f0 - zh * x0);
-    acc[3] += sh * (p[3] * f1 - zh * x1);
-    p[0] = p[1] = p[2] = p[3] = 0.f;
-}
-
-template <int G, bool S32>
 __global__ void __launch_bounds__(kW4Threads, 2)
-    mbt_w4_kernel(const __grid_constant__ CUtensorMap map, const W4Args a) {
-    constexpr int kStages = W4Seg<G>::kStages;
+    mbt_w4_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ W4Args a) {
     extern __shared__ __align__(1024) unsigned char dyn_smem[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kW4Segs];
+    constexpr int kStages = W4Step<G>::kStages;
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 2];
     __shared__ int abort_flag;
-    __shared__ float red[kW4Tokens][kW4Rows];
+    __shared__ __align__(16) float red[2][kW4Tokens][kW4Rows];   // [half of the columns]
+    using Step = W4Step<G>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * kW4Tokens;
-    const int tokens = static_cast<int>(a.T - t0 < kW4Tokens ? a.T - t0 : kW4Tokens);
-    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.slices));
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(a.slices)) * kW4Rows;
-    const int64_t segs = (a.K + kW4Seg - 1) / kW4Seg;
-    const int64_t seg0 = rank * segs / a.slices, seg1 = (rank + 1) * segs / a.slices;
-    const int64_t all_steps = (a.K + kW4Step - 1) / kW4Step;
-    const int64_t step0 = seg0 * 2, step1 = seg1 * 2 < all_steps ? seg1 * 2 : all_steps;
-    W4Rings r;
-    r.q = (smem_u32(dyn_smem) + (kSwizzleAtomBytes - 1)) & ~uint32_t(kSwizzleAtomBytes - 1);
-    r.x = r.q + kStages * kW4StageBytes;
-    r.x_bytes = static_cast<uint32_t>(kW4Seg * 2 * tokens);
-    r.seg_bytes = r.x_bytes + W4Seg<G>::kMeta + W4Seg<G>::kScales;
-    r.full_q = smem_u32(bars);
-    r.empty_q = r.full_q + 8 * kStages;
-    r.full_x = r.empty_q + 8 * kStages;
-    r.empty_x = r.full_x + 8 * kW4Segs;
+    // (aligned by its address in the shared window, as the swizzle is)
+    unsigned char *const ring = dyn_smem + ((0u - smem_u32(dyn_smem)) & (kSwizzleAtomBytes - 1));
+    unsigned char *const xbuf = ring + Step::kStages * Step::kStage;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages;
+    const uint32_t full_r = empty + 8 * kStages, empty_r = full_r + 8;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(r.full_q + 8 * i, 1);
-            mbar_init(r.empty_q + 8 * i, kW4Consumers);
+            mbar_init(full + 8 * i, 1 + kW4Stagers);
+            mbar_init(empty + 8 * i, kW4Consumers);
         }
-        for (int i = 0; i < kW4Segs; ++i) {
-            mbar_init(r.full_x + 8 * i, 64);
-            mbar_init(r.empty_x + 8 * i, kW4Consumers);
-        }
+        mbar_init(full_r, kW4Consumers);
+        mbar_init(empty_r, 1);
         abort_flag = 0;
         fence_barrier_init();
     }
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const WaitCtl w{kDefaultWaitBudgetNs, &abort_flag, a.status};
+    const int64_t u0 = blockIdx.x * a.units / gridDim.x, u1 = (blockIdx.x + 1) * a.units / gridDim.x;
 
-    if (warp == kW4Consumers) {
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 1;
-            int64_t issued = 0;
-            for (int64_t s = step0; s < step1; ++s) {
-                if (!wait_bounded(r.empty_q + 8 * stage, phase, w, true)) {
+    if (warp == kW4Consumers) {                 // producer
+        if (lane != 0) return;
+        uint32_t stage = 0, phase = 1;
+        int64_t issued = 0;
+        for (int64_t i = u0; i < u1; ++i) {
+            const W4Unit u(a, i);
+            for (int64_t s = u.step0; s < u.step1; ++s) {
+                if (!arrived(empty + 8 * stage, phase, w)) {
                     report_timeout(w, 0, stage, phase);
                     abort_flag = 1;
-                    // the copies still in flight land before the CTA leaves
+                    // the copies still in flight land before the CTA leaves (the
+                    // stagers' arrivals may be missing: the wait is bounded)
                     for (int64_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
-                        wait_bounded(r.full_q + 8 * static_cast<uint32_t>(k % kStages),
+                        wait_bounded(full + 8 * static_cast<uint32_t>(k % kStages),
                                      static_cast<uint32_t>(k / kStages & 1), w, false);
-                    break;
+                    return;
                 }
-                mbar_arrive_expect_tx(r.full_q + 8 * stage, kW4StageBytes);
-                tma_load_2d(r.q + stage * kW4StageBytes, &map, static_cast<int32_t>(s * (kW4Step / 2)),
-                            static_cast<int32_t>(row0), r.full_q + 8 * stage);
+                mbar_arrive_expect_tx(full + 8 * stage, kW4QBytes);
+                const uint32_t dst = smem_u32(ring) + stage * Step::kStage;
+                const int32_t col = static_cast<int32_t>(s * (kW4Step / 2));
+                const int32_t row = static_cast<int32_t>(u.block * kW4Rows);
+                tma_load_2d(dst, &map, col, row, full + 8 * stage);
+                tma_load_2d(dst + kW4BoxBytes, &map, col + kBoxRowBytes, row, full + 8 * stage);
                 ++issued;
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
         }
-    } else if (warp > kW4Consumers) {
-        const int u = static_cast<int>(threadIdx.x) - 32 * (kW4Consumers + 1);
-        uint32_t buf = 0, phase = 1;
-        for (int64_t s = seg0; s < seg1; ++s) {
-            // (a warp goes on, or gives up, as one)
-            if (!__all_sync(0xffffffffu, wait_bounded(r.empty_x + 8 * buf, phase, w, true))) {
-                report_timeout(w, 0, kMaxStages + buf, phase);
+        return;
+    }
+
+    if (warp == kW4Consumers + 1) {             // flush
+        uint32_t phase = 0;
+        for (int64_t i = u0; i < u1; ++i, phase ^= 1) {
+            const W4Unit u(a, i);
+            if (!__all_sync(0xffffffffu, arrived(full_r, phase, w))) {
+                report_timeout(w, 1, kMaxStages, phase);
                 abort_flag = 1;
-                break;
+                return;
             }
-            const uint32_t at = r.x + buf * r.seg_bytes;
-            stage_scales<G, S32>(a, s, row0, u, at + r.x_bytes + W4Seg<G>::kMeta);
-            stage_x<G>(a, s, t0, tokens, u, at, at + r.x_bytes);
-            mbar_arrive(r.full_x + 8 * buf);
-            if (++buf == kW4Segs) buf = 0, phase ^= 1;
+            // lane: four rows of q, every other row of x
+            const int n = (lane & 15) * 4;
+            const int64_t n0 = u.block * kW4Rows + n;
+#pragma unroll 1
+            for (int t = lane >> 4; t < u.tokens; t += 2) {
+                const float4 lo = *reinterpret_cast<const float4 *>(&red[0][t][n]);
+                const float4 hi = *reinterpret_cast<const float4 *>(&red[1][t][n]);
+                const float4 y = make_float4(lo.x + hi.x, lo.y + hi.y, lo.z + hi.z, lo.w + hi.w);
+                if (a.slices == 1)
+                    store_y(a, u.t0 + t, n0, y);
+                else
+                    *reinterpret_cast<float4 *>(a.partial + ((u.t0 + t) * a.slices + u.slice) * a.blocks * kW4Rows + n0) = y;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_r);
         }
-    } else {
-        // ldmatrix: lane l gives the address of row l % 8 (+ 8 for odd eights) of chunk l / 16
-        const int lrow = warp * 16 + (lane & 15);
-        const uint32_t laddr = static_cast<uint32_t>(lrow) * 128u;
-        const uint32_t lchunk = static_cast<uint32_t>(lane >> 4), lswz = static_cast<uint32_t>(lrow & 7);
-        const int tok = lane >> 2 < tokens ? lane >> 2 : tokens - 1;
-        const uint32_t xlane = static_cast<uint32_t>(tok * 4 + (lane & 3)) * 16u;
-        const uint32_t xchunk = static_cast<uint32_t>(tokens) * 64u;
-        constexpr int kN = kW4Step / G;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f}, p[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t stage = 0, phase = 0, buf = 0, xphase = 0;
-        for (int64_t s = step0; s < step1; ++s) {
-            bool ok = (s & 1) || wait_bounded(r.full_x + 8 * buf, xphase, w, true);
-            ok = ok && wait_bounded(r.full_q + 8 * stage, phase, w, true);
-            if (!__all_sync(0xffffffffu, ok)) {
+        return;
+    }
+
+    if (warp > kW4Consumers) {                  // staging warps
+        constexpr int kAhead = G == 32 ? 2 : 4;   // steps loaded ahead
+        const int local = static_cast<int>(threadIdx.x) - 32 * (kW4Consumers + 2);
+        RowScales<G> r[kAhead];
+        // two walks over the same steps: one loads, the other stores kAhead steps later
+        int64_t li = u0, ls = 0, le = 0, lrow = 0;
+        if (li < u1) {
+            const W4Unit u(a, li);
+            ls = u.step0, le = u.step1, lrow = u.block * kW4Rows + local;
+        }
+        auto load_next = [&](RowScales<G> &into) {
+            if (li >= u1) return;
+            into.load(a, lrow, ls * Step::kGroups);
+            if (++ls == le && ++li < u1) {
+                const W4Unit u(a, li);
+                ls = u.step0, le = u.step1, lrow = u.block * kW4Rows + local;
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) load_next(r[k]);
+        uint32_t stage = 0, phase = 1;
+        int64_t i = u0, s = 0, e = 0, row = 0;
+        if (i < u1) {
+            const W4Unit u(a, i);
+            s = u.step0, e = u.step1, row = u.block * kW4Rows + local;
+        }
+        while (i < u1) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (i >= u1) break;
+                // (a warp goes on, or gives up, as one)
+                if (!__all_sync(0xffffffffu, arrived(empty + 8 * stage, phase, w))) {
+                    report_timeout(w, 0, stage, phase);
+                    abort_flag = 1;
+                    return;
+                }
+                r[k].store(a, row, s * Step::kGroups, local,
+                           reinterpret_cast<uint2 *>(ring + stage * Step::kStage + kW4QBytes));
+                mbar_arrive(full + 8 * stage);
+                if (++stage == kStages) stage = 0, phase ^= 1;
+                load_next(r[k]);
+                if (++s == e && ++i < u1) {
+                    const W4Unit u(a, i);
+                    s = u.step0, e = u.step1, row = u.block * kW4Rows + local;
+                }
+            }
+        }
+        return;
+    }
+
+    // consumers: rows 16 (warp % 4) .. of the unit, half warp / 4 of a step's columns
+    const int half = warp >> 2, rows = (warp & 3) * 16;
+    // ldmatrix: lane l gives the address of row l % 16 of chunk l / 16
+    const int lrow = rows + (lane & 15);
+    const uint32_t lbase = smem_u32(ring) + half * kW4BoxBytes + static_cast<uint32_t>(lrow) * 128u;
+    const uint32_t lchunk = static_cast<uint32_t>(lane >> 4), lswz = static_cast<uint32_t>(lrow & 7);
+    constexpr int kHalfGroups = Step::kGroups / 2;
+    uint32_t stage = 0, phase = 0, rphase = 1;
+    int64_t staged = -1;                        // slice (of eight rows of x) in xbuf
+    bool alive = true;                          // no wait of this warp has run out
+    for (int64_t i = u0; i < u1; ++i) {
+        const W4Unit u(a, i);
+        const int pitch = x_pitch(a.slice_steps * kW4Step);
+        float *const meta = reinterpret_cast<float *>(xbuf + pitch * a.x_rows);
+        if (i / a.blocks != staged) {
+            // a warp whose wait has run out still takes part in the barriers
+            staged = i / a.blocks;
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Consumers) : "memory");
+            stage_x<G>(a, u.step0 * kW4Step, static_cast<int>(u.step1 - u.step0) * kW4Step, u.t0,
+                       u.tokens, xbuf, pitch, meta);
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Consumers) : "memory");
+        }
+        const int tok = lane >> 2 < u.tokens ? lane >> 2 : u.tokens - 1;
+        const uint4 *x = reinterpret_cast<const uint4 *>(xbuf + tok * pitch) + (lane & 3) + half * 32;
+        const float2 *m = reinterpret_cast<const float2 *>(meta) + half * kHalfGroups * 4 + (lane & 3);
+        float acc[4] = {};
+        for (int64_t s = u.step0; s < u.step1 && alive; ++s) {
+            if (!__all_sync(0xffffffffu, arrived(full + 8 * stage, phase, w))) {
                 report_timeout(w, 1, stage, phase);
                 abort_flag = 1;
+                alive = false;
                 break;
             }
-            const uint32_t q = r.q + stage * kW4StageBytes + laddr;
-            const uint32_t half = static_cast<uint32_t>(s & 1);
-            const uint32_t seg = r.x + buf * r.seg_bytes;
-            const uint32_t x = seg + half * 8u * xchunk + xlane;
-            const uint32_t meta = seg + r.x_bytes + half * kN * 64u + (lane & 3) * 16u;
-            const uint32_t scales = seg + r.x_bytes + W4Seg<G>::kMeta +
-                                    half * kN * (8u * kW4Rows) + static_cast<uint32_t>(warp * 128 + (lane >> 2) * 16);
-            uint32_t v[4][4];
+            const uint32_t q = lbase + stage * Step::kStage;
+            const uint4 *scales =
+                reinterpret_cast<const uint4 *>(ring + stage * Step::kStage + kW4QBytes) +
+                half * kHalfGroups * (kW4Rows / 2) + rows / 2 + (lane >> 2);
+            // 64 columns a turn (128 where a group has them): a body that stays in
+            // the instruction cache next to the scheduler
+            constexpr int kChunks = G / 32 > 2 ? G / 32 : 2;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 8; c0 += kChunks) {
+                float p[4], p2[4], sl, sh;
+                __half2 zl, zh, zl64, zh64;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ldmatrix_x4(v[c], q + ((2u * c + lchunk) ^ lswz) * 16u);
+                for (int c = 0; c < kChunks; c += 2) {
+                    uint32_t v[4];
+                    ldmatrix_x4(v, q + ((static_cast<uint32_t>(c0 + c) + lchunk) ^ lswz) * 16u);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int k = (c + h) * 32;
+                        const uint4 b = x[4 * (c + h)];
+                        if (k % G == 0) {
+                            const uint4 s = scales[k / G * (kW4Rows / 2)];
+                            sl = __uint_as_float(s.x);
+                            sh = __uint_as_float(s.z);
+                            zl = as_half2(s.y);
+                            zh = as_half2(s.w);
+                            zl64 = __hsub2(as_half2(0x63806380u), zl);   // 960 - (1024 + z)
+                            zh64 = __hsub2(as_half2(0x63806380u), zh);
+                        }
+                        const uint32_t lo = v[2 * h], hi = v[2 * h + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+                        const uint32_t a0 = low_nibbles(lo, zl), a1 = low_nibbles(hi, zh);
+                        const uint32_t a2 = high_nibbles(lo, zl64), a3 = high_nibbles(hi, zh64);
+                        const uint32_t a4 = low_nibbles(lo8, zl), a5 = low_nibbles(hi8, zh);
+                        const uint32_t a6 = high_nibbles(lo8, zl64), a7 = high_nibbles(hi8, zh64);
+                        if (k % G == 0) {
+                            mma_f16<true>(p, a0, a1, a2, a3, b.x, b.y);
+                            mma_f16<true>(p2, a4, a5, a6, a7, b.z, b.w);
+                        } else {
+                            mma_f16<false>(p, a0, a1, a2, a3, b.x, b.y);
+                            mma_f16<false>(p2, a4, a5, a6, a7, b.z, b.w);
+                        }
+                        if ((k + 32) % G != 0) continue;
+                        const float2 f = m[k / G * 4];
+                        const float f0l = f.x * sl, f1l = f.y * sl, f0h = f.x * sh, f1h = f.y * sh;
+                        acc[0] += (p[0] + p2[0]) * f0l;
+                        acc[1] += (p[1] + p2[1]) * f1l;
+                        acc[2] += (p[2] + p2[2]) * f0h;
+                        acc[3] += (p[3] + p2[3]) * f1h;
+                    }
+                }
+                x += 4 * kChunks;
+                m += kChunks * 32 / G * 4;
+                scales += kChunks * 32 / G * (kW4Rows / 2);
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(r.empty_q + 8 * stage);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t wl = v[c >> 1][2 * (c & 1)], wh = v[c >> 1][2 * (c & 1) + 1];
-                const uint4 b = lds128(x + static_cast<uint32_t>(c) * xchunk);
-                const uint32_t wl8 = wl >> 8, wh8 = wh >> 8;
-                mma_f16(p, wl & 0x000f000fu, wh & 0x000f000fu, wl & 0x00f000f0u, wh & 0x00f000f0u, b.x, b.y);
-                mma_f16(p, wl8 & 0x000f000fu, wh8 & 0x000f000fu, wl8 & 0x00f000f0u, wh8 & 0x00f000f0u, b.z, b.w);
-                if ((c + 1) * 32 % G == 0)
-                    flush_group(acc, p, scales + c * 32 / G * (8u * kW4Rows), meta + c * 32 / G * 64u);
-            }
+            if (lane == 0) mbar_arrive(empty + 8 * stage);
             if (++stage == kStages) stage = 0, phase ^= 1;
-            if ((s & 1) || s + 1 == step1) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(r.empty_x + 8 * buf);
-                if (++buf == kW4Segs) buf = 0, xphase ^= 1;
-            }
+            x += 32;                            // the other half's
+            m += kHalfGroups * 4;
         }
-        const int n = warp * 16 + (lane >> 2), t = 2 * (lane & 3);
-        red[t][n] = acc[0];
-        red[t + 1][n] = acc[1];
-        red[t][n + 8] = acc[2];
-        red[t + 1][n + 8] = acc[3];
+        if (alive && !__all_sync(0xffffffffu, arrived(empty_r, rphase, w))) {
+            report_timeout(w, 1, kMaxStages, rphase);
+            abort_flag = 1;
+            alive = false;
+        }
+        if (!alive) continue;
+        const int n = rows + (lane >> 2), t = 2 * (lane & 3);
+        red[half][t][n] = acc[0];
+        red[half][t + 1][n] = acc[1];
+        red[half][t][n + 8] = acc[2];
+        red[half][t + 1][n + 8] = acc[3];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_r);
+        rphase ^= 1;
     }
-    // the slices' sums, in rank order; CTA `rank` finishes its share of the rows
-    namespace cg = cooperative_groups;
-    cg::cluster_group cluster = cg::this_cluster();
-    __syncwarp();
-    cluster.sync();
-    const int rows = kW4Rows / a.slices;
-    for (int i = threadIdx.x; i < tokens * rows; i += kW4Threads) {
-        const int t = i / rows, n = rank * rows + i % rows;
-        if (row0 + n >= a.N) continue;
-        float y = 0.f;
-        for (int c = 0; c < a.slices; ++c) y += *cluster.map_shared_rank(&red[t][n], c);
-        store_any(a.out, a.odt, (t0 + t) * a.ld_out + row0 + n, y);
-    }
-    cluster.sync();   // no CTA leaves while its sums may still be read
 }
 
 bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -452,45 +591,41 @@ __global__ void mbt_w4_zero_kernel(void *out, int dtype, int64_t N, int64_t ld) 
         store_any(out, dtype, blockIdx.y * ld + n, 0.f);
 }
 
-template <int G, bool S32>
-cudaError_t launch_w4(const CUtensorMap &map, const W4Args &a, dim3 grid, cudaStream_t stream) {
-    const int tokens = static_cast<int>(std::min<int64_t>(a.T, kW4Tokens));
-    constexpr int kFixed = kSwizzleAtomBytes + W4Seg<G>::kStages * kW4StageBytes +
-                           kW4Segs * (W4Seg<G>::kMeta + W4Seg<G>::kScales);
-    const size_t smem = kFixed + kW4Segs * kW4Seg * 2 * tokens;
-    static_assert(kFixed + kW4Segs * kW4Seg * 2 * kW4Tokens <= kW4MaxSmem,
-                  "the largest launch fits the limit set below");
+// The slices' sums of four outputs a thread, in slice order.
+__global__ void __launch_bounds__(128) mbt_w4_slices_kernel(const W4Args a) {
+    const int64_t n = (blockIdx.x * 128ll + threadIdx.x) * 4, t = blockIdx.y, pitch = a.blocks * kW4Rows;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n >= a.N) return;
+    const float *part = a.partial + t * a.slices * pitch + n;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = 0; c < a.slices; ++c) {
+        const float4 v = *reinterpret_cast<const float4 *>(part + c * pitch);
+        y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+    }
+    store_y(a, t, n, y);
+}
+
+// Shared memory of a unit's part of x, with its factors.
+int64_t x_bytes(int64_t steps, int rows, int group) {
+    return x_pitch(static_cast<int>(steps * kW4Step)) * rows + steps * kW4Step / group * kW4Tokens * 4;
+}
+
+template <int G>
+cudaError_t launch_w4(const CUtensorMap &map, const W4Args &a, int grid, cudaStream_t stream) {
+    constexpr int kFixed = kSwizzleAtomBytes + W4Step<G>::kStages * W4Step<G>::kStage;
+    const int smem = kFixed + static_cast<int>(x_bytes(a.slice_steps, a.x_rows, G));
     static std::atomic<bool> raised[64];   // per device: the kernel's shared-memory limit is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !raised[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(mbt_w4_kernel<G, S32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kW4MaxSmem);
+        e = cudaFuncSetAttribute(mbt_w4_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kFixed + kW4XBytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) raised[dev].store(true, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kW4Threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(a.slices);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mbt_w4_kernel<G, S32>, map, a);
-}
-
-template <int G>
-cudaError_t launch_w4_group(const CUtensorMap &map, const W4Args &a, dim3 grid, cudaStream_t stream) {
-    return a.sdt == MBT_F32 ? launch_w4<G, true>(map, a, grid, stream)
-                            : launch_w4<G, false>(map, a, grid, stream);
+    return launch_pipeline(mbt_w4_kernel<G>, grid, kW4Threads, smem, stream, map, a);
 }
 
 }  // namespace
@@ -527,7 +662,7 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
         ld_q % 16 != 0)
         return MBT_ERR_ALIGN;
     const int64_t token_blocks = (T + kW4Tokens - 1) / kW4Tokens;
-    if (token_blocks > 65535 || (K == 0 && T > 65535)) return MBT_ERR_UNSUPPORTED;
+    if (T > 65535) return MBT_ERR_UNSUPPORTED;   // (a grid's second dimension)
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) {
         const dim3 grid(static_cast<unsigned>(std::min<int64_t>((N + 255) / 256, 1024)),
@@ -557,28 +692,51 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
     a.sdt = scale_dtype;
     a.odt = out_dtype;
     a.x_row_scale = x_group == 0;
-    // a segment's scales of a row as vectors: whole ones, aligned in every row
-    const int per_seg = kW4Seg / group;
-    const int vec = std::min<int>(per_seg, 16 / static_cast<int>(type_bytes(scale_dtype)));
-    a.vec_scales = a.groups % vec == 0 && aligned(scales, vec * type_bytes(scale_dtype));
+    // a step's scales of a row as vectors: whole ones, aligned in every row
+    const int vec = std::min(kW4Step / group, 8);
+    a.vec_scales = scale_dtype != MBT_F32 && a.groups % vec == 0 && aligned(scales, 2 * static_cast<uintptr_t>(vec));
     a.vec_zeros = a.groups % 4 == 0 && aligned(zeros, 4);
     const uintptr_t xb = type_bytes(dtype);
     a.vec_x = aligned(x, 8 * xb) && (T == 1 || ld_x * static_cast<int64_t>(xb) % (8 * static_cast<int64_t>(xb)) == 0);
-    // Slices along K until there are CTAs for 1.6 per SM (two fit, and loads in
-    // flight on every SM are what counts), each at least one segment of x.
-    const int64_t blocks = (N + kW4Rows - 1) / kW4Rows * token_blocks;
-    const int64_t segs = (K + kW4Seg - 1) / kW4Seg;
-    int slices = 1;
-    while (slices < kW4MaxSlices && slices * 2 <= segs && blocks * slices * 10 < 16 * sms) slices *= 2;
-    a.slices = slices;
-    if ((N + kW4Rows - 1) / kW4Rows * slices > 0x7fffffff) return MBT_ERR_UNSUPPORTED;
+    a.x_rows = static_cast<int32_t>(std::min<int64_t>(T, kW4Tokens));
+    a.blocks = (N + kW4Rows - 1) / kW4Rows;
+    const int64_t steps = (K + kW4Step - 1) / kW4Step, ctas = 2 * sms;
+    // Slices of K: at least as many as x's part of shared memory asks for; among
+    // the counts up to four times that (or one per step, or a unit for each CTA),
+    // the one with the least time for the busiest CTA, counted in steps, a unit
+    // costing 0.3 of a step beside its own.
+    int64_t longest = 1;
+    while (longest < steps && x_bytes(longest + 1, a.x_rows, group) <= kW4XBytes)
+        ++longest;
+    const int64_t fewest = (steps + longest - 1) / longest;
+    const int64_t most = std::min(steps, std::max(4 * fewest, ctas / (a.blocks * token_blocks)));
+    int64_t best = -1, slices = fewest;
+    for (int64_t s = fewest; s <= most; ++s) {
+        const int64_t units = token_blocks * a.blocks * s;
+        const int64_t cost = (units + ctas - 1) / ctas * (10 * ((steps + s - 1) / s) + 3);
+        if (best < 0 || cost < best) best = cost, slices = s;
+    }
+    a.slices = static_cast<int32_t>(slices);
+    a.slice_steps = static_cast<int32_t>((steps + slices - 1) / slices);
+    a.units = token_blocks * slices * a.blocks;
+    if (a.slices > 1) {
+        void *scratch = nullptr;
+        rc = owned_scratch(stream, static_cast<size_t>(a.slices) * T * a.blocks * kW4Rows * sizeof(float),
+                           &scratch);
+        if (rc != MBT_OK) return rc;
+        a.partial = static_cast<float *>(scratch);
+    }
     alignas(64) CUtensorMap map;
     rc = encode_bytes_map(&map, q, N, K / 2, ld_q, kW4Rows);
     if (rc != MBT_OK) return rc;
-    const dim3 grid(static_cast<unsigned>((N + kW4Rows - 1) / kW4Rows * slices),
-                    static_cast<unsigned>(token_blocks));
-    const cudaError_t e = group == 32   ? launch_w4_group<32>(map, a, grid, st)
-                          : group == 64 ? launch_w4_group<64>(map, a, grid, st)
-                                        : launch_w4_group<128>(map, a, grid, st);
-    return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
+    const int grid = static_cast<int>(std::min<int64_t>(a.units, ctas));
+    const cudaError_t e = group == 32   ? launch_w4<32>(map, a, grid, st)
+                          : group == 64 ? launch_w4<64>(map, a, grid, st)
+                                        : launch_w4<128>(map, a, grid, st);
+    if (e != cudaSuccess) return MBT_ERR_CUDA;
+    if (a.slices > 1) {
+        const dim3 sums(static_cast<unsigned>((N + 511) / 512), static_cast<unsigned>(T));
+        if (launch_grid(mbt_w4_slices_kernel, sums, 128, st, a) != cudaSuccess) return MBT_ERR_CUDA;
+    }
+    return MBT_OK;
 }

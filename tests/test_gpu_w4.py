@@ -134,7 +134,7 @@ def test_empty_and_streams():
     assert torch.equal(got, want)
     out = torch.zeros_like(want)
     g = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(g):
+    with torch.cuda.graph(g, stream=st):   # the library's workspace for st is there
         mbt.tile_w4_matvec(x, q, s, z, out=out)
     g.replay()
     torch.cuda.synchronize()
