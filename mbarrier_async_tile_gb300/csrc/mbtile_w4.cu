@@ -294,15 +294,30 @@ struct RowScales {
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 __device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
 
-// Nibbles 0 and 4 of w, less z (z1024 = 1024 + z), from bits 0..3 of each half.
-__device__ __forceinline__ uint32_t low_nibbles(uint32_t w, __half2 z1024) {
-    return as_bits(__hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), z1024));
-}
-
-// Nibbles 1 and 5 of w, less z (z64 = -(64 + z)), from bits 4..7 of each half.
-__device__ __forceinline__ uint32_t high_nibbles(uint32_t w, __half2 z64) {
-    return as_bits(__hfma2(as_half2((w & 0x00f000f0u) | 0x64006400u), as_half2(0x2c002c00u), z64));
-}
+// The conversion's constants, in registers: an instruction takes one immediate,
+// and the compiler, which knows the values, would move the others in every time.
+struct Nibbles {
+    uint32_t low, high, k1024, sixteenth;
+    __device__ __forceinline__ Nibbles() {
+        asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(low));
+        asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(high));
+        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
+        asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(sixteenth));
+    }
+    static __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    // nibbles 0 and 4 of w, less z (z1024 = 1024 + z), from bits 0..3 of each half
+    __device__ __forceinline__ uint32_t lower(uint32_t w, __half2 z1024) const {
+        return as_bits(__hsub2(as_half2(and_or(w, low, k1024)), z1024));
+    }
+    // nibbles 1 and 5 of w, less z (z64 = -(64 + z)), from bits 4..7 of each half
+    __device__ __forceinline__ uint32_t upper(uint32_t w, __half2 z64) const {
+        return as_bits(__hfma2(as_half2(and_or(w, high, k1024)), as_half2(sixteenth), z64));
+    }
+};
 
 // wait_bounded with its first probe in line.
 __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity, const WaitCtl &w) {
@@ -480,6 +495,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     const uint32_t lchunk = static_cast<uint32_t>(lane >> 4), lswz = static_cast<uint32_t>(lrow & 7);
     constexpr int kHalfGroups = Step::kGroups / 2;
     uint32_t stage = 0, phase = 0, rphase = 1;
+    const Nibbles nib;
     int64_t staged = -1;                        // slice (of eight rows of x) in xbuf
     bool alive = true;                          // no wait of this warp has run out
     for (int64_t i = u0; i < u1; ++i) {
@@ -534,10 +550,10 @@ __global__ void __launch_bounds__(kW4Threads, 2)
                             zh64 = __hsub2(as_half2(0x63806380u), zh);
                         }
                         const uint32_t lo = v[2 * h], hi = v[2 * h + 1], lo8 = lo >> 8, hi8 = hi >> 8;
-                        const uint32_t a0 = low_nibbles(lo, zl), a1 = low_nibbles(hi, zh);
-                        const uint32_t a2 = high_nibbles(lo, zl64), a3 = high_nibbles(hi, zh64);
-                        const uint32_t a4 = low_nibbles(lo8, zl), a5 = low_nibbles(hi8, zh);
-                        const uint32_t a6 = high_nibbles(lo8, zl64), a7 = high_nibbles(hi8, zh64);
+                        const uint32_t a0 = nib.lower(lo, zl), a1 = nib.lower(hi, zh);
+                        const uint32_t a2 = nib.upper(lo, zl64), a3 = nib.upper(hi, zh64);
+                        const uint32_t a4 = nib.lower(lo8, zl), a5 = nib.lower(hi8, zh);
+                        const uint32_t a6 = nib.upper(lo8, zl64), a7 = nib.upper(hi8, zh64);
                         if (k % G == 0) {
                             mma_f16<true>(p, a0, a1, a2, a3, b.x, b.y);
                             mma_f16<true>(p2, a4, a5, a6, a7, b.z, b.w);
