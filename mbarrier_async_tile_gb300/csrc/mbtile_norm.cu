@@ -139,6 +139,230 @@ __global__ void __launch_bounds__(kRowThreads) mbt_rmsnorm_rows_kernel(const Nor
     }
 }
 
+// ---------------------------------------------------------------------------
+// Forward, 16-byte accesses
+// ---------------------------------------------------------------------------
+// Rows of any length and pitch are cut into 16-byte chunks by address, not from
+// their first element: a row that starts `off` elements into a chunk has its
+// first and last chunk in part, and everything between is moved 16 bytes at a
+// time.  (All matrices of a call must start rows at the same place in a chunk;
+// mbt_rmsnorm_rows_kernel takes the others.)
+
+// Elements [lo, hi) of the chunk at p, the others 0; and their store.
+template <int DT>
+__device__ __noinline__ uint4 load_part(const typename Elem<DT>::type *p, int lo, int hi) {
+    using T = typename Elem<DT>::type;
+    union {
+        uint4 v;
+        T e[Elem<DT>::kVec];
+    } u;
+    u.v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < Elem<DT>::kVec; ++e)
+        if (e >= lo && e < hi) u.e[e] = p[e];
+    return u.v;
+}
+
+template <int DT>
+__device__ __noinline__ void store_part(typename Elem<DT>::type *p, uint4 v, int lo, int hi) {
+    using T = typename Elem<DT>::type;
+    union {
+        uint4 v;
+        T e[Elem<DT>::kVec];
+    } u;
+    u.v = v;
+#pragma unroll
+    for (int e = 0; e < Elem<DT>::kVec; ++e)
+        if (e >= lo && e < hi) p[e] = u.e[e];
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 load_chunk(const typename Elem<DT>::type *p, int lo, int hi) {
+    constexpr int V = Elem<DT>::kVec;
+    // (not a read-only load: outputs may be the inputs themselves)
+    if (lo <= 0 && hi >= V) return *reinterpret_cast<const uint4 *>(p);
+    return load_part<DT>(p, lo, hi);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_chunk(typename Elem<DT>::type *p, const uint4 &v, int lo, int hi) {
+    constexpr int V = Elem<DT>::kVec;
+    if (lo <= 0 && hi >= V)
+        *reinterpret_cast<uint4 *>(p) = v;
+    else
+        store_part<DT>(p, v, lo, hi);
+}
+
+// How the weight is read: none, as 16-byte vectors of x's type or of fp32, or by
+// element (rows that start inside a chunk, other types).
+enum { kNoWeight = 0, kSameWeight = 1, kF32Weight = 2, kAnyWeight = 3 };
+
+template <int DT>
+__device__ __forceinline__ void load_weight(const void *w, int mode, int wdt, float woff, int64_t j,
+                                            int64_t N, float (&f)[Elem<DT>::kVec]) {
+    constexpr int V = Elem<DT>::kVec;
+    if (mode == kNoWeight) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = 1.f;
+        return;
+    }
+    if (mode == kSameWeight) {
+        unpack<DT>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const typename Elem<DT>::type *>(w) + j)), f);
+    } else if (mode == kF32Weight) {
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + j + e));
+            f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+        }
+    } else {
+#pragma unroll 1
+        for (int e = 0; e < V; ++e) {
+            const float v = j + e >= 0 && j + e < N ? load_any(w, wdt, j + e) : 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i == e) f[i] = v;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] += woff;
+}
+
+struct NormVecArgs {
+    NormArgs a;
+    int32_t tpr, wmode;      // threads per row (a power of two), weight access
+    int32_t phased;          // rows may start inside a chunk
+};
+
+// `tpr` threads hold a row in registers, C chunks each: one pass over memory.
+// Bound by device memory; rows in flight on an SM (CTAs that fit) hide the
+// latency between a row's loads and its stores.
+template <int DT, int C, bool RES, bool Q>
+__global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant__ NormVecArgs va) {
+    using T = typename Elem<DT>::type;
+    constexpr int V = Elem<DT>::kVec;
+    __shared__ float red[32];
+    __shared__ uint32_t redm[32];
+    const NormArgs &a = va.a;
+    const int tpr = va.tpr, t = threadIdx.x & (tpr - 1);
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const bool live = i < a.M;
+    const int off = va.phased ? static_cast<int>((i * a.ld_x) & (V - 1)) : 0;
+    const int64_t end = live ? a.N + off : 0;          // in elements from the first chunk
+    const T *x = static_cast<const T *>(a.x) + i * a.ld_x - off;
+    const T *r = static_cast<const T *>(a.res) + i * a.ld_res - off;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    uint4 xv[C], rv[RES ? C : 1];
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+        const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
+        xv[k] = make_uint4(0, 0, 0, 0);
+        if (RES) rv[k] = make_uint4(0, 0, 0, 0);
+        if (p >= end) continue;
+        const int lo = p < off ? off : 0, hi = end - p < V ? static_cast<int>(end - p) : V;
+        xv[k] = load_chunk<DT>(x + p, lo, hi);
+        if (RES) rv[k] = load_chunk<DT>(r + p, lo, hi);
+    }
+    auto h_of = [&](int k, float (&h)[V]) {
+        unpack<DT>(xv[k], h);
+        if (RES) {
+            float f[V];
+            unpack<DT>(rv[k], f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) h[e] += f[e];
+        }
+    };
+    float ss = 0.f;
+    uint32_t amax = 0;
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+        float h[V];
+        h_of(k, h);
+#pragma unroll
+        for (int e = 0; e < V; ++e) ss += h[e] * h[e];
+        const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
+        if (Q && a.quant == 0 && p < end) {
+            float w[V];
+            load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p - off, a.N, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) amax = max(amax, magnitude(h[e] * w[e]));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o >= tpr) continue;
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (Q) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    }
+    if (tpr > 32) {                                    // one row per CTA
+        if ((t & 31) == 0) {
+            red[t >> 5] = ss;
+            if (Q) redm[t >> 5] = amax;
+        }
+        __syncthreads();
+        const int warps = tpr >> 5, l = t & 31;
+        ss = l < warps ? red[l] : 0.f;
+        ss = warp_sum(ss);
+        if (Q) amax = __reduce_max_sync(0xffffffffu, l < warps ? redm[l] : 0u);
+    }
+    const float rstd = 1.f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+    float scale = 0.f, inv = 0.f;
+    if (Q && a.quant == 0) {
+        scale = group_scale(magnitude(__uint_as_float(amax) * rstd));
+        inv = 1.f / scale;
+    }
+    if (live && t == 0) {
+        a.rstd[i] = rstd;
+        if (Q && a.quant == 0) a.scales[i] = scale;
+    }
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+        const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
+        if (!Q && p >= end) continue;
+        const int lo = p < off ? off : 0, hi = end - p < V ? static_cast<int>(end - p) : V;
+        float h[V], y[V];
+        h_of(k, h);
+        if (RES && p < end && a.res_out)
+            store_chunk<DT>(static_cast<T *>(a.res_out) + i * a.ld_res_out - off + p, pack<DT>(h), lo, hi);
+        if (p < end) {
+            load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p - off, a.N, y);
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] *= h[e] * rstd;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = 0.f;
+        }
+        if constexpr (!Q) {
+            store_chunk<DT>(static_cast<T *>(a.out) + i * a.ld_out - off + p, pack<DT>(y), lo, hi);
+        } else {
+            if (a.quant > 0) {                         // (rows start at a chunk)
+                uint32_t m = 0;
+#pragma unroll
+                for (int e = 0; e < V; ++e) m = max(m, magnitude(y[e]));
+                for (int o = 1; o < a.quant / V; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                scale = group_scale(m);
+                inv = 1.f / scale;
+                if (p < end && p % a.quant == 0) a.scales[i * a.groups + p / a.quant] = scale;
+            }
+            if (p >= end) continue;
+            uint32_t q[V / 4];
+#pragma unroll
+            for (int e = 0; e < V; e += 4)
+                q[e / 4] = to_e4m3x2(y[e] * inv, y[e + 1] * inv) |
+                           to_e4m3x2(y[e + 2] * inv, y[e + 3] * inv) << 16;
+            uint8_t *o = static_cast<uint8_t *>(a.out) + i * a.ld_out - off + p;
+            if (lo == 0 && hi == V && (reinterpret_cast<uintptr_t>(o) & (V - 1)) == 0) {
+                if constexpr (V == 8)
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(q[0], q[1]);
+                else
+                    *reinterpret_cast<uint32_t *>(o) = q[0];
+            } else {
+#pragma unroll 1
+                for (int e = lo; e < hi; ++e) o[e] = static_cast<uint8_t>((V == 8 && e >= 4 ? q[V / 4 - 1] : q[0]) >> (8 * (e & 3)));
+            }
+        }
+    }
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads) mbt_rmsnorm_dx_rows_kernel(const NormGradArgs a) {
     using T = typename Elem<DT>::type;
@@ -210,6 +434,66 @@ bool pitch(int64_t *ld, int64_t M, int64_t N) {
     return *ld >= N && (M == 0 || *ld <= kMaxIndex / M);
 }
 
+// Where the rows of a matrix start in 16-byte chunks: -1 if not known from the
+// first row on, else the pitch's part beyond whole chunks (0: every row at a chunk).
+int phase_of(const void *p, int64_t ld, int64_t es) {
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return -1;
+    return static_cast<int>(ld * es % 16);
+}
+
+int weight_mode(const void *w, int wdt, int dtype, bool phased) {
+    if (!w) return kNoWeight;
+    if (phased || reinterpret_cast<uintptr_t>(w) % 16 != 0) return kAnyWeight;
+    return wdt == dtype ? kSameWeight : wdt == MBT_F32 ? kF32Weight : kAnyWeight;
+}
+
+template <int DT, int C>
+cudaError_t launch_forward(const NormVecArgs &va, dim3 grid, int threads, cudaStream_t s) {
+    const bool q = va.a.quant != MBT_QUANT_NONE;
+    if (va.a.res)
+        return q ? launch_grid(mbt_rmsnorm_kernel<DT, C, true, true>, grid, threads, s, va)
+                 : launch_grid(mbt_rmsnorm_kernel<DT, C, true, false>, grid, threads, s, va);
+    return q ? launch_grid(mbt_rmsnorm_kernel<DT, C, false, true>, grid, threads, s, va)
+             : launch_grid(mbt_rmsnorm_kernel<DT, C, false, false>, grid, threads, s, va);
+}
+
+template <int DT>
+cudaError_t forward(const NormArgs &a, cudaStream_t s) {
+    constexpr int V = Elem<DT>::kVec, es = 16 / V;
+    const int ph = phase_of(a.x, a.ld_x, es);
+    bool same = ph >= 0 && a.N > 0;
+    if (a.res) same = same && phase_of(a.res, a.ld_res, es) == ph;
+    if (a.res_out) same = same && phase_of(a.res_out, a.ld_res_out, es) == ph;
+    if (a.quant == MBT_QUANT_NONE) same = same && phase_of(a.out, a.ld_out, es) == ph;
+    if (a.quant > 0) same = same && ph == 0;           // a group is whole lanes' chunks
+    if (a.M == 1 && ph >= 0 && !same)                  // (no pitch then)
+        same = phase_of(a.x, 0, es) == 0 && (!a.res || phase_of(a.res, 0, es) == 0) &&
+               (!a.res_out || phase_of(a.res_out, 0, es) == 0) &&
+               (a.quant != MBT_QUANT_NONE || phase_of(a.out, 0, es) == 0) && a.N > 0;
+    NormVecArgs va{a, 0, 0, a.M > 1 && ph > 0};
+    const int64_t chunks = (a.N + (va.phased ? V - 1 : 0) + V - 1) / V;
+    if (!same || chunks > 4 * 1024) {
+        const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.M, 1 << 20)));
+        return launch_grid(mbt_rmsnorm_rows_kernel<DT>, grid, kRowThreads, s, a);
+    }
+    // Two chunks a thread while that keeps a row within a CTA; a warp at least
+    // where groups of up to 128 columns are reduced, and all of a CTA for a few
+    // rows, where the time is one row's latency.
+    int tpr = a.quant > 0 ? 32 : 8;
+    while (tpr < 1024 && (tpr * 2 < chunks || (a.M < 64 && tpr < chunks))) tpr *= 2;
+    va.tpr = tpr;
+    va.wmode = weight_mode(a.w, a.wdt, DT, va.phased);
+    // (a vector of the weight past its end: only whole chunks read as vectors)
+    if (a.N % V != 0 && va.wmode != kNoWeight) va.wmode = kAnyWeight;
+    const int threads = tpr > 32 ? tpr : 128, rows = threads / tpr;
+    if ((a.M + rows - 1) / rows > 0x7fffffff) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>((a.M + rows - 1) / rows));
+    const int64_t c = (chunks + tpr - 1) / tpr;
+    return c <= 1   ? launch_forward<DT, 1>(va, grid, threads, s)
+           : c <= 2 ? launch_forward<DT, 2>(va, grid, threads, s)
+                    : launch_forward<DT, 4>(va, grid, threads, s);
+}
+
 }  // namespace
 }  // namespace mbt
 
@@ -241,11 +525,9 @@ extern "C" int tile_rmsnorm(const void *x, const void *residual, const void *wei
                      ld_res_out, quant > 0 ? (N + quant - 1) / quant : 1,
                      weight_dtype, quant, eps, weight_offset};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(M, 1 << 20)));
-    const cudaError_t e = dtype == MBT_F16 ? launch_grid(mbt_rmsnorm_rows_kernel<MBT_F16>, grid, kRowThreads, s, a)
-                          : dtype == MBT_BF16
-                              ? launch_grid(mbt_rmsnorm_rows_kernel<MBT_BF16>, grid, kRowThreads, s, a)
-                              : launch_grid(mbt_rmsnorm_rows_kernel<MBT_F32>, grid, kRowThreads, s, a);
+    const cudaError_t e = dtype == MBT_F16    ? forward<MBT_F16>(a, s)
+                          : dtype == MBT_BF16 ? forward<MBT_BF16>(a, s)
+                                              : forward<MBT_F32>(a, s);
     return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
 }
 
