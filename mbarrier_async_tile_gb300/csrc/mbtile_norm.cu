@@ -194,37 +194,82 @@ __device__ __forceinline__ void store_chunk(typename Elem<DT>::type *p, const ui
 }
 
 // How the weight is read: none, as 16-byte vectors of x's type or of fp32, or by
-// element (rows that start inside a chunk, other types).
+// element (other alignments and types).
 enum { kNoWeight = 0, kSameWeight = 1, kF32Weight = 2, kAnyWeight = 3 };
 
+// Eight words, moved down by `words` (0..4) and, with `half`, by 16 bits more: the
+// first four.  The amounts are the same in a whole warp.
+__device__ __forceinline__ uint4 shift_words(uint4 lo, uint4 hi, int words, bool half) {
+    uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int s = 4; s > 0; s >>= 1)
+        if (words & s)
+#pragma unroll
+            for (int i = 0; i + s < 8; ++i) v[i] = v[i + s];
+    if (half)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// The weights of the row chunk whose first element is column j = p - off, 0 out of
+// range: with off > 0 they lie in two of the weight's own chunks.
 template <int DT>
-__device__ __forceinline__ void load_weight(const void *w, int mode, int wdt, float woff, int64_t j,
-                                            int64_t N, float (&f)[Elem<DT>::kVec]) {
+__device__ __forceinline__ void load_weight(const void *w, int mode, int wdt, float woff, int64_t p,
+                                            int off, int64_t N, float (&f)[Elem<DT>::kVec]) {
+    using T = typename Elem<DT>::type;
     constexpr int V = Elem<DT>::kVec;
+    const int64_t j = p - off;
     if (mode == kNoWeight) {
 #pragma unroll
         for (int e = 0; e < V; ++e) f[e] = 1.f;
         return;
     }
     if (mode == kSameWeight) {
-        unpack<DT>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const typename Elem<DT>::type *>(w) + j)), f);
-    } else if (mode == kF32Weight) {
+        const T *wt = static_cast<const T *>(w);
+        auto chunk = [&](int64_t q) {      // the weight's own chunk from element q on
+            return q < N ? load_chunk<DT>(wt + q, 0, N - q < V ? static_cast<int>(N - q) : V)
+                         : make_uint4(0, 0, 0, 0);
+        };
+        uint4 v = chunk(p);
+        if (off) {
+            const uint4 u = p >= V ? chunk(p - V) : make_uint4(0, 0, 0, 0);
+            constexpr int es = 16 / V;
+            const int bytes = (V - off) * es;
+            v = shift_words(u, v, bytes >> 2, (bytes & 2) != 0);
+        }
+        unpack<DT>(v, f);
+    } else if (mode == kF32Weight && off == 0 && p + V <= N) {
 #pragma unroll
         for (int e = 0; e < V; e += 4) {
             const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + j + e));
             f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
         }
     } else {
-#pragma unroll 1
-        for (int e = 0; e < V; ++e) {
-            const float v = j + e >= 0 && j + e < N ? load_any(w, wdt, j + e) : 0.f;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i == e) f[i] = v;
-        }
+        for (int e = 0; e < V; ++e) f[e] = j + e >= 0 && j + e < N ? load_any(w, wdt, j + e) : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) f[e] += woff;
+}
+
+// V values times inv as e4m3 at o, elements [lo, hi) of them.
+template <int V>
+__device__ __forceinline__ void store_e4m3(uint8_t *o, const float (&y)[V], float inv, int lo, int hi) {
+    uint32_t q[V / 4];
+#pragma unroll
+    for (int e = 0; e < V; e += 4)
+        q[e / 4] = to_e4m3x2(y[e] * inv, y[e + 1] * inv) | to_e4m3x2(y[e + 2] * inv, y[e + 3] * inv) << 16;
+    if (lo <= 0 && hi >= V && (reinterpret_cast<uintptr_t>(o) & (V - 1)) == 0) {
+        if constexpr (V == 8)
+            *reinterpret_cast<uint2 *>(o) = make_uint2(q[0], q[1]);
+        else
+            *reinterpret_cast<uint32_t *>(o) = q[0];
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        if (e >= lo && e < hi) o[e] = static_cast<uint8_t>(q[e / 4] >> (8 * (e & 3)));
 }
 
 struct NormVecArgs {
@@ -282,7 +327,7 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
         const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
         if (Q && a.quant == 0 && p < end) {
             float w[V];
-            load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p - off, a.N, w);
+            load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p, off, a.N, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) amax = max(amax, magnitude(h[e] * w[e]));
         }
@@ -324,7 +369,7 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
         if (RES && p < end && a.res_out)
             store_chunk<DT>(static_cast<T *>(a.res_out) + i * a.ld_res_out - off + p, pack<DT>(h), lo, hi);
         if (p < end) {
-            load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p - off, a.N, y);
+            load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p, off, a.N, y);
 #pragma unroll
             for (int e = 0; e < V; ++e) y[e] *= h[e] * rstd;
         } else {
@@ -344,22 +389,399 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
                 if (p < end && p % a.quant == 0) a.scales[i * a.groups + p / a.quant] = scale;
             }
             if (p >= end) continue;
-            uint32_t q[V / 4];
+            store_e4m3<V>(static_cast<uint8_t *>(a.out) + i * a.ld_out - off + p, y, inv, off - p,
+                          static_cast<int>(end - p));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Rows through a ring in shared memory
+// ---------------------------------------------------------------------------
+// A persistent CTA per SM; a producer warp keeps the next rows of every input
+// matrix on their way into a ring of stages by 1-D bulk copies (the row's
+// 16-byte-aligned window of bytes, so any pitch will do), and 16 consumer warps
+// work on the stage that has landed: `rows` rows at a time, tpr threads each, a
+// thread always the same columns.  That keeps the weight, and the gradient of the
+// weight, in registers for the whole kernel, and loads under way while rows are
+// reduced and written.
+constexpr int kRingConsumers = 512;
+constexpr int kRingThreads = kRingConsumers + 32;
+constexpr int kRingStages = 8;
+constexpr int kRingBytes = 208 * 1024;   // shared memory for the stages
+
+struct RingArgs {
+    const char *in[3];       // forward: x, residual; backward: dy, h, dresidual
+    int64_t ld[3];           // pitches in bytes
+    int32_t inputs;
+    int32_t tpr, rows;       // threads per row, rows per stage
+    int32_t stages;
+    int32_t slot;            // bytes of a row's window, at most
+    int32_t phased;          // rows may start inside a chunk
+    int32_t wmode;
+    int32_t *status;
+};
+
+struct RowWindow {
+    int off;                 // elements from the window's first byte to the row's
+    int64_t start;           // bytes from the matrix to the window
+    int bytes;               // copied; the last row's partial last chunk is not
+                             // (the bytes after it may be nobody's)
+};
+
+template <int DT>
+__device__ __forceinline__ RowWindow row_window(int64_t row, int64_t M, int64_t N, int64_t ld, bool phased) {
+    constexpr int es = 16 / Elem<DT>::kVec;
+    RowWindow w;
+    const int64_t at = row * ld;
+    const int lead = phased ? static_cast<int>(at & 15) : 0;
+    w.off = lead / es;
+    w.start = at - lead;
+    const int need = lead + static_cast<int>(N) * es;
+    w.bytes = row == M - 1 ? need & ~15 : (need + 15) & ~15;
+    return w;
+}
+
+template <int DT>
+__device__ void ring_produce(const RingArgs &r, int64_t M, int64_t N, uint32_t ring, uint32_t full,
+                             uint32_t empty, const WaitCtl &w) {
+    const int lane = threadIdx.x & 31;
+    uint32_t stage = 0, phase = 1;
+    int64_t issued = 0;
+    for (int64_t g = blockIdx.x; g * r.rows < M; g += gridDim.x) {
+        if (!__all_sync(0xffffffffu, wait_bounded(empty + 8 * stage, phase, w, true))) {
+            if (lane == 0) {
+                report_timeout(w, 0, stage, phase);
+                *w.abort = 1;
+                for (int64_t k = issued > r.stages ? issued - r.stages : 0; k < issued; ++k)
+                    wait_bounded(full + 8 * static_cast<uint32_t>(k % r.stages),
+                                 static_cast<uint32_t>(k / r.stages & 1), w, false);
+            }
+            return;
+        }
+        const int64_t left = M - g * r.rows;
+        const int rows = left < r.rows ? static_cast<int>(left) : r.rows;
+        uint32_t total = 0;
+        for (int i = lane; i < rows * r.inputs; i += 32)
+            total += row_window<DT>(g * r.rows + i % rows, M, N, r.ld[i / rows], r.phased).bytes;
+        total = __reduce_add_sync(0xffffffffu, total);
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, total);
+        __syncwarp();
+        const uint32_t base = ring + stage * static_cast<uint32_t>(r.slot * r.rows * r.inputs);
+        for (int i = lane; i < rows * r.inputs; i += 32) {
+            const int m = i / rows, k = i - m * rows;
+            const RowWindow win = row_window<DT>(g * r.rows + k, M, N, r.ld[m], r.phased);
+            if (win.bytes > 0)
+                bulk_load_1d(base + static_cast<uint32_t>((m * r.rows + k) * r.slot), r.in[m] + win.start,
+                             static_cast<uint32_t>(win.bytes), full + 8 * stage);
+        }
+        ++issued;
+        if (++stage == static_cast<uint32_t>(r.stages)) stage = 0, phase ^= 1;
+    }
+}
+
+// The sum of v (and the largest amax) over a row's tpr threads, in all of them.
+// red: two sets of 16 words for sums and 16 for magnitudes, used in turn, so that
+// one barrier per row is enough.
+template <bool MAX>
+__device__ __forceinline__ void row_reduce(float &v, uint32_t &amax, int tpr, float *red, int turn) {
 #pragma unroll
-            for (int e = 0; e < V; e += 4)
-                q[e / 4] = to_e4m3x2(y[e] * inv, y[e + 1] * inv) |
-                           to_e4m3x2(y[e + 2] * inv, y[e + 3] * inv) << 16;
-            uint8_t *o = static_cast<uint8_t *>(a.out) + i * a.ld_out - off + p;
-            if (lo == 0 && hi == V && (reinterpret_cast<uintptr_t>(o) & (V - 1)) == 0) {
-                if constexpr (V == 8)
-                    *reinterpret_cast<uint2 *>(o) = make_uint2(q[0], q[1]);
-                else
-                    *reinterpret_cast<uint32_t *>(o) = q[0];
-            } else {
-#pragma unroll 1
-                for (int e = lo; e < hi; ++e) o[e] = static_cast<uint8_t>((V == 8 && e >= 4 ? q[V / 4 - 1] : q[0]) >> (8 * (e & 3)));
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o >= tpr) continue;
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (MAX) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    }
+    if (tpr <= 32) return;
+    const int warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp & ~(warps - 1), lane = threadIdx.x & 31;
+    float *s = red + turn * 32;
+    uint32_t *m = reinterpret_cast<uint32_t *>(s + 16);
+    if (lane == 0) {
+        s[warp] = v;
+        if (MAX) m[warp] = amax;
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + first / warps), "r"(tpr) : "memory");
+    v = lane < warps ? s[first + lane] : 0.f;
+    v = warp_sum(v);
+    if (MAX) amax = __reduce_max_sync(0xffffffffu, lane < warps ? m[first + lane] : 0u);
+}
+
+// A chunk of an input: from the stage, or (the last row's partial last chunk) from
+// the matrix itself, whose row the window begins at.
+template <int DT>
+__device__ __forceinline__ uint4 ring_chunk(uint32_t slot, const char *window, int p, int copied, int end) {
+    constexpr int V = Elem<DT>::kVec, es = 16 / V;
+    if (p * es < copied) return lds128(slot + static_cast<uint32_t>(p * es));
+    return load_part<DT>(reinterpret_cast<const typename Elem<DT>::type *>(window) + p, 0, end - p);
+}
+
+struct RingShared {
+    uint64_t bars[2 * kRingStages];
+    float red[2][32];
+    int abort_flag;
+};
+
+__device__ __forceinline__ void ring_init(RingShared &sh, int stages, int consumer_warps) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(smem_u32(&sh.bars[i]), 1);
+            mbar_init(smem_u32(&sh.bars[kRingStages + i]), static_cast<uint32_t>(consumer_warps));
+        }
+        sh.abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A consumer thread's weights, C chunks of them, 0 past the row.
+template <int DT, int C>
+__device__ __forceinline__ void ring_weights(const RingArgs &r, const void *w, int wdt, float woff, int t,
+                                             int off, int64_t N, float (&wt)[C][Elem<DT>::kVec]) {
+    constexpr int V = Elem<DT>::kVec;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int p = (t + c * r.tpr) * V;
+        if (p < N + off)
+            load_weight<DT>(w, r.wmode, wdt, woff, p, off, N, wt[c]);
+        else
+#pragma unroll
+            for (int e = 0; e < V; ++e) wt[c][e] = 0.f;
+    }
+}
+
+// Where a row slot is: its row, and the stage's windows of it.  (The host makes the
+// grid such that all rows of a slot start at the same place in a chunk.)
+template <int DT>
+struct RingRow {
+    int64_t i;
+    bool live;
+    RowWindow win;           // the same in every input but for its start
+    uint32_t slot, step;     // shared-memory address in the first input, distance to the next
+    __device__ __forceinline__ RingRow(const RingArgs &r, int64_t g, int k, int64_t M, int64_t N, uint32_t ring,
+                                       uint32_t stage) {
+        i = g * r.rows + k;
+        live = i < M;
+        win = row_window<DT>(live ? i : 0, M, N, r.ld[0], r.phased);
+        step = static_cast<uint32_t>(r.rows * r.slot);
+        slot = ring + stage * step * static_cast<uint32_t>(r.inputs) + static_cast<uint32_t>(k * r.slot);
+    }
+    __device__ __forceinline__ uint4 chunk(const RingArgs &r, int m, int p, int end) const {
+        constexpr int es = 16 / Elem<DT>::kVec;
+        return ring_chunk<DT>(slot + static_cast<uint32_t>(m) * step, r.in[m] + i * r.ld[m] - win.off * es, p,
+                              win.bytes, end);
+    }
+};
+
+// C chunks of every row per thread.  dw: in registers over all of the CTA's rows,
+// then over the row slots in shared memory; one partial sum per CTA and column is
+// left for mbt_rmsnorm_dw_finish_kernel.
+template <int DT, int C, bool RES>
+__global__ void __launch_bounds__(kRingThreads, 1)
+    mbt_rmsnorm_backward_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ RingArgs r) {
+    using T = typename Elem<DT>::type;
+    constexpr int V = Elem<DT>::kVec;
+    extern __shared__ __align__(128) unsigned char dyn_smem[];
+    __shared__ __align__(8) RingShared sh;
+    ring_init(sh, r.stages, kRingConsumers / 32);
+    const uint32_t ring = smem_u32(dyn_smem), full = smem_u32(&sh.bars[0]), empty = smem_u32(&sh.bars[kRingStages]);
+    const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, r.status};
+    if (threadIdx.x >= kRingConsumers) {
+        ring_produce<DT>(r, a.M, a.N, ring, full, empty, w);
+        return;
+    }
+    const int t = threadIdx.x & (r.tpr - 1), k = threadIdx.x / r.tpr;
+    const int64_t first = blockIdx.x * static_cast<int64_t>(r.rows) + k;
+    const int off = row_window<DT>(first < a.M ? first : 0, a.M, a.N, r.ld[0], r.phased).off;
+    float wt[C][V], dw[C][V];
+    ring_weights<DT, C>(r, a.w, a.wdt, a.woff, t, off, a.N, wt);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[c][e] = 0.f;
+    const float inv_n = 1.f / static_cast<float>(a.N);
+    uint32_t stage = 0, phase = 0;
+    int turn = 0;
+    bool alive = true;
+    float next_rstd = first < a.M ? __ldg(a.rstd + first) : 0.f;
+    for (int64_t g = blockIdx.x; g * r.rows < a.M; g += gridDim.x) {
+        const RingRow<DT> row(r, g, k, a.M, a.N, ring, stage);
+        const float rstd = next_rstd;
+        const int64_t ni = row.i + static_cast<int64_t>(gridDim.x) * r.rows;
+        if (ni < a.M) next_rstd = __ldg(a.rstd + ni);
+        if (alive && !wait_bounded(full + 8 * stage, phase, w, true)) {
+            report_timeout(w, 1, stage, phase);
+            sh.abort_flag = 1;
+            alive = false;                   // (still takes part in the barriers)
+        }
+        const int end = row.live && alive ? static_cast<int>(a.N) + off : 0;
+        float dot = 0.f;
+        uint32_t none = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int p = (t + c * r.tpr) * V;
+            if (p >= end) continue;
+            float dy[V], h[V];
+            unpack<DT>(row.chunk(r, 0, p, end), dy);
+            unpack<DT>(row.chunk(r, 1, p, end), h);
+            if (p < off || p + V > end)      // other rows' elements in the window
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (p + e < off || p + e >= end) dy[e] = h[e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                dot += dy[e] * wt[c][e] * h[e];
+                dw[c][e] += dy[e] * (h[e] * rstd);
             }
         }
+        row_reduce<false>(dot, none, r.tpr, sh.red[0], turn);
+        turn ^= 1;
+        const float scale = rstd * (dot * rstd * inv_n);   // times h rstd gives xh mean(g xh)
+        T *dx = static_cast<T *>(a.dx) + (row.live ? row.i : 0) * a.ld_dx - off;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int p = (t + c * r.tpr) * V;
+            if (p >= end) continue;
+            float dy[V], h[V], d[V];
+            unpack<DT>(row.chunk(r, 0, p, end), dy);
+            unpack<DT>(row.chunk(r, 1, p, end), h);
+#pragma unroll
+            for (int e = 0; e < V; ++e) d[e] = rstd * (dy[e] * wt[c][e] - h[e] * scale);
+            if constexpr (RES) {
+                float f[V];
+                unpack<DT>(row.chunk(r, 2, p, end), f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) d[e] += f[e];
+            }
+            store_chunk<DT>(dx + p, pack<DT>(d), off - p, end - p);
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * stage);
+        if (++stage == static_cast<uint32_t>(r.stages)) stage = 0, phase ^= 1;
+    }
+    if (!a.dw) return;
+    // every stage has been read: its memory takes the row slots' sums
+    float *slots = reinterpret_cast<float *>(dyn_smem);
+    asm volatile("bar.sync 15, %0;" ::"n"(kRingConsumers) : "memory");
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int j = (t + c * r.tpr) * V + e - off;
+            if (j >= 0 && j < a.N) slots[k * a.N + j] = dw[c][e];
+        }
+    asm volatile("bar.sync 15, %0;" ::"n"(kRingConsumers) : "memory");
+    for (int j = threadIdx.x; j < a.N; j += kRingConsumers) {
+        float sum = slots[j];
+        for (int s = 1; s < r.rows; ++s) sum += slots[s * a.N + j];
+        a.partial[blockIdx.x * a.N + j] = sum;
+    }
+}
+
+template <int DT, int C, bool RES, bool Q>
+__global__ void __launch_bounds__(kRingThreads, 1)
+    mbt_rmsnorm_ring_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RingArgs r) {
+    using T = typename Elem<DT>::type;
+    constexpr int V = Elem<DT>::kVec;
+    extern __shared__ __align__(128) unsigned char dyn_smem[];
+    __shared__ __align__(8) RingShared sh;
+    ring_init(sh, r.stages, kRingConsumers / 32);
+    const uint32_t ring = smem_u32(dyn_smem), full = smem_u32(&sh.bars[0]), empty = smem_u32(&sh.bars[kRingStages]);
+    const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, r.status};
+    if (threadIdx.x >= kRingConsumers) {
+        ring_produce<DT>(r, a.M, a.N, ring, full, empty, w);
+        return;
+    }
+    const int t = threadIdx.x & (r.tpr - 1), k = threadIdx.x / r.tpr;
+    const int64_t first = blockIdx.x * static_cast<int64_t>(r.rows) + k;
+    const int off = row_window<DT>(first < a.M ? first : 0, a.M, a.N, r.ld[0], r.phased).off;
+    float wt[C][V];
+    ring_weights<DT, C>(r, a.w, a.wdt, a.woff, t, off, a.N, wt);
+    const float inv_n = 1.f / static_cast<float>(a.N);
+    uint32_t stage = 0, phase = 0;
+    int turn = 0;
+    bool alive = true;
+    for (int64_t g = blockIdx.x; g * r.rows < a.M; g += gridDim.x) {
+        const RingRow<DT> row(r, g, k, a.M, a.N, ring, stage);
+        if (alive && !wait_bounded(full + 8 * stage, phase, w, true)) {
+            report_timeout(w, 1, stage, phase);
+            sh.abort_flag = 1;
+            alive = false;                   // (still takes part in the barriers)
+        }
+        const int end = row.live && alive ? static_cast<int>(a.N) + off : 0;
+        auto h_of = [&](int p, float (&h)[V]) {
+            unpack<DT>(row.chunk(r, 0, p, end), h);
+            if constexpr (RES) {
+                float f[V];
+                unpack<DT>(row.chunk(r, 1, p, end), f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) h[e] += f[e];
+            }
+            if (p < off || p + V > end)      // other rows' elements in the window
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (p + e < off || p + e >= end) h[e] = 0.f;
+        };
+        float ss = 0.f;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int p = (t + c * r.tpr) * V;
+            if (p >= end) continue;
+            float h[V];
+            h_of(p, h);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                ss += h[e] * h[e];
+                if (Q && a.quant == 0) amax = max(amax, magnitude(h[e] * wt[c][e]));
+            }
+        }
+        row_reduce<Q>(ss, amax, r.tpr, sh.red[0], turn);
+        turn ^= 1;
+        const float rstd = 1.f / sqrtf(ss * inv_n + a.eps);
+        float scale = 0.f, inv = 0.f;
+        if (Q && a.quant == 0) {
+            scale = group_scale(magnitude(__uint_as_float(amax) * rstd));
+            inv = 1.f / scale;
+        }
+        if (row.live && t == 0) {
+            a.rstd[row.i] = rstd;
+            if (Q && a.quant == 0) a.scales[row.i] = scale;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int p = (t + c * r.tpr) * V;
+            if (!(Q && a.quant > 0) && p >= end) continue;
+            float y[V];
+            if (p < end) {
+                h_of(p, y);
+                if (RES && a.res_out)
+                    store_chunk<DT>(static_cast<T *>(a.res_out) + row.i * a.ld_res_out - off + p, pack<DT>(y),
+                                    off - p, end - p);
+#pragma unroll
+                for (int e = 0; e < V; ++e) y[e] = y[e] * rstd * wt[c][e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) y[e] = 0.f;
+            }
+            if constexpr (!Q) {
+                store_chunk<DT>(static_cast<T *>(a.out) + row.i * a.ld_out - off + p, pack<DT>(y), off - p, end - p);
+            } else {
+                if (a.quant > 0) {           // (rows start at a chunk)
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) m = max(m, magnitude(y[e]));
+                    for (int o = 1; o < a.quant / V; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    scale = group_scale(m);
+                    inv = 1.f / scale;
+                    if (p < end && p % a.quant == 0) a.scales[row.i * a.groups + p / a.quant] = scale;
+                    if (p >= end) continue;
+                }
+                store_e4m3<V>(static_cast<uint8_t *>(a.out) + row.i * a.ld_out - off + p, y, inv, off - p, end - p);
+            }
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * stage);
+        if (++stage == static_cast<uint32_t>(r.stages)) stage = 0, phase ^= 1;
     }
 }
 
@@ -407,14 +829,24 @@ __global__ void __launch_bounds__(kColThreads) mbt_rmsnorm_dw_rows_kernel(const 
     a.partial[s * a.N + j] = sum;
 }
 
-// dw from its partial sums, in split order.
-__global__ void __launch_bounds__(kColThreads) mbt_rmsnorm_dw_finish_kernel(const NormGradArgs a) {
+// dw from its partial sums: 32 columns a CTA, 16 threads a column, each adding
+// every 16th split, then in thread order.
+constexpr int kFinishRows = 16;
+__global__ void __launch_bounds__(32 * kFinishRows) mbt_rmsnorm_dw_finish_kernel(const NormGradArgs a) {
+    __shared__ float part[kFinishRows][32];
+    const int l = threadIdx.x & 31, s0 = threadIdx.x >> 5;
+    const int64_t j = blockIdx.x * 32ll + l;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x;
-    if (j >= a.N) return;
     float sum = 0.f;
-#pragma unroll 8
-    for (int64_t s = 0; s < a.splits; ++s) sum += a.partial[s * a.N + j];
+    if (j < a.N) {
+#pragma unroll 10
+        for (int64_t s = s0; s < a.splits; s += kFinishRows) sum += a.partial[s * a.N + j];
+    }
+    part[s0][l] = sum;
+    __syncthreads();
+    if (s0 != 0 || j >= a.N) return;
+#pragma unroll
+    for (int s = 1; s < kFinishRows; ++s) sum += part[s][l];
     a.dw[j] = sum;
 }
 
@@ -441,10 +873,108 @@ int phase_of(const void *p, int64_t ld, int64_t es) {
     return static_cast<int>(ld * es % 16);
 }
 
-int weight_mode(const void *w, int wdt, int dtype, bool phased) {
+int weight_mode(const void *w, int wdt, int dtype) {
     if (!w) return kNoWeight;
-    if (phased || reinterpret_cast<uintptr_t>(w) % 16 != 0) return kAnyWeight;
+    if (reinterpret_cast<uintptr_t>(w) % 16 != 0) return kAnyWeight;
     return wdt == dtype ? kSameWeight : wdt == MBT_F32 ? kF32Weight : kAnyWeight;
+}
+
+// Rows, threads, stages of a ring over these matrices.  False where it does not
+// apply: rows too long for a CTA's registers or two stages, matrices whose rows
+// start at different places in a chunk.
+struct RingPlan {
+    RingArgs r;
+    int chunks;              // of 16 bytes per thread
+    int grid, smem;
+};
+
+bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, int64_t N, int es, int ph,
+               int min_tpr, int sms, RingPlan *plan) {
+    const int V = 16 / es, most = V == 8 ? 4 : 8;
+    RingArgs &r = plan->r;
+    r = RingArgs{};
+    r.inputs = inputs;
+    for (int i = 0; i < inputs; ++i) {
+        r.in[i] = static_cast<const char *>(in[i]);
+        r.ld[i] = ld[i] * es;
+    }
+    r.phased = M > 1 && ph > 0;
+    const int64_t chunks = (N + (r.phased ? V - 1 : 0) + V - 1) / V;
+    int tpr = min_tpr;
+    while (tpr < kRingConsumers && static_cast<int64_t>(tpr) * most < chunks) tpr *= 2;
+    if (static_cast<int64_t>(tpr) * most < chunks) return false;
+    // fewer rows at a time, by more threads each, until every CTA has a few turns
+    while (tpr < kRingConsumers && tpr < chunks && M * tpr < 4ll * sms * kRingConsumers) tpr *= 2;
+    r.tpr = tpr;
+    r.rows = kRingConsumers / tpr;
+    r.slot = static_cast<int32_t>((N * es + (r.phased ? 16 - es : 0) + 15) / 16 * 16);
+    const int64_t stage = static_cast<int64_t>(r.slot) * r.rows * inputs;
+    r.stages = static_cast<int32_t>(std::min<int64_t>(kRingStages, kRingBytes / stage));
+    if (r.stages < 2) return false;
+    plan->chunks = static_cast<int>((chunks + tpr - 1) / tpr);
+    plan->smem = static_cast<int>(std::max<int64_t>(r.stages * stage, r.rows * N * 4));
+    const int64_t groups = (M + r.rows - 1) / r.rows;
+    // a slot's rows, grid x rows apart, all start at the same place in a chunk
+    plan->grid = static_cast<int>(std::min<int64_t>(groups, r.phased ? sms / 8 * 8 : sms));
+    return plan->grid > 0;
+}
+
+template <class K, class A>
+cudaError_t launch_ring(K kernel, const RingPlan &p, cudaStream_t s, const A &a) {
+    // (set on every call: a kernel's limit is a property of the device it is loaded on)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pipeline(kernel, p.grid, kRingThreads, p.smem, s, a, p.r);
+}
+
+template <int DT, int C>
+cudaError_t launch_ring_forward(const RingPlan &p, const NormArgs &a, cudaStream_t s) {
+    const bool q = a.quant != MBT_QUANT_NONE;
+    if (a.res)
+        return q ? launch_ring(mbt_rmsnorm_ring_kernel<DT, C, true, true>, p, s, a)
+                 : launch_ring(mbt_rmsnorm_ring_kernel<DT, C, true, false>, p, s, a);
+    return q ? launch_ring(mbt_rmsnorm_ring_kernel<DT, C, false, true>, p, s, a)
+             : launch_ring(mbt_rmsnorm_ring_kernel<DT, C, false, false>, p, s, a);
+}
+
+template <int DT, int C>
+cudaError_t launch_ring_backward(const RingPlan &p, const NormGradArgs &a, cudaStream_t s) {
+    return a.dres ? launch_ring(mbt_rmsnorm_backward_kernel<DT, C, true>, p, s, a)
+                  : launch_ring(mbt_rmsnorm_backward_kernel<DT, C, false>, p, s, a);
+}
+
+cudaError_t launch_finish(const NormGradArgs &a, cudaStream_t s) {
+    return launch_grid(mbt_rmsnorm_dw_finish_kernel, dim3(static_cast<unsigned>((a.N + 31) / 32)), 32 * kFinishRows, s, a);
+}
+
+// The gradient through the ring; *done says whether it applied.
+template <int DT>
+int ring_backward(NormGradArgs a, cudaStream_t s, int sms, bool *done) {
+    constexpr int V = Elem<DT>::kVec, es = 16 / V;
+    const int ph = phase_of(a.h, a.ld_h, es);
+    bool same = ph >= 0 && phase_of(a.dy, a.ld_dy, es) == ph && phase_of(a.dx, a.ld_dx, es) == ph;
+    if (a.dres) same = same && phase_of(a.dres, a.ld_dres, es) == ph;
+    const void *in[3] = {a.dy, a.h, a.dres};
+    const int64_t ld[3] = {a.ld_dy, a.ld_h, a.ld_dres};
+    RingPlan p;
+    *done = same && ring_plan(in, ld, a.dres ? 3 : 2, a.M, a.N, es, ph, 8, sms, &p);
+    if (!*done) return MBT_OK;
+    int rc = device_status_word(&p.r.status);
+    if (rc != MBT_OK) return rc;
+    p.r.wmode = weight_mode(a.w, a.wdt, DT);
+    a.splits = p.grid;
+    if (a.dw) {
+        void *scratch = nullptr;
+        rc = owned_scratch(s, static_cast<size_t>(a.splits) * a.N * 4, &scratch);
+        if (rc != MBT_OK) return rc;
+        a.partial = static_cast<float *>(scratch);
+    }
+    constexpr int k = V == 8 ? 1 : 2;
+    cudaError_t e = p.chunks <= k       ? launch_ring_backward<DT, k>(p, a, s)
+                    : p.chunks <= 2 * k ? launch_ring_backward<DT, 2 * k>(p, a, s)
+                                        : launch_ring_backward<DT, 4 * k>(p, a, s);
+    if (e == cudaSuccess && a.dw) e = launch_finish(a, s);
+    return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
 }
 
 template <int DT, int C>
@@ -455,6 +985,12 @@ cudaError_t launch_forward(const NormVecArgs &va, dim3 grid, int threads, cudaSt
                  : launch_grid(mbt_rmsnorm_kernel<DT, C, true, false>, grid, threads, s, va);
     return q ? launch_grid(mbt_rmsnorm_kernel<DT, C, false, true>, grid, threads, s, va)
              : launch_grid(mbt_rmsnorm_kernel<DT, C, false, false>, grid, threads, s, va);
+}
+
+// The ring's start (weights, barriers, the first rows' latency) is paid once per
+// call: worth it from about a row's worth of 16 MB on.
+bool ring_forward_pays(const NormArgs &a, int64_t es, int sms) {
+    return a.M * a.N * es >= (16ll << 20) && a.M >= 4 * sms;
 }
 
 template <int DT>
@@ -470,6 +1006,20 @@ cudaError_t forward(const NormArgs &a, cudaStream_t s) {
         same = phase_of(a.x, 0, es) == 0 && (!a.res || phase_of(a.res, 0, es) == 0) &&
                (!a.res_out || phase_of(a.res_out, 0, es) == 0) &&
                (a.quant != MBT_QUANT_NONE || phase_of(a.out, 0, es) == 0) && a.N > 0;
+    int sms = 0, optin = 0;
+    if (device_limits(&sms, &optin) != MBT_OK) return cudaErrorUnknown;
+    const void *in[2] = {a.x, a.res};
+    const int64_t ld[2] = {a.ld_x, a.ld_res};
+    RingPlan p;
+    if (same && ring_forward_pays(a, es, sms) &&
+        ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, a.quant > 0 ? 32 : 8, sms, &p)) {
+        if (device_status_word(&p.r.status) != MBT_OK) return cudaErrorUnknown;
+        p.r.wmode = weight_mode(a.w, a.wdt, DT);
+        constexpr int k = V == 8 ? 1 : 2;
+        return p.chunks <= k       ? launch_ring_forward<DT, k>(p, a, s)
+               : p.chunks <= 2 * k ? launch_ring_forward<DT, 2 * k>(p, a, s)
+                                   : launch_ring_forward<DT, 4 * k>(p, a, s);
+    }
     NormVecArgs va{a, 0, 0, a.M > 1 && ph > 0};
     const int64_t chunks = (a.N + (va.phased ? V - 1 : 0) + V - 1) / V;
     if (!same || chunks > 4 * 1024) {
@@ -482,9 +1032,7 @@ cudaError_t forward(const NormArgs &a, cudaStream_t s) {
     int tpr = a.quant > 0 ? 32 : 8;
     while (tpr < 1024 && (tpr * 2 < chunks || (a.M < 64 && tpr < chunks))) tpr *= 2;
     va.tpr = tpr;
-    va.wmode = weight_mode(a.w, a.wdt, DT, va.phased);
-    // (a vector of the weight past its end: only whole chunks read as vectors)
-    if (a.N % V != 0 && va.wmode != kNoWeight) va.wmode = kAnyWeight;
+    va.wmode = weight_mode(a.w, a.wdt, DT);
     const int threads = tpr > 32 ? tpr : 128, rows = threads / tpr;
     if ((a.M + rows - 1) / rows > 0x7fffffff) return cudaErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>((a.M + rows - 1) / rows));
@@ -559,6 +1107,11 @@ extern "C" int tile_rmsnorm_backward(const void *dy, const void *h, const float 
     if (rc != MBT_OK) return rc;
     NormGradArgs a{dy, h, weight, dresidual, rstd, dx, dweight, nullptr, M, N, ld_dy, ld_h, ld_dres,
                    ld_dx, 1, weight_dtype, weight_offset};
+    bool done = false;
+    rc = dtype == MBT_F16    ? ring_backward<MBT_F16>(a, s, sms, &done)
+         : dtype == MBT_BF16 ? ring_backward<MBT_BF16>(a, s, sms, &done)
+                             : ring_backward<MBT_F32>(a, s, sms, &done);
+    if (rc != MBT_OK || done) return rc;
     const unsigned cols = static_cast<unsigned>((N + kColThreads - 1) / kColThreads);
     cudaError_t e = cudaSuccess;
     if (dweight) {
@@ -574,7 +1127,7 @@ extern "C" int tile_rmsnorm_backward(const void *dy, const void *h, const float 
         e = dtype == MBT_F16    ? launch_grid(mbt_rmsnorm_dw_rows_kernel<MBT_F16>, grid, kColThreads, s, a)
             : dtype == MBT_BF16 ? launch_grid(mbt_rmsnorm_dw_rows_kernel<MBT_BF16>, grid, kColThreads, s, a)
                                 : launch_grid(mbt_rmsnorm_dw_rows_kernel<MBT_F32>, grid, kColThreads, s, a);
-        if (e == cudaSuccess) e = launch_grid(mbt_rmsnorm_dw_finish_kernel, dim3(cols), kColThreads, s, a);
+        if (e == cudaSuccess) e = launch_finish(a, s);
         if (e != cudaSuccess) return MBT_ERR_CUDA;
     }
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(M, 1 << 20)));
