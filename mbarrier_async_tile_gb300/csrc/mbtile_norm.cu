@@ -565,8 +565,11 @@ struct RingRow {
         step = static_cast<uint32_t>(r.rows * r.slot);
         slot = ring + stage * step * static_cast<uint32_t>(r.inputs) + static_cast<uint32_t>(k * r.slot);
     }
+    // (PART: rows may begin or end inside a chunk)
+    template <bool PART>
     __device__ __forceinline__ uint4 chunk(const RingArgs &r, int m, int p, int end) const {
         constexpr int es = 16 / Elem<DT>::kVec;
+        if constexpr (!PART) return lds128(slot + static_cast<uint32_t>(m) * step + static_cast<uint32_t>(p * es));
         return ring_chunk<DT>(slot + static_cast<uint32_t>(m) * step, r.in[m] + i * r.ld[m] - win.off * es, p,
                               win.bytes, end);
     }
@@ -575,7 +578,7 @@ struct RingRow {
 // C chunks of every row per thread.  dw: in registers over all of the CTA's rows,
 // then over the row slots in shared memory; one partial sum per CTA and column is
 // left for mbt_rmsnorm_dw_finish_kernel.
-template <int DT, int C, bool RES>
+template <int DT, int C, bool RES, bool PART>
 __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_rmsnorm_backward_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ RingArgs r) {
     using T = typename Elem<DT>::type;
@@ -591,7 +594,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     }
     const int t = threadIdx.x & (r.tpr - 1), k = threadIdx.x / r.tpr;
     const int64_t first = blockIdx.x * static_cast<int64_t>(r.rows) + k;
-    const int off = row_window<DT>(first < a.M ? first : 0, a.M, a.N, r.ld[0], r.phased).off;
+    const int off = PART ? row_window<DT>(first < a.M ? first : 0, a.M, a.N, r.ld[0], r.phased).off : 0;
     float wt[C][V], dw[C][V];
     ring_weights<DT, C>(r, a.w, a.wdt, a.woff, t, off, a.N, wt);
 #pragma unroll
@@ -616,43 +619,58 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         const int end = row.live && alive ? static_cast<int>(a.N) + off : 0;
         float dot = 0.f;
         uint32_t none = 0;
+        {
+            uint4 vy[C], vh[C];              // all loads under way before the first use
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int p = (t + c * r.tpr) * V;
-            if (p >= end) continue;
-            float dy[V], h[V];
-            unpack<DT>(row.chunk(r, 0, p, end), dy);
-            unpack<DT>(row.chunk(r, 1, p, end), h);
-            if (p < off || p + V > end)      // other rows' elements in the window
+            for (int c = 0; c < C; ++c) {
+                const int p = (t + c * r.tpr) * V;
+                vy[c] = vh[c] = make_uint4(0, 0, 0, 0);
+                if (p >= end) continue;
+                vy[c] = row.template chunk<PART>(r, 0, p, end);
+                vh[c] = row.template chunk<PART>(r, 1, p, end);
+            }
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (p + e < off || p + e >= end) dy[e] = h[e] = 0.f;
+            for (int c = 0; c < C; ++c) {
+                const int p = (t + c * r.tpr) * V;
+                float dy[V], h[V];
+                unpack<DT>(vy[c], dy);
+                unpack<DT>(vh[c], h);
+                if (PART && (p < off || p + V > end))   // other rows' elements in the window
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                dot += dy[e] * wt[c][e] * h[e];
-                dw[c][e] += dy[e] * (h[e] * rstd);
+                    for (int e = 0; e < V; ++e)
+                        if (p + e < off || p + e >= end) dy[e] = h[e] = 0.f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float x = dy[e] * h[e];
+                    dot += x * wt[c][e];
+                    dw[c][e] += x * rstd;
+                }
             }
         }
         row_reduce<false>(dot, none, r.tpr, sh.red[0], turn);
         turn ^= 1;
-        const float scale = rstd * (dot * rstd * inv_n);   // times h rstd gives xh mean(g xh)
+        const float scale2 = rstd * rstd * rstd * (dot * inv_n);   // times h gives rstd xh mean(g xh)
         T *dx = static_cast<T *>(a.dx) + (row.live ? row.i : 0) * a.ld_dx - off;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int p = (t + c * r.tpr) * V;
             if (p >= end) continue;
-            float dy[V], h[V], d[V];
-            unpack<DT>(row.chunk(r, 0, p, end), dy);
-            unpack<DT>(row.chunk(r, 1, p, end), h);
+            const uint4 vy = row.template chunk<PART>(r, 0, p, end), vh = row.template chunk<PART>(r, 1, p, end);
+            uint4 vr = make_uint4(0, 0, 0, 0);
+            if constexpr (RES) vr = row.template chunk<PART>(r, 2, p, end);
+            float dy[V], h[V], d[V], f[V];
+            unpack<DT>(vy, dy);
+            unpack<DT>(vh, h);
+            unpack<DT>(vr, f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) d[e] = rstd * (dy[e] * wt[c][e] - h[e] * scale);
-            if constexpr (RES) {
-                float f[V];
-                unpack<DT>(row.chunk(r, 2, p, end), f);
-#pragma unroll
-                for (int e = 0; e < V; ++e) d[e] += f[e];
+            for (int e = 0; e < V; ++e) {
+                d[e] = rstd * (dy[e] * wt[c][e]) - h[e] * scale2;
+                if constexpr (RES) d[e] += f[e];
             }
-            store_chunk<DT>(dx + p, pack<DT>(d), off - p, end - p);
+            if constexpr (PART)
+                store_chunk<DT>(dx + p, pack<DT>(d), off - p, end - p);
+            else
+                *reinterpret_cast<uint4 *>(dx + p) = pack<DT>(d);
         }
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * stage);
@@ -677,7 +695,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     }
 }
 
-template <int DT, int C, bool RES, bool Q>
+template <int DT, int C, bool RES, bool Q, bool PART>
 __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_rmsnorm_ring_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RingArgs r) {
     using T = typename Elem<DT>::type;
@@ -693,7 +711,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     }
     const int t = threadIdx.x & (r.tpr - 1), k = threadIdx.x / r.tpr;
     const int64_t first = blockIdx.x * static_cast<int64_t>(r.rows) + k;
-    const int off = row_window<DT>(first < a.M ? first : 0, a.M, a.N, r.ld[0], r.phased).off;
+    const int off = PART ? row_window<DT>(first < a.M ? first : 0, a.M, a.N, r.ld[0], r.phased).off : 0;
     float wt[C][V];
     ring_weights<DT, C>(r, a.w, a.wdt, a.woff, t, off, a.N, wt);
     const float inv_n = 1.f / static_cast<float>(a.N);
@@ -709,17 +727,26 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
         const int end = row.live && alive ? static_cast<int>(a.N) + off : 0;
         auto h_of = [&](int p, float (&h)[V]) {
-            unpack<DT>(row.chunk(r, 0, p, end), h);
+            const uint4 vx = row.template chunk<PART>(r, 0, p, end);
+            uint4 vr = make_uint4(0, 0, 0, 0);
+            if constexpr (RES) vr = row.template chunk<PART>(r, 1, p, end);
+            unpack<DT>(vx, h);
             if constexpr (RES) {
                 float f[V];
-                unpack<DT>(row.chunk(r, 1, p, end), f);
+                unpack<DT>(vr, f);
 #pragma unroll
                 for (int e = 0; e < V; ++e) h[e] += f[e];
             }
-            if (p < off || p + V > end)      // other rows' elements in the window
+            if (PART && (p < off || p + V > end))   // other rows' elements in the window
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     if (p + e < off || p + e >= end) h[e] = 0.f;
+        };
+        auto put = [&](T *to, int p, const float (&v)[V]) {
+            if constexpr (PART)
+                store_chunk<DT>(to - off + p, pack<DT>(v), off - p, end - p);
+            else
+                *reinterpret_cast<uint4 *>(to + p) = pack<DT>(v);
         };
         float ss = 0.f;
         uint32_t amax = 0;
@@ -755,8 +782,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             if (p < end) {
                 h_of(p, y);
                 if (RES && a.res_out)
-                    store_chunk<DT>(static_cast<T *>(a.res_out) + row.i * a.ld_res_out - off + p, pack<DT>(y),
-                                    off - p, end - p);
+                    put(static_cast<T *>(a.res_out) + row.i * a.ld_res_out, p, y);
 #pragma unroll
                 for (int e = 0; e < V; ++e) y[e] = y[e] * rstd * wt[c][e];
             } else {
@@ -764,7 +790,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 for (int e = 0; e < V; ++e) y[e] = 0.f;
             }
             if constexpr (!Q) {
-                store_chunk<DT>(static_cast<T *>(a.out) + row.i * a.ld_out - off + p, pack<DT>(y), off - p, end - p);
+                put(static_cast<T *>(a.out) + row.i * a.ld_out, p, y);
             } else {
                 if (a.quant > 0) {           // (rows start at a chunk)
                     uint32_t m = 0;
@@ -885,6 +911,7 @@ int weight_mode(const void *w, int wdt, int dtype) {
 struct RingPlan {
     RingArgs r;
     int chunks;              // of 16 bytes per thread
+    bool part;               // rows begin or end inside a chunk
     int grid, smem;
 };
 
@@ -912,6 +939,7 @@ bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, 
     r.stages = static_cast<int32_t>(std::min<int64_t>(kRingStages, kRingBytes / stage));
     if (r.stages < 2) return false;
     plan->chunks = static_cast<int>((chunks + tpr - 1) / tpr);
+    plan->part = r.phased || N % V != 0;
     plan->smem = static_cast<int>(std::max<int64_t>(r.stages * stage, r.rows * N * 4));
     const int64_t groups = (M + r.rows - 1) / r.rows;
     // a slot's rows, grid x rows apart, all start at the same place in a chunk
@@ -927,20 +955,31 @@ cudaError_t launch_ring(K kernel, const RingPlan &p, cudaStream_t s, const A &a)
     return launch_pipeline(kernel, p.grid, kRingThreads, p.smem, s, a, p.r);
 }
 
+template <int DT, int C, bool RES, bool Q>
+cudaError_t launch_ring_forward_q(const RingPlan &p, const NormArgs &a, cudaStream_t s) {
+    return p.part ? launch_ring(mbt_rmsnorm_ring_kernel<DT, C, RES, Q, true>, p, s, a)
+                  : launch_ring(mbt_rmsnorm_ring_kernel<DT, C, RES, Q, false>, p, s, a);
+}
+
 template <int DT, int C>
 cudaError_t launch_ring_forward(const RingPlan &p, const NormArgs &a, cudaStream_t s) {
     const bool q = a.quant != MBT_QUANT_NONE;
     if (a.res)
-        return q ? launch_ring(mbt_rmsnorm_ring_kernel<DT, C, true, true>, p, s, a)
-                 : launch_ring(mbt_rmsnorm_ring_kernel<DT, C, true, false>, p, s, a);
-    return q ? launch_ring(mbt_rmsnorm_ring_kernel<DT, C, false, true>, p, s, a)
-             : launch_ring(mbt_rmsnorm_ring_kernel<DT, C, false, false>, p, s, a);
+        return q ? launch_ring_forward_q<DT, C, true, true>(p, a, s)
+                 : launch_ring_forward_q<DT, C, true, false>(p, a, s);
+    return q ? launch_ring_forward_q<DT, C, false, true>(p, a, s)
+             : launch_ring_forward_q<DT, C, false, false>(p, a, s);
+}
+
+template <int DT, int C, bool RES>
+cudaError_t launch_ring_backward_r(const RingPlan &p, const NormGradArgs &a, cudaStream_t s) {
+    return p.part ? launch_ring(mbt_rmsnorm_backward_kernel<DT, C, RES, true>, p, s, a)
+                  : launch_ring(mbt_rmsnorm_backward_kernel<DT, C, RES, false>, p, s, a);
 }
 
 template <int DT, int C>
 cudaError_t launch_ring_backward(const RingPlan &p, const NormGradArgs &a, cudaStream_t s) {
-    return a.dres ? launch_ring(mbt_rmsnorm_backward_kernel<DT, C, true>, p, s, a)
-                  : launch_ring(mbt_rmsnorm_backward_kernel<DT, C, false>, p, s, a);
+    return a.dres ? launch_ring_backward_r<DT, C, true>(p, a, s) : launch_ring_backward_r<DT, C, false>(p, a, s);
 }
 
 cudaError_t launch_finish(const NormGradArgs &a, cudaStream_t s) {
