@@ -398,15 +398,15 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 // Rows through a ring in shared memory
 // ---------------------------------------------------------------------------
-// A persistent CTA per SM; a producer warp keeps the next rows of every input
-// matrix on their way into a ring of stages by 1-D bulk copies (the row's
-// 16-byte-aligned window of bytes, so any pitch will do), and 16 consumer warps
-// work on the stage that has landed: `rows` rows at a time, tpr threads each, a
-// thread always the same columns.  That keeps the weight, and the gradient of the
-// weight, in registers for the whole kernel, and loads under way while rows are
-// reduced and written.
-constexpr int kRingConsumers = 512;
-constexpr int kRingThreads = kRingConsumers + 32;
+// A persistent CTA per SM keeps the next rows of every input matrix on their way
+// into a ring of stages by 1-D bulk copies (the row's 16-byte-aligned window of
+// bytes, so any pitch will do), and 16 warps work on the stage that has landed:
+// `rows` rows at a time, tpr threads each, a thread always the same columns.  That
+// keeps the weight, and the gradient of the weight, in registers for the whole
+// kernel, and loads under way while rows are reduced and written.  Warp 0 refills
+// a stage once every warp has read it: a warp of its own for that would be the
+// 17th and cost each thread 32 of its 128 registers.
+constexpr int kRingThreads = 512;
 constexpr int kRingStages = 8;
 constexpr int kRingBytes = 208 * 1024;   // shared memory for the stages
 
@@ -442,43 +442,78 @@ __device__ __forceinline__ RowWindow row_window(int64_t row, int64_t M, int64_t 
     return w;
 }
 
+// Warp 0: the copies of row group g into `stage`.
 template <int DT>
-__device__ void ring_produce(const RingArgs &r, int64_t M, int64_t N, uint32_t ring, uint32_t full,
-                             uint32_t empty, const WaitCtl &w) {
+__device__ __forceinline__ void ring_fill(const RingArgs &r, int64_t M, int64_t N, uint32_t ring, uint32_t full,
+                                          uint32_t stage, int64_t g) {
     const int lane = threadIdx.x & 31;
-    uint32_t stage = 0, phase = 1;
-    int64_t issued = 0;
-    for (int64_t g = blockIdx.x; g * r.rows < M; g += gridDim.x) {
-        if (!__all_sync(0xffffffffu, wait_bounded(empty + 8 * stage, phase, w, true))) {
-            if (lane == 0) {
-                report_timeout(w, 0, stage, phase);
-                *w.abort = 1;
-                for (int64_t k = issued > r.stages ? issued - r.stages : 0; k < issued; ++k)
-                    wait_bounded(full + 8 * static_cast<uint32_t>(k % r.stages),
-                                 static_cast<uint32_t>(k / r.stages & 1), w, false);
-            }
-            return;
-        }
-        const int64_t left = M - g * r.rows;
-        const int rows = left < r.rows ? static_cast<int>(left) : r.rows;
-        uint32_t total = 0;
-        for (int i = lane; i < rows * r.inputs; i += 32)
-            total += row_window<DT>(g * r.rows + i % rows, M, N, r.ld[i / rows], r.phased).bytes;
-        total = __reduce_add_sync(0xffffffffu, total);
-        if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, total);
-        __syncwarp();
-        const uint32_t base = ring + stage * static_cast<uint32_t>(r.slot * r.rows * r.inputs);
-        for (int i = lane; i < rows * r.inputs; i += 32) {
-            const int m = i / rows, k = i - m * rows;
-            const RowWindow win = row_window<DT>(g * r.rows + k, M, N, r.ld[m], r.phased);
-            if (win.bytes > 0)
-                bulk_load_1d(base + static_cast<uint32_t>((m * r.rows + k) * r.slot), r.in[m] + win.start,
-                             static_cast<uint32_t>(win.bytes), full + 8 * stage);
-        }
-        ++issued;
-        if (++stage == static_cast<uint32_t>(r.stages)) stage = 0, phase ^= 1;
+    const int64_t left = M - g * r.rows;
+    const int rows = left < r.rows ? static_cast<int>(left) : r.rows;
+    uint32_t total = 0;
+    for (int i = lane; i < rows * r.inputs; i += 32)
+        total += row_window<DT>(g * r.rows + i % rows, M, N, r.ld[i / rows], r.phased).bytes;
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, total);
+    __syncwarp();
+    const uint32_t base = ring + stage * static_cast<uint32_t>(r.slot * r.rows * r.inputs);
+    for (int i = lane; i < rows * r.inputs; i += 32) {
+        const int m = i / rows, k = i - m * rows;
+        const RowWindow win = row_window<DT>(g * r.rows + k, M, N, r.ld[m], r.phased);
+        if (win.bytes > 0)
+            bulk_load_1d(base + static_cast<uint32_t>((m * r.rows + k) * r.slot), r.in[m] + win.start,
+                         static_cast<uint32_t>(win.bytes), full + 8 * stage);
     }
 }
+
+// The ring's position, the same in every warp.
+struct RingState {
+    uint32_t ring, full, empty, stage = 0, phase = 0;
+    WaitCtl w;
+    bool alive = true;       // no wait of this warp has run out
+
+    // The first rows of the CTA.
+    template <int DT>
+    __device__ __forceinline__ void start(const RingArgs &r, int64_t M, int64_t N) {
+        if (threadIdx.x >= 32) return;
+        for (int s = 0; s < r.stages; ++s) {
+            const int64_t g = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+            if (g * r.rows < M) ring_fill<DT>(r, M, N, ring, full, static_cast<uint32_t>(s), g);
+        }
+    }
+    // A warp whose wait has run out goes through the rows without work, so that
+    // the CTA's barriers are complete.
+    __device__ __forceinline__ void wait() {
+        if (alive && !__all_sync(0xffffffffu, mbar_try_wait(full + 8 * stage, phase) ||
+                                                  wait_bounded(full + 8 * stage, phase, w, true))) {
+            report_timeout(w, 1, stage, phase);
+            *w.abort = 1;
+            alive = false;
+        }
+    }
+    // This warp has read the stage of group g.
+    template <int DT>
+    __device__ __forceinline__ void release(const RingArgs &r, int64_t M, int64_t N, int64_t g) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * stage);
+        const int64_t next = g + static_cast<int64_t>(r.stages) * gridDim.x;
+        if (threadIdx.x < 32 && alive && next * r.rows < M) {
+            if (__all_sync(0xffffffffu, wait_bounded(empty + 8 * stage, phase, w, true))) {
+                ring_fill<DT>(r, M, N, ring, full, stage, next);
+            } else {
+                report_timeout(w, 0, stage, phase);
+                *w.abort = 1;
+                alive = false;
+            }
+        }
+        if (++stage == static_cast<uint32_t>(r.stages)) stage = 0, phase ^= 1;
+    }
+    // After a wait that ran out: the copies under way land before the CTA leaves.
+    __device__ __forceinline__ void drain(int stages) {
+        if (threadIdx.x != 0 || !*w.abort) return;
+        for (int s = 0; s < stages; ++s)
+            for (uint32_t p = 0; p < 2; ++p) wait_bounded(full + 8 * s, p, w, false);
+    }
+};
 
 // The sum of v (and the largest amax) over a row's tpr threads, in all of them.
 // red: two sets of 16 words for sums and 16 for magnitudes, used in turn, so that
@@ -520,11 +555,11 @@ struct RingShared {
     int abort_flag;
 };
 
-__device__ __forceinline__ void ring_init(RingShared &sh, int stages, int consumer_warps) {
+__device__ __forceinline__ void ring_init(RingShared &sh, int stages) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             mbar_init(smem_u32(&sh.bars[i]), 1);
-            mbar_init(smem_u32(&sh.bars[kRingStages + i]), static_cast<uint32_t>(consumer_warps));
+            mbar_init(smem_u32(&sh.bars[kRingStages + i]), kRingThreads / 32);
         }
         sh.abort_flag = 0;
         fence_barrier_init();
@@ -533,21 +568,51 @@ __device__ __forceinline__ void ring_init(RingShared &sh, int stages, int consum
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// A consumer thread's weights, C chunks of them, 0 past the row.
-template <int DT, int C>
-__device__ __forceinline__ void ring_weights(const RingArgs &r, const void *w, int wdt, float woff, int t,
-                                             int off, int64_t N, float (&wt)[C][Elem<DT>::kVec]) {
-    constexpr int V = Elem<DT>::kVec;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int p = (t + c * r.tpr) * V;
-        if (p < N + off)
-            load_weight<DT>(w, r.wmode, wdt, woff, p, off, N, wt[c]);
-        else
-#pragma unroll
-            for (int e = 0; e < V; ++e) wt[c][e] = 0.f;
-    }
+// Tells the compiler that v may have changed, so that it unpacks v again instead of
+// keeping its fp32 values (twice the registers) from an earlier use.
+__device__ __forceinline__ void forget(uint4 &v) {
+    asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
 }
+
+// A thread's weights, C chunks of them, 0 past the row.  Where rows are whole
+// chunks the weight is of x's type, and stays packed.
+template <int DT, int C, bool PART>
+struct RingWeights {
+    static constexpr int V = Elem<DT>::kVec;
+    float f[PART ? C : 1][V];
+    uint4 raw[PART ? 1 : C];
+    float woff;
+    __device__ __forceinline__ void load(const RingArgs &r, const void *w, int wdt, float offset, int t, int off,
+                                         int64_t N) {
+        woff = offset;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int p = (t + c * r.tpr) * V;
+            if constexpr (PART) {
+                if (p < N + off)
+                    load_weight<DT>(w, r.wmode, wdt, woff, p, off, N, f[c]);
+                else
+#pragma unroll
+                    for (int e = 0; e < V; ++e) f[c][e] = 0.f;
+            } else {
+                raw[c] = make_uint4(0, 0, 0, 0);
+                if (p < N)
+                    raw[c] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const typename Elem<DT>::type *>(w) + p));
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int c, float (&v)[V]) {
+        if constexpr (PART) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = f[c][e];
+        } else {
+            if constexpr (DT != MBT_F32) forget(raw[c]);
+            unpack<DT>(raw[c], v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += woff;
+        }
+    }
+};
 
 // Where a row slot is: its row, and the stage's windows of it.  (The host makes the
 // grid such that all rows of a slot start at the same place in a chunk.)
@@ -585,86 +650,85 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     constexpr int V = Elem<DT>::kVec;
     extern __shared__ __align__(128) unsigned char dyn_smem[];
     __shared__ __align__(8) RingShared sh;
-    ring_init(sh, r.stages, kRingConsumers / 32);
-    const uint32_t ring = smem_u32(dyn_smem), full = smem_u32(&sh.bars[0]), empty = smem_u32(&sh.bars[kRingStages]);
-    const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, r.status};
-    if (threadIdx.x >= kRingConsumers) {
-        ring_produce<DT>(r, a.M, a.N, ring, full, empty, w);
-        return;
-    }
+    ring_init(sh, r.stages);
+    RingState q{smem_u32(dyn_smem), smem_u32(&sh.bars[0]), smem_u32(&sh.bars[kRingStages]), 0, 0,
+                WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status}};
+    q.start<DT>(r, a.M, a.N);
     const int t = threadIdx.x & (r.tpr - 1), k = threadIdx.x / r.tpr;
     const int64_t first = blockIdx.x * static_cast<int64_t>(r.rows) + k;
     const int off = PART ? row_window<DT>(first < a.M ? first : 0, a.M, a.N, r.ld[0], r.phased).off : 0;
-    float wt[C][V], dw[C][V];
-    ring_weights<DT, C>(r, a.w, a.wdt, a.woff, t, off, a.N, wt);
+    RingWeights<DT, C, PART> wt;
+    wt.load(r, a.w, a.wdt, a.woff, t, off, a.N);
+    float dw[C][V];
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int e = 0; e < V; ++e) dw[c][e] = 0.f;
     const float inv_n = 1.f / static_cast<float>(a.N);
-    uint32_t stage = 0, phase = 0;
     int turn = 0;
-    bool alive = true;
     float next_rstd = first < a.M ? __ldg(a.rstd + first) : 0.f;
     for (int64_t g = blockIdx.x; g * r.rows < a.M; g += gridDim.x) {
-        const RingRow<DT> row(r, g, k, a.M, a.N, ring, stage);
+        const RingRow<DT> row(r, g, k, a.M, a.N, q.ring, q.stage);
         const float rstd = next_rstd;
         const int64_t ni = row.i + static_cast<int64_t>(gridDim.x) * r.rows;
         if (ni < a.M) next_rstd = __ldg(a.rstd + ni);
-        if (alive && !wait_bounded(full + 8 * stage, phase, w, true)) {
-            report_timeout(w, 1, stage, phase);
-            sh.abort_flag = 1;
-            alive = false;                   // (still takes part in the barriers)
+        q.wait();
+        const int end = row.live && q.alive ? static_cast<int>(a.N) + off : 0;
+        uint4 vy[C], vh[C], vr[RES ? C : 1];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int p = (t + c * r.tpr) * V;
+            vy[c] = vh[c] = make_uint4(0, 0, 0, 0);
+            if (p >= end) continue;
+            vy[c] = row.template chunk<PART>(r, 0, p, end);
+            vh[c] = row.template chunk<PART>(r, 1, p, end);
         }
-        const int end = row.live && alive ? static_cast<int>(a.N) + off : 0;
         float dot = 0.f;
         uint32_t none = 0;
-        {
-            uint4 vy[C], vh[C];              // all loads under way before the first use
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int p = (t + c * r.tpr) * V;
-                vy[c] = vh[c] = make_uint4(0, 0, 0, 0);
-                if (p >= end) continue;
-                vy[c] = row.template chunk<PART>(r, 0, p, end);
-                vh[c] = row.template chunk<PART>(r, 1, p, end);
-            }
+        for (int c = 0; c < C; ++c) {
+            const int p = (t + c * r.tpr) * V;
+            float dy[V], h[V], w[V];
+            unpack<DT>(vy[c], dy);
+            unpack<DT>(vh[c], h);
+            wt.get(c, w);
+            if (PART && (p < off || p + V > end))   // other rows' elements in the window
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int p = (t + c * r.tpr) * V;
-                float dy[V], h[V];
-                unpack<DT>(vy[c], dy);
-                unpack<DT>(vh[c], h);
-                if (PART && (p < off || p + V > end))   // other rows' elements in the window
+                for (int e = 0; e < V; ++e)
+                    if (p + e < off || p + e >= end) dy[e] = h[e] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        if (p + e < off || p + e >= end) dy[e] = h[e] = 0.f;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float x = dy[e] * h[e];
-                    dot += x * wt[c][e];
-                    dw[c][e] += x * rstd;
-                }
+            for (int e = 0; e < V; ++e) {
+                const float x = dy[e] * h[e];
+                dot += x * w[e];
+                dw[c][e] += x * rstd;
             }
         }
         row_reduce<false>(dot, none, r.tpr, sh.red[0], turn);
         turn ^= 1;
-        const float scale2 = rstd * rstd * rstd * (dot * inv_n);   // times h gives rstd xh mean(g xh)
+        const float scale = rstd * rstd * rstd * (dot * inv_n);   // times h gives rstd xh mean(g xh)
         T *dx = static_cast<T *>(a.dx) + (row.live ? row.i : 0) * a.ld_dx - off;
+        if constexpr (RES)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int p = (t + c * r.tpr) * V;
+                vr[c] = make_uint4(0, 0, 0, 0);
+                if (p < end) vr[c] = row.template chunk<PART>(r, 2, p, end);
+            }
+        q.release<DT>(r, a.M, a.N, g);       // the row is in registers now
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int p = (t + c * r.tpr) * V;
             if (p >= end) continue;
-            const uint4 vy = row.template chunk<PART>(r, 0, p, end), vh = row.template chunk<PART>(r, 1, p, end);
-            uint4 vr = make_uint4(0, 0, 0, 0);
-            if constexpr (RES) vr = row.template chunk<PART>(r, 2, p, end);
-            float dy[V], h[V], d[V], f[V];
-            unpack<DT>(vy, dy);
-            unpack<DT>(vh, h);
-            unpack<DT>(vr, f);
+            float dy[V], h[V], d[V], f[V], w[V];
+            forget(vy[c]);
+            forget(vh[c]);
+            unpack<DT>(vy[c], dy);
+            unpack<DT>(vh[c], h);
+            wt.get(c, w);
+            if constexpr (RES) unpack<DT>(vr[c], f);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                d[e] = rstd * (dy[e] * wt[c][e]) - h[e] * scale2;
+                d[e] = rstd * (dy[e] * w[e]) - h[e] * scale;
                 if constexpr (RES) d[e] += f[e];
             }
             if constexpr (PART)
@@ -672,14 +736,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             else
                 *reinterpret_cast<uint4 *>(dx + p) = pack<DT>(d);
         }
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * stage);
-        if (++stage == static_cast<uint32_t>(r.stages)) stage = 0, phase ^= 1;
     }
+    q.drain(r.stages);
     if (!a.dw) return;
     // every stage has been read: its memory takes the row slots' sums
     float *slots = reinterpret_cast<float *>(dyn_smem);
-    asm volatile("bar.sync 15, %0;" ::"n"(kRingConsumers) : "memory");
+    asm volatile("bar.sync 15, %0;" ::"n"(kRingThreads) : "memory");
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -687,8 +749,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             const int j = (t + c * r.tpr) * V + e - off;
             if (j >= 0 && j < a.N) slots[k * a.N + j] = dw[c][e];
         }
-    asm volatile("bar.sync 15, %0;" ::"n"(kRingConsumers) : "memory");
-    for (int j = threadIdx.x; j < a.N; j += kRingConsumers) {
+    asm volatile("bar.sync 15, %0;" ::"n"(kRingThreads) : "memory");
+    for (int j = threadIdx.x; j < a.N; j += kRingThreads) {
         float sum = slots[j];
         for (int s = 1; s < r.rows; ++s) sum += slots[s * a.N + j];
         a.partial[blockIdx.x * a.N + j] = sum;
@@ -702,38 +764,37 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     constexpr int V = Elem<DT>::kVec;
     extern __shared__ __align__(128) unsigned char dyn_smem[];
     __shared__ __align__(8) RingShared sh;
-    ring_init(sh, r.stages, kRingConsumers / 32);
-    const uint32_t ring = smem_u32(dyn_smem), full = smem_u32(&sh.bars[0]), empty = smem_u32(&sh.bars[kRingStages]);
-    const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, r.status};
-    if (threadIdx.x >= kRingConsumers) {
-        ring_produce<DT>(r, a.M, a.N, ring, full, empty, w);
-        return;
-    }
+    ring_init(sh, r.stages);
+    RingState q{smem_u32(dyn_smem), smem_u32(&sh.bars[0]), smem_u32(&sh.bars[kRingStages]), 0, 0,
+                WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status}};
+    q.start<DT>(r, a.M, a.N);
     const int t = threadIdx.x & (r.tpr - 1), k = threadIdx.x / r.tpr;
     const int64_t first = blockIdx.x * static_cast<int64_t>(r.rows) + k;
     const int off = PART ? row_window<DT>(first < a.M ? first : 0, a.M, a.N, r.ld[0], r.phased).off : 0;
-    float wt[C][V];
-    ring_weights<DT, C>(r, a.w, a.wdt, a.woff, t, off, a.N, wt);
+    RingWeights<DT, C, PART> wt;
+    wt.load(r, a.w, a.wdt, a.woff, t, off, a.N);
     const float inv_n = 1.f / static_cast<float>(a.N);
-    uint32_t stage = 0, phase = 0;
     int turn = 0;
-    bool alive = true;
     for (int64_t g = blockIdx.x; g * r.rows < a.M; g += gridDim.x) {
-        const RingRow<DT> row(r, g, k, a.M, a.N, ring, stage);
-        if (alive && !wait_bounded(full + 8 * stage, phase, w, true)) {
-            report_timeout(w, 1, stage, phase);
-            sh.abort_flag = 1;
-            alive = false;                   // (still takes part in the barriers)
+        const RingRow<DT> row(r, g, k, a.M, a.N, q.ring, q.stage);
+        q.wait();
+        const int end = row.live && q.alive ? static_cast<int>(a.N) + off : 0;
+        uint4 vx[C], vr[RES ? C : 1];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int p = (t + c * r.tpr) * V;
+            vx[c] = make_uint4(0, 0, 0, 0);
+            if constexpr (RES) vr[c] = make_uint4(0, 0, 0, 0);
+            if (p >= end) continue;
+            vx[c] = row.template chunk<PART>(r, 0, p, end);
+            if constexpr (RES) vr[c] = row.template chunk<PART>(r, 1, p, end);
         }
-        const int end = row.live && alive ? static_cast<int>(a.N) + off : 0;
-        auto h_of = [&](int p, float (&h)[V]) {
-            const uint4 vx = row.template chunk<PART>(r, 0, p, end);
-            uint4 vr = make_uint4(0, 0, 0, 0);
-            if constexpr (RES) vr = row.template chunk<PART>(r, 1, p, end);
-            unpack<DT>(vx, h);
+        q.release<DT>(r, a.M, a.N, g);       // the row is in registers now
+        auto h_of = [&](int c, int p, float (&h)[V]) {
+            unpack<DT>(vx[c], h);
             if constexpr (RES) {
                 float f[V];
-                unpack<DT>(vr, f);
+                unpack<DT>(vr[c], f);
 #pragma unroll
                 for (int e = 0; e < V; ++e) h[e] += f[e];
             }
@@ -753,13 +814,15 @@ __global__ void __launch_bounds__(kRingThreads, 1)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int p = (t + c * r.tpr) * V;
-            if (p >= end) continue;
             float h[V];
-            h_of(p, h);
+            h_of(c, p, h);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                ss += h[e] * h[e];
-                if (Q && a.quant == 0) amax = max(amax, magnitude(h[e] * wt[c][e]));
+            for (int e = 0; e < V; ++e) ss += h[e] * h[e];
+            if (Q && a.quant == 0) {
+                float w[V];
+                wt.get(c, w);
+#pragma unroll
+                for (int e = 0; e < V; ++e) amax = max(amax, magnitude(h[e] * w[e]));
             }
         }
         row_reduce<Q>(ss, amax, r.tpr, sh.red[0], turn);
@@ -780,11 +843,15 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             if (!(Q && a.quant > 0) && p >= end) continue;
             float y[V];
             if (p < end) {
-                h_of(p, y);
+                float w[V];
+                wt.get(c, w);
+                forget(vx[c]);
+                if constexpr (RES) forget(vr[c]);
+                h_of(c, p, y);
                 if (RES && a.res_out)
                     put(static_cast<T *>(a.res_out) + row.i * a.ld_res_out, p, y);
 #pragma unroll
-                for (int e = 0; e < V; ++e) y[e] = y[e] * rstd * wt[c][e];
+                for (int e = 0; e < V; ++e) y[e] = y[e] * rstd * w[e];
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) y[e] = 0.f;
@@ -805,10 +872,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 store_e4m3<V>(static_cast<uint8_t *>(a.out) + row.i * a.ld_out - off + p, y, inv, off - p, end - p);
             }
         }
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * stage);
-        if (++stage == static_cast<uint32_t>(r.stages)) stage = 0, phase ^= 1;
     }
+    q.drain(r.stages);
 }
 
 template <int DT>
@@ -911,7 +976,7 @@ int weight_mode(const void *w, int wdt, int dtype) {
 struct RingPlan {
     RingArgs r;
     int chunks;              // of 16 bytes per thread
-    bool part;               // rows begin or end inside a chunk
+    bool part;               // rows begin or end inside a chunk, or the weight is of another type
     int grid, smem;
 };
 
@@ -928,12 +993,12 @@ bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, 
     r.phased = M > 1 && ph > 0;
     const int64_t chunks = (N + (r.phased ? V - 1 : 0) + V - 1) / V;
     int tpr = min_tpr;
-    while (tpr < kRingConsumers && static_cast<int64_t>(tpr) * most < chunks) tpr *= 2;
+    while (tpr < kRingThreads && static_cast<int64_t>(tpr) * most < chunks) tpr *= 2;
     if (static_cast<int64_t>(tpr) * most < chunks) return false;
     // fewer rows at a time, by more threads each, until every CTA has a few turns
-    while (tpr < kRingConsumers && tpr < chunks && M * tpr < 4ll * sms * kRingConsumers) tpr *= 2;
+    while (tpr < kRingThreads && tpr < chunks && M * tpr < 4ll * sms * kRingThreads) tpr *= 2;
     r.tpr = tpr;
-    r.rows = kRingConsumers / tpr;
+    r.rows = kRingThreads / tpr;
     r.slot = static_cast<int32_t>((N * es + (r.phased ? 16 - es : 0) + 15) / 16 * 16);
     const int64_t stage = static_cast<int64_t>(r.slot) * r.rows * inputs;
     r.stages = static_cast<int32_t>(std::min<int64_t>(kRingStages, kRingBytes / stage));
@@ -1001,6 +1066,7 @@ int ring_backward(NormGradArgs a, cudaStream_t s, int sms, bool *done) {
     int rc = device_status_word(&p.r.status);
     if (rc != MBT_OK) return rc;
     p.r.wmode = weight_mode(a.w, a.wdt, DT);
+    p.part = p.part || p.r.wmode != kSameWeight;
     a.splits = p.grid;
     if (a.dw) {
         void *scratch = nullptr;
@@ -1054,6 +1120,7 @@ cudaError_t forward(const NormArgs &a, cudaStream_t s) {
         ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, a.quant > 0 ? 32 : 8, sms, &p)) {
         if (device_status_word(&p.r.status) != MBT_OK) return cudaErrorUnknown;
         p.r.wmode = weight_mode(a.w, a.wdt, DT);
+        p.part = p.part || p.r.wmode != kSameWeight;
         constexpr int k = V == 8 ? 1 : 2;
         return p.chunks <= k       ? launch_ring_forward<DT, k>(p, a, s)
                : p.chunks <= 2 * k ? launch_ring_forward<DT, 2 * k>(p, a, s)
