@@ -47,12 +47,17 @@ def _fn() -> _Functions:
     return _functions
 
 
+# (the current device and stream as torch's own generated code asks for them: the
+# public calls build objects that cost more than a small kernel's launch)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 def _stream(stream, device: torch.device) -> int:
     """Handle of `stream`, or of the current stream; the tensors' device must be current."""
-    index = torch.cuda.current_device()
-    if device.index != index:
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{index}")
-    return torch.cuda.current_stream(index).cuda_stream if stream is None else stream.cuda_stream
+    index = device.index
+    if index != _current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{_current_device()}")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
@@ -66,7 +71,7 @@ def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: torch.d
     """Row pitch of a matrix that must have this shape, type and device."""
     if not isinstance(t, torch.Tensor) or t.shape != shape:
         raise ValueError(f"{name} must be a tensor of shape {tuple(shape)}")
-    if t.dtype != dtype or t.device != device:
+    if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
     M, N = shape
     if M == 0 or N == 0:
@@ -140,26 +145,31 @@ def tile_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None,
         res_p = residual.data_ptr()
         if residual_out is None:
             residual_out = _empty(shape, dtype, device, stream)
-        ld_ro = _rows(residual_out, "residual_out", shape, dtype, device)
+        else:
+            ld_ro = _rows(residual_out, "residual_out", shape, dtype, device)
         ro_p = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     out_dtype = dtype if quant is None else E4M3
+    ld_out = 0
     if out is None:
         out = _empty(shape, out_dtype, device, stream)
-        ld_out = N
     else:
         ld_out = _rows(out, "out", shape, out_dtype, device)
     if quant is not None:
-        groups = 1 if quant == 0 else -(-N // quant)
+        groups = -(-N // quant) if quant else 1
         if scales is None:
             scales = _empty((M, groups), torch.float32, device, stream)
-        s_p = _dense(scales, "scales", (M, groups), _F32, device)
+            s_p = scales.data_ptr()
+        else:
+            s_p = _dense(scales, "scales", (M, groups), _F32, device)
     elif scales is not None:
         raise ValueError("scales need quant")
     if rstd is None:
         rstd = _empty(M, torch.float32, device, stream)
-    rstd_p = _dense(rstd, "rstd", (M,), _F32, device)
+        rstd_p = rstd.data_ptr()
+    else:
+        rstd_p = _dense(rstd, "rstd", (M,), _F32, device)
     # (an address of 0 where a tensor is empty; the call then asks for none)
     _check(_fn().tile_rmsnorm(x.data_ptr(), res_p, w_p, out.data_ptr(), ro_p, s_p, rstd_p, M, N,
                               ld_x, ld_res, ld_out, ld_ro, DTYPE_CODE[dtype], w_code, _QUANT[quant],
@@ -190,14 +200,17 @@ def tile_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
         w_code = DTYPE_CODE[weight.dtype]
         if dweight is None:
             dweight = _empty(N, torch.float32, device, stream)
-    if dweight is not None:
+            dw_p = dweight.data_ptr()
+    if dweight is not None and not dw_p:
         dw_p = _dense(dweight, "dweight", (N,), _F32, device)
     if dresidual is not None:
         ld_res = _rows(dresidual, "dresidual", shape, dtype, device)
         res_p = dresidual.data_ptr()
+    ld_dx = 0
     if dx is None:
         dx = _empty(shape, dtype, device, stream)
-    ld_dx = _rows(dx, "dx", shape, dtype, device)
+    else:
+        ld_dx = _rows(dx, "dx", shape, dtype, device)
     _check(_fn().tile_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), rstd_p, w_p, res_p,
                                        dx.data_ptr(), dw_p, M, N, ld_dy, ld_h, ld_res, ld_dx,
                                        DTYPE_CODE[dtype], w_code, weight_offset, handle),
@@ -245,9 +258,11 @@ def tile_w4_matvec(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor,
         if out_dtype not in DTYPE_CODE:
             raise ValueError(f"unsupported out_dtype {out_dtype}")
         out = _empty((T, N), out_dtype, device, stream)
+        ld_out = 0
     elif out.dtype not in DTYPE_CODE or out_dtype not in (None, out.dtype):
         raise ValueError(f"out has dtype {out.dtype}")
-    ld_out = _rows(out, "out", (T, N), out.dtype, device)
+    else:
+        ld_out = _rows(out, "out", (T, N), out.dtype, device)
     _check(_fn().tile_w4_matvec(x.data_ptr(), xs_p, q.data_ptr(), s_p, z_p, out.data_ptr(), T, N, K,
                                 ld_x, ld_q, ld_out, group, x_group, _CODE[x.dtype],
                                 DTYPE_CODE[scales.dtype], DTYPE_CODE[out.dtype], handle),
@@ -260,6 +275,9 @@ class _AdamwTensor(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("param", "grad", "exp_avg", "exp_avg_sq",
                                                      "master", "m_scales", "v_scales")]
     _fields_.append(("n", ctypes.c_int64))
+
+
+_ROW_WORDS = ctypes.sizeof(_AdamwTensor) // 8
 
 
 class AdamwTensors:
@@ -292,6 +310,9 @@ class AdamwTensors:
         if master is not None and self.dtype == torch.float32:
             raise ValueError("master weights go with 16-bit params")
         self._rows = (_AdamwTensor * max(1, count))()
+        # the rows' grad fields, one every _ROW_WORDS words
+        self._grad_pointers = (ctypes.c_uint64 * (max(1, count) * _ROW_WORDS - 1)).from_buffer(
+            self._rows, _AdamwTensor.grad.offset)
         self.sizes = []
         types = {"exp_avg": (self.state_dtype,), "exp_avg_sq": (self.state_dtype,), "master": _F32,
                  "m_scales": _F32, "v_scales": _F32}
@@ -327,10 +348,12 @@ def tile_adamw(tensors: AdamwTensors, grads, *, step: int, lr: float, beta1: flo
     if dtype not in DTYPE_CODE:
         raise ValueError(f"grads have unsupported dtype {dtype}")
     handle = _stream(stream, device)
-    for k, (g, n) in enumerate(zip(grads, tensors.sizes)):
-        if g.dtype != dtype or g.numel() != n or g.device != device or not g.is_contiguous():
-            raise ValueError(f"grads[{k}] must be a contiguous {dtype} tensor of {n} elements on {device}")
-        rows[k].grad = g.data_ptr()
+    index, pointers, at = device.index, tensors._grad_pointers, 0
+    for g, n in zip(grads, tensors.sizes):
+        if g.dtype is not dtype or g.numel() != n or g.get_device() != index or not g.is_contiguous():
+            raise ValueError(f"grads[{at // _ROW_WORDS}] must be a contiguous {dtype} tensor of {n} elements on {device}")
+        pointers[at] = g.data_ptr()
+        at += _ROW_WORDS
     gs_p = 0
     if grad_scale is not None:
         gs_p = _dense(grad_scale, "grad_scale", grad_scale.shape, _F32, device)
