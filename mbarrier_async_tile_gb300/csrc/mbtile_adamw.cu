@@ -45,6 +45,7 @@ struct AdamScalars {
     float inv_bc2;     // 1 / sqrt(bc2)
     float eps;
     float b1, b2, c1, c2;   // c = 1 - b
+    float minus_zero;  // -0, not known to the compiler
     const float *grad_scale;
     uint32_t seed;
     int32_t pdt, gdt;  // element types of parameters and gradients
@@ -67,12 +68,16 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
     return h ^ (h >> 16);
 }
 
+// 16 random bits r as what is added to a value's mantissa: r 2^4 + 2^3.
+__device__ __forceinline__ uint32_t dither_low(uint32_t h) { return (h << 4 & 0xFFFF0u) | 8u; }
+__device__ __forceinline__ uint32_t dither_high(uint32_t h) { return (h >> 12 & 0xFFFF0u) | 8u; }
+
 // t >= 0 rounded to a multiple of its e4m3 spacing, up with the probability of
-// the part cut off: 20 mantissa bits are cut, 16 of them compared with r.
+// the part cut off: 20 mantissa bits are cut, 16 of them compared with the dither's.
 // Below 2^-6 the spacing is that of 2^-6, which adding 2^-6 gives.
-__device__ __forceinline__ float round_at_random(float t, uint32_t r) {
+__device__ __forceinline__ float round_at_random(float t, uint32_t dither) {
     const float low = t < 0.015625f ? 0.015625f : 0.f;
-    const uint32_t b = __float_as_uint(t + low) + (r << 4 | 8u);
+    const uint32_t b = __float_as_uint(t + low) + dither;
     const float y = __uint_as_float(b & ~0xFFFFFu) - low;
     return t > 0.f ? fmaxf(y, 0.001953125f) : t;
 }
@@ -139,46 +144,145 @@ __device__ __forceinline__ uint2 e4m3x8_put(const float (&f)[8]) {
     return q;
 }
 
-// New p, m and v of eight elements.  EXACT (8-bit states): every operation is
-// rounded by itself, as the formulas read, so that m, sqrt(v) and with them the
-// codes do not depend on how a compiler fuses products and sums.
-template <bool EXACT>
-__device__ __forceinline__ void update(const AdamScalars &s, float gscale, float (&p)[8],
-                                       const float (&g)[8], float (&m)[8], float (&v)[8],
-                                       float (&root)[8]) {
+// New p, m and v of eight elements, states in fp32.  sqrt and division to 1 and 2
+// ulp: only p sees them.
+__device__ __forceinline__ void update32(const AdamScalars &s, float gscale, float (&p)[8],
+                                         const float (&g)[8], float (&m)[8], float (&v)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const float gk = g[k] * gscale;
-        if constexpr (EXACT) {
-            m[k] = __fadd_rn(__fmul_rn(s.b1, m[k]), __fmul_rn(s.c1, gk));
-            v[k] = __fadd_rn(__fmul_rn(s.b2, v[k]), __fmul_rn(__fmul_rn(s.c2, gk), gk));
-            root[k] = __fsqrt_rn(v[k]);
-        } else {
-            m[k] = s.b1 * m[k] + s.c1 * gk;
-            v[k] = s.b2 * v[k] + s.c2 * gk * gk;
-            root[k] = sqrt_approx(v[k]);   // to 1 ulp; only p sees it
-        }
-        p[k] = s.decay * p[k] - s.step_size * __fdividef(m[k], root[k] * s.inv_bc2 + s.eps);
+        m[k] = s.b1 * m[k] + s.c1 * gk;
+        v[k] = s.b2 * v[k] + s.c2 * gk * gk;
+        p[k] = s.decay * p[k] - s.step_size * __fdividef(m[k], sqrt_approx(v[k]) * s.inv_bc2 + s.eps);
     }
 }
 
-// A block's new codes and scales: eight elements a lane, the warp holds the block.
-__device__ __forceinline__ void block_codes(float (&m)[8], float (&root)[8], const uint32_t (&r)[8],
-                                            float *ms, float *vs) {
+// Two fp32 values in one instruction, each rounded as alone.
+struct Pair {
+    uint64_t v;
+    __device__ __forceinline__ Pair() {}
+    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    explicit __device__ __forceinline__ Pair(float a) : Pair(a, a) {}
+    __device__ __forceinline__ float2 get() const {
+        float2 f;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+        return f;
+    }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// a / b rounded to nearest: b's reciprocal rounded to nearest and one correction
+// (Markstein, IBM J. Res. Dev. 34, 1990).  nb = -b, ib = 1 / b.
+__device__ __forceinline__ Pair divide(Pair a, Pair nb, Pair ib) {
+    const Pair q = a * ib;
+    return fma2(fma2(q, nb, a), ib, q);
+}
+
+// New p and 8-bit states of a block, eight elements a lane: m and v come in as
+// values, m and root leave as codes' values, ms and vs as scales.  Every operation
+// of the states is rounded by itself, as the formulas read, so that the codes do
+// not depend on how products and sums are fused.  Packed pairs halve the
+// arithmetic, which is what bounds this form (40 instructions an element against
+// 10 bytes of bf16 parameters and gradients).
+__device__ __forceinline__ void update8(const AdamScalars &s, float gscale, float (&p)[8], const float (&g)[8],
+                                        float (&m)[8], float (&v)[8], float (&root)[8], const uint32_t (&r)[8],
+                                        float *ms, float *vs) {
+    Pair mp[4], vp[4];
+    const Pair b1(s.b1), c1(s.c1), b2(s.b2), c2(s.c2), gs(gscale);
+    // Products that are summed must not be fused with the sum, which the assembler
+    // does with packed ones: fused with an addend of -0 that it does not know.
+    const Pair zero(s.minus_zero);
     uint32_t am = 0, av = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        am = max(am, magnitude(m[k]));
-        av = max(av, magnitude(root[k]));
+    for (int k = 0; k < 4; ++k) {
+        const Pair gp = Pair(g[2 * k], g[2 * k + 1]) * gs;
+        mp[k] = fma2(b1, Pair(m[2 * k], m[2 * k + 1]), zero) + fma2(c1, gp, zero);
+        vp[k] = fma2(b2, Pair(v[2 * k], v[2 * k + 1]), zero) + fma2(c2 * gp, gp, zero);
+        const float2 a = mp[k].get(), b = vp[k].get();
+        am = max(am, max(magnitude(a.x), magnitude(a.y)));
+        av = max(av, max(__float_as_uint(b.x), __float_as_uint(b.y)));   // (v >= 0, or NaN)
     }
     am = __reduce_max_sync(0xffffffffu, am);
     av = __reduce_max_sync(0xffffffffu, av);
     *ms = group_scale(am);
-    *vs = group_scale(av);
+    *vs = group_scale(magnitude(__fsqrt_rn(__uint_as_float(av))));   // (the largest root is the largest's)
+    if (max(am, av) >= 0x7f800000u) {
+        // an infinity or NaN in the block: the plain functions
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            float mk = 0.f, vk = 0.f, pk = 0.f;
+            uint32_t rk = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        m[k] = __fdiv_rn(m[k], *ms);
-        root[k] = round_at_random(__fdiv_rn(root[k], *vs), r[k]);
+            for (int i = 0; i < 8; ++i) {
+                const float2 a = mp[i / 2].get(), b = vp[i / 2].get();
+                if (i == k) mk = i & 1 ? a.y : a.x, vk = i & 1 ? b.y : b.x, pk = p[i], rk = r[i];
+            }
+            const float x = __fsqrt_rn(vk);
+            pk = s.decay * pk - s.step_size * (mk / (x * s.inv_bc2 + s.eps));
+            const float cm = __fdiv_rn(mk, *ms), cv = round_at_random(__fdiv_rn(x, *vs), rk);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i == k) p[i] = pk, m[i] = cm, root[i] = cv;
+        }
+        return;
+    }
+    const Pair nms(-*ms), ims(__frcp_rn(*ms)), nvs(-*vs), ivs(__frcp_rn(*vs));
+    float least = kE4m3Max;
+    const Pair half(0.5f), minus(-1.f), ibc(s.inv_bc2), eps(s.eps), decay(s.decay), step(-s.step_size);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        // sqrt from its reciprocal's approximation and one correction, as above
+        const float2 b = vp[k].get();
+        const Pair y(rsqrt_approx(fmaxf(b.x, 1.17549435e-38f)), rsqrt_approx(fmaxf(b.y, 1.17549435e-38f)));
+        const Pair x0 = vp[k] * y;
+        const Pair x = fma2(fma2(x0 * minus, x0, vp[k]), y * half, x0);
+        const float2 d = fma2(x, ibc, eps).get();
+        const Pair up = mp[k] * Pair(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 np = fma2(up, step, Pair(p[2 * k], p[2 * k + 1]) * decay).get();
+        p[2 * k] = np.x;
+        p[2 * k + 1] = np.y;
+        const float2 cm = divide(mp[k], nms, ims).get(), cv = divide(x, nvs, ivs).get();
+        m[2 * k] = cm.x;
+        m[2 * k + 1] = cm.y;
+        root[2 * k] = cv.x;
+        root[2 * k + 1] = cv.y;
+        least = fminf(least, fminf(cv.x, cv.y));
+    }
+    // below the normal codes (2^-6: 1 / 28672 of the block's largest) the rounding
+    // takes twice the instructions; blocks without such an element go without
+    if (__any_sync(0xffffffffu, least < 0.015625f)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) root[k] = round_at_random(root[k], r[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            root[k] = __uint_as_float((__float_as_uint(root[k]) + r[k]) & ~0xFFFFFu);
     }
 }
 
@@ -242,19 +346,16 @@ __global__ void __launch_bounds__(kAdamThreads)
                 m[r].get(fm, MBT_F32);
                 v[r].get(fv, MBT_F32);
             }
-            update<STATE8>(s, gscale, fp, fg, fm, fv, root);
-            if constexpr (MASTER) put8<true>(t.w, i, fp, MBT_F32);
-            put8<PWIDE>(t.p, i, fp, s.pdt);
             if constexpr (STATE8) {
                 uint32_t rnd[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t h = mix32((counter + static_cast<uint32_t>(i / 2 + k)) ^ s.seed);
-                    rnd[2 * k] = h & 0xffffu;
-                    rnd[2 * k + 1] = h >> 16;
+                    rnd[2 * k] = dither_low(h);
+                    rnd[2 * k + 1] = dither_high(h);
                 }
                 float nms, nvs;
-                block_codes(fm, root, rnd, &nms, &nvs);
+                update8(s, gscale, fp, fg, fm, fv, root, rnd, &nms, &nvs);
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(t.m) + i) = e4m3x8_put(fm);
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(t.v) + i) = e4m3x8_put(root);
                 if (lane == 0) {
@@ -262,9 +363,12 @@ __global__ void __launch_bounds__(kAdamThreads)
                     t.vs[i / kAdamBlock] = nvs;
                 }
             } else {
+                update32(s, gscale, fp, fg, fm, fv);
                 put8<true>(t.m, i, fm, MBT_F32);
                 put8<true>(t.v, i, fv, MBT_F32);
             }
+            if constexpr (MASTER) put8<true>(t.w, i, fp, MBT_F32);
+            put8<PWIDE>(t.p, i, fp, s.pdt);
         }
         return;
     }
@@ -299,22 +403,23 @@ __global__ void __launch_bounds__(kAdamThreads)
                 fv[k] = static_cast<const float *>(t.v)[i];
             }
         }
-        update<STATE8>(s, gscale, fp, fg, fm, fv, root);
-        uint32_t rnd[8];
         if constexpr (STATE8) {
             // elements past the end have m = v = 0 and leave the block's scales alone
+            uint32_t rnd[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int64_t i = base + 32 * k + lane;
                 const uint32_t h = mix32((counter + static_cast<uint32_t>(i / 2)) ^ s.seed);
-                rnd[k] = i & 1 ? h >> 16 : h & 0xffffu;
+                rnd[k] = i & 1 ? dither_high(h) : dither_low(h);
             }
             float nms, nvs;
-            block_codes(fm, root, rnd, &nms, &nvs);
+            update8(s, gscale, fp, fg, fm, fv, root, rnd, &nms, &nvs);
             if (lane == 0) {
                 t.ms[base / kAdamBlock] = nms;
                 t.vs[base / kAdamBlock] = nvs;
             }
+        } else {
+            update32(s, gscale, fp, fg, fm, fv);
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -436,6 +541,7 @@ extern "C" int tile_adamw(const mbt_adamw_tensor *tensors, int64_t count, int pa
     s.b2 = static_cast<float>(beta2);
     s.c1 = static_cast<float>(1.0 - beta1);
     s.c2 = static_cast<float>(1.0 - beta2);
+    s.minus_zero = -0.f;
     s.grad_scale = grad_scale;
     s.seed = seed;
     s.pdt = param_dtype;
