@@ -76,8 +76,9 @@ struct W4Args {
     int32_t slices;             // of K, in whole steps
     int32_t slice_steps;        // steps of the longest slice
     int32_t x_rows;             // most rows of x in a unit
-    int64_t blocks;             // of 64 rows of q
-    int64_t units;              // eights of rows of x * slices * blocks
+    int32_t blocks;             // of 64 rows of q
+    int32_t units;              // eights of rows of x * slices * blocks
+    int32_t steps;              // of K
     float *partial;             // [t][slice][64 blocks], with more than one slice
     int32_t vec_scales;         // a step's 16-bit scales of a row are aligned vectors
     int32_t vec_zeros;
@@ -146,7 +147,7 @@ __device__ __forceinline__ uint4 load_x(const W4Args &a, int64_t at) {
 
 // Eight columns of x (as loaded) as B elements, scaled by 2^e with the e of their
 // group, `lanes` neighbouring lanes, which is returned as 2^-e in *down.
-__device__ __noinline__ uint4 convert_x(uint4 v, int xdt, int lanes, float *down) {
+__device__ __forceinline__ uint4 convert_x(uint4 v, int xdt, int lanes, float *down) {
     float f[8];
     if (xdt == MBT_E4M3) {
         uint32_t h[4];
@@ -158,7 +159,7 @@ __device__ __noinline__ uint4 convert_x(uint4 v, int xdt, int lanes, float *down
     uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
                           __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
     m = max(m & 0xffffu, m >> 16);
-#pragma unroll 1
+#pragma unroll
     for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     uint32_t top;                           // bits of the largest magnitude, as fp32
     if (xdt == MBT_BF16) {
@@ -333,19 +334,22 @@ __device__ __noinline__ void store_y(const W4Args &a, int64_t t, int64_t n, floa
     }
 }
 
-// A CTA's run of units, and what unit i is.
+// What unit i is.  (All counts fit 32 bits, and a 64-bit division is a hundred
+// instructions.)
 struct W4Unit {
-    int64_t t0, block, slice, step0, step1;   // first row of x, block of q, slice, its steps
+    int t0, block, slice, step0, step1;   // first row of x, block of q, slice, its steps
     int tokens;
-    __device__ __forceinline__ W4Unit(const W4Args &a, int64_t i) {
-        const int64_t steps = (a.K + kW4Step - 1) / kW4Step;
-        block = i % a.blocks;
-        const int64_t r = i / a.blocks;
-        slice = r % a.slices;
-        t0 = r / a.slices * kW4Tokens;
-        tokens = static_cast<int>(a.T - t0 < kW4Tokens ? a.T - t0 : kW4Tokens);
-        step0 = slice * steps / a.slices;
-        step1 = (slice + 1) * steps / a.slices;
+    __device__ __forceinline__ W4Unit(const W4Args &a, int i) {
+        const int r = i / a.blocks;
+        block = i - r * a.blocks;
+        const int eight = r / a.slices;
+        slice = r - eight * a.slices;
+        t0 = eight * kW4Tokens;
+        tokens = min(static_cast<int>(a.T) - t0, kW4Tokens);
+        // the first `longer` slices have a step more than the others
+        const int each = a.steps / a.slices, longer = a.steps - each * a.slices;
+        step0 = slice * each + min(slice, longer);
+        step1 = step0 + each + (slice < longer);
     }
 };
 
@@ -377,15 +381,16 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const WaitCtl w{kDefaultWaitBudgetNs, &abort_flag, a.status};
-    const int64_t u0 = blockIdx.x * a.units / gridDim.x, u1 = (blockIdx.x + 1) * a.units / gridDim.x;
+    const int u0 = static_cast<int>(static_cast<uint64_t>(blockIdx.x) * a.units / gridDim.x);
+    const int u1 = static_cast<int>(static_cast<uint64_t>(blockIdx.x + 1) * a.units / gridDim.x);
 
     if (warp == kW4Consumers) {                 // producer
         if (lane != 0) return;
         uint32_t stage = 0, phase = 1;
         int64_t issued = 0;
-        for (int64_t i = u0; i < u1; ++i) {
+        for (int i = u0; i < u1; ++i) {
             const W4Unit u(a, i);
-            for (int64_t s = u.step0; s < u.step1; ++s) {
+            for (int s = u.step0; s < u.step1; ++s) {
                 if (!arrived(empty + 8 * stage, phase, w)) {
                     report_timeout(w, 0, stage, phase);
                     abort_flag = 1;
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
 
     if (warp == kW4Consumers + 1) {             // flush
         uint32_t phase = 0;
-        for (int64_t i = u0; i < u1; ++i, phase ^= 1) {
+        for (int i = u0; i < u1; ++i, phase ^= 1) {
             const W4Unit u(a, i);
             if (!__all_sync(0xffffffffu, arrived(full_r, phase, w))) {
                 report_timeout(w, 1, kMaxStages, phase);
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
             }
             // lane: four rows of q, every other row of x
             const int n = (lane & 15) * 4;
-            const int64_t n0 = u.block * kW4Rows + n;
+            const int64_t n0 = static_cast<int64_t>(u.block) * kW4Rows + n;
 #pragma unroll 1
             for (int t = lane >> 4; t < u.tokens; t += 2) {
                 const float4 lo = *reinterpret_cast<const float4 *>(&red[0][t][n]);
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
                 if (a.slices == 1)
                     store_y(a, u.t0 + t, n0, y);
                 else
-                    *reinterpret_cast<float4 *>(a.partial + ((u.t0 + t) * a.slices + u.slice) * a.blocks * kW4Rows + n0) = y;
+                    *reinterpret_cast<float4 *>(a.partial + (static_cast<int64_t>(u.t0 + t) * a.slices + u.slice) * a.blocks * kW4Rows + n0) = y;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty_r);
@@ -442,26 +447,28 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         const int local = static_cast<int>(threadIdx.x) - 32 * (kW4Consumers + 2);
         RowScales<G> r[kAhead];
         // two walks over the same steps: one loads, the other stores kAhead steps later
-        int64_t li = u0, ls = 0, le = 0, lrow = 0;
+        int li = u0, ls = 0, le = 0;
+        int64_t lrow = 0;
         if (li < u1) {
             const W4Unit u(a, li);
-            ls = u.step0, le = u.step1, lrow = u.block * kW4Rows + local;
+            ls = u.step0, le = u.step1, lrow = static_cast<int64_t>(u.block) * kW4Rows + local;
         }
         auto load_next = [&](RowScales<G> &into) {
             if (li >= u1) return;
-            into.load(a, lrow, ls * Step::kGroups);
+            into.load(a, lrow, static_cast<int64_t>(ls) * Step::kGroups);
             if (++ls == le && ++li < u1) {
                 const W4Unit u(a, li);
-                ls = u.step0, le = u.step1, lrow = u.block * kW4Rows + local;
+                ls = u.step0, le = u.step1, lrow = static_cast<int64_t>(u.block) * kW4Rows + local;
             }
         };
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) load_next(r[k]);
         uint32_t stage = 0, phase = 1;
-        int64_t i = u0, s = 0, e = 0, row = 0;
+        int i = u0, s = 0, e = 0;
+        int64_t row = 0;
         if (i < u1) {
             const W4Unit u(a, i);
-            s = u.step0, e = u.step1, row = u.block * kW4Rows + local;
+            s = u.step0, e = u.step1, row = static_cast<int64_t>(u.block) * kW4Rows + local;
         }
         while (i < u1) {
 #pragma unroll
@@ -473,14 +480,14 @@ __global__ void __launch_bounds__(kW4Threads, 2)
                     abort_flag = 1;
                     return;
                 }
-                r[k].store(a, row, s * Step::kGroups, local,
+                r[k].store(a, row, static_cast<int64_t>(s) * Step::kGroups, local,
                            reinterpret_cast<uint2 *>(ring + stage * Step::kStage + kW4QBytes));
                 mbar_arrive(full + 8 * stage);
                 if (++stage == kStages) stage = 0, phase ^= 1;
                 load_next(r[k]);
                 if (++s == e && ++i < u1) {
                     const W4Unit u(a, i);
-                    s = u.step0, e = u.step1, row = u.block * kW4Rows + local;
+                    s = u.step0, e = u.step1, row = static_cast<int64_t>(u.block) * kW4Rows + local;
                 }
             }
         }
@@ -496,9 +503,9 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     constexpr int kHalfGroups = Step::kGroups / 2;
     uint32_t stage = 0, phase = 0, rphase = 1;
     const Nibbles nib;
-    int64_t staged = -1;                        // slice (of eight rows of x) in xbuf
+    int staged = -1;                        // slice (of eight rows of x) in xbuf
     bool alive = true;                          // no wait of this warp has run out
-    for (int64_t i = u0; i < u1; ++i) {
+    for (int i = u0; i < u1; ++i) {
         const W4Unit u(a, i);
         const int pitch = x_pitch(a.slice_steps * kW4Step);
         float *const meta = reinterpret_cast<float *>(xbuf + pitch * a.x_rows);
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
             // a warp whose wait has run out still takes part in the barriers
             staged = i / a.blocks;
             asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Consumers) : "memory");
-            stage_x<G>(a, u.step0 * kW4Step, static_cast<int>(u.step1 - u.step0) * kW4Step, u.t0,
+            stage_x<G>(a, static_cast<int64_t>(u.step0) * kW4Step, (u.step1 - u.step0) * kW4Step, u.t0,
                        u.tokens, xbuf, pitch, meta);
             asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Consumers) : "memory");
         }
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         const uint4 *x = reinterpret_cast<const uint4 *>(xbuf + tok * pitch) + (lane & 3) + half * 32;
         const float2 *m = reinterpret_cast<const float2 *>(meta) + half * kHalfGroups * 4 + (lane & 3);
         float acc[4] = {};
-        for (int64_t s = u.step0; s < u.step1 && alive; ++s) {
+        for (int s = u.step0; s < u.step1 && alive; ++s) {
             if (!__all_sync(0xffffffffu, arrived(full + 8 * stage, phase, w))) {
                 report_timeout(w, 1, stage, phase);
                 abort_flag = 1;
@@ -525,60 +532,50 @@ __global__ void __launch_bounds__(kW4Threads, 2)
             const uint4 *scales =
                 reinterpret_cast<const uint4 *>(ring + stage * Step::kStage + kW4QBytes) +
                 half * kHalfGroups * (kW4Rows / 2) + rows / 2 + (lane >> 2);
-            // 64 columns a turn (128 where a group has them): a body that stays in
-            // the instruction cache next to the scheduler
-            constexpr int kChunks = G / 32 > 2 ? G / 32 : 2;
-#pragma unroll 1
-            for (int c0 = 0; c0 < 8; c0 += kChunks) {
-                float p[4], p2[4], sl, sh;
-                __half2 zl, zh, zl64, zh64;
+            uint32_t v[4][4];
 #pragma unroll
-                for (int c = 0; c < kChunks; c += 2) {
-                    uint32_t v[4];
-                    ldmatrix_x4(v, q + ((static_cast<uint32_t>(c0 + c) + lchunk) ^ lswz) * 16u);
+            for (int c = 0; c < 4; ++c) ldmatrix_x4(v[c], q + ((2u * c + lchunk) ^ lswz) * 16u);
+            float p[4], p2[4], sl, sh;
+            __half2 zl, zh, zl64, zh64;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int k = (c + h) * 32;
-                        const uint4 b = x[4 * (c + h)];
-                        if (k % G == 0) {
-                            const uint4 s = scales[k / G * (kW4Rows / 2)];
-                            sl = __uint_as_float(s.x);
-                            sh = __uint_as_float(s.z);
-                            zl = as_half2(s.y);
-                            zh = as_half2(s.w);
-                            zl64 = __hsub2(as_half2(0x63806380u), zl);   // 960 - (1024 + z)
-                            zh64 = __hsub2(as_half2(0x63806380u), zh);
-                        }
-                        const uint32_t lo = v[2 * h], hi = v[2 * h + 1], lo8 = lo >> 8, hi8 = hi >> 8;
-                        const uint32_t a0 = nib.lower(lo, zl), a1 = nib.lower(hi, zh);
-                        const uint32_t a2 = nib.upper(lo, zl64), a3 = nib.upper(hi, zh64);
-                        const uint32_t a4 = nib.lower(lo8, zl), a5 = nib.lower(hi8, zh);
-                        const uint32_t a6 = nib.upper(lo8, zl64), a7 = nib.upper(hi8, zh64);
-                        if (k % G == 0) {
-                            mma_f16<true>(p, a0, a1, a2, a3, b.x, b.y);
-                            mma_f16<true>(p2, a4, a5, a6, a7, b.z, b.w);
-                        } else {
-                            mma_f16<false>(p, a0, a1, a2, a3, b.x, b.y);
-                            mma_f16<false>(p2, a4, a5, a6, a7, b.z, b.w);
-                        }
-                        if ((k + 32) % G != 0) continue;
-                        const float2 f = m[k / G * 4];
-                        const float f0l = f.x * sl, f1l = f.y * sl, f0h = f.x * sh, f1h = f.y * sh;
-                        acc[0] += (p[0] + p2[0]) * f0l;
-                        acc[1] += (p[1] + p2[1]) * f1l;
-                        acc[2] += (p[2] + p2[2]) * f0h;
-                        acc[3] += (p[3] + p2[3]) * f1h;
-                    }
+            for (int c = 0; c < 8; ++c) {
+                const int k = c * 32;
+                const uint4 b = x[4 * c];
+                if (k % G == 0) {
+                    const uint4 s = scales[k / G * (kW4Rows / 2)];
+                    sl = __uint_as_float(s.x);
+                    sh = __uint_as_float(s.z);
+                    zl = as_half2(s.y);
+                    zh = as_half2(s.w);
+                    zl64 = __hsub2(as_half2(0x63806380u), zl);   // 960 - (1024 + z)
+                    zh64 = __hsub2(as_half2(0x63806380u), zh);
                 }
-                x += 4 * kChunks;
-                m += kChunks * 32 / G * 4;
-                scales += kChunks * 32 / G * (kW4Rows / 2);
+                const uint32_t lo = v[c >> 1][2 * (c & 1)], hi = v[c >> 1][2 * (c & 1) + 1];
+                const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+                const uint32_t a0 = nib.lower(lo, zl), a1 = nib.lower(hi, zh);
+                const uint32_t a2 = nib.upper(lo, zl64), a3 = nib.upper(hi, zh64);
+                const uint32_t a4 = nib.lower(lo8, zl), a5 = nib.lower(hi8, zh);
+                const uint32_t a6 = nib.upper(lo8, zl64), a7 = nib.upper(hi8, zh64);
+                if (k % G == 0) {
+                    mma_f16<true>(p, a0, a1, a2, a3, b.x, b.y);
+                    mma_f16<true>(p2, a4, a5, a6, a7, b.z, b.w);
+                } else {
+                    mma_f16<false>(p, a0, a1, a2, a3, b.x, b.y);
+                    mma_f16<false>(p2, a4, a5, a6, a7, b.z, b.w);
+                }
+                if ((k + 32) % G != 0) continue;
+                const float2 f = m[k / G * 4];
+                const float f0l = f.x * sl, f1l = f.y * sl, f0h = f.x * sh, f1h = f.y * sh;
+                acc[0] += (p[0] + p2[0]) * f0l;
+                acc[1] += (p[1] + p2[1]) * f1l;
+                acc[2] += (p[2] + p2[2]) * f0h;
+                acc[3] += (p[3] + p2[3]) * f1h;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * stage);
             if (++stage == kStages) stage = 0, phase ^= 1;
-            x += 32;                            // the other half's
-            m += kHalfGroups * 4;
+            x += 64;
+            m += Step::kGroups * 4;
         }
         if (alive && !__all_sync(0xffffffffu, arrived(empty_r, rphase, w))) {
             report_timeout(w, 1, kMaxStages, rphase);
@@ -609,7 +606,7 @@ __global__ void mbt_w4_zero_kernel(void *out, int dtype, int64_t N, int64_t ld) 
 
 // The slices' sums of four outputs a thread, in slice order.
 __global__ void __launch_bounds__(128) mbt_w4_slices_kernel(const W4Args a) {
-    const int64_t n = (blockIdx.x * 128ll + threadIdx.x) * 4, t = blockIdx.y, pitch = a.blocks * kW4Rows;
+    const int64_t n = (blockIdx.x * 128ll + threadIdx.x) * 4, t = blockIdx.y, pitch = static_cast<int64_t>(a.blocks) * kW4Rows;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n >= a.N) return;
     const float *part = a.partial + t * a.slices * pitch + n;
@@ -715,7 +712,8 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
     const uintptr_t xb = type_bytes(dtype);
     a.vec_x = aligned(x, 8 * xb) && (T == 1 || ld_x * static_cast<int64_t>(xb) % (8 * static_cast<int64_t>(xb)) == 0);
     a.x_rows = static_cast<int32_t>(std::min<int64_t>(T, kW4Tokens));
-    a.blocks = (N + kW4Rows - 1) / kW4Rows;
+    const int64_t blocks = (N + kW4Rows - 1) / kW4Rows;
+    a.blocks = static_cast<int32_t>(blocks);
     const int64_t steps = (K + kW4Step - 1) / kW4Step, ctas = 2 * sms;
     // Slices of K: at least as many as x's part of shared memory asks for; among
     // the counts up to four times that (or one per step, or a unit for each CTA),
@@ -725,19 +723,21 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
     while (longest < steps && x_bytes(longest + 1, a.x_rows, group) <= kW4XBytes)
         ++longest;
     const int64_t fewest = (steps + longest - 1) / longest;
-    const int64_t most = std::min(steps, std::max(4 * fewest, ctas / (a.blocks * token_blocks)));
+    const int64_t most = std::min(steps, std::max(4 * fewest, ctas / (blocks * token_blocks)));
     int64_t best = -1, slices = fewest;
     for (int64_t s = fewest; s <= most; ++s) {
-        const int64_t units = token_blocks * a.blocks * s;
+        const int64_t units = token_blocks * blocks * s;
         const int64_t cost = (units + ctas - 1) / ctas * (10 * ((steps + s - 1) / s) + 3);
         if (best < 0 || cost < best) best = cost, slices = s;
     }
     a.slices = static_cast<int32_t>(slices);
     a.slice_steps = static_cast<int32_t>((steps + slices - 1) / slices);
-    a.units = token_blocks * slices * a.blocks;
+    a.steps = static_cast<int32_t>(steps);
+    if (token_blocks * slices * blocks > 0x7fffffff) return MBT_ERR_UNSUPPORTED;
+    a.units = static_cast<int32_t>(token_blocks * slices * blocks);
     if (a.slices > 1) {
         void *scratch = nullptr;
-        rc = owned_scratch(stream, static_cast<size_t>(a.slices) * T * a.blocks * kW4Rows * sizeof(float),
+        rc = owned_scratch(stream, static_cast<size_t>(slices) * T * blocks * kW4Rows * sizeof(float),
                            &scratch);
         if (rc != MBT_OK) return rc;
         a.partial = static_cast<float *>(scratch);
