@@ -6,11 +6,15 @@
 //
 // The work is cut into units of 64 rows of q by a slice of K short enough for
 // its part of x to stay in shared memory; slice by slice, the units are dealt out
-// evenly to the CTAs (two per SM), so that a CTA stages x once or twice.  Warp
-// roles:
+// evenly to the CTAs (two per SM), so that a CTA takes its part of x once or twice.
+// A small kernel before this one brings x into the form that the tensor
+// instructions read (done by the CTAs themselves it took 5 of 40 us at 16384 x
+// 16384 and 8 rows of x); this one starts while that runs and loads its first
+// stages of q meanwhile.  Warp roles:
 //   8 consumer warps: 16 rows each, the two halves of a step's columns;
 //   a producer thread: steps of 64 rows x 512 columns (two boxes of 64 x 128
-//   bytes) of q by bulk tensor copies into a ring of 128-byte-swizzled stages;
+//   bytes) of q by bulk tensor copies into a ring of 128-byte-swizzled stages, and
+//   a slice's part of x by one bulk copy;
 //   2 staging warps: a step's scales and zero points, converted once per CTA
 //   into the same stages, from registers loaded several steps ahead;
 //   a flush warp: takes a finished unit's sums from the consumers and, where K is
@@ -68,6 +72,7 @@ struct W4Args {
     const void *s;
     const uint8_t *z;
     const float *xs;
+    unsigned char *xb;          // x as B elements, see x_block
     void *out;
     int64_t T, N, K, ld_x, ld_out;
     int64_t groups, x_groups;   // scales of a row of q, of a row of x
@@ -181,43 +186,41 @@ __device__ __forceinline__ uint4 convert_x(uint4 v, int xdt, int lanes, float *d
                       Elem<MBT_F16>::round2(f[2], f[6]), Elem<MBT_F16>::round2(f[3], f[7]));
 }
 
-// Bytes of a row of x in shared memory: rows lie 64 bytes apart in the banks, so
-// that a warp's reads of 8 rows x 64 bytes do not collide.
-__host__ __device__ constexpr int x_pitch(int columns) { return columns * 2 + 64; }
+// x as B elements, step by step: a block for every eight rows of x and 512 columns,
+// the rows kXPitch bytes apart (64 bytes apart in the banks: a warp's reads of 8
+// rows x 64 bytes do not collide), then 2^-e of each group, [group][8].
+constexpr int kXPitch = kW4Step * 2 + 64;
+__host__ __device__ constexpr int x_block(int rows, int group) {
+    return rows * kXPitch + kW4Step / group * kW4Tokens * 4;
+}
 
-// Columns [k0, k0 + columns) of up to eight rows of x as B elements at xbuf, and
-// 2^-e of each group at meta, [group][8].  All consumer threads take part; columns
-// is a multiple of kW4Step.
+constexpr int kW4XThreads = 128;
+
+// Eight columns of one row of x per thread; a CTA holds whole steps' halves of a row.
 template <int G>
-__device__ __forceinline__ void stage_x(const W4Args &a, int64_t k0, int columns, int64_t t0,
-                                        int tokens, unsigned char *xbuf, int pitch, float *meta) {
-    constexpr int kBatch = 4, kThreads = 32 * kW4Consumers;   // kBatch loads in flight per thread
-    const int per_row = columns / 8, units = per_row * tokens;
-    for (int i0 = threadIdx.x; i0 < units; i0 += kThreads * kBatch) {
-        uint4 raw[kBatch];
-        float xs[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * kThreads;
-            const int t = i / per_row, u = i - t * per_row;
-            const int64_t k = k0 + 8 * u;
-            raw[b] = make_uint4(0, 0, 0, 0);
-            xs[b] = 1.f;
-            if (i >= units || k >= a.K) continue;
-            raw[b] = load_x(a, (t0 + t) * a.ld_x + k);
-            if (a.xs) xs[b] = __ldg(a.xs + (t0 + t) * a.x_groups + (a.x_row_scale ? 0 : k / 128));
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * kThreads;
-            if (i >= units) break;          // whole warps: units is a multiple of 64
-            const int t = i / per_row, u = i - t * per_row;
-            float down;
-            const uint4 v = convert_x(raw[b], a.xdt, G / 8, &down);
-            *reinterpret_cast<uint4 *>(xbuf + t * pitch + u * 16) = v;
-            if (u % (G / 8) == 0) meta[u / (G / 8) * kW4Tokens + t] = down * xs[b];
-        }
+__global__ void __launch_bounds__(kW4XThreads) mbt_w4_x_kernel(const __grid_constant__ W4Args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // what ran before is done: the main kernel may start, and read q and the scales
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int u = static_cast<int>(blockIdx.x) * kW4XThreads + static_cast<int>(threadIdx.x);
+    const int t = static_cast<int>(blockIdx.y);
+    const int64_t k = 8ll * u;
+    if (k >= static_cast<int64_t>(a.steps) * kW4Step) return;   // whole warps
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    float xs = 1.f, down;
+    if (k < a.K) {
+        raw = load_x(a, t * a.ld_x + k);
+        if (a.xs) xs = __ldg(a.xs + t * a.x_groups + (a.x_row_scale ? 0 : k / 128));
     }
+    const uint4 v = convert_x(raw, a.xdt, G / 8, &down);
+    const int64_t eight = t / kW4Tokens, step = u / (kW4Step / 8);
+    const int row = t % kW4Tokens, rows = min(static_cast<int>(a.T - eight * kW4Tokens), kW4Tokens);
+    const int c = u % (kW4Step / 8);
+    // (every eight but the last has eight rows)
+    unsigned char *block = a.xb + (eight * a.steps * x_block(kW4Tokens, G)) + step * x_block(rows, G);
+    *reinterpret_cast<uint4 *>(block + row * kXPitch + c * 16) = v;
+    if (c % (G / 8) == 0)
+        reinterpret_cast<float *>(block + rows * kXPitch)[c / (G / 8) * kW4Tokens + row] = down * xs;
 }
 
 // Element i of a row's scales or zero points, any type.
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     mbt_w4_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ W4Args a) {
     extern __shared__ __align__(1024) unsigned char dyn_smem[];
     constexpr int kStages = W4Step<G>::kStages;
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 2];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
     __shared__ int abort_flag;
     __shared__ __align__(16) float red[2][kW4Tokens][kW4Rows];   // [half of the columns]
     using Step = W4Step<G>;
@@ -368,6 +371,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     unsigned char *const xbuf = ring + Step::kStages * Step::kStage;
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages;
     const uint32_t full_r = empty + 8 * kStages, empty_r = full_r + 8;
+    const uint32_t full_x = empty_r + 8, empty_x = full_x + 8;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1 + kW4Stagers);
@@ -375,32 +379,40 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         }
         mbar_init(full_r, kW4Consumers);
         mbar_init(empty_r, 1);
+        mbar_init(full_x, 1);
+        mbar_init(empty_x, kW4Consumers);
         abort_flag = 0;
         fence_barrier_init();
     }
     __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The kernel before (mbt_w4_x_kernel) has waited for everything before it, so q,
+    // the scales and the zero points may be read; x as B elements and the
+    // workspace's sums only after griddepcontrol.wait.  The slices' sums' kernel
+    // may be set up from now on.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const WaitCtl w{kDefaultWaitBudgetNs, &abort_flag, a.status};
     const int u0 = static_cast<int>(static_cast<uint64_t>(blockIdx.x) * a.units / gridDim.x);
     const int u1 = static_cast<int>(static_cast<uint64_t>(blockIdx.x + 1) * a.units / gridDim.x);
 
     if (warp == kW4Consumers) {                 // producer
         if (lane != 0) return;
-        uint32_t stage = 0, phase = 1;
+        uint32_t stage = 0, phase = 1, xphase = 1;
         int64_t issued = 0;
+        int staged = -1, x_copies = 0;
+        auto give_up = [&](uint32_t st, uint32_t ph) {
+            report_timeout(w, 0, st, ph);
+            abort_flag = 1;
+            // the copies still in flight land before the CTA leaves (the stagers'
+            // arrivals may be missing: the wait is bounded)
+            for (int64_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+                wait_bounded(full + 8 * static_cast<uint32_t>(k % kStages),
+                             static_cast<uint32_t>(k / kStages & 1), w, false);
+            if (x_copies) wait_bounded(full_x, static_cast<uint32_t>(x_copies - 1) & 1u, w, false);
+        };
         for (int i = u0; i < u1; ++i) {
             const W4Unit u(a, i);
             for (int s = u.step0; s < u.step1; ++s) {
-                if (!arrived(empty + 8 * stage, phase, w)) {
-                    report_timeout(w, 0, stage, phase);
-                    abort_flag = 1;
-                    // the copies still in flight land before the CTA leaves (the
-                    // stagers' arrivals may be missing: the wait is bounded)
-                    for (int64_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
-                        wait_bounded(full + 8 * static_cast<uint32_t>(k % kStages),
-                                     static_cast<uint32_t>(k / kStages & 1), w, false);
-                    return;
-                }
+                if (!arrived(empty + 8 * stage, phase, w)) return give_up(stage, phase);
                 mbar_arrive_expect_tx(full + 8 * stage, kW4QBytes);
                 const uint32_t dst = smem_u32(ring) + stage * Step::kStage;
                 const int32_t col = static_cast<int32_t>(s * (kW4Step / 2));
@@ -409,6 +421,21 @@ __global__ void __launch_bounds__(kW4Threads, 2)
                 tma_load_2d(dst + kW4BoxBytes, &map, col + kBoxRowBytes, row, full + 8 * stage);
                 ++issued;
                 if (++stage == kStages) stage = 0, phase ^= 1;
+                // a new slice's x, behind as much of q as the ring takes at first
+                if (i / a.blocks != staged && (s + 1 == u.step1 || s + 1 - u.step0 == kStages)) {
+                    staged = i / a.blocks;
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    if (!arrived(empty_x, xphase, w)) return give_up(kStages, xphase);
+                    xphase ^= 1;
+                    const int block = x_block(u.tokens, G);
+                    const uint32_t bytes = static_cast<uint32_t>((u.step1 - u.step0) * block);
+                    mbar_arrive_expect_tx(full_x, bytes);
+                    bulk_load_1d(smem_u32(xbuf),
+                                 a.xb + static_cast<int64_t>(u.t0 / kW4Tokens) * a.steps * x_block(kW4Tokens, G) +
+                                     static_cast<int64_t>(u.step0) * block,
+                                 bytes, full_x);
+                    ++x_copies;
+                }
             }
         }
         return;
@@ -416,6 +443,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
 
     if (warp == kW4Consumers + 1) {             // flush
         uint32_t phase = 0;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         for (int i = u0; i < u1; ++i, phase ^= 1) {
             const W4Unit u(a, i);
             if (!__all_sync(0xffffffffu, arrived(full_r, phase, w))) {
@@ -501,25 +529,28 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     const uint32_t lbase = smem_u32(ring) + half * kW4BoxBytes + static_cast<uint32_t>(lrow) * 128u;
     const uint32_t lchunk = static_cast<uint32_t>(lane >> 4), lswz = static_cast<uint32_t>(lrow & 7);
     constexpr int kHalfGroups = Step::kGroups / 2;
-    uint32_t stage = 0, phase = 0, rphase = 1;
+    uint32_t stage = 0, phase = 0, rphase = 1, xphase = 0;
     const Nibbles nib;
     int staged = -1;                        // slice (of eight rows of x) in xbuf
     bool alive = true;                          // no wait of this warp has run out
     for (int i = u0; i < u1; ++i) {
         const W4Unit u(a, i);
-        const int pitch = x_pitch(a.slice_steps * kW4Step);
-        float *const meta = reinterpret_cast<float *>(xbuf + pitch * a.x_rows);
         if (i / a.blocks != staged) {
-            // a warp whose wait has run out still takes part in the barriers
+            // done with the last slice's x (every warp arrives, also one whose wait has run out)
+            if (staged >= 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty_x);
+            }
             staged = i / a.blocks;
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Consumers) : "memory");
-            stage_x<G>(a, static_cast<int64_t>(u.step0) * kW4Step, (u.step1 - u.step0) * kW4Step, u.t0,
-                       u.tokens, xbuf, pitch, meta);
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Consumers) : "memory");
+            if (alive && !__all_sync(0xffffffffu, arrived(full_x, xphase, w))) {
+                report_timeout(w, 1, kStages, xphase);
+                abort_flag = 1;
+                alive = false;
+            }
+            xphase ^= 1;
         }
-        const int tok = lane >> 2 < u.tokens ? lane >> 2 : u.tokens - 1;
-        const uint4 *x = reinterpret_cast<const uint4 *>(xbuf + tok * pitch) + (lane & 3) + half * 32;
-        const float2 *m = reinterpret_cast<const float2 *>(meta) + half * kHalfGroups * 4 + (lane & 3);
+        const int tok = lane >> 2 < u.tokens ? lane >> 2 : u.tokens - 1, block = x_block(u.tokens, G);
+        const unsigned char *xs = xbuf;
         float acc[4] = {};
         for (int s = u.step0; s < u.step1 && alive; ++s) {
             if (!__all_sync(0xffffffffu, arrived(full + 8 * stage, phase, w))) {
@@ -529,6 +560,9 @@ __global__ void __launch_bounds__(kW4Threads, 2)
                 break;
             }
             const uint32_t q = lbase + stage * Step::kStage;
+            const uint4 *x = reinterpret_cast<const uint4 *>(xs + tok * kXPitch) + (lane & 3) + half * 32;
+            const float2 *m = reinterpret_cast<const float2 *>(xs + u.tokens * kXPitch) + half * kHalfGroups * 4 +
+                              (lane & 3);
             const uint4 *scales =
                 reinterpret_cast<const uint4 *>(ring + stage * Step::kStage + kW4QBytes) +
                 half * kHalfGroups * (kW4Rows / 2) + rows / 2 + (lane >> 2);
@@ -574,8 +608,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * stage);
             if (++stage == kStages) stage = 0, phase ^= 1;
-            x += 64;
-            m += Step::kGroups * 4;
+            xs += block;
         }
         if (alive && !__all_sync(0xffffffffu, arrived(empty_r, rphase, w))) {
             report_timeout(w, 1, kMaxStages, rphase);
@@ -620,9 +653,7 @@ __global__ void __launch_bounds__(128) mbt_w4_slices_kernel(const W4Args a) {
 }
 
 // Shared memory of a unit's part of x, with its factors.
-int64_t x_bytes(int64_t steps, int rows, int group) {
-    return x_pitch(static_cast<int>(steps * kW4Step)) * rows + steps * kW4Step / group * kW4Tokens * 4;
-}
+int64_t x_bytes(int64_t steps, int rows, int group) { return steps * x_block(rows, group); }
 
 template <int G>
 cudaError_t launch_w4(const CUtensorMap &map, const W4Args &a, int grid, cudaStream_t stream) {
@@ -638,6 +669,10 @@ cudaError_t launch_w4(const CUtensorMap &map, const W4Args &a, int grid, cudaStr
         if (e != cudaSuccess) return e;
         if (dev < 64) raised[dev].store(true, std::memory_order_relaxed);
     }
+    const dim3 units(static_cast<unsigned>((a.steps * (kW4Step / 8) + kW4XThreads - 1) / kW4XThreads),
+                     static_cast<unsigned>(a.T));
+    e = launch_grid(mbt_w4_x_kernel<G>, units, kW4XThreads, stream, a);
+    if (e != cudaSuccess) return e;
     return launch_pipeline(mbt_w4_kernel<G>, grid, kW4Threads, smem, stream, map, a);
 }
 
@@ -735,13 +770,14 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
     a.steps = static_cast<int32_t>(steps);
     if (token_blocks * slices * blocks > 0x7fffffff) return MBT_ERR_UNSUPPORTED;
     a.units = static_cast<int32_t>(token_blocks * slices * blocks);
-    if (a.slices > 1) {
-        void *scratch = nullptr;
-        rc = owned_scratch(stream, static_cast<size_t>(slices) * T * blocks * kW4Rows * sizeof(float),
-                           &scratch);
-        if (rc != MBT_OK) return rc;
-        a.partial = static_cast<float *>(scratch);
-    }
+    // workspace: x as B elements, then the slices' sums
+    const int64_t xb_bytes = (token_blocks * steps * x_block(kW4Tokens, group) + 255) / 256 * 256;
+    const int64_t sum_bytes = slices > 1 ? slices * T * blocks * kW4Rows * 4 : 0;
+    void *scratch = nullptr;
+    rc = owned_scratch(stream, static_cast<size_t>(xb_bytes + sum_bytes), &scratch);
+    if (rc != MBT_OK) return rc;
+    a.xb = static_cast<unsigned char *>(scratch);
+    a.partial = reinterpret_cast<float *>(a.xb + xb_bytes);
     alignas(64) CUtensorMap map;
     rc = encode_bytes_map(&map, q, N, K / 2, ld_q, kW4Rows);
     if (rc != MBT_OK) return rc;
