@@ -16,7 +16,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libmbtile.so")
 SOURCES = ["mbtile_kernels.cu", "mbtile_host.cpp", "mbtile_noalloc.cu", "mbtile_hostio.cpp",
-           "mbtile_probe.cu", "mbtile_norm.cu", "mbtile_w4.cu", "mbtile_adamw.cu"]
+           "mbtile_probe.cu", "mbtile_norm.cu", "mbtile_norm_f16.cu", "mbtile_norm_bf16.cu",
+           "mbtile_norm_f32.cu", "mbtile_w4.cu", "mbtile_adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE]
 

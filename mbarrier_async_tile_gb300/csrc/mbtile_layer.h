@@ -5,6 +5,33 @@
 
 namespace mbt {
 
+struct NormArgs {
+    const void *x, *res, *w;
+    void *out, *res_out;
+    float *scales, *rstd;
+    int64_t M, N, ld_x, ld_res, ld_out, ld_res_out;
+    int64_t groups;          // scales per row
+    int32_t wdt, quant;      // quant: -1 none, 0 a scale per row, else columns per scale
+    float eps, woff;
+};
+
+struct NormGradArgs {
+    const void *dy, *h, *w, *dres;
+    const float *rstd;
+    void *dx;
+    float *dw, *partial;     // partial: [splits][N]
+    int64_t M, N, ld_dy, ld_h, ld_dres, ld_dx;
+    int64_t splits;
+    int32_t wdt;
+    float woff;
+};
+
+// (mbtile_norm_f16.cu, _bf16.cu, _f32.cu)  The calls after their checks, M > 0 (the gradient: N > 0 too).
+template <int DT>
+cudaError_t norm_forward(const NormArgs &a, cudaStream_t s);
+template <int DT>
+int norm_backward(const NormGradArgs &a, cudaStream_t s);
+
 // (mbtile_host.cpp)  2-D tiled map over `rows` rows of `row_bytes` bytes, `ld`
 // bytes apart: box = 128 bytes x box_rows rows, 128-byte swizzle, zero fill.
 int encode_bytes_map(CUtensorMap *map, const void *src, int64_t rows, int64_t row_bytes, int64_t ld,
