@@ -398,6 +398,7 @@ struct RingArgs {
     int32_t slot;            // bytes of a row's window, at most
     int32_t phased;          // rows may start inside a chunk
     int32_t wmode;
+    uint32_t zero;           // 0, not known to the compiler
     int32_t *status;
 };
 
@@ -538,10 +539,12 @@ __device__ __forceinline__ void ring_init(RingShared &sh, int stages) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Tells the compiler that v may have changed, so that it unpacks v again instead of
-// keeping its fp32 values (twice the registers) from an earlier use.
-__device__ __forceinline__ void forget(uint4 &v) {
-    asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
+// v, in a form that neither compiler nor assembler knows to be v (zero is a kernel
+// argument and something of the row), so that it is unpacked where it is used
+// instead of its fp32 values (twice the registers) being kept from pass to pass,
+// and those of the weight from row to row.
+__device__ __forceinline__ uint4 again(const uint4 &v, uint32_t zero) {
+    return make_uint4(v.x ^ zero, v.y ^ zero, v.z ^ zero, v.w ^ zero);
 }
 
 // A thread's weights, C chunks of them, 0 past the row: packed in x's type, or
@@ -576,13 +579,12 @@ struct RingWeights {
         }
         if (w == nullptr) woff = 0.f;
     }
-    __device__ __forceinline__ void get(int c, float (&v)[V]) {
+    __device__ __forceinline__ void get(int c, uint32_t zero, float (&v)[V]) const {
         if constexpr (W32) {
 #pragma unroll
             for (int e = 0; e < V; ++e) v[e] = f[c][e];
         } else {
-            forget(raw[c]);
-            unpack<DT>(raw[c], v);
+            unpack<DT>(again(raw[c], zero), v);
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] += woff;
@@ -648,6 +650,11 @@ struct RingThread {
     }
 };
 
+// Rows from `first` on, `step` apart.
+__device__ __forceinline__ int row_turns(int64_t M, int64_t first, int64_t step) {
+    return first < M ? static_cast<int>((M - first + step - 1) / step) : 0;
+}
+
 // C chunks of every row per thread.  dw: in registers over all of the CTA's rows,
 // then over the row slots in shared memory; one partial sum per CTA and column is
 // left for mbt_rmsnorm_dw_finish_kernel.
@@ -672,18 +679,22 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         for (int e = 0; e < V; ++e) dw[c][e] = 0.f;
     const float inv_n = 1.f / static_cast<float>(a.N);
     const int64_t rows = static_cast<int64_t>(gridDim.x) * r.rows;   // from one row of a slot to the next
-    const int64_t dx_step = rows * a.ld_dx;
     T *dx = static_cast<T *>(a.dx) + th.first * a.ld_dx - th.off + th.t * V;
     const int chunk = r.tpr * V;
     int turn = 0;
     float next_rstd = th.first < a.M ? __ldg(a.rstd + th.first) : 0.f;
-    int64_t i = th.first;
-    for (int64_t g = blockIdx.x; g * r.rows < a.M; g += gridDim.x, i += rows, dx += dx_step) {
+    const float *rstd_at = a.rstd + th.first;
+    const int turns = row_turns(a.M, static_cast<int64_t>(blockIdx.x) * r.rows, rows);
+    const int mine = row_turns(a.M, th.first, rows);
+    for (int n = 0; n < turns; ++n, dx += rows * a.ld_dx) {
+        const uint32_t z1 = r.zero & n, z2 = r.zero & ~n;
         const float rstd = next_rstd;
-        if (i + rows < a.M) next_rstd = __ldg(a.rstd + i + rows);
+        rstd_at += rows;
+        if (n + 1 < mine) next_rstd = __ldg(rstd_at);
         q.wait();
-        const int have = i < a.M && q.alive ? th.count : 0;
-        uint4 vy[C], vh[C], vr[RES ? C : 1];
+        const int have = n < mine && q.alive ? th.count : 0;
+        const int64_t i = PART ? th.first + n * rows : 0;   // (only parts of chunks ask for the row)
+        uint4 vy[C], vh[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             vy[c] = vh[c] = make_uint4(0, 0, 0, 0);
@@ -712,7 +723,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             float dy[V], h[V], w[V];
             unpack<DT>(vy[c], dy);
             unpack<DT>(vh[c], h);
-            wt.get(c, w);
+            wt.get(c, z1, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float x = dy[e] * h[e];
@@ -723,25 +734,19 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         row_reduce<false>(dot, none, r.tpr, sh.red[0], turn);
         turn ^= 1;
         const float scale = rstd * rstd * rstd * (dot * inv_n);   // times h gives rstd xh mean(g xh)
-        if constexpr (RES) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                vr[c] = make_uint4(0, 0, 0, 0);
-                if (c < have) vr[c] = th.chunk(q.stage, 2, c);
-                if (PART && have && th.tail) th.last_chunk(r, 2, c, i, a.M, vr[c]);
-            }
-        }
-        q.release<DT>(r, a.M, a.N, g);       // the row is in registers now
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if (c >= have) continue;
+            uint4 vr = make_uint4(0, 0, 0, 0);
+            if constexpr (RES) {
+                vr = th.chunk(q.stage, 2, c);
+                if (PART && th.tail) th.last_chunk(r, 2, c, i, a.M, vr);
+            }
             float dy[V], h[V], d[V], f[V], w[V];
-            forget(vy[c]);
-            forget(vh[c]);
-            unpack<DT>(vy[c], dy);
-            unpack<DT>(vh[c], h);
-            wt.get(c, w);
-            if constexpr (RES) unpack<DT>(vr[c], f);
+            unpack<DT>(again(vy[c], z2), dy);
+            unpack<DT>(again(vh[c], z2), h);
+            wt.get(c, z2, w);
+            if constexpr (RES) unpack<DT>(vr, f);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 d[e] = rstd * (dy[e] * w[e]) - h[e] * scale;
@@ -749,6 +754,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             }
             th.put(dx + c * chunk, c, d);
         }
+        q.release<DT>(r, a.M, a.N, blockIdx.x + static_cast<int64_t>(n) * gridDim.x);
     }
     q.drain(r.stages);
     if (!a.dw) return;
@@ -793,10 +799,13 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     const bool write_res = RES && a.res_out != nullptr;
     const int chunk = r.tpr * V;
     int turn = 0;
-    int64_t i = th.first;
-    for (int64_t g = blockIdx.x; g * r.rows < a.M; g += gridDim.x, i += rows, out += out_step, res += res_step) {
+    const int turns = row_turns(a.M, static_cast<int64_t>(blockIdx.x) * r.rows, rows);
+    const int mine = row_turns(a.M, th.first, rows);
+    for (int n = 0; n < turns; ++n, out += out_step, res += res_step) {
+        const uint32_t z1 = r.zero & n, z2 = r.zero & ~n;
         q.wait();
-        const int have = i < a.M && q.alive ? th.count : 0;
+        const int have = n < mine && q.alive ? th.count : 0;
+        const int64_t i = th.first + n * rows;
         float h[C][V];
         {
             uint4 vx[C], vr[RES ? C : 1];
@@ -825,7 +834,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 }
             }
         }
-        q.release<DT>(r, a.M, a.N, g);       // the row is in registers now
+        q.release<DT>(r, a.M, a.N, blockIdx.x + static_cast<int64_t>(n) * gridDim.x);   // the row is in registers now
         if (PART && have && (th.head || th.tail))
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -838,7 +847,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             for (int e = 0; e < V; ++e) ss += h[c][e] * h[c][e];
             if (Q && a.quant == 0) {
                 float w[V];
-                wt.get(c, w);
+                wt.get(c, z2, w);
 #pragma unroll
                 for (int e = 0; e < V; ++e) amax = max(amax, magnitude(h[c][e] * w[e]));
             }
@@ -851,7 +860,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             scale = group_scale(magnitude(__uint_as_float(amax) * rstd));
             inv = 1.f / scale;
         }
-        if (th.t == 0 && i < a.M) {
+        if (th.t == 0 && n < mine) {
             a.rstd[i] = rstd;
             if (Q && a.quant == 0) a.scales[i] = scale;
         }
@@ -860,7 +869,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         for (int c = 0; c < C; ++c) {
             if (c < have && write_res) th.put(res + c * chunk, c, h[c]);
             float w[V];
-            wt.get(c, w);
+            wt.get(c, z1, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) h[c][e] = h[c][e] * rstd * w[e];
             if constexpr (!Q) {
