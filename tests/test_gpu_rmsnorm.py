@@ -96,14 +96,59 @@ def test_pitches_and_offsets(pad, offset, N, quant):
     assert bool((raw[:, :8 * es] == 0x55).all()) and bool((raw[:, (8 + N) * es:] == 0x55).all())
 
 
+# enough rows for the persistent kernels, whole chunks and rows that begin inside one
+LARGE = [(700, 16384), (2600, 4096), (1300, 16383), (2100, 5001), (40000, 256), (9001, 1032), (620, 20480)]
+
+
+@pytest.mark.parametrize("M,N", LARGE)
+@pytest.mark.parametrize("dtype,wdt", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32"), ("bf16", None), ("f32", "f16")])
+@pytest.mark.parametrize("residual", [False, True])
+def test_many_rows(M, N, dtype, wdt, residual):
+    dt = TYPES[dtype]
+    x = randn((M, N), dt, 60)
+    r = randn((M, N), dt, 61, 3.0) if residual else None
+    w = None if wdt is None else randn(N, TYPES[wdt], 62)
+    off = 0.5 if wdt == "f16" else 0.0
+    got = mbt.tile_rmsnorm(x, w, r, eps=1e-5, weight_offset=off)
+    check_forward(x, w, r, got, 1e-5, off, None)
+    h = x if r is None else got.residual
+    dy = randn((M, N), dt, 63)
+    dx, dw = mbt.tile_rmsnorm_backward(dy, h, got.rstd, w, dresidual=r, weight_offset=off)
+    if wdt is None:
+        dw = torch.empty(N, device="cuda")
+        dx, dw = mbt.tile_rmsnorm_backward(dy, h, got.rstd, w, dresidual=r, dweight=dw)
+    check_backward(dy, h, got.rstd, w, r, dx, dw, off)
+    assert mbt.tile_status()[0] == 0
+
+
+@pytest.mark.parametrize("M,N", LARGE)
+@pytest.mark.parametrize("quant", [0, 32, 64, 128])
+def test_many_rows_e4m3(M, N, quant):
+    x, w, r = randn((M, N), torch.bfloat16, 64), randn(N, torch.bfloat16, 65), randn((M, N), torch.bfloat16, 66)
+    check_forward(x, w, r, mbt.tile_rmsnorm(x, w, r, eps=1e-6, quant=quant), 1e-6, 0.0, quant)
+
+
+@pytest.mark.parametrize("pad", [8, 3])
+def test_many_rows_with_pitches(pad):
+    M, N, dt = 2600, 4001, torch.bfloat16
+    x, r, dy = (pitched(randn((M, N), dt, 67 + k), pad) for k in range(3))
+    w = randn(N, dt, 70)
+    wide = [torch.zeros(M, N + pad, dtype=dt, device="cuda") for _ in range(3)]
+    got = mbt.tile_rmsnorm(x, w, r, out=wide[0][:, :N], residual_out=wide[1][:, :N], eps=1e-6)
+    check_forward(x, w, r, got, 1e-6, 0.0, None)
+    dx, dw = mbt.tile_rmsnorm_backward(dy, x, got.rstd, w, dresidual=r, dx=wide[2][:, :N])
+    check_backward(dy, x, got.rstd, w, r, dx, dw)
+    assert all(bool((t[:, N:] == 0).all()) for t in wide)
+
+
 def test_in_place():
-    for N in (1024, 1001):
-        x, r, w = randn((65, N), torch.bfloat16, 13), randn((65, N), torch.bfloat16, 14), randn(N, torch.bfloat16, 15)
+    for rows, N in ((65, 1024), (65, 1001), (2600, 4001)):
+        x, r, w = randn((rows, N), torch.bfloat16, 13), randn((rows, N), torch.bfloat16, 14), randn(N, torch.bfloat16, 15)
         want = mbt.tile_rmsnorm(x, w, r)
         x2, r2 = x.clone(), r.clone()
         got = mbt.tile_rmsnorm(x2, w, r2, out=x2, residual_out=r2)
         assert torch.equal(got.out, want.out) and torch.equal(r2, want.residual)
-        dy, dr = randn((65, N), torch.bfloat16, 16), randn((65, N), torch.bfloat16, 17)
+        dy, dr = randn((rows, N), torch.bfloat16, 16), randn((rows, N), torch.bfloat16, 17)
         dx, dw = mbt.tile_rmsnorm_backward(dy, r2, got.rstd, w, dresidual=dr)
         for target in ("dy", "dres"):
             a, b = dy.clone(), dr.clone()
