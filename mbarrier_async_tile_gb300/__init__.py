@@ -154,13 +154,20 @@ def _load():
         lib.tile_host_release.argtypes = []
         lib.tile_workspace_release.argtypes = [vp]
         lib.tile_read_checksum.argtypes = [vp, ctypes.c_size_t, vp, vp]
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        lib.tile_rmsnorm.argtypes = [vp] * 7 + [i64] * 6 + [i32] * 3 + [f32, f32, vp]
+        lib.tile_rmsnorm_backward.argtypes = [vp] * 7 + [i64] * 6 + [i32] * 2 + [f32, vp]
+        lib.tile_w4_matvec.argtypes = [vp] * 6 + [i64] * 6 + [i32] * 5 + [vp]
+        lib.tile_adamw.argtypes = ([vp, i64, i32, i32, i32, i64] + [f64] * 5 +
+                                   [vp, ctypes.c_uint32, vp])
         for name in ("tile_copy", "tile_copy_ex", "tile_rowsum", "tile_rowsum_ex",
                      "tile_copy_rowsum", "tile_copy_rowsum_ex",
                      "tile_rowsum_workspace_bytes", "tile_copy_rowsum_workspace_bytes",
                      "tile_plan", "tile_plan_device", "tile_status", "tile_device_info",
                      "tile_copy_host", "tile_rowsum_host", "tile_colsum_host",
                      "tile_host_release", "tile_workspace_release", "tile_read_checksum",
-                     "tile_colsum", "tile_colsum_ex", "tile_colsum_workspace_bytes"):
+                     "tile_colsum", "tile_colsum_ex", "tile_colsum_workspace_bytes",
+                     "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw"):
             getattr(lib, name).restype = ctypes.c_int
         _C = lib
         return lib

@@ -18,7 +18,7 @@ def built_library():
 
 
 def norm(x=A, res=0, w=B, out=C_, ro=0, scales=0, rstd=D, M=4, N=64, ld=(0, 0, 0, 0), dt=0, wdt=0, quant=-1, eps=1e-6):
-    return layer._fn().tile_rmsnorm(x, res, w, out, ro, scales, rstd, M, N, *ld, dt, wdt, quant, eps, 0.0, None)
+    return mbt.C.tile_rmsnorm(x, res, w, out, ro, scales, rstd, M, N, *ld, dt, wdt, quant, eps, 0.0, None)
 
 
 @pytest.mark.parametrize("bad,code", [
@@ -36,7 +36,7 @@ def test_norm_of_no_rows():
 
 
 def grad(dy=A, h=B, rstd=C_, w=D, dres=0, dx=A, dw=D, M=4, N=64, ld=(0, 0, 0, 0), dt=1, wdt=1):
-    return layer._fn().tile_rmsnorm_backward(dy, h, rstd, w, dres, dx, dw, M, N, *ld, dt, wdt, 0.0, None)
+    return mbt.C.tile_rmsnorm_backward(dy, h, rstd, w, dres, dx, dw, M, N, *ld, dt, wdt, 0.0, None)
 
 
 @pytest.mark.parametrize("bad,code", [
@@ -49,7 +49,7 @@ def test_norm_gradient_argument_errors(bad, code):
 
 
 def w4(x=A, xs=0, q=B, s=C_, z=0, out=D, T=1, N=64, K=128, ld=(0, 0, 0), group=128, xg=0, dt=1, sdt=1, odt=1):
-    return layer._fn().tile_w4_matvec(x, xs, q, s, z, out, T, N, K, *ld, group, xg, dt, sdt, odt, None)
+    return mbt.C.tile_w4_matvec(x, xs, q, s, z, out, T, N, K, *ld, group, xg, dt, sdt, odt, None)
 
 
 @pytest.mark.parametrize("bad,code", [
@@ -67,7 +67,7 @@ def adamw(row=None, count=1, pdt=2, gdt=2, sdt=2, step=1, lr=1e-3, gs=0, **kw):
     t = layer._AdamwTensor(param=A, grad=B, exp_avg=C_, exp_avg_sq=D, n=10)
     for k, v in (row or {}).items():
         setattr(t, k, v)
-    return layer._fn().tile_adamw(ctypes.byref(t), count, pdt, gdt, sdt, step, lr, kw.get("b1", 0.9), 0.999, 1e-8, 0.0,
+    return mbt.C.tile_adamw(ctypes.byref(t), count, pdt, gdt, sdt, step, lr, kw.get("b1", 0.9), 0.999, 1e-8, 0.0,
                                   gs, 0, None)
 
 
