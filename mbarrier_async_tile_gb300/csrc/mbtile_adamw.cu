@@ -4,9 +4,15 @@
 //   p' = p (1 - lr wd) - (lr / bc1) m' / (sqrt(v') / sqrt(bc2) + eps)
 //
 // with bc = 1 - b^step, all in fp32.  Every element is read and written once,
-// so the bound is device memory.  A launch takes a table of tensors as a kernel
-// parameter (no upload, nothing kept between calls); a CTA finds its chunk's
-// tensor in the table's running chunk counts.
+// so the bound with fp32 states is device memory (28 bytes an element in fp32:
+// 100 M elements 399 us, 7.0 TB/s; bf16 with an fp32 master copy, 40 M: 168 us,
+// 6.7 TB/s).  A launch takes a table of tensors as a kernel parameter (no upload,
+// nothing kept between calls); a CTA finds its chunk's tensor in the table's
+// running chunk counts.  A chunk is two 8-element accesses of each thread, all
+// of whose loads are under way before the first is used: with one, each CTA's
+// search and start are paid twice as often (8-bit states, 300 M bf16: 1038 us
+// against 649), and a loop over more chunks in a CTA leaves the memory idle
+// between them (819).
 //
 // 8-bit states: blocks of 256 elements share an fp32 scale; one warp holds a
 // block (8 elements a lane), so a block's largest magnitude is one warp
@@ -208,8 +214,10 @@ __device__ __forceinline__ Pair divide(Pair a, Pair nb, Pair ib) {
 // values, m and root leave as codes' values, ms and vs as scales.  Every operation
 // of the states is rounded by itself, as the formulas read, so that the codes do
 // not depend on how products and sums are fused.  Packed pairs halve the
-// arithmetic, which is what bounds this form (40 instructions an element against
-// 10 bytes of bf16 parameters and gradients).
+// arithmetic, which is what bounds this form: about 64 instructions an element
+// with the loads, hash and conversions, against 10 bytes of bf16 parameters,
+// gradients and states (300 M elements: 644 us, 4.7 TB/s, with 76 % of the issue
+// slots taken; with fp32 parameters and gradients, 16 bytes, 100 M: 259 us, 6.2 TB/s).
 __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, float (&p)[8], const float (&g)[8],
                                         float (&m)[8], float (&v)[8], float (&root)[8], const uint32_t (&r)[8],
                                         float *ms, float *vs) {
@@ -286,8 +294,11 @@ __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, floa
     }
 }
 
+// Four CTAs an SM: held to 64 registers the 8-bit forms keep a third more warps
+// to cover each other's chains (fp32 100 M: 298 -> 259 us, bf16 300 M: 649 -> 644)
+// for some 100 bytes a thread kept in local memory; five CTAs keep more there (697).
 template <bool PWIDE, bool GWIDE, bool MASTER, bool STATE8, int TABLE>
-__global__ void __launch_bounds__(kAdamThreads)
+__global__ void __launch_bounds__(kAdamThreads, 4)
     mbt_adamw_kernel(const __grid_constant__ AdamTable<TABLE> a) {
     const AdamScalars &s = a.s;
     // the chunk's tensor: the first whose running count is above the chunk
