@@ -68,6 +68,10 @@ constexpr int kW4Tokens = 8;
 constexpr int kW4XBytes = 36352;
 
 struct W4Args {
+    const uint8_t *q;           // few rows of x: q read without a tensor map
+    int64_t ld_q;
+    int32_t group_shift;        // log2 of the columns a scale covers
+    int32_t few_split;          // warps of a CTA that share a row of q
     const void *x;
     const void *s;
     const uint8_t *z;
@@ -90,6 +94,14 @@ struct W4Args {
     int32_t vec_x;              // eight columns of x are one aligned vector
     int32_t *status;
 };
+
+}  // namespace
+}  // namespace mbt
+
+#include "mbtile_w4_few.cuh"
+
+namespace mbt {
+namespace {
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -740,6 +752,19 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
     a.sdt = scale_dtype;
     a.odt = out_dtype;
     a.x_row_scale = x_group == 0;
+    const int64_t xe = static_cast<int64_t>(type_bytes(dtype));
+    if (few_pays(T, N, K) && aligned(x, 16) && (T == 1 || ld_x * xe % 16 == 0)) {
+        a.q = q;
+        a.ld_q = ld_q;
+        a.group_shift = group == 32 ? 5 : group == 64 ? 6 : 7;
+        a.few_split = K <= kFewChunk ? 1 : K <= 2 * kFewChunk ? 2 : kFewWarps;
+        const int64_t rows = kFewRows * (kFewWarps / a.few_split);
+        const dim3 grid(static_cast<unsigned>((N + rows - 1) / rows));
+        const cudaError_t e = dtype == MBT_F16    ? launch_few<MBT_F16>(a, grid, st)
+                              : dtype == MBT_BF16 ? launch_few<MBT_BF16>(a, grid, st)
+                                                  : launch_few<MBT_E4M3>(a, grid, st);
+        return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
+    }
     // a step's scales of a row as vectors: whole ones, aligned in every row
     const int vec = std::min(kW4Step / group, 8);
     a.vec_scales = scale_dtype != MBT_F32 && a.groups % vec == 0 && aligned(scales, 2 * static_cast<uintptr_t>(vec));

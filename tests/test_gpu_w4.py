@@ -171,3 +171,50 @@ def test_refusals():
     with pytest.raises(mbt.MbtError) as e:
         mbt.tile_w4_matvec(x[:, :48], q[:, :24].contiguous(), s[:, :1].contiguous())
     assert e.value.code == -3
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+@pytest.mark.parametrize("K", [32, 992, 1024, 1056, 2048, 2080, 4096, 5120, 8224])
+@pytest.mark.parametrize("xdt", ["f16", "bf16", "e4m3"])
+def test_few_rows(T, K, xdt):
+    """One to four rows: K around the columns that a warp takes, N not a multiple of its rows."""
+    group, N = (32, 64, 128)[K // 32 % 3], 1 + K % 7 + 16 * T
+    q, s, z = weights(N, K, group, 20, torch.float32 if K == 1056 else torch.float16, zeros=K % 64 == 0)
+    if xdt == "e4m3":
+        n = mbt.tile_rmsnorm(randn((T, K), torch.bfloat16, 21, 4.0), None, None, quant=128 if T % 2 else 0)
+        x, xs = n.out, n.scales
+    else:
+        x, xs = randn((T, K), TYPES[xdt], 21), None
+    out = mbt.tile_w4_matvec(x, q, s, z, group=group, x_scales=xs, out_dtype=torch.float32)
+    check(x, q, s, z, group, xs, out)
+    assert torch.equal(out, mbt.tile_w4_matvec(x, q, s, z, group=group, x_scales=xs, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_few_rows_non_finite(T):
+    """What lies past K in x and in the scales stays out; rows of x stay apart."""
+    x = pitched(randn((T, 1056), torch.bfloat16, 22), 32, 0)
+    q, s, z = weights(37, 1056, 128, 23)
+    want = mbt.tile_w4_matvec(x, q, s, z)
+    check(x, q, s, z, 128, None, want)
+    s[0, 0] = float("inf")   # (the first scale of all, of row 0 only)
+    got = mbt.tile_w4_matvec(x, q, s, z)
+    assert torch.equal(got[:, 1:], want[:, 1:]) and not bool(got[:, 0].isfinite().any())
+    x[T - 1, 1055] = float("nan")
+    got = mbt.tile_w4_matvec(x, q, s, z)
+    assert torch.equal(got[:T - 1, 1:], want[:T - 1, 1:]) and not bool(got[T - 1].isfinite().any())
+
+
+def test_few_rows_in_a_capture():
+    """No workspace: the first call on a stream may be captured."""
+    x = randn((2, 2048), torch.float16, 24)
+    q, s, z = weights(500, 2048, 64, 25)
+    want = mbt.tile_w4_matvec(x, q, s, z, group=64)
+    out, st = torch.zeros_like(want), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        mbt.tile_w4_matvec(x, q, s, z, group=64, out=out)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
