@@ -387,13 +387,17 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
 // registers were slower in the forward: bf16 4096 x 4096 28.3 us against 24.4.)
 constexpr int kRingThreads = 512;
 constexpr int kRingStages = 8;
+constexpr int kRingBars = kRingThreads / 32 * kRingStages;   // of all units
 constexpr int kRingBytes = 208 * 1024;   // shared memory for the stages
 
 struct RingArgs {
     const char *in[3];       // forward: x, residual; backward: dy, h, dresidual
     int64_t ld[3];           // pitches in bytes
     int32_t inputs;
-    int32_t tpr, rows;       // threads per row, rows per stage
+    int32_t tpr, rows;       // threads per row, rows at a time
+    int32_t unit_threads;    // that share a ring: a row's, or a warp of several rows
+    int32_t unit_rows;
+    uint32_t stage_bytes;    // of a unit
     int32_t stages;
     int32_t slot;            // bytes of a row's window, at most
     int32_t phased;          // rows may start inside a chunk
@@ -422,43 +426,51 @@ __device__ __forceinline__ RowWindow row_window(int64_t row, int64_t M, int64_t 
     return w;
 }
 
-// Warp 0: the copies of row group g into `stage`.
+// The unit's first warp: the copies of its rows from `row` on to `to`.
 template <int DT>
-__device__ __forceinline__ void ring_fill(const RingArgs &r, int64_t M, int64_t N, uint32_t ring, uint32_t full,
-                                          uint32_t stage, int64_t g) {
+__device__ __forceinline__ void ring_fill(const RingArgs &r, int64_t M, int64_t N, uint32_t to, uint32_t full,
+                                          int64_t row) {
     const int lane = threadIdx.x & 31;
-    const int64_t left = M - g * r.rows;
-    const int rows = left < r.rows ? static_cast<int>(left) : r.rows;
+    const int rows = static_cast<int>(min(M - row, static_cast<int64_t>(r.unit_rows)));
     uint32_t total = 0;
     for (int i = lane; i < rows * r.inputs; i += 32)
-        total += row_window<DT>(g * r.rows + i % rows, M, N, r.ld[i / rows], r.phased).bytes;
+        total += row_window<DT>(row + i % rows, M, N, r.ld[i / rows], r.phased).bytes;
     total = __reduce_add_sync(0xffffffffu, total);
-    if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, total);
+    if (lane == 0) mbar_arrive_expect_tx(full, total);
     __syncwarp();
-    const uint32_t base = ring + stage * static_cast<uint32_t>(r.slot * r.rows * r.inputs);
     for (int i = lane; i < rows * r.inputs; i += 32) {
         const int m = i / rows, k = i - m * rows;
-        const RowWindow win = row_window<DT>(g * r.rows + k, M, N, r.ld[m], r.phased);
+        const RowWindow win = row_window<DT>(row + k, M, N, r.ld[m], r.phased);
         if (win.bytes > 0)
-            bulk_load_1d(base + static_cast<uint32_t>((m * r.rows + k) * r.slot), r.in[m] + win.start,
-                         static_cast<uint32_t>(win.bytes), full + 8 * stage);
+            bulk_load_1d(to + static_cast<uint32_t>((m * r.unit_rows + k) * r.slot), r.in[m] + win.start,
+                         static_cast<uint32_t>(win.bytes), full);
     }
 }
 
-// The ring's position, the same in every warp.
+// A unit's ring and its position in it, the same in every one of its warps.
 struct RingState {
-    uint32_t ring, full, empty, stage = 0, phase = 0;
+    uint32_t ring, full, empty;   // shared memory: the stages, their barriers
+    int64_t row, step;            // the first of the unit's rows to be copied next, from turn to turn
+    bool lead;                    // its first warp
     WaitCtl w;
-    bool alive = true;       // no wait of this warp has run out
+    uint32_t stage = 0, phase = 0;
+    bool alive = true;            // no wait of this warp has run out
 
-    // The first rows of the CTA.
+    __device__ __forceinline__ RingState(const RingArgs &r, uint32_t memory, uint32_t bars, const WaitCtl &wait) : w(wait) {
+        const uint32_t unit = threadIdx.x / r.unit_threads;
+        ring = memory + unit * r.stages * r.stage_bytes;
+        full = bars + 8 * unit * r.stages;
+        empty = full + 8 * kRingBars;
+        row = static_cast<int64_t>(blockIdx.x) * r.rows + unit * r.unit_rows;
+        step = static_cast<int64_t>(gridDim.x) * r.rows;
+        lead = threadIdx.x - unit * r.unit_threads < 32;
+    }
+    // The unit's first rows.
     template <int DT>
     __device__ __forceinline__ void start(const RingArgs &r, int64_t M, int64_t N) {
-        if (threadIdx.x >= 32) return;
-        for (int s = 0; s < r.stages; ++s) {
-            const int64_t g = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
-            if (g * r.rows < M) ring_fill<DT>(r, M, N, ring, full, static_cast<uint32_t>(s), g);
-        }
+        if (!lead) return;
+        for (int s = 0; s < r.stages; ++s, row += step)
+            if (row < M) ring_fill<DT>(r, M, N, ring + s * r.stage_bytes, full + 8 * s, row);
     }
     // A warp whose wait has run out goes through the rows without work, so that
     // the CTA's barriers are complete.
@@ -470,15 +482,15 @@ struct RingState {
             alive = false;
         }
     }
-    // This warp has read the stage of group g.
+    // This warp has read its stage.
     template <int DT>
-    __device__ __forceinline__ void release(const RingArgs &r, int64_t M, int64_t N, int64_t g) {
+    __device__ __forceinline__ void release(const RingArgs &r, int64_t M, int64_t N) {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * stage);
-        const int64_t next = g + static_cast<int64_t>(r.stages) * gridDim.x;
-        if (threadIdx.x < 32 && alive && next * r.rows < M) {
+        if (lead && alive && row < M) {
             if (__all_sync(0xffffffffu, wait_bounded(empty + 8 * stage, phase, w, true))) {
-                ring_fill<DT>(r, M, N, ring, full, stage, next);
+                ring_fill<DT>(r, M, N, ring + stage * r.stage_bytes, full + 8 * stage, row);
+                row += step;
             } else {
                 report_timeout(w, 0, stage, phase);
                 *w.abort = 1;
@@ -489,7 +501,7 @@ struct RingState {
     }
     // After a wait that ran out: the copies under way land before the CTA leaves.
     __device__ __forceinline__ void drain(int stages) {
-        if (threadIdx.x != 0 || !*w.abort) return;
+        if (!lead || (threadIdx.x & 31) != 0 || !*w.abort) return;
         for (int s = 0; s < stages; ++s)
             for (uint32_t p = 0; p < 2; ++p) wait_bounded(full + 8 * s, p, w, false);
     }
@@ -521,20 +533,18 @@ __device__ __forceinline__ void row_reduce(float &v, uint32_t &amax, int tpr, fl
 }
 
 struct RingShared {
-    uint64_t bars[2 * kRingStages];
+    uint64_t bars[2 * kRingBars];    // full, empty: of each unit's stages
     float red[2][64];
     int abort_flag;
 };
 
-__device__ __forceinline__ void ring_init(RingShared &sh, int stages) {
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < stages; ++i) {
-            mbar_init(smem_u32(&sh.bars[i]), 1);
-            mbar_init(smem_u32(&sh.bars[kRingStages + i]), blockDim.x / 32);
-        }
-        sh.abort_flag = 0;
-        fence_barrier_init();
+__device__ __forceinline__ void ring_init(RingShared &sh, const RingArgs &r) {
+    for (int i = threadIdx.x; i < r.stages * kRingThreads / r.unit_threads; i += kRingThreads) {
+        mbar_init(smem_u32(&sh.bars[i]), 1);
+        mbar_init(smem_u32(&sh.bars[kRingBars + i]), r.unit_threads / 32);
     }
+    if (threadIdx.x == 0) sh.abort_flag = 0;
+    fence_barrier_init();
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -602,7 +612,7 @@ struct RingThread {
     int count;               // chunks of this thread
     bool head, tail;         // its first, its last chunk is not the row's alone
     int64_t first;           // first row
-    uint32_t addr, chunk_step, input_step, stage_step;   // shared memory
+    uint32_t addr, chunk_step, input_step, stage_bytes;   // shared memory
 
     __device__ __forceinline__ RingThread(const RingArgs &r, int64_t M, int64_t N, uint32_t ring) {
         t = threadIdx.x & (r.tpr - 1);
@@ -615,13 +625,13 @@ struct RingThread {
         head = PART && off > 0 && t == 0;
         tail = PART && end % V != 0 && count > 0 && t + (count - 1) * r.tpr == chunks - 1;
         chunk_step = static_cast<uint32_t>(r.tpr) * 16u;
-        input_step = static_cast<uint32_t>(r.rows * r.slot);
-        stage_step = input_step * static_cast<uint32_t>(r.inputs);
-        addr = ring + static_cast<uint32_t>(k * r.slot + t * 16);
+        input_step = static_cast<uint32_t>(r.unit_rows * r.slot);
+        stage_bytes = r.stage_bytes;
+        addr = ring + static_cast<uint32_t>(k % r.unit_rows * r.slot + t * 16);
     }
     // Chunk c of input m in the stage at `stage`.
     __device__ __forceinline__ uint4 chunk(uint32_t stage, int m, int c) const {
-        return lds128(addr + stage * stage_step + static_cast<uint32_t>(m) * input_step +
+        return lds128(addr + stage * stage_bytes + static_cast<uint32_t>(m) * input_step +
                       static_cast<uint32_t>(c) * chunk_step);
     }
     __device__ __forceinline__ bool whole(int c) const {
@@ -665,9 +675,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     constexpr int V = Elem<DT>::kVec;
     extern __shared__ __align__(128) unsigned char dyn_smem[];
     __shared__ __align__(8) RingShared sh;
-    ring_init(sh, r.stages);
-    RingState q{smem_u32(dyn_smem), smem_u32(&sh.bars[0]), smem_u32(&sh.bars[kRingStages]), 0, 0,
-                WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status}};
+    ring_init(sh, r);
+    RingState q(r, smem_u32(dyn_smem), smem_u32(&sh.bars[0]), WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status});
     q.start<DT>(r, a.M, a.N);
     const RingThread<DT, C, PART> th(r, a.M, a.N, q.ring);
     RingWeights<DT, C, PART, W32> wt;
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     int turn = 0;
     float next_rstd = th.first < a.M ? __ldg(a.rstd + th.first) : 0.f;
     const float *rstd_at = a.rstd + th.first;
-    const int turns = row_turns(a.M, static_cast<int64_t>(blockIdx.x) * r.rows, rows);
+    const int turns = row_turns(a.M, th.first - th.k % r.unit_rows, rows);
     const int mine = row_turns(a.M, th.first, rows);
     for (int n = 0; n < turns; ++n, dx += rows * a.ld_dx) {
         const uint32_t z1 = r.zero & n, z2 = r.zero & ~n;
@@ -754,7 +763,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             }
             th.put(dx + c * chunk, c, d);
         }
-        q.release<DT>(r, a.M, a.N, blockIdx.x + static_cast<int64_t>(n) * gridDim.x);
+        q.release<DT>(r, a.M, a.N);
     }
     q.drain(r.stages);
     if (!a.dw) return;
@@ -784,9 +793,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     constexpr int V = Elem<DT>::kVec;
     extern __shared__ __align__(128) unsigned char dyn_smem[];
     __shared__ __align__(8) RingShared sh;
-    ring_init(sh, r.stages);
-    RingState q{smem_u32(dyn_smem), smem_u32(&sh.bars[0]), smem_u32(&sh.bars[kRingStages]), 0, 0,
-                WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status}};
+    ring_init(sh, r);
+    RingState q(r, smem_u32(dyn_smem), smem_u32(&sh.bars[0]), WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status});
     q.start<DT>(r, a.M, a.N);
     const RingThread<DT, C, PART> th(r, a.M, a.N, q.ring);
     RingWeights<DT, C, PART, W32> wt;
@@ -799,7 +807,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     const bool write_res = RES && a.res_out != nullptr;
     const int chunk = r.tpr * V;
     int turn = 0;
-    const int turns = row_turns(a.M, static_cast<int64_t>(blockIdx.x) * r.rows, rows);
+    const int turns = row_turns(a.M, th.first - th.k % r.unit_rows, rows);
     const int mine = row_turns(a.M, th.first, rows);
     for (int n = 0; n < turns; ++n, out += out_step, res += res_step) {
         const uint32_t z1 = r.zero & n, z2 = r.zero & ~n;
@@ -834,7 +842,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 }
             }
         }
-        q.release<DT>(r, a.M, a.N, blockIdx.x + static_cast<int64_t>(n) * gridDim.x);   // the row is in registers now
+        q.release<DT>(r, a.M, a.N);   // the row is in registers now
         if (PART && have && (th.head || th.tail))
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -1012,11 +1020,16 @@ bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, 
     int tpr = min_tpr;
     while (tpr < kRingThreads && static_cast<int64_t>(tpr) * usual < chunks) tpr *= 2;
     if (static_cast<int64_t>(tpr) * most < chunks) return false;
-    // ... but fewer rows at a time, by more threads each, until every CTA has a few turns
-    while (tpr < kRingThreads && tpr < chunks && M * tpr < 4ll * sms * kRingThreads) tpr *= 2;
+    // ... but fewer rows at a time, by more threads each, until every CTA has a turn
+    // (gradient of 64 x 4096: 9.6 us without, 6.7 with; waiting for four turns each
+    // took 17.3 us against 15.9 of 1024 x 4096)
+    while (tpr < kRingThreads && tpr < chunks && M * tpr < static_cast<int64_t>(sms) * kRingThreads) tpr *= 2;
     r.tpr = tpr;
     r.rows = kRingThreads / tpr;
+    r.unit_threads = std::max(tpr, 32);
+    r.unit_rows = r.unit_threads / tpr;
     r.slot = static_cast<int32_t>((N * es + (r.phased ? 16 - es : 0) + 15) / 16 * 16);
+    r.stage_bytes = static_cast<uint32_t>(r.slot) * r.unit_rows * inputs;
     const int64_t stage = static_cast<int64_t>(r.slot) * r.rows * inputs;
     r.stages = static_cast<int32_t>(std::min<int64_t>(kRingStages, kRingBytes / stage));
     if (r.stages < 2) return false;
@@ -1148,10 +1161,18 @@ cudaError_t launch_forward(const NormVecArgs &va, dim3 grid, int threads, cudaSt
              : launch_grid(mbt_rmsnorm_kernel<DT, C, false, false>, grid, threads, s, va);
 }
 
-// The ring's start (weights, barriers, the first rows' latency) is paid once per
-// call: worth it from about a row's worth of 16 MB on.
-bool ring_forward_pays(const NormArgs &a, int64_t es, int sms) {
-    return a.M * a.N * es >= (16ll << 20) && a.M >= 4 * sms;
+// Where the ring is faster than a row in registers (us, ring / registers, bf16):
+//  - its start (weights, barriers, the first rows' latency) is paid once per call:
+//    512 x 8192 9.4 / 8.3, 1024 x 8192 13.8 / 16.2, fp16 16384 x 16384 351 / 429;
+//  - rows of up to 1 KB are a warp's at most in registers, with no barrier:
+//    131072 x 256 81 / 41, 131072 x 512 101 / 81; fp32 65536 x 512 46 / 61;
+//  - two matrices read keep enough bytes on their way with short rows as well:
+//    65536 x 2048 185 / 161, 4096 x 4096 24.2 / 26.1; rows that start inside a
+//    chunk do not: 65537 x 1001 112 / 128; nor does the arithmetic of an 8-bit output.
+bool ring_forward_pays(const NormArgs &a, int64_t es, int sms, int phase) {
+    const int64_t row = a.N * es;
+    if (a.M * row < (16ll << 20) || a.M < 4 * sms || row <= 1024) return false;
+    return row > 4096 || !a.res || phase != 0 || a.quant != MBT_QUANT_NONE;
 }
 
 template <int DT>
@@ -1172,7 +1193,7 @@ cudaError_t forward_any(const NormArgs &a, cudaStream_t s) {
     const void *in[2] = {a.x, a.res};
     const int64_t ld[2] = {a.ld_x, a.ld_res};
     RingPlan p;
-    if (same && ring_forward_pays(a, es, sms) &&
+    if (same && ring_forward_pays(a, es, sms, ph) &&
         ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, V == 8 ? 5 : 8, a.quant > 0 ? 32 : 8, sms, &p)) {
         if (device_status_word(&p.r.status) != MBT_OK) return cudaErrorUnknown;
         p.r.wmode = weight_mode(a.w, a.wdt, DT);
@@ -1188,7 +1209,7 @@ cudaError_t forward_any(const NormArgs &a, cudaStream_t s) {
     // where groups of up to 128 columns are reduced, and all of a CTA for a few
     // rows, where the time is one row's latency.
     int tpr = a.quant > 0 ? 32 : 8;
-    while (tpr < 1024 && (tpr * 2 < chunks || (a.M < 64 && tpr < chunks))) tpr *= 2;
+    while (tpr < 1024 && (tpr * 2 < chunks || (tpr < chunks && a.M * tpr * 2 <= 1024ll * sms))) tpr *= 2;
     va.tpr = tpr;
     va.wmode = weight_mode(a.w, a.wdt, DT);
     const int threads = tpr > 32 ? tpr : 128, rows = threads / tpr;
