@@ -148,6 +148,15 @@ __device__ __forceinline__ uint32_t magnitude(float v) {
     return __float_as_uint(v) & 0x7fffffffu;
 }
 
+// The largest magnitude of m (one already) and the values of f, two at a time.
+template <int V>
+__device__ __forceinline__ uint32_t magnitude_max(uint32_t m, const float (&f)[V]) {
+    float r = __uint_as_float(m);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(r), "f"(f[e]), "f"(f[e + 1]));
+    return __float_as_uint(r);
+}
+
 // The scale of a group from its largest magnitude (NaN stays NaN).
 __device__ __forceinline__ float group_scale(uint32_t amax) {
     const float s = __uint_as_float(amax) * (1.f / kE4m3Max);

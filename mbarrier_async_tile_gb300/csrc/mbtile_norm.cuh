@@ -233,9 +233,12 @@ __device__ __forceinline__ void load_weight(const void *w, int mode, int wdt, fl
 template <int V>
 __device__ __forceinline__ void store_e4m3(uint8_t *o, const float (&y)[V], float inv, int lo, int hi) {
     uint32_t q[V / 4];
+    const Pair ii(inv);
 #pragma unroll
-    for (int e = 0; e < V; e += 4)
-        q[e / 4] = to_e4m3x2(y[e] * inv, y[e + 1] * inv) | to_e4m3x2(y[e + 2] * inv, y[e + 3] * inv) << 16;
+    for (int e = 0; e < V; e += 4) {
+        const float2 a = (Pair(y[e], y[e + 1]) * ii).get(), b = (Pair(y[e + 2], y[e + 3]) * ii).get();
+        q[e / 4] = to_e4m3x2(a.x, a.y) | to_e4m3x2(b.x, b.y) << 16;
+    }
     if (lo <= 0 && hi >= V && (reinterpret_cast<uintptr_t>(o) & (V - 1)) == 0) {
         if constexpr (V == 8)
             *reinterpret_cast<uint2 *>(o) = make_uint2(q[0], q[1]);
@@ -305,7 +308,8 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
             float w[V];
             load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p, off, a.N, w);
 #pragma unroll
-            for (int e = 0; e < V; ++e) amax = max(amax, magnitude(h[e] * w[e]));
+            for (int e = 0; e < V; ++e) w[e] *= h[e];
+            amax = magnitude_max(amax, w);
         }
     }
 #pragma unroll
@@ -356,9 +360,7 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
             store_chunk<DT>(static_cast<T *>(a.out) + i * a.ld_out - off + p, pack<DT>(y), lo, hi);
         } else {
             if (a.quant > 0) {                         // (rows start at a chunk)
-                uint32_t m = 0;
-#pragma unroll
-                for (int e = 0; e < V; ++e) m = max(m, magnitude(y[e]));
+                uint32_t m = magnitude_max(0u, y);
                 for (int o = 1; o < a.quant / V; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
                 scale = group_scale(m);
                 inv = 1.f / scale;
@@ -857,7 +859,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 float w[V];
                 wt.get(c, z2, w);
 #pragma unroll
-                for (int e = 0; e < V; ++e) amax = max(amax, magnitude(h[c][e] * w[e]));
+                for (int e = 0; e < V; ++e) w[e] *= h[c][e];
+                amax = magnitude_max(amax, w);
             }
         }
         row_reduce<Q>(ss, amax, r.tpr, sh.red[0], turn);
@@ -878,14 +881,16 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             if (c < have && write_res) th.put(res + c * chunk, c, h[c]);
             float w[V];
             wt.get(c, z1, w);
+            const Pair rr(rstd);
 #pragma unroll
-            for (int e = 0; e < V; ++e) h[c][e] = h[c][e] * rstd * w[e];
+            for (int e = 0; e < V; e += 2) {
+                const float2 y = (Pair(h[c][e], h[c][e + 1]) * rr * Pair(w[e], w[e + 1])).get();
+                h[c][e] = y.x, h[c][e + 1] = y.y;
+            }
             if constexpr (!Q) {
                 if (c < have) th.put(out + c * chunk, c, h[c]);
             } else if (a.quant > 0) {        // (rows start at a chunk)
-                gmax[c] = 0;
-#pragma unroll
-                for (int e = 0; e < V; ++e) gmax[c] = max(gmax[c], magnitude(h[c][e]));
+                gmax[c] = magnitude_max(0u, h[c]);
             }
         }
         if constexpr (Q) {
