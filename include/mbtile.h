@@ -31,8 +31,9 @@
  *   - All data pointers are DEVICE pointers owned by the caller, except in
  *     the host-buffer forms (tile_copy_host, tile_rowsum_host).  The library
  *     allocates device memory in two places only: the host-buffer forms'
- *     staging pool, and the sum workspace it keeps per (device, stream) for
- *     row and column sums called without a workspace of the caller's (see
+ *     staging pool, and the workspace it keeps per (device, stream) for row
+ *     and column sums called without a workspace of the caller's, for
+ *     tile_rmsnorm_backward with dweight and for tile_w4_matvec (see
  *     tile_rowsum; allocated in stream order with cudaMallocAsync on the
  *     first such call on a stream, freed by tile_workspace_release).  Besides
  *     those it keeps per-device caches (SM count, shared-memory limit, the
@@ -507,10 +508,9 @@ int tile_colsum_host(const void *src, float *out, int64_t M, int64_t N, int tile
 /* Frees the current device's idle staging sets of the host-buffer forms. */
 int tile_host_release(void);
 
-/* Frees, in stream order (cudaFreeAsync on `stream`), the sum workspace the
- * library keeps for (current device, stream); the next row or column sum
- * without a caller's workspace on that stream allocates a new one.  MBT_OK
- * when there is none. */
+/* Frees, in stream order (cudaFreeAsync on `stream`), the workspace the
+ * library keeps for (current device, stream); the next call on that stream
+ * that needs one allocates it anew.  MBT_OK when there is none. */
 int tile_workspace_release(void *stream);
 
 /*
@@ -608,10 +608,15 @@ int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd, cons
  *   zeros         optional, uint8 of the same shape, values 0..15; NULL: 8.
  *   group         32, 64 or 128; K a multiple of 32 (MBT_ERR_UNSUPPORTED).
  * Made for 1 to 8 rows of x; more are taken eight at a time, each reading q
- * again.  Where K is sliced over CTAs the slices' sums are added in slice order
- * (equal calls give equal bits), in the library's workspace for (device,
- * stream), see tile_rowsum: make the first call on a stream, with the largest
- * shape, before a capture on it.  A NaN or infinity in row t of x makes values of row t of out NaN or
+ * again (T up to 65535, MBT_ERR_UNSUPPORTED).  Up to four rows of x with a q of
+ * few elements (N K up to 96 Mi for one row, 48 Mi / T for more; x 16-byte aligned
+ * with a pitch of whole 16 bytes) take one kernel and no workspace.  All other
+ * calls take x in the tensor instructions' form and, where K is sliced over CTAs,
+ * the slices' sums from the library's workspace for (device, stream), see
+ * tile_rowsum: make the first call on a stream, with the largest shape, before a
+ * capture on it (MBT_ERR_WORKSPACE where it would have to grow in one).  Sums are
+ * added in a fixed order: equal calls give equal bits.  A NaN or infinity in
+ * row t of x makes values of row t of out NaN or
  * infinite and leaves the other rows alone.  T = 0 or N = 0 does nothing,
  * K = 0 writes zeros.
  */

@@ -259,7 +259,10 @@ struct NormVecArgs {
 
 // `tpr` threads hold a row in registers, C chunks each: one pass over memory.
 // Bound by device memory; rows in flight on an SM (CTAs that fit) hide the
-// latency between a row's loads and its stores.
+// latency between a row's loads and its stores (bf16, residual: 131072 x 512
+// 81 us, 6.6 TB/s; 256 x 8192 3.6 us, 4.6 TB/s from L2; one row of 8192 to e4m3 3.4
+// us, the latency of a launch and a row).  To e4m3 the short rows are bound by
+// instructions (131072 x 512 by groups of 128: 97 us, 2.1 TB/s).
 template <int DT, int C, bool RES, bool Q>
 __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant__ NormVecArgs va) {
     using T = typename Elem<DT>::type;
@@ -376,17 +379,26 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 // Rows through a ring in shared memory
 // ---------------------------------------------------------------------------
-// A persistent CTA per SM keeps the next rows of every input matrix on their way
-// into a ring of stages by 1-D bulk copies (the row's 16-byte-aligned window of
-// bytes, so any pitch will do), and 16 warps work on the stage that has landed:
-// `rows` rows at a time, tpr threads each, a thread always the same columns.  That
-// keeps the weight, and the gradient of the weight, in registers for the whole
-// kernel, and loads under way while rows are reduced and written.  Warp 0 refills
-// a stage once every warp has read it: a warp of its own for that would be the
-// 17th and cost each thread 32 of its 128 registers.  A row costs a thread some 200
-// instructions whatever its length (barriers, shuffles, addresses), so threads
-// take up to 32 elements each rather than rows fewer threads.  (32 warps of half the
-// registers were slower in the forward: bf16 4096 x 4096 28.3 us against 24.4.)
+// A persistent CTA per SM of 16 warps, cut into units: the tpr threads of a row, or
+// a warp that holds several short rows.  Each unit keeps its next rows of every
+// input matrix on their way into stages of its own by 1-D bulk copies (the row's
+// 16-byte-aligned window of bytes, so any pitch will do) and works on the stage that
+// has landed, a thread always on the same columns.  That keeps the weight, and the
+// gradient of the weight, in registers for the whole kernel, and loads under way
+// while rows are reduced and written.  A unit's first warp refills a stage once
+// the unit has read it; one ring for the whole CTA made every unit wait for the
+// slowest (gradient of bf16 65536 x 128: 42.9 us, 20.9 with units; 16384 x 2048 55.5
+// and 51.8), and a warp of its own for refilling would be the 17th and cost each
+// thread 32 of its 128 registers.  A row costs a thread 200 to 300 instructions
+// whatever its length (barrier, shuffles, addresses), so threads take up to 32
+// elements each rather than rows fewer threads.  (32 warps of half the registers
+// were slower in the forward: bf16 4096 x 4096 28.3 us against 24.4.)
+//
+// Long rows are bound by device memory (fp16 16384 x 16384, residual: gradient
+// 316 us, 6.8 TB/s; forward 365 us, 5.9 TB/s); calls of a few turns by the start, the
+// last turn's latency and that overhead (bf16 4096 x 4096, residual: 23.2 us, 5.8
+// TB/s; gradient 32.2, 4.2; bf16 2047 x 8192 to e4m3 by groups of 128: 29.0, 4.0, with
+// 46 % of the issue slots taken; fp32 4097 x 8191 at an odd pitch: 63.3, 4.2).
 constexpr int kRingThreads = 512;
 constexpr int kRingStages = 8;
 constexpr int kRingBars = kRingThreads / 32 * kRingStages;   // of all units
@@ -1210,9 +1222,11 @@ cudaError_t forward_any(const NormArgs &a, cudaStream_t s) {
         const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.M, 1 << 20)));
         return launch_grid(mbt_rmsnorm_rows_kernel<DT>, grid, kRowThreads, s, a);
     }
-    // Two chunks a thread while that keeps a row within a CTA; a warp at least
-    // where groups of up to 128 columns are reduced, and all of a CTA for a few
-    // rows, where the time is one row's latency.
+    // One chunk a thread where all rows then fit the device at once (at 1024
+    // threads an SM), as the time is one row's latency: bf16 600 x 2048 2.6 us against
+    // 2.9 with two.  Else two, as long as that keeps a row within a CTA: 256 x 8192 3.6
+    // us against 5.3 with one and 4.2 with four.  A warp at least where groups of up
+    // to 128 columns are reduced.
     int tpr = a.quant > 0 ? 32 : 8;
     while (tpr < 1024 && (tpr * 2 < chunks || (tpr < chunks && a.M * tpr * 2 <= 1024ll * sms))) tpr *= 2;
     va.tpr = tpr;
