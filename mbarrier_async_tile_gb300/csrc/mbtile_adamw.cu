@@ -187,9 +187,9 @@ __device__ __forceinline__ Pair divide(Pair a, Pair nb, Pair ib) {
 // values, m and root leave as codes' values, ms and vs as scales.  Every operation
 // of the states is rounded by itself, as the formulas read, so that the codes do
 // not depend on how products and sums are fused.  Packed pairs halve the
-// arithmetic, which is what bounds this form: about 64 instructions an element
+// arithmetic, which is what bounds this form: about 70 instructions an element
 // with the loads, hash and conversions, against 10 bytes of bf16 parameters,
-// gradients and states (300 M elements: 644 us, 4.7 TB/s, with 76 % of the issue
+// gradients and states (300 M elements: 644 us, 4.7 TB/s, with 81 % of the issue
 // slots taken; with fp32 parameters and gradients, 16 bytes, 100 M: 259 us, 6.2 TB/s).
 __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, float (&p)[8], const float (&g)[8],
                                         float (&m)[8], float (&v)[8], float (&root)[8], const uint32_t (&r)[8],

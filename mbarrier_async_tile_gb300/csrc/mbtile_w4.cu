@@ -7,7 +7,7 @@
 // fp16 16384 x 16384 by groups of 64 with zero points and 8 rows of x takes 42 us, 3.5
 // TB/s, and e4m3 8191 x 8192 by groups of 32 and 3 rows 16.3 us, 2.3 TB/s: the ring
 // alone streams the former in 25 us, the consumers' conversions and scales take
-// 55 % of the issue slots beside it, and the kernels before and after it and the
+// 53 % of the issue slots beside it, and the kernels before and after it and the
 // start some 7 us.
 //
 // The work is cut into units of 64 rows of q by a slice of K short enough for
