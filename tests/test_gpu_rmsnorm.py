@@ -121,6 +121,22 @@ def test_many_rows(M, N, dtype, wdt, residual):
     assert mbt.tile_status()[0] == 0
 
 
+@pytest.mark.parametrize("M,N", [(30000, 100), (50001, 24), (20011, 64), (9000, 1000), (40, 8192)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dres", [False, True])
+def test_many_short_rows_backward(M, N, dtype, dres):
+    """Several rows to a warp, whole and partial chunks; fewer rows than the device takes at once."""
+    dt = TYPES[dtype]
+    dy, h, w = randn((M, N), dt, 65), randn((M, N), dt, 66, 2.0), randn(N, dt, 67)
+    r = randn((M, N), dt, 68) if dres else None
+    rstd = 1 / torch.sqrt(h.float().square().mean(1) + 1e-5)
+    dx, dw = mbt.tile_rmsnorm_backward(dy, h, rstd, w, dresidual=r)
+    check_backward(dy, h, rstd, w, r, dx, dw, 0.0)
+    again = mbt.tile_rmsnorm_backward(dy, h, rstd, w, dresidual=r)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+    assert mbt.tile_status()[0] == 0
+
+
 @pytest.mark.parametrize("M,N", LARGE)
 @pytest.mark.parametrize("quant", [0, 32, 64, 128])
 def test_many_rows_e4m3(M, N, quant):
