@@ -138,9 +138,9 @@ __device__ __forceinline__ void e4m3x8_get(const uint2 &q, float scale, float (&
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const uint32_t w = (k < 2 ? q.x : q.y) >> (16 * (k & 1));
-        const float2 h = Elem<MBT_F16>::widen2(e4m3x2_to_half2(w));
-        f[2 * k] = h.x * scale;
-        f[2 * k + 1] = h.y * scale;
+        const float2 h = Elem<MBT_F16>::widen2(e4m3x2_to_half2(w)), v = (Pair(h.x, h.y) * Pair(scale)).get();
+        f[2 * k] = v.x;
+        f[2 * k + 1] = v.y;
     }
 }
 
@@ -187,9 +187,9 @@ __device__ __forceinline__ Pair divide(Pair a, Pair nb, Pair ib) {
 // values, m and root leave as codes' values, ms and vs as scales.  Every operation
 // of the states is rounded by itself, as the formulas read, so that the codes do
 // not depend on how products and sums are fused.  Packed pairs halve the
-// arithmetic, which is what bounds this form: about 70 instructions an element
+// arithmetic, which is what bounds this form: about 68 instructions an element
 // with the loads, hash and conversions, against 10 bytes of bf16 parameters,
-// gradients and states (300 M elements: 644 us, 4.7 TB/s, with 81 % of the issue
+// gradients and states (300 M elements: 635 us, 4.8 TB/s, with 79 % of the issue
 // slots taken; with fp32 parameters and gradients, 16 bytes, 100 M: 259 us, 6.2 TB/s).
 __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, float (&p)[8], const float (&g)[8],
                                         float (&m)[8], float (&v)[8], float (&root)[8], const uint32_t (&r)[8],
@@ -206,8 +206,9 @@ __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, floa
         mp[k] = fma2(b1, Pair(m[2 * k], m[2 * k + 1]), zero) + fma2(c1, gp, zero);
         vp[k] = fma2(b2, Pair(v[2 * k], v[2 * k + 1]), zero) + fma2(c2 * gp, gp, zero);
         const float2 a = mp[k].get(), b = vp[k].get();
-        am = max(am, max(magnitude(a.x), magnitude(a.y)));
-        av = max(av, max(__float_as_uint(b.x), __float_as_uint(b.y)));   // (v >= 0, or NaN)
+        const float af[2] = {a.x, a.y}, bf[2] = {b.x, b.y};
+        am = magnitude_max(am, af);
+        av = magnitude_max(av, bf);
     }
     am = __reduce_max_sync(0xffffffffu, am);
     av = __reduce_max_sync(0xffffffffu, av);
@@ -253,7 +254,7 @@ __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, floa
         m[2 * k + 1] = cm.y;
         root[2 * k] = cv.x;
         root[2 * k + 1] = cv.y;
-        least = fminf(least, fminf(cv.x, cv.y));
+        asm("min.f32 %0, %1, %2, %3;" : "=f"(least) : "f"(least), "f"(cv.x), "f"(cv.y));
     }
     // below the normal codes (2^-6: 1 / 28672 of the block's largest) the rounding
     // takes twice the instructions; blocks without such an element go without (300 M
@@ -326,7 +327,11 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
                 e4m3x8_get(m8[r], ms[r], fm);
                 e4m3x8_get(v8[r], vs[r], fv);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) fv[k] *= fv[k];
+                for (int k = 0; k < 8; k += 2) {
+                    const Pair x(fv[k], fv[k + 1]);
+                    const float2 v = (x * x).get();
+                    fv[k] = v.x, fv[k + 1] = v.y;
+                }
             } else {
                 m[r].get(fm, MBT_F32);
                 v[r].get(fv, MBT_F32);
