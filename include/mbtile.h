@@ -562,9 +562,10 @@ enum { MBT_QUANT_NONE = -1, MBT_QUANT_ROW = 0 };
  *   quant         MBT_QUANT_NONE: out has x's type.  MBT_QUANT_ROW, 32, 64 or
  *                 128: out is e4m3, scales[i][j / quant] (dense, one per row
  *                 with MBT_QUANT_ROW, ceil(N / quant) otherwise; the last group
- *                 may be short) = max(largest |y| of the group / 448, 2^-126),
- *                 out = y / scale rounded to nearest even.  A group with a NaN
- *                 has a NaN scale.
+ *                 may be short) = max(largest |y| of the group * (1 / 448),
+ *                 2^-126), with MBT_QUANT_ROW of the largest |h (weight +
+ *                 weight_offset)| * rstd; out = y / scale in fp32, rounded to
+ *                 nearest even.  A group with a NaN has a NaN scale.
  *   rstd          fp32[M], always written (tile_rmsnorm_backward reads it).
  * M = 0 does nothing; N = 0 writes rstd = 1 / sqrt(eps) only (and, with
  * MBT_QUANT_ROW, the smallest scale).

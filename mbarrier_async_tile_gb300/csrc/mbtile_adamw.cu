@@ -176,13 +176,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-// a / b rounded to nearest: b's reciprocal rounded to nearest and one correction
-// (Markstein, IBM J. Res. Dev. 34, 1990).  nb = -b, ib = 1 / b.
-__device__ __forceinline__ Pair divide(Pair a, Pair nb, Pair ib) {
-    const Pair q = a * ib;
-    return fma2(fma2(q, nb, a), ib, q);
-}
-
 // New p and 8-bit states of a block, eight elements a lane: m and v come in as
 // values, m and root leave as codes' values, ms and vs as scales.  Every operation
 // of the states is rounded by itself, as the formulas read, so that the codes do

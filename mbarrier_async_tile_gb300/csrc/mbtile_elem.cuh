@@ -142,6 +142,13 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
     return r;
 }
 
+// a / b rounded to nearest: b's reciprocal rounded to nearest and one correction
+// (Markstein, IBM J. Res. Dev. 34, 1990).  nb = -b, ib = 1 / b.
+__device__ __forceinline__ Pair divide(Pair a, Pair nb, Pair ib) {
+    const Pair q = a * ib;
+    return fma2(fma2(q, nb, a), ib, q);
+}
+
 // |v| as an integer that orders as the magnitude does, with NaN above infinity:
 // the largest magnitude of a group is then NaN if any value is.
 __device__ __forceinline__ uint32_t magnitude(float v) {
@@ -162,6 +169,22 @@ __device__ __forceinline__ float group_scale(uint32_t amax) {
     const float s = __uint_as_float(amax) * (1.f / kE4m3Max);
     return s < kMinScale ? kMinScale : s;
 }
+
+// Division by a group's scale: minus the quotient rounded to nearest, as divide()
+// has it, but that a zero keeps its sign.  (An infinite scale is left out of the
+// correction, which would be infinity times 0 for the group's finite values.)
+struct Divisor {
+    float scale = 0.f, minus_inv = 0.f;
+    Divisor() = default;
+    explicit __device__ __forceinline__ Divisor(float s) {
+        scale = s < __uint_as_float(0x7f800000u) ? s : 0.f;
+        minus_inv = -__frcp_rn(s);
+    }
+    __device__ __forceinline__ float2 minus(float a, float b) const {
+        const Pair y(a, b), mi(minus_inv), mq = y * mi;
+        return fma2(fma2(mq, Pair(scale), y), mi, mq).get();
+    }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

@@ -68,14 +68,13 @@ __global__ void __launch_bounds__(kRowThreads) mbt_rmsnorm_rows_kernel(const Nor
         if (threadIdx.x == 0) a.rstd[i] = rstd;
         if (a.quant <= 0) {
             const float scale = group_scale(magnitude(__uint_as_float(amax) * rstd));
-            const float inv = 1.f / scale;
             if (a.quant == 0 && threadIdx.x == 0) a.scales[i] = scale;
             for (int64_t j = threadIdx.x; j < a.N; j += kRowThreads) {
                 const float h = h_at(j);
                 const float y = h * rstd * weight_at(a.w, a.wdt, a.woff, j);
                 if (a.quant == 0)
                     static_cast<uint8_t *>(a.out)[i * a.ld_out + j] =
-                        static_cast<uint8_t>(to_e4m3x2(y * inv, 0.f));
+                        static_cast<uint8_t>(to_e4m3x2(y / scale, 0.f));
                 else
                     static_cast<T *>(a.out)[i * a.ld_out + j] = Elem<DT>::round(y);
                 if (ro) ro[j] = Elem<DT>::round(h);
@@ -108,7 +107,7 @@ __global__ void __launch_bounds__(kRowThreads) mbt_rmsnorm_rows_kernel(const Nor
                 const float scale = group_scale(m[k]);
                 if (j < a.N) {
                     static_cast<uint8_t *>(a.out)[i * a.ld_out + j] =
-                        static_cast<uint8_t>(to_e4m3x2(y[k] * (1.f / scale), 0.f));
+                        static_cast<uint8_t>(to_e4m3x2(y[k] / scale, 0.f));
                     if (j % a.quant == 0) a.scales[i * a.groups + j / a.quant] = scale;
                 }
             }
@@ -230,15 +229,14 @@ __device__ __forceinline__ void load_weight(const void *w, int mode, int wdt, fl
     for (int e = 0; e < V; ++e) f[e] += woff;
 }
 
-// V values times inv as e4m3 at o, elements [lo, hi) of them.
+// V values by their scale as e4m3 at o, elements [lo, hi) of them.
 template <int V>
-__device__ __forceinline__ void store_e4m3(uint8_t *o, const float (&y)[V], float inv, int lo, int hi) {
+__device__ __forceinline__ void store_e4m3(uint8_t *o, const float (&y)[V], const Divisor &by, int lo, int hi) {
     uint32_t q[V / 4];
-    const Pair ii(inv);
 #pragma unroll
     for (int e = 0; e < V; e += 4) {
-        const float2 a = (Pair(y[e], y[e + 1]) * ii).get(), b = (Pair(y[e + 2], y[e + 3]) * ii).get();
-        q[e / 4] = to_e4m3x2(a.x, a.y) | to_e4m3x2(b.x, b.y) << 16;
+        const float2 a = by.minus(y[e], y[e + 1]), b = by.minus(y[e + 2], y[e + 3]);
+        q[e / 4] = (to_e4m3x2(a.x, a.y) | to_e4m3x2(b.x, b.y) << 16) ^ 0x80808080u;
     }
     if (lo <= 0 && hi >= V && (reinterpret_cast<uintptr_t>(o) & (V - 1)) == 0) {
         if constexpr (V == 8)
@@ -334,10 +332,11 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
         if (Q) amax = __reduce_max_sync(0xffffffffu, l < warps ? redm[l] : 0u);
     }
     const float rstd = 1.f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
-    float scale = 0.f, inv = 0.f;
+    float scale = 0.f;
+    Divisor by;
     if (Q && a.quant == 0) {
         scale = group_scale(magnitude(__uint_as_float(amax) * rstd));
-        inv = 1.f / scale;
+        by = Divisor(scale);
     }
     if (live && t == 0) {
         a.rstd[i] = rstd;
@@ -367,11 +366,11 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
                 uint32_t m = magnitude_max(0u, y);
                 for (int o = 1; o < a.quant / V; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
                 scale = group_scale(m);
-                inv = 1.f / scale;
+                by = Divisor(scale);
                 if (p < end && p % a.quant == 0) a.scales[i * a.groups + p / a.quant] = scale;
             }
             if (p >= end) continue;
-            store_e4m3<V>(static_cast<uint8_t *>(a.out) + i * a.ld_out - off + p, y, inv, off - p,
+            store_e4m3<V>(static_cast<uint8_t *>(a.out) + i * a.ld_out - off + p, y, by, off - p,
                           static_cast<int>(end - p));
         }
     }
@@ -879,10 +878,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         row_reduce<Q>(ss, amax, r.tpr, sh.red[0], turn);
         turn ^= 1;
         const float rstd = rsqrtf(ss * inv_n + a.eps);
-        float scale = 0.f, inv = 0.f;
+        float scale = 0.f;
+        Divisor by;
         if (Q && a.quant == 0) {
             scale = group_scale(magnitude(__uint_as_float(amax) * rstd));
-            inv = 1.f / scale;
+            by = Divisor(scale);
         }
         if (th.t == 0 && n < mine) {
             a.rstd[i] = rstd;
@@ -920,11 +920,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 if (c >= have) continue;
                 if (a.quant > 0) {
                     scale = group_scale(gmax[c]);
-                    inv = __frcp_rn(scale);
+                    by = Divisor(scale);
                     const int p = th.t * V + c * chunk;
                     if (p % a.quant == 0) a.scales[i * a.groups + p / a.quant] = scale;
                 }
-                store_e4m3<V>(out + c * chunk, h[c], inv, th.lo(c), th.hi(c));
+                store_e4m3<V>(out + c * chunk, h[c], by, th.lo(c), th.hi(c));
             }
         }
     }

@@ -324,3 +324,17 @@ def test_refusals():
                 dict(dresidual=x.t()), dict(dx=x.float()), dict(dweight=w)):
         with pytest.raises(ValueError):
             mbt.tile_rmsnorm_backward(**({"dy": x, "h": x, "rstd": ok.rstd, "weight": w} | bad))
+
+
+@pytest.mark.parametrize("M,N", [(512, 8192), (40, 300001), (700, 16384), (3000, 4104)])
+@pytest.mark.parametrize("quant", [0, 32, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_e4m3_codes_are_quotients(M, N, quant, dtype):
+    """Every code is y / scale of the scale that comes with it, rounded to nearest even, in each of the kernels."""
+    dt = TYPES[dtype]
+    x, r, w = randn((M, N), dt, 71), randn((M, N), dt, 72, 2.0), randn(N, dt, 73)
+    got = mbt.tile_rmsnorm(x, w, r, quant=quant)
+    y = (x.float() + r.float()) * got.rstd[:, None] * w.float()
+    scales = got.scales.repeat_interleave(quant or N, 1)[:, :N]
+    want = (y / scales).clamp(-448, 448).to(E4M3)
+    assert torch.equal(got.out.view(torch.uint8), want.view(torch.uint8))
