@@ -756,7 +756,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
         row_reduce<false>(dot, none, r.tpr, sh.red[0], turn);
         turn ^= 1;
-        const float scale = rstd * rstd * rstd * (dot * inv_n);   // times h gives rstd xh mean(g xh)
+        // times h gives xh mean(g xh); from the sum on, as powers of rstd alone leave
+        // fp32's range at rows that are themselves within it
+        const float proj = rstd * (rstd * (dot * inv_n));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if (c >= have) continue;
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             if constexpr (RES) unpack<DT>(vr, f);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                d[e] = rstd * (dy[e] * w[e]) - h[e] * scale;
+                d[e] = rstd * (dy[e] * w[e] - h[e] * proj);
                 if constexpr (RES) d[e] += f[e];
             }
             th.put(dx + c * chunk, c, d);

@@ -338,3 +338,20 @@ def test_e4m3_codes_are_quotients(M, N, quant, dtype):
     scales = got.scales.repeat_interleave(quant or N, 1)[:, :N]
     want = (y / scales).clamp(-448, 448).to(E4M3)
     assert torch.equal(got.out.view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("rms,eps", [(1e15, 1e-6), (1e17, 1e-6), (1e-15, 0.0), (3e-18, 0.0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,offset", [(64, 4096, 0), (64, 4096, 1), (900, 1000, 0), (7, 30000, 0)])
+def test_backward_at_any_magnitude(rms, eps, dtype, M, N, offset):
+    """Large and small rows, with dy along h so that the projection counts (an offset of 1: the element-wise kernels)."""
+    dt = TYPES[dtype]
+    n = randn((M, N), torch.float32, 74)
+    if N > 4096:
+        n = n.clamp(-2, 2)   # (the sum of 30000 squares of 1e17 stays in fp32's range)
+    h, w = pitched((n * rms).to(dt), 0, offset), 1 + randn(N, torch.float32, 75, 0.2)
+    dy = (0.7 * n + randn((M, N), torch.float32, 76, 0.5)).to(dt)
+    rstd = mbt.tile_rmsnorm(h, w, None, eps=eps).rstd
+    dx, dw = mbt.tile_rmsnorm_backward(dy, h, rstd, w)
+    assert (dy.double() * w.double() * h.double() * rstd.double()[:, None]).mean().item() > 0.4
+    check_backward(dy, h, rstd, w, None, dx, dw)
