@@ -9,6 +9,7 @@
 #include "mbtile_elem.cuh"
 #include "mbtile_layer.h"
 #include "mbtile_ptx.cuh"
+#include "mbtile_rows.h"
 
 namespace mbt {
 namespace {
@@ -407,6 +408,8 @@ constexpr int kRingBytes = 208 * 1024;   // shared memory for the stages
 struct RingArgs {
     const char *in[3];       // forward: x, residual; backward: dy, h, dresidual
     int64_t ld[3];           // pitches in bytes
+    int64_t tail[3];         // first rows whose last chunk is not copied
+    int32_t row_bytes;
     int32_t inputs;
     int32_t tpr, rows;       // threads per row, rows at a time
     int32_t unit_threads;    // that share a ring: a row's, or a warp of several rows
@@ -420,41 +423,19 @@ struct RingArgs {
     int32_t *status;
 };
 
-struct RowWindow {
-    int off;                 // elements from the window's first byte to the row's
-    int64_t start;           // bytes from the matrix to the window
-    int bytes;               // copied; the last row's partial last chunk is not
-                             // (the bytes after it may be nobody's)
-};
-
-template <int DT>
-__device__ __forceinline__ RowWindow row_window(int64_t row, int64_t M, int64_t N, int64_t ld, bool phased) {
-    constexpr int es = 16 / Elem<DT>::kVec;
-    RowWindow w;
-    const int64_t at = row * ld;
-    const int lead = phased ? static_cast<int>(at & 15) : 0;
-    w.off = lead / es;
-    w.start = at - lead;
-    const int need = lead + static_cast<int>(N) * es;
-    w.bytes = row == M - 1 ? need & ~15 : (need + 15) & ~15;
-    return w;
-}
-
 // The unit's first warp: the copies of its rows from `row` on to `to`.
-template <int DT>
-__device__ __forceinline__ void ring_fill(const RingArgs &r, int64_t M, int64_t N, uint32_t to, uint32_t full,
-                                          int64_t row) {
+__device__ __forceinline__ void ring_fill(const RingArgs &r, int64_t M, uint32_t to, uint32_t full, int64_t row) {
     const int lane = threadIdx.x & 31;
     const int rows = static_cast<int>(min(M - row, static_cast<int64_t>(r.unit_rows)));
     uint32_t total = 0;
     for (int i = lane; i < rows * r.inputs; i += 32)
-        total += row_window<DT>(row + i % rows, M, N, r.ld[i / rows], r.phased).bytes;
+        total += row_window(row + i % rows, r.tail[i / rows], r.row_bytes, r.ld[i / rows], r.phased).bytes;
     total = __reduce_add_sync(0xffffffffu, total);
     if (lane == 0) mbar_arrive_expect_tx(full, total);
     __syncwarp();
     for (int i = lane; i < rows * r.inputs; i += 32) {
         const int m = i / rows, k = i - m * rows;
-        const RowWindow win = row_window<DT>(row + k, M, N, r.ld[m], r.phased);
+        const RowWindow win = row_window(row + k, r.tail[m], r.row_bytes, r.ld[m], r.phased);
         if (win.bytes > 0)
             bulk_load_1d(to + static_cast<uint32_t>((m * r.unit_rows + k) * r.slot), r.in[m] + win.start,
                          static_cast<uint32_t>(win.bytes), full);
@@ -480,11 +461,10 @@ struct RingState {
         lead = threadIdx.x - unit * r.unit_threads < 32;
     }
     // The unit's first rows.
-    template <int DT>
-    __device__ __forceinline__ void start(const RingArgs &r, int64_t M, int64_t N) {
+    __device__ __forceinline__ void start(const RingArgs &r, int64_t M) {
         if (!lead) return;
         for (int s = 0; s < r.stages; ++s, row += step)
-            if (row < M) ring_fill<DT>(r, M, N, ring + s * r.stage_bytes, full + 8 * s, row);
+            if (row < M) ring_fill(r, M, ring + s * r.stage_bytes, full + 8 * s, row);
     }
     // A warp whose wait has run out goes through the rows without work, so that
     // the CTA's barriers are complete.
@@ -497,13 +477,12 @@ struct RingState {
         }
     }
     // This warp has read its stage.
-    template <int DT>
-    __device__ __forceinline__ void release(const RingArgs &r, int64_t M, int64_t N) {
+    __device__ __forceinline__ void release(const RingArgs &r, int64_t M) {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * stage);
         if (lead && alive && row < M) {
             if (__all_sync(0xffffffffu, wait_bounded(empty + 8 * stage, phase, w, true))) {
-                ring_fill<DT>(r, M, N, ring + stage * r.stage_bytes, full + 8 * stage, row);
+                ring_fill(r, M, ring + stage * r.stage_bytes, full + 8 * stage, row);
                 row += step;
             } else {
                 report_timeout(w, 0, stage, phase);
@@ -632,7 +611,7 @@ struct RingThread {
         t = threadIdx.x & (r.tpr - 1);
         k = threadIdx.x / r.tpr;
         first = static_cast<int64_t>(blockIdx.x) * r.rows + k;
-        off = PART ? row_window<DT>(first < M ? first : 0, M, N, r.ld[0], r.phased).off : 0;
+        off = PART ? row_window(first < M ? first : 0, M, 0, r.ld[0], r.phased).lead / (16 / V) : 0;
         end = static_cast<int>(N) + off;
         const int chunks = (end + V - 1) / V;
         count = t < chunks ? min(C, (chunks - t + r.tpr - 1) / r.tpr) : 0;
@@ -654,11 +633,11 @@ struct RingThread {
     // Elements of chunk c that are the row's: [lo, hi).
     __device__ __forceinline__ int lo(int c) const { return head && c == 0 ? off : 0; }
     __device__ __forceinline__ int hi(int c) const { return tail && c == count - 1 ? end & (V - 1) : V; }
-    // The matrix's last row's partial last chunk is not copied: from the matrix itself.
-    __device__ __forceinline__ void last_chunk(const RingArgs &r, int m, int c, int64_t row, int64_t M, uint4 &v) const {
+    // The matrix's partial last chunk is not copied: from the matrix itself.
+    __device__ __forceinline__ void last_chunk(const RingArgs &r, int m, int c, int64_t row, uint4 &v) const {
         using T = typename Elem<DT>::type;
-        if (row == M - 1 && tail && c == count - 1)
-            v = load_part<DT>(reinterpret_cast<const T *>(r.in[m] + row * r.ld[m]) - off + (t + c * r.tpr) * V, 0, hi(c));
+        if (row >= r.tail[m] && tail && c == count - 1)
+            v = load_part<DT>(reinterpret_cast<const T *>(r.in[m] + row * r.ld[m]) - off + (t + c * r.tpr) * V, lo(c), hi(c));
     }
     // Other rows' elements to 0.
     __device__ __forceinline__ void mask(int c, float (&v)[V]) const {
@@ -691,7 +670,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     __shared__ __align__(8) RingShared sh;
     ring_init(sh, r);
     RingState q(r, smem_u32(dyn_smem), smem_u32(&sh.bars[0]), WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status});
-    q.start<DT>(r, a.M, a.N);
+    q.start(r, a.M);
     const RingThread<DT, C, PART> th(r, a.M, a.N, q.ring);
     RingWeights<DT, C, PART, W32> wt;
     wt.load(r, a.w, a.wdt, a.woff, th.t, th.off, a.N);
@@ -729,8 +708,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 if (th.whole(c)) continue;
-                th.last_chunk(r, 0, c, i, a.M, vy[c]);
-                th.last_chunk(r, 1, c, i, a.M, vh[c]);
+                th.last_chunk(r, 0, c, i, vy[c]);
+                th.last_chunk(r, 1, c, i, vh[c]);
                 float f[V];
                 unpack<DT>(vy[c], f);
                 th.mask(c, f);
@@ -765,7 +744,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             uint4 vr = make_uint4(0, 0, 0, 0);
             if constexpr (RES) {
                 vr = th.chunk(q.stage, 2, c);
-                if (PART && th.tail) th.last_chunk(r, 2, c, i, a.M, vr);
+                if (PART && th.tail) th.last_chunk(r, 2, c, i, vr);
             }
             float dy[V], h[V], d[V], f[V], w[V];
             unpack<DT>(again(vy[c], z2), dy);
@@ -779,7 +758,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             }
             th.put(dx + c * chunk, c, d);
         }
-        q.release<DT>(r, a.M, a.N);
+        q.release(r, a.M);
     }
     q.drain(r.stages);
     if (!a.dw) return;
@@ -811,7 +790,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     __shared__ __align__(8) RingShared sh;
     ring_init(sh, r);
     RingState q(r, smem_u32(dyn_smem), smem_u32(&sh.bars[0]), WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status});
-    q.start<DT>(r, a.M, a.N);
+    q.start(r, a.M);
     const RingThread<DT, C, PART> th(r, a.M, a.N, q.ring);
     RingWeights<DT, C, PART, W32> wt;
     wt.load(r, a.w, a.wdt, a.woff, th.t, th.off, a.N);
@@ -844,8 +823,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             if (PART && have && th.tail)
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    th.last_chunk(r, 0, c, i, a.M, vx[c]);
-                    if constexpr (RES) th.last_chunk(r, 1, c, i, a.M, vr[c]);
+                    th.last_chunk(r, 0, c, i, vx[c]);
+                    if constexpr (RES) th.last_chunk(r, 1, c, i, vr[c]);
                 }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
@@ -858,7 +837,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 }
             }
         }
-        q.release<DT>(r, a.M, a.N);   // the row is in registers now
+        q.release(r, a.M);   // the row is in registers now
         if (PART && have && (th.head || th.tail))
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -1030,6 +1009,7 @@ bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, 
     for (int i = 0; i < inputs; ++i) {
         r.in[i] = static_cast<const char *>(in[i]);
         r.ld[i] = ld[i] * es;
+        r.tail[i] = first_tail_row(M, N * es, ld[i] * es);
     }
     r.phased = M > 1 && ph > 0;
     const int64_t chunks = (N + (r.phased ? V - 1 : 0) + V - 1) / V;
@@ -1048,6 +1028,7 @@ bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, 
     r.rows = kRingThreads / tpr;
     r.unit_threads = std::max(tpr, 32);
     r.unit_rows = r.unit_threads / tpr;
+    r.row_bytes = static_cast<int32_t>(N * es);
     r.slot = static_cast<int32_t>((N * es + (r.phased ? 16 - es : 0) + 15) / 16 * 16);
     r.stage_bytes = static_cast<uint32_t>(r.slot) * r.unit_rows * inputs;
     const int64_t stage = static_cast<int64_t>(r.slot) * r.rows * inputs;

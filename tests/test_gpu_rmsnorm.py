@@ -355,3 +355,26 @@ def test_backward_at_any_magnitude(rms, eps, dtype, M, N, offset):
     dx, dw = mbt.tile_rmsnorm_backward(dy, h, rstd, w)
     assert (dy.double() * w.double() * h.double() * rstd.double()[:, None]).mean().item() > 0.4
     check_backward(dy, h, rstd, w, None, dx, dw)
+
+
+@pytest.mark.parametrize("N", [1, 2, 3, 5, 7])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("pad", [0, 1, 4])
+def test_narrow_matrices_backward(N, dtype, pad):
+    """Rows shorter than 16 bytes, several of which end in the matrix's last chunk."""
+    dt = TYPES[dtype]
+    for M in (1, 2, 3, 4, 5, 6, 7, 8, 9, 500, 4001):
+        dy, h, d = (pitched(randn((M, N), dt, 97 + k), pad * (k + 1)) for k in range(3))
+        w = randn(N, dt, 77)
+        rstd = 1 / torch.sqrt(h.float().square().mean(1) + 1e-2)
+        store = torch.full((M * (N + pad) + 64,), 7.0, dtype=dt, device="cuda")
+        dx = store[:M * (N + pad)].view(M, N + pad)[:, :N]
+        got, dw = mbt.tile_rmsnorm_backward(dy, h, rstd, w, dresidual=d, dx=dx)
+        check_backward(dy, h, rstd, w, d, got, dw)
+        dx.fill_(7.0)
+        assert bool((store == 7).all())
+        a = dy.contiguous().clone()
+        want, wdw = mbt.tile_rmsnorm_backward(a.clone(), h.contiguous(), rstd, w)
+        mine, mdw = mbt.tile_rmsnorm_backward(a, h.contiguous(), rstd, w, dx=a)
+        assert torch.equal(mine, want) and torch.equal(mdw, wdw)
+    assert mbt.tile_status()[0] == 0
