@@ -76,8 +76,10 @@
  *     records MBT_ERR_TIMEOUT in the per-device status word (or in the call's
  *     own buffer, mbt_opts.status) and returns; tile_status reports the
  *     word.
- *   - Thread safety: entry points may be called from several host threads.
- *     Concurrent calls must not share a workspace.
+ *   - Thread safety: entry points may be called from several host threads, on
+ *     one stream too: each call is then as a whole before or after another, as
+ *     it holds the library's workspace of the stream (if it uses it) until its
+ *     last launch.  Concurrent calls must not share a workspace of the caller's.
  */
 #ifndef MBTILE_H
 #define MBTILE_H

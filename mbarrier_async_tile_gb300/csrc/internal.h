@@ -219,9 +219,29 @@ cudaError_t read_and_clear_status(int32_t info[4]);
 
 // (mbtile_host.cpp)  SM count and opt-in shared memory of the current device.
 int device_limits(int *num_sms, int *smem_optin);
-// (mbtile_host.cpp)  At least `bytes` bytes of the partial-sum part of the
-// library's workspace for (current device, stream), 256-byte aligned, contents
-// undefined; the sums' tickets are left as they are.
-int owned_scratch(void *stream, size_t bytes, void **scratch);
+struct OwnedWorkspace;
+
+// (mbtile_host.cpp)  A call's hold of the library's workspace for (current device,
+// stream).  Stream order alone does not keep the workspace to one call where host
+// threads share a stream: another call's launches, or its growth of the workspace,
+// could come between this one's taking it and its last launch.  So a call keeps its
+// hold until that launch; other calls on the stream wait for it.
+class WorkspaceHold {
+public:
+    WorkspaceHold() = default;
+    WorkspaceHold(const WorkspaceHold &) = delete;
+    WorkspaceHold &operator=(const WorkspaceHold &) = delete;
+    ~WorkspaceHold();
+    // At least `groups` ticket words a set and `partial_bytes` of partial sums.
+    int take(void *stream, int64_t groups, size_t partial_bytes);
+    // For take()'s groups: this call's tickets, those it clears, the partial sums.
+    void sums(int32_t **ticket, int32_t **clear, int64_t *clear_n, float **partial);
+    // take() of the part for partial sums alone, 256-byte aligned, contents
+    // undefined; the sums' tickets are left as they are.
+    int scratch(void *stream, size_t bytes, void **memory);
+
+private:
+    OwnedWorkspace *w_ = nullptr;
+};
 
 }  // namespace mbt

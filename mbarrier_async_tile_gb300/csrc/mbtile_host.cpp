@@ -6,11 +6,25 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <new>
 #include <thread>
 #include <tuple>
 
 #include "internal.h"
 #include "mbtile_layer.h"
+
+namespace mbt {
+
+// The library's workspace of one (device, stream); see g_owned below.
+struct OwnedWorkspace {
+    std::mutex mutex;           // held by the call that uses it
+    char *base = nullptr;
+    int64_t ticket_cap = 0;     // words per ticket set (a multiple of 64)
+    size_t partial_bytes = 0;
+    uint64_t uses = 0;
+};
+
+}  // namespace mbt
 
 namespace {
 
@@ -812,15 +826,8 @@ int flat_launch(int op, const void *src, void *dst, float *out, int64_t M, int64
 // partial slots need no clearing: a band's last contributor reads only slots
 // its co-contributors wrote in the same call.  The per-thread default stream
 // is a different stream in every host thread, so its key includes the thread.
-struct OwnedWorkspace {
-    char *base = nullptr;
-    int64_t ticket_cap = 0;     // words per ticket set (a multiple of 64)
-    size_t partial_bytes = 0;
-    uint64_t uses = 0;
-};
-
-std::mutex g_owned_mutex;
-std::map<std::tuple<int, uintptr_t, size_t>, OwnedWorkspace> g_owned;
+std::mutex g_owned_mutex;   // of the map; its entries stay where they are
+std::map<std::tuple<int, uintptr_t, size_t>, mbt::OwnedWorkspace> g_owned;
 
 std::tuple<int, uintptr_t, size_t> owned_key(int dev, void *stream) {
     const size_t thread =
@@ -830,58 +837,16 @@ std::tuple<int, uintptr_t, size_t> owned_key(int dev, void *stream) {
     return std::make_tuple(dev, reinterpret_cast<uintptr_t>(stream), thread);
 }
 
-// The workspace of (current device, stream), grown to `groups` ticket words a
-// set and `partial_bytes` of partial sums.  The caller holds g_owned_mutex.
-int grow_owned(void *stream, int64_t groups, size_t partial_bytes, OwnedWorkspace **out) {
+// The entry of (current device, stream).
+int owned_entry(void *stream, mbt::OwnedWorkspace **w) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MBT_ERR_CUDA;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    OwnedWorkspace &w = g_owned[owned_key(dev, stream)];
-    if (w.base == nullptr || w.ticket_cap < groups || w.partial_bytes < partial_bytes) {
-        // Allocating inside a stream capture would end the capture with an error.
-        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-        if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return MBT_ERR_CUDA;
-        if (cap != cudaStreamCaptureStatusNone) return MBT_ERR_WORKSPACE;
-        OwnedWorkspace nw;
-        nw.ticket_cap = round_up(std::max<int64_t>({groups, w.ticket_cap, 64}), 64);
-        nw.partial_bytes = static_cast<size_t>(round_up(
-            static_cast<int64_t>(std::max({partial_bytes, w.partial_bytes,
-                                           static_cast<size_t>(kOwnedMinPartialBytes)})),
-            256));
-        const size_t total = static_cast<size_t>(2 * nw.ticket_cap * 4) + nw.partial_bytes;
-        void *p = nullptr;
-        if (cudaMallocAsync(&p, total, s) != cudaSuccess) return MBT_ERR_CUDA;
-        if (cudaMemsetAsync(p, 0, total, s) != cudaSuccess) {
-            cudaFreeAsync(p, s);
-            return MBT_ERR_CUDA;
-        }
-        // The old buffer served this stream only: freed after its last use.
-        if (w.base != nullptr && cudaFreeAsync(w.base, s) != cudaSuccess) {
-            cudaFreeAsync(p, s);
-            return MBT_ERR_CUDA;
-        }
-        nw.base = static_cast<char *>(p);
-        w = nw;
+    try {
+        std::lock_guard<std::mutex> lock(g_owned_mutex);
+        *w = &g_owned[owned_key(dev, stream)];
+    } catch (const std::bad_alloc &) {
+        return MBT_ERR_CUDA;
     }
-    *out = &w;
-    return MBT_OK;
-}
-
-// Tickets for `groups` reduction groups and `partial_bytes` of partial sums
-// from the library's workspace for (current device, stream).
-int owned_workspace(void *stream, int64_t groups, size_t partial_bytes, int32_t **ticket,
-                    int32_t **clear, int64_t *clear_n, float **partial) {
-    std::lock_guard<std::mutex> lock(g_owned_mutex);
-    OwnedWorkspace *grown = nullptr;
-    const int rc = grow_owned(stream, groups, partial_bytes, &grown);
-    if (rc != MBT_OK) return rc;
-    OwnedWorkspace &w = *grown;
-    const int64_t parity = static_cast<int64_t>(w.uses++ & 1u);
-    int32_t *sets = reinterpret_cast<int32_t *>(w.base);
-    *ticket = sets + parity * w.ticket_cap;
-    *clear = sets + (1 - parity) * w.ticket_cap;
-    *clear_n = w.ticket_cap;
-    *partial = reinterpret_cast<float *>(w.base + 2 * w.ticket_cap * 4);
     return MBT_OK;
 }
 
@@ -916,11 +881,11 @@ int rowsum_launch(const void *src, void *dst, float *out, int64_t M, int64_t N, 
     RowsumArgs a{};
     a.p = pipe_args(plan, M, N, tile_m, stages, dtype, o);
     a.out = out;
+    mbt::WorkspaceHold hold;
     if (own) {
-        rc = owned_workspace(stream, plan.tiles_m,
-                             plan.workspace_bytes - round_up(plan.tiles_m * 4, 256), &a.ticket,
-                             &a.clear_ticket, &a.clear_n, &a.partial);
+        rc = hold.take(stream, plan.tiles_m, plan.workspace_bytes - round_up(plan.tiles_m * 4, 256));
         if (rc != MBT_OK) return rc;
+        hold.sums(&a.ticket, &a.clear_ticket, &a.clear_n, &a.partial);
     } else if (plan.split) {
         char *ws = static_cast<char *>(o.workspace);
         a.ticket = reinterpret_cast<int32_t *>(ws);
@@ -971,11 +936,11 @@ int colsum_launch(const void *src, float *out, int64_t M, int64_t N, int64_t ld_
     a.p = pipe_args(plan, M, N, tile_m, stages, dtype, o);
     a.p.col_group = plan.col_group;
     a.out = out;
+    mbt::WorkspaceHold hold;
     if (own) {
-        rc = owned_workspace(stream, plan.tiles_n,
-                             plan.workspace_bytes - round_up(plan.tiles_n * 4, 256), &a.ticket,
-                             &a.clear_ticket, &a.clear_n, &a.partial);
+        rc = hold.take(stream, plan.tiles_n, plan.workspace_bytes - round_up(plan.tiles_n * 4, 256));
         if (rc != MBT_OK) return rc;
+        hold.sums(&a.ticket, &a.clear_ticket, &a.clear_n, &a.partial);
     } else if (plan.split) {
         char *ws = static_cast<char *>(o.workspace);
         a.ticket = reinterpret_cast<int32_t *>(ws);
@@ -1060,13 +1025,59 @@ int device_status_word(int32_t **word) {
     return MBT_OK;
 }
 
-int owned_scratch(void *stream, size_t bytes, void **scratch) {
-    std::lock_guard<std::mutex> lock(g_owned_mutex);
-    OwnedWorkspace *w = nullptr;
-    const int rc = grow_owned(stream, 0, bytes, &w);
+WorkspaceHold::~WorkspaceHold() {
+    if (w_ != nullptr) w_->mutex.unlock();
+}
+
+int WorkspaceHold::take(void *stream, int64_t groups, size_t partial_bytes) {
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int rc = owned_entry(stream, &w_);
     if (rc != MBT_OK) return rc;
-    *scratch = w->base + 2 * w->ticket_cap * 4;
+    w_->mutex.lock();
+    OwnedWorkspace &w = *w_;
+    if (w.base != nullptr && w.ticket_cap >= groups && w.partial_bytes >= partial_bytes) return MBT_OK;
+    // Allocating inside a stream capture would end the capture with an error.
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return MBT_ERR_CUDA;
+    if (cap != cudaStreamCaptureStatusNone) return MBT_ERR_WORKSPACE;
+    const int64_t ticket_cap = round_up(std::max<int64_t>({groups, w.ticket_cap, 64}), 64);
+    const size_t partial = static_cast<size_t>(round_up(
+        static_cast<int64_t>(std::max({partial_bytes, w.partial_bytes,
+                                       static_cast<size_t>(kOwnedMinPartialBytes)})),
+        256));
+    const size_t total = static_cast<size_t>(2 * ticket_cap * 4) + partial;
+    void *p = nullptr;
+    if (cudaMallocAsync(&p, total, s) != cudaSuccess) return MBT_ERR_CUDA;
+    if (cudaMemsetAsync(p, 0, total, s) != cudaSuccess) {
+        cudaFreeAsync(p, s);
+        return MBT_ERR_CUDA;
+    }
+    // The old buffer served this stream only: freed after its last use.
+    if (w.base != nullptr && cudaFreeAsync(w.base, s) != cudaSuccess) {
+        cudaFreeAsync(p, s);
+        return MBT_ERR_CUDA;
+    }
+    w.base = static_cast<char *>(p);
+    w.ticket_cap = ticket_cap;
+    w.partial_bytes = partial;
+    w.uses = 0;
     return MBT_OK;
+}
+
+void WorkspaceHold::sums(int32_t **ticket, int32_t **clear, int64_t *clear_n, float **partial) {
+    OwnedWorkspace &w = *w_;
+    const int64_t parity = static_cast<int64_t>(w.uses++ & 1u);
+    int32_t *sets = reinterpret_cast<int32_t *>(w.base);
+    *ticket = sets + parity * w.ticket_cap;
+    *clear = sets + (1 - parity) * w.ticket_cap;
+    *clear_n = w.ticket_cap;
+    *partial = reinterpret_cast<float *>(w.base + 2 * w.ticket_cap * 4);
+}
+
+int WorkspaceHold::scratch(void *stream, size_t bytes, void **memory) {
+    const int rc = take(stream, 0, bytes);
+    if (rc == MBT_OK) *memory = w_->base + 2 * w_->ticket_cap * 4;
+    return rc;
 }
 
 }  // namespace mbt
@@ -1250,15 +1261,15 @@ int tile_stage_image(const void *src, int64_t M, int64_t N, int64_t ld, int tile
 }
 
 int tile_workspace_release(void *stream) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MBT_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(g_owned_mutex);
-    auto it = g_owned.find(owned_key(dev, stream));
-    if (it == g_owned.end()) return MBT_OK;
-    const cudaError_t e =
-        it->second.base ? cudaFreeAsync(it->second.base, static_cast<cudaStream_t>(stream))
-                        : cudaSuccess;
-    g_owned.erase(it);
+    mbt::OwnedWorkspace *w = nullptr;
+    const int rc = owned_entry(stream, &w);
+    if (rc != MBT_OK) return rc;
+    std::lock_guard<std::mutex> lock(w->mutex);
+    if (w->base == nullptr) return MBT_OK;
+    const cudaError_t e = cudaFreeAsync(w->base, static_cast<cudaStream_t>(stream));
+    w->base = nullptr;
+    w->ticket_cap = 0;
+    w->partial_bytes = 0;
     return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
 }
 

@@ -1141,9 +1141,10 @@ int backward_by_ring(NormGradArgs a, cudaStream_t s, int sms, bool *done) {
     if (rc != MBT_OK) return rc;
     p.r.wmode = weight_mode(a.w, a.wdt, DT);
     a.splits = p.grid;
+    WorkspaceHold hold;
     if (a.dw) {
         void *scratch = nullptr;
-        rc = owned_scratch(s, static_cast<size_t>(a.splits) * a.N * 4, &scratch);
+        rc = hold.scratch(s, static_cast<size_t>(a.splits) * a.N * 4, &scratch);
         if (rc != MBT_OK) return rc;
         a.partial = static_cast<float *>(scratch);
     }
@@ -1239,8 +1240,9 @@ int backward_any(NormGradArgs a, cudaStream_t s) {
         // enough CTAs of 128 columns to fill the device, at least 32 rows each
         a.splits = std::max<int64_t>(1, std::min<int64_t>((a.M + 31) / 32, 16 * sms / cols));
         a.splits = std::min<int64_t>(a.splits, 65535);
+        WorkspaceHold hold;
         void *scratch = nullptr;
-        rc = owned_scratch(s, static_cast<size_t>(a.splits) * a.N * 4, &scratch);
+        rc = hold.scratch(s, static_cast<size_t>(a.splits) * a.N * 4, &scratch);
         if (rc != MBT_OK) return rc;
         a.partial = static_cast<float *>(scratch);
         const dim3 grid(static_cast<unsigned>(cols), static_cast<unsigned>(a.splits));

@@ -807,7 +807,8 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
     const int64_t xb_bytes = (token_blocks * steps * x_block(kW4Tokens, group) + 255) / 256 * 256;
     const int64_t sum_bytes = slices > 1 ? slices * T * blocks * kW4Rows * 4 : 0;
     void *scratch = nullptr;
-    rc = owned_scratch(stream, static_cast<size_t>(xb_bytes + sum_bytes), &scratch);
+    WorkspaceHold hold;
+    rc = hold.scratch(stream, static_cast<size_t>(xb_bytes + sum_bytes), &scratch);
     if (rc != MBT_OK) return rc;
     a.xb = static_cast<unsigned char *>(scratch);
     a.partial = reinterpret_cast<float *>(a.xb + xb_bytes);
