@@ -306,6 +306,10 @@ int tile_copy_ex(const void *src, void *dst, int64_t M, int64_t N, int tile_m,
  * any stream capture on it (an allocation during a capture would break the
  * capture, so it returns MBT_ERR_WORKSPACE instead).  Calls on one stream are
  * ordered, so they may share it; calls on different streams have their own.
+ * A captured call uses the workspace of the stream it was captured on: replay
+ * the graph on that stream, or ordered with the calls on it.  A buffer that a
+ * capture has taken stays allocated when a later call needs a larger one, until
+ * tile_workspace_release.
  * Free it with tile_workspace_release before destroying a stream whose
  * handle a new stream could take while the old one's work is still running.
  * A call that stops on a timed-out wait may leave band tickets set; the
@@ -512,7 +516,8 @@ int tile_host_release(void);
 
 /* Frees, in stream order (cudaFreeAsync on `stream`), the workspace the
  * library keeps for (current device, stream); the next call on that stream
- * that needs one allocates it anew.  MBT_OK when there is none. */
+ * that needs one allocates it anew.  Graphs captured with it are not to be
+ * replayed after this.  MBT_OK when there is none. */
 int tile_workspace_release(void *stream);
 
 /*

@@ -9,6 +9,7 @@
 #include <new>
 #include <thread>
 #include <tuple>
+#include <vector>
 
 #include "internal.h"
 #include "mbtile_layer.h"
@@ -22,6 +23,8 @@ struct OwnedWorkspace {
     int64_t ticket_cap = 0;     // words per ticket set (a multiple of 64)
     size_t partial_bytes = 0;
     uint64_t uses = 0;
+    bool captured = false;          // a captured call uses the buffer
+    std::vector<char *> outgrown;   // captured buffers, which graphs may still be replayed on
 };
 
 }  // namespace mbt
@@ -1035,10 +1038,15 @@ int WorkspaceHold::take(void *stream, int64_t groups, size_t partial_bytes) {
     if (rc != MBT_OK) return rc;
     w_->mutex.lock();
     OwnedWorkspace &w = *w_;
-    if (w.base != nullptr && w.ticket_cap >= groups && w.partial_bytes >= partial_bytes) return MBT_OK;
-    // Allocating inside a stream capture would end the capture with an error.
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return MBT_ERR_CUDA;
+    const bool known = cudaStreamIsCapturing(s, &cap) == cudaSuccess;
+    if (!known) cudaGetLastError();   // (the legacy stream, while a stream that blocks it captures)
+    if (w.base != nullptr && w.ticket_cap >= groups && w.partial_bytes >= partial_bytes) {
+        w.captured = w.captured || cap != cudaStreamCaptureStatusNone;
+        return MBT_OK;
+    }
+    // Allocating inside a stream capture would end the capture with an error.
+    if (!known) return MBT_ERR_CUDA;
     if (cap != cudaStreamCaptureStatusNone) return MBT_ERR_WORKSPACE;
     const int64_t ticket_cap = round_up(std::max<int64_t>({groups, w.ticket_cap, 64}), 64);
     const size_t partial = static_cast<size_t>(round_up(
@@ -1052,11 +1060,23 @@ int WorkspaceHold::take(void *stream, int64_t groups, size_t partial_bytes) {
         cudaFreeAsync(p, s);
         return MBT_ERR_CUDA;
     }
-    // The old buffer served this stream only: freed after its last use.
-    if (w.base != nullptr && cudaFreeAsync(w.base, s) != cudaSuccess) {
+    // The old buffer served this stream only: freed after its last use, unless a
+    // graph's launches hold its address.
+    bool done = w.base == nullptr;
+    if (w.captured) {
+        try {
+            w.outgrown.push_back(w.base);
+            done = true;
+        } catch (const std::bad_alloc &) {
+        }
+    } else if (!done) {
+        done = cudaFreeAsync(w.base, s) == cudaSuccess;
+    }
+    if (!done) {
         cudaFreeAsync(p, s);
         return MBT_ERR_CUDA;
     }
+    w.captured = false;
     w.base = static_cast<char *>(p);
     w.ticket_cap = ticket_cap;
     w.partial_bytes = partial;
@@ -1265,8 +1285,14 @@ int tile_workspace_release(void *stream) {
     const int rc = owned_entry(stream, &w);
     if (rc != MBT_OK) return rc;
     std::lock_guard<std::mutex> lock(w->mutex);
-    if (w->base == nullptr) return MBT_OK;
-    const cudaError_t e = cudaFreeAsync(w->base, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = w->base != nullptr ? cudaFreeAsync(w->base, s) : cudaSuccess;
+    for (char *p : w->outgrown) {
+        const cudaError_t f = cudaFreeAsync(p, s);
+        if (f != cudaSuccess) e = f;
+    }
+    w->outgrown.clear();
+    w->captured = false;
     w->base = nullptr;
     w->ticket_cap = 0;
     w->partial_bytes = 0;

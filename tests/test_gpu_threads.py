@@ -96,3 +96,37 @@ def test_calls_of_threads_on_one_stream(grow):
     assert all(right)
     assert mbt.tile_status()[0] == 0
     mbt.tile_workspace_release(stream)
+
+
+def test_graphs_outlive_the_growth_of_the_workspace():
+    """A captured product and gradient are replayed after larger calls on their stream, and others on other streams."""
+    small = [product(8, 512, 4096, 20), gradient(500, 1024, 21)]
+    large = product(8, 4096, 16384, 24)
+    others = [product(8, 512, 4096, 25 + k) for k in range(6)]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for call, *_ in small:
+        assert call(stream.cuda_stream) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        codes = [call(stream.cuda_stream) for call, *_ in small]
+    assert codes == [0, 0]
+    assert large[0](stream.cuda_stream) == 0
+    stream.synchronize()
+    streams = [torch.cuda.Stream() for _ in others]
+    for _ in range(20):
+        for (call, *_), st in zip(others, streams):
+            assert call(st.cuda_stream) == 0
+        for _, out, *_ in small:
+            out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        for (call, *_), st in zip(others, streams):
+            assert call(st.cuda_stream) == 0
+        torch.cuda.synchronize()
+        for _, out, want, _ in (*small, large, *others):
+            assert torch.equal(out, want)
+    del graph
+    for st in (stream, *streams):
+        mbt.tile_workspace_release(st)
+    assert mbt.tile_status()[0] == 0
