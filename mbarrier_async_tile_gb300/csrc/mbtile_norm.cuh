@@ -41,6 +41,18 @@ __device__ __forceinline__ float weight_at(const void *w, int wdt, float woff, i
     return w ? load_any(w, wdt, j) + woff : 1.f;
 }
 
+// The sum of v in pairs.  The last sums of dw are taken like this, several side by
+// side and then in pairs, as rounding errors grow with the root of the additions that
+// a term goes through (fp32, 16000 x 64: 2.8 u with all in series).
+template <int V>
+__device__ __forceinline__ float pair_sum(float (&v)[V]) {
+#pragma unroll
+    for (int n = V / 2; n > 0; n /= 2)
+#pragma unroll
+        for (int k = 0; k < n; ++k) v[k] += v[k + n];
+    return v[0];
+}
+
 // Any strides and lengths: a CTA per row, two passes over it (the second one's
 // reads hit the caches), one element per access, which bounds it by instructions
 // and latency (bf16 1024 x 65536, residual: 396 us, 1.4 TB/s).
@@ -775,7 +787,15 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     asm volatile("bar.sync 15, %0;" ::"n"(kRingThreads) : "memory");
     for (int j = threadIdx.x; j < a.N; j += kRingThreads) {
         float sum = slots[j];
-        for (int s = 1; s < r.rows; ++s) sum += slots[s * a.N + j];
+        if (r.rows < 8) {
+            for (int s = 1; s < r.rows; ++s) sum += slots[s * a.N + j];
+        } else {
+            float eight[8] = {};
+            for (int s = 0; s < r.rows; s += 8)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) eight[k] += slots[(s + k) * a.N + j];
+            sum = pair_sum(eight);
+        }
         a.partial[blockIdx.x * a.N + j] = sum;
     }
 }
@@ -948,33 +968,50 @@ __global__ void __launch_bounds__(kColThreads) mbt_rmsnorm_dw_rows_kernel(const 
     const int64_t j = static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x;
     if (j >= a.N) return;
     const int64_t s = blockIdx.y, lo = s * a.M / a.splits, hi = (s + 1) * a.M / a.splits;
-    float sum = 0.f;
-#pragma unroll 4
-    for (int64_t i = lo; i < hi; ++i)
-        sum += Elem<DT>::widen(static_cast<const T *>(a.dy)[i * a.ld_dy + j]) *
+    auto term = [&](int64_t i) {
+        return Elem<DT>::widen(static_cast<const T *>(a.dy)[i * a.ld_dy + j]) *
                (Elem<DT>::widen(static_cast<const T *>(a.h)[i * a.ld_h + j]) * a.rstd[i]);
+    };
+    float sum = 0.f;
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        float part[4] = {};
+        const int n = static_cast<int>(min(hi - i0, int64_t{32}));
+        int i = 0;
+        for (; i + 16 <= n; i += 16)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) part[k % 4] += term(i0 + i + k);
+        for (; i + 4 <= n; i += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) part[k] += term(i0 + i + k);
+        for (; i < n; ++i) part[0] += term(i0 + i);
+        sum += pair_sum(part);
+    }
     a.partial[s * a.N + j] = sum;
 }
 
 // dw from its partial sums: 32 columns a CTA, 16 threads a column, each adding
-// every 16th split, then in thread order.
+// every 16th split, four sums side by side, then the threads' in pairs.
 constexpr int kFinishRows = 16;
 __global__ void __launch_bounds__(32 * kFinishRows) mbt_rmsnorm_dw_finish_kernel(const NormGradArgs a) {
     __shared__ float part[kFinishRows][32];
     const int l = threadIdx.x & 31, s0 = threadIdx.x >> 5;
     const int64_t j = blockIdx.x * 32ll + l;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float sum = 0.f;
+    float sum[4] = {};
     if (j < a.N) {
 #pragma unroll 10
-        for (int64_t s = s0; s < a.splits; s += kFinishRows) sum += a.partial[s * a.N + j];
+        for (int64_t s = s0; s < a.splits; s += kFinishRows) {
+            const float v = sum[0] + a.partial[s * a.N + j];
+            sum[0] = sum[1], sum[1] = sum[2], sum[2] = sum[3], sum[3] = v;
+        }
     }
-    part[s0][l] = sum;
+    part[s0][l] = pair_sum(sum);
     __syncthreads();
     if (s0 != 0 || j >= a.N) return;
+    float all[kFinishRows];
 #pragma unroll
-    for (int s = 1; s < kFinishRows; ++s) sum += part[s][l];
-    a.dw[j] = sum;
+    for (int s = 0; s < kFinishRows; ++s) all[s] = part[s][l];
+    a.dw[j] = pair_sum(all);
 }
 
 // Where the rows of a matrix start in 16-byte chunks: -1 if not known from the
@@ -1226,7 +1263,7 @@ cudaError_t forward_any(const NormArgs &a, cudaStream_t s) {
 }
 
 // Any strides and lengths: column sums of dw in splits of rows, then dx, which may
-// overwrite dy (bf16 2048 x 32768, residual, too long for the ring: 410 us, 1.3 TB/s).
+// overwrite dy (bf16 2048 x 32768, residual, too long for the ring: 422 us, 1.3 TB/s).
 template <int DT>
 int backward_any(NormGradArgs a, cudaStream_t s) {
     int sms = 0, smem = 0;

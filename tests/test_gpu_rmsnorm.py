@@ -378,3 +378,22 @@ def test_narrow_matrices_backward(N, dtype, pad):
         mine, mdw = mbt.tile_rmsnorm_backward(a, h.contiguous(), rstd, w, dx=a)
         assert torch.equal(mine, want) and torch.equal(mdw, wdw)
     assert mbt.tile_status()[0] == 0
+
+
+@pytest.mark.parametrize("M,N,dtype", [(16000, 64, "f32"), (16000, 64, "bf16"), (4096, 30000, "f32")])
+def test_dweight_error_of_many_rows(M, N, dtype):
+    """The sum over the rows is as exact as a balanced one.
+
+    One rounding is off by 0.43 u of the rounded value on the average (uniform within half an ulp, mantissas spread
+    logarithmically); of independent terms, each level of a balanced order adds one such error of the result, a series
+    of k additions k / 2.  Up to 24 of them in all (a term's own, the rows of a thread, then eights, fours and pairs):
+    2.1 u, and a tenth for the spread over the columns.  (64 row slots in series alone would be 32.)"""
+    dt, off, norm = TYPES[dtype], 0.0, 0.0
+    for seed in range(4 if N < 1000 else 1):
+        h, dy, w = randn((M, N), dt, 80 + 3 * seed), randn((M, N), dt, 81 + 3 * seed), randn(N, dt, 82)
+        rstd = (h.double().square().mean(1) + 1e-6).rsqrt().float()
+        dw = mbt.tile_rmsnorm_backward(dy, h, rstd, w)[1]
+        want = (dy.double() * h.double() * rstd.double()[:, None]).sum(0)
+        off += (dw.double() - want).square().sum().item()
+        norm += want.square().sum().item()
+    assert (off / norm) ** 0.5 <= 2.3 * U
