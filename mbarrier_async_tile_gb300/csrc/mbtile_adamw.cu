@@ -232,9 +232,10 @@ __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, floa
     const Pair half(0.5f), minus(-1.f), ibc(s.inv_bc2), eps(s.eps), decay(s.decay), step(-s.step_size);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        // sqrt from its reciprocal's approximation and one correction, as above
+        // sqrt from its reciprocal's approximation and one correction (Markstein, as
+        // above); the smallest value above 0 stands for 0 in the reciprocal, which stays finite
         const float2 b = vp[k].get();
-        const Pair y(rsqrt_approx(fmaxf(b.x, 1.17549435e-38f)), rsqrt_approx(fmaxf(b.y, 1.17549435e-38f)));
+        const Pair y(rsqrt_approx(fmaxf(b.x, 1.4e-45f)), rsqrt_approx(fmaxf(b.y, 1.4e-45f)));
         const Pair x0 = vp[k] * y;
         const Pair x = fma2(fma2(x0 * minus, x0, vp[k]), y * half, x0);
         const float2 d = fma2(x, ibc, eps).get();

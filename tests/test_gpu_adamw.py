@@ -232,3 +232,23 @@ def test_refusals():
             mbt.tile_adamw(table, f(), **({"step": 1, "lr": 1e-3} | bad))
         assert err.value.code == -1
     mbt.tile_adamw(mbt.AdamwTensors([], [], []), [], step=1, lr=1e-3)
+
+
+@pytest.mark.parametrize("size", [1e-18, 1e-19, 1e-20])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_8_bit_states_of_tiny_gradients(size, shift):
+    """v below fp32's normal range: its root is the update's divisor (eps = 0) and the stored code."""
+    n, lr, seed = 4096 + 100, 0.1, 77
+    g = shifted((0.5 + randn(n, torch.float32, 90).abs().clamp_max(1)) * randn(n, torch.float32, 91).sign() * size, shift)
+    z = lambda k, dt=torch.float32: [torch.zeros(k, device="cuda").to(dt)]  # noqa: E731
+    p, m, v, ms, vs = z(n), z(n, E4M3), z(n, E4M3), z(-(-n // BLOCK)), z(-(-n // BLOCK))
+    mbt.tile_adamw(mbt.AdamwTensors(p, m, v, m_scales=ms, v_scales=vs), [g], step=1, lr=lr, eps=0.0, seed=seed)
+    root = (g * 0.001 * g).double().sqrt()    # (v as fp32 holds it)
+    assert bool((root > 0).all()) and float(root.max()) < 2.0 ** -63
+    want = -lr * g.double() / (root / math.sqrt(0.001))
+    assert worst(p[0], want, 64 * U * want.abs()) <= 1
+    scale = blocks(root).amax(1) / 448
+    assert worst(vs[0], scale, 4 * U * scale) <= 1
+    t = (blocks(root) / scale[:, None]).view(-1)[:n]
+    # rounded up or down: within one spacing
+    assert worst(v[0].float(), t, 2 * e4m3_half_spacing(t * (1 + 64 * U)) * (1 + 64 * U)) <= 1
