@@ -613,7 +613,8 @@ int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd, cons
  *                 for even k, in the high half for odd; 16-byte aligned, the
  *                 pitch ld_q (bytes; 0 => K / 2) a multiple of 16.
  *   scales        N x ceil(K / group), dense, of scale_dtype (fp16, bf16, fp32).
- *   zeros         optional, uint8 of the same shape, values 0..15; NULL: 8.
+ *   zeros         optional, uint8 of the same shape, of which the low four bits
+ *                 count; NULL: 8.
  *   group         32, 64 or 128; K a multiple of 32 (MBT_ERR_UNSUPPORTED).
  * Made for 1 to 8 rows of x; more are taken eight at a time, each reading q
  * again (T up to 65535, MBT_ERR_UNSUPPORTED).  Up to four rows of x with a q of

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, T == 1 ? 6 : T == 2 && XDT != 
         Pair add01[kFewRows], add23[kFewRows], p[kFewRows][T];
 #pragma unroll
         for (int r = 0; r < kFewRows; ++r) {
-            const float bias = __uint_as_float(zero[r] | 0xcb000000u), z = bias + 8388608.f;   // -(2^23 + z), -z
+            const float bias = __uint_as_float((zero[r] & 15u) | 0xcb000000u), z = bias + 8388608.f;   // -(2^23 + z), -z
             add01[r] = Pair(bias, z - 524288.f);
             add23[r] = Pair(z - 32768.f, z - 2048.f);
 #pragma unroll

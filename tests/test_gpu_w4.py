@@ -218,3 +218,11 @@ def test_few_rows_in_a_capture():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [1, 4, 8])
+def test_zero_points_are_four_bits(T):
+    """Only the low four bits of a zero point count, in every kernel."""
+    x = randn((T, 1056), torch.bfloat16, 30)
+    q, s, z = weights(70, 1056, 32, 31, zeros=True)
+    assert torch.equal(mbt.tile_w4_matvec(x, q, s, z | 0x50, group=32), mbt.tile_w4_matvec(x, q, s, z, group=32))
