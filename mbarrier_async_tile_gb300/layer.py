@@ -10,7 +10,6 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
-import os
 from typing import NamedTuple
 
 import torch
@@ -31,10 +30,7 @@ def _ext():
     global _compiled
     if _compiled is None:
         _load()
-        path = _build.BINDING_PATH
-        if not os.path.exists(path):
-            raise RuntimeError(f"the layer operators' binding is not built ({path}); run __graft_entry__.build() "
-                               "or mbarrier_async_tile_gb300._build.build()")
+        path = _build.require_binding()
         loader = importlib.machinery.ExtensionFileLoader("_mbtile_torch", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mbtile_torch", loader))
         loader.exec_module(module)
