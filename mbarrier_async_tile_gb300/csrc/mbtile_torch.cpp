@@ -92,6 +92,11 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device device) 
     return at::detail::empty_cuda(shape, type, device, c10::nullopt);
 }
 
+// Autograd is told that a tensor of the caller's was written.
+void written(const at::Tensor &t) {
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // None or a tensor.
 bool given(PyObject *o) { return o != Py_None; }
 
@@ -204,6 +209,7 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                 stream),
                    "tile_rmsnorm"))
             return nullptr;
+        for (const at::Tensor *t : {&out, &scales, &residual_out, &rstd}) written(*t);
         return Py_BuildValue("(NNNN)", wrap(out), wrap(scales), wrap(residual_out), wrap(rstd));
     });
 }
@@ -256,6 +262,8 @@ PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                          static_cast<float>(offset), stream),
                    "tile_rmsnorm_backward"))
             return nullptr;
+        written(dx);
+        written(dw);
         return Py_BuildValue("(NN)", wrap(dx), wrap(dw));
     });
 }
@@ -318,15 +326,17 @@ PyObject *w4_matvec(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                   code_of(out.scalar_type()), stream),
                    "tile_w4_matvec"))
             return nullptr;
+        written(out);
         return THPVariable_Wrap(out);
     });
 }
 
 // (address of the descriptors, their sizes as a tuple, device index, parameter code,
-// state code, grads, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
+// state code, grads, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed, the
+// tensors that are written as a tuple)
 PyObject *adamw(PyObject *, PyObject *const *a, Py_ssize_t n) {
     double v[5];
-    if (!arity(n, 14)) return nullptr;
+    if (!arity(n, 15)) return nullptr;
     for (int i = 0; i < 5; ++i)
         if (!number(a[7 + i], &v[i])) return nullptr;
     auto *t = static_cast<mbt_adamw_tensor *>(PyLong_AsVoidPtr(a[0]));
@@ -362,6 +372,7 @@ PyObject *adamw(PyObject *, PyObject *const *a, Py_ssize_t n) {
                               v[2], v[3], v[4], scale, static_cast<uint32_t>(seed), stream),
                    "tile_adamw"))
             return nullptr;
+        for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(a[14]); ++k) written(tensor(PyTuple_GET_ITEM(a[14], k), "params"));
         return Py_NewRef(Py_None);
     });
     Py_DECREF(grads);

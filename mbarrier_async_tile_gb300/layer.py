@@ -4,6 +4,11 @@ matrix-vector product, the AdamW step (see include/mbtile.h).
 The signatures and documentation; checks, allocation of results that the caller
 does not provide, and the call are compiled (csrc/mbtile_torch.cpp).  If the
 compiled parts are missing, every call raises; there is no fallback path.
+
+Autograd sees none of the operators: results carry no gradient, whatever the
+inputs require (the gradient of the norm is a call of its own).  It is told which
+of the caller's tensors a call has written: a graph that saved one of them before
+raises in its backward pass.
 """
 from __future__ import annotations
 
@@ -172,6 +177,7 @@ class AdamwTensors:
                 if not name.endswith("scales") and t.numel() != n:
                     raise ValueError(f"{name}[{k}] must have {n} elements")
             sizes.append(n)
+        self._written = (*self.params, *(t for tensors in self._kept.values() if tensors for t in tensors))
         self.sizes = tuple(sizes)
         self._address = ctypes.addressof(self._rows)
 
@@ -186,4 +192,5 @@ def tile_adamw(tensors: AdamwTensors, grads, *, step: int, lr: float, beta1: flo
     ``grad_scale``: optional fp32 device scalar that multiplies the gradients.
     ``seed``: of the 8-bit states' rounding; another one each step."""
     _call("adamw", stream, tensors._address, tensors.sizes, tensors.device.index or 0, DTYPE_CODE[tensors.dtype],
-          _CODE[tensors.state_dtype], grads, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
+          _CODE[tensors.state_dtype], grads, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed,
+          tensors._written)

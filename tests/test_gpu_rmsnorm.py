@@ -397,3 +397,21 @@ def test_dweight_error_of_many_rows(M, N, dtype):
         off += (dw.double() - want).square().sum().item()
         norm += want.square().sum().item()
     assert (off / norm) ** 0.5 <= 2.3 * U
+
+
+def test_given_results_raise_their_version():
+    """Autograd notices that a tensor it saved was overwritten."""
+    x, w = randn((4, 64), torch.float32, 95), randn(64, torch.float32, 96)
+    out, ro, rstd, dx, dw = torch.empty_like(x), x.clone(), torch.empty(4, device="cuda"), torch.empty_like(x), torch.empty_like(w)
+    before = [t._version for t in (out, ro, rstd, dx, dw)]
+    mbt.tile_rmsnorm(x, w, x, out=out, residual_out=ro, rstd=rstd)
+    mbt.tile_rmsnorm_backward(x, ro, rstd, w, dx=dx, dweight=dw)
+    assert [t._version for t in (out, ro, rstd, dx, dw)] == [b + 1 for b in before]
+    p = torch.ones(64, device="cuda", requires_grad=True)
+    loss = (p * p).sum()
+    state = mbt.AdamwTensors([p.detach()], [torch.zeros(64, device="cuda")], [torch.zeros(64, device="cuda")])
+    mbt.tile_adamw(state, [torch.ones(64, device="cuda")], step=1, lr=0.1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():   # (no versions there)
+        mbt.tile_rmsnorm(x.clone(), w, out=torch.empty_like(x))
