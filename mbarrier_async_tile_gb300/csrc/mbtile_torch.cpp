@@ -333,13 +333,14 @@ PyObject *w4_matvec(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // (address of the descriptors, their sizes as a tuple, device index, parameter code,
 // state code, grads, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed, the
-// tensors that are written as a tuple)
+// tensors that are written as a tuple, address of their addresses)
 PyObject *adamw(PyObject *, PyObject *const *a, Py_ssize_t n) {
     double v[5];
-    if (!arity(n, 15)) return nullptr;
+    if (!arity(n, 16)) return nullptr;
     for (int i = 0; i < 5; ++i)
         if (!number(a[7 + i], &v[i])) return nullptr;
     auto *t = static_cast<mbt_adamw_tensor *>(PyLong_AsVoidPtr(a[0]));
+    const void *const *addresses = static_cast<const void *const *>(PyLong_AsVoidPtr(a[15]));
     const long index = PyLong_AsLong(a[2]), pcode = PyLong_AsLong(a[3]), scode = PyLong_AsLong(a[4]);
     const long long step = PyLong_AsLongLong(a[6]);
     const unsigned long seed = PyLong_AsUnsignedLongMask(a[13]);
@@ -347,6 +348,12 @@ PyObject *adamw(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PyObject *grads = PySequence_Fast(a[5], "grads must be a sequence of tensors");
     if (!grads) return nullptr;
     PyObject *r = guarded([&]() -> PyObject * {
+        // a tensor whose data were replaced meanwhile would be updated where it lay
+        const Py_ssize_t all = PyTuple_GET_SIZE(a[14]);
+        for (Py_ssize_t k = 0; k < all; ++k)
+            if (tensor(PyTuple_GET_ITEM(a[14], k), "params").const_data_ptr() != addresses[k])
+                throw BadArgument("tensor " + std::to_string(k) + " (params, exp_avg, exp_avg_sq, ... in turn) has "
+                                  "other data than when the AdamwTensors was made");
         const Py_ssize_t count = PySequence_Fast_GET_SIZE(grads);
         if (count != PyTuple_GET_SIZE(a[1])) throw BadArgument("grads must have one tensor per parameter");
         const at::Device device(at::kCUDA, static_cast<c10::DeviceIndex>(index));
@@ -372,7 +379,7 @@ PyObject *adamw(PyObject *, PyObject *const *a, Py_ssize_t n) {
                               v[2], v[3], v[4], scale, static_cast<uint32_t>(seed), stream),
                    "tile_adamw"))
             return nullptr;
-        for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(a[14]); ++k) written(tensor(PyTuple_GET_ITEM(a[14], k), "params"));
+        for (Py_ssize_t k = 0; k < all; ++k) written(tensor(PyTuple_GET_ITEM(a[14], k), "params"));
         return Py_NewRef(Py_None);
     });
     Py_DECREF(grads);

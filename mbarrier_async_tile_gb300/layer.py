@@ -133,6 +133,8 @@ class _AdamwTensor(ctypes.Structure):
 
 class AdamwTensors:
     """The tensors that :func:`tile_adamw` updates, checked once; it holds them.
+    Their data stay where they are: replace one's (``p.data = ...``) and make the
+    object anew.
 
     ``params``: fp32, fp16 or bf16, all of one type.  ``exp_avg``, ``exp_avg_sq``:
     fp32, or e4m3 with fp32 ``m_scales`` and ``v_scales`` of ceil(n / 256)
@@ -177,7 +179,9 @@ class AdamwTensors:
                 if not name.endswith("scales") and t.numel() != n:
                     raise ValueError(f"{name}[{k}] must have {n} elements")
             sizes.append(n)
+        # the tensors that a step writes, and where their data are: replaced data (t.data = ...) are refused
         self._written = (*self.params, *(t for tensors in self._kept.values() if tensors for t in tensors))
+        self._addresses = (ctypes.c_void_p * max(1, len(self._written)))(*(t.data_ptr() for t in self._written))
         self.sizes = tuple(sizes)
         self._address = ctypes.addressof(self._rows)
 
@@ -193,4 +197,4 @@ def tile_adamw(tensors: AdamwTensors, grads, *, step: int, lr: float, beta1: flo
     ``seed``: of the 8-bit states' rounding; another one each step."""
     _call("adamw", stream, tensors._address, tensors.sizes, tensors.device.index or 0, DTYPE_CODE[tensors.dtype],
           _CODE[tensors.state_dtype], grads, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed,
-          tensors._written)
+          tensors._written, ctypes.addressof(tensors._addresses))

@@ -252,3 +252,19 @@ def test_8_bit_states_of_tiny_gradients(size, shift):
     t = (blocks(root) / scale[:, None]).view(-1)[:n]
     # rounded up or down: within one spacing
     assert worst(v[0].float(), t, 2 * e4m3_half_spacing(t * (1 + 64 * U)) * (1 + 64 * U)) <= 1
+
+
+def test_replaced_data_are_refused():
+    """A parameter or state whose data were replaced: an error, and nothing written where they lay."""
+    make_ = lambda: [torch.ones(100, device="cuda") for _ in range(3)]  # noqa: E731
+    g = [torch.ones(100, device="cuda")]
+    for k in range(3):
+        t = make_()
+        table = mbt.AdamwTensors([t[0]], [t[1]], [t[2]])
+        old = t[k].detach()
+        t[k].data = torch.full((100,), 2.0, device="cuda")
+        with pytest.raises(ValueError, match="other data"):
+            mbt.tile_adamw(table, g, step=1, lr=0.1)
+        assert bool((old == 1).all()) and all(bool((x == (2 if i == k else 1)).all()) for i, x in enumerate(t))
+        mbt.tile_adamw(mbt.AdamwTensors([t[0]], [t[1]], [t[2]]), g, step=1, lr=0.1)
+        assert bool((t[k] != 2).all())
