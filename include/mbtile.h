@@ -617,7 +617,8 @@ int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd, cons
  *                 count; NULL: 8.
  *   group         32, 64 or 128; K a multiple of 32 (MBT_ERR_UNSUPPORTED).
  * Made for 1 to 8 rows of x; more are taken eight at a time, each reading q
- * again (T up to 65535, MBT_ERR_UNSUPPORTED).  Up to four rows of x with a q of
+ * again, and in several launches where one would take more than 128 MiB of
+ * workspace or 65535 rows.  Up to four rows of x with a q of
  * few elements (N K up to 96 Mi for one row, 48 Mi / T for more; x 16-byte aligned
  * with a pitch of whole 16 bytes) take one kernel and no workspace.  All other
  * calls take x in the tensor instructions' form and, where K is sliced over CTAs,

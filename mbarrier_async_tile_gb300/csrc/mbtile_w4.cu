@@ -72,6 +72,7 @@ constexpr int kW4QBytes = 2 * kW4BoxBytes;
 constexpr int kW4Tokens = 8;
 // Bytes of a unit's part of x, which with the stages leave room for two CTAs per SM.
 constexpr int kW4XBytes = 36352;
+constexpr int64_t kW4MostScratch = 128 << 20;   // bytes of workspace, unless eight rows of x take more
 
 struct W4Args {
     const uint8_t *q;           // few rows of x: q read without a tensor map
@@ -728,7 +729,20 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
         ld_q % 16 != 0)
         return MBT_ERR_ALIGN;
     const int64_t token_blocks = (T + kW4Tokens - 1) / kW4Tokens;
-    if (T > 65535) return MBT_ERR_UNSUPPORTED;   // (a grid's second dimension)
+    // The call for the first half of the rows, in whole eights, and for the others.
+    auto in_halves = [&]() {
+        const int64_t first = token_blocks / 2 * kW4Tokens;
+        const int64_t xg = x_group ? (K + x_group - 1) / x_group : 1;
+        const int rc = tile_w4_matvec(x, x_scales, q, scales, zeros, out, first, N, K, ld_x, ld_q, ld_out, group,
+                                      x_group, dtype, scale_dtype, out_dtype, stream);
+        if (rc != MBT_OK) return rc;
+        return tile_w4_matvec(static_cast<const char *>(x) + first * ld_x * static_cast<int64_t>(type_bytes(dtype)),
+                              x_scales ? x_scales + first * xg : nullptr, q, scales, zeros,
+                              static_cast<char *>(out) + first * ld_out * static_cast<int64_t>(type_bytes(out_dtype)),
+                              T - first, N, K, ld_x, ld_q, ld_out, group, x_group, dtype, scale_dtype, out_dtype,
+                              stream);
+    };
+    if (T > 65535) return in_halves();   // (a grid's second dimension)
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) {
         const dim3 grid(static_cast<unsigned>(std::min<int64_t>((N + 255) / 256, 1024)),
@@ -806,6 +820,9 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
     // workspace: x as B elements, then the slices' sums
     const int64_t xb_bytes = (token_blocks * steps * x_block(kW4Tokens, group) + 255) / 256 * 256;
     const int64_t sum_bytes = slices > 1 ? slices * T * blocks * kW4Rows * 4 : 0;
+    // many rows of x would take gigabytes (4096 against 16384 x 16384: 2.1 GiB), and
+    // gain nothing from being one launch
+    if (xb_bytes + sum_bytes > kW4MostScratch && token_blocks > 1) return in_halves();
     void *scratch = nullptr;
     WorkspaceHold hold;
     rc = hold.scratch(stream, static_cast<size_t>(xb_bytes + sum_bytes), &scratch);

@@ -226,3 +226,23 @@ def test_zero_points_are_four_bits(T):
     x = randn((T, 1056), torch.bfloat16, 30)
     q, s, z = weights(70, 1056, 32, 31, zeros=True)
     assert torch.equal(mbt.tile_w4_matvec(x, q, s, z | 0x50, group=32), mbt.tile_w4_matvec(x, q, s, z, group=32))
+
+
+def test_many_rows_take_little_workspace():
+    """Rows of x past one launch's, and a workspace that does not grow with them."""
+    x = randn((70000, 64), torch.bfloat16, 32)
+    q, s, z = weights(40, 64, 32, 33, zeros=True)
+    check(x, q, s, z, 32, None, mbt.tile_w4_matvec(x, q, s, z, group=32))
+    T, N, K = 2051, 4096, 16384
+    n = mbt.tile_rmsnorm(randn((T, K), torch.bfloat16, 34, 2.0), None, quant=128)
+    q, s, z = weights(N, K, 128, 35)
+    out = torch.zeros(T, N + 8, dtype=torch.bfloat16, device="cuda")[:, :N]
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    mbt.tile_w4_matvec(n.out, q, s, group=128, x_scales=n.scales, out=out, stream=st)
+    st.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] < 300 << 20
+    check(n.out, q, s, None, 128, n.scales, out)
+    mbt.tile_workspace_release(st)
