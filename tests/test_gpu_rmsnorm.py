@@ -415,3 +415,18 @@ def test_given_results_raise_their_version():
         loss.backward()
     with torch.inference_mode():   # (no versions there)
         mbt.tile_rmsnorm(x.clone(), w, out=torch.empty_like(x))
+
+
+@pytest.mark.parametrize("M,N,quant", [(2600, 4096, 32), (2600, 4096, 128), (2500, 4104, 64), (2500, 4104, 128),
+                                       (1300, 8191, 0), (2100, 5001, 0), (620, 20480, 64), (650, 16392, 128)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("residual,wdt", [(False, "same"), (True, "f32"), (True, None), (False, "other")])
+def test_many_rows_e4m3_types(M, N, quant, dtype, residual, wdt):
+    """The persistent kernel's 8-bit output for every type of rows and weights, lengths that end inside a group."""
+    dt = TYPES[dtype]
+    x = randn((M, N), dt, 85)
+    r = randn((M, N), dt, 86, 2.0) if residual else None
+    other = torch.float16 if dtype == "bf16" else torch.bfloat16
+    w = None if wdt is None else randn(N, {"same": dt, "f32": torch.float32, "other": other}[wdt], 87)
+    check_forward(x, w, r, mbt.tile_rmsnorm(x, w, r, eps=1e-6, quant=quant), 1e-6, 0.0, quant)
+    assert mbt.tile_status()[0] == 0
