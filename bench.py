@@ -8,7 +8,9 @@ matrix; row sum: read of the matrix + write of the fp32 sums) / device time,
 1 GB = 1e9 B.  Inputs are far larger than the 129 MB L2, so no flush is needed
 between steps.
 
-Default (--impl mbtile) prints one JSON line on rank 0.  --impl reference times
+Default (--impl mbtile) prints one short JSON line on rank 0 (headline()), and
+before it, on stderr, the whole record: per-kernel timings, roofline, sweep,
+1-D bulk-copy points, notes.  --impl reference times
 the CPU oracle (the plain restatement used by the tests) on a bounded sample of
 the same workload.  --sweep prints one extra line per stage / warp / CTA point.
 """
@@ -52,8 +54,8 @@ GRAPH_CHUNK = 50   # steps per captured CUDA graph
 # code it was taken on (kernel_source_sha); reported only while that code is
 # unchanged.
 NCU_TRAFFIC: dict = {
-    "copy": {"src_sha": "e102672aaf294d6a", "bytes_per_launch": 536938240 + 485307136},
-    "rowsum": {"src_sha": "e102672aaf294d6a", "bytes_per_launch": 1073840384 + 2676736},
+    "copy": {"src_sha": "45751abfe323524f", "bytes_per_launch": 536938240 + 485307136},
+    "rowsum": {"src_sha": "45751abfe323524f", "bytes_per_launch": 1073840384 + 2676736},
 }
 
 def copy_bytes(c=COPY):
@@ -1335,6 +1337,25 @@ def bench_reference(args):
     }
 
 
+def headline(out: dict) -> dict:
+    """The record's part that the stdout line carries: whoever reads the line may
+    get no more than its last 1500 characters."""
+    def pick(d, *keys):
+        return {k: d[k] for k in keys if k in d}
+
+    line = pick(out, "metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better",
+                "scaling", "vs_baseline", "dtype", "data")
+    line["config"] = pick(out["config"], "workload", "copy_stages", "rowsum_stages", "l2", "parallelism")
+    line |= pick(out, "frac_of_peak", "value_one_stream", "value_host_launched", "value_graph_replay")
+    line["kernels"] = {k: pick(v, "ms", "gbs") for k, v in out["kernels"].items()}
+    line["roofline"] = pick(out["roofline"], "bound", "kernel", "achieved", "peak", "unit", "frac", "traffic")
+    line["e2e"] = pick(out["e2e"], "value", "unit", "h2d_bytes_per_step", "d2h_bytes_per_step", "link_bound")
+    if "cpu_baseline" in out:
+        line["cpu_baseline"] = pick(out["cpu_baseline"], "value", "unit", "cores", "kind")
+    line |= pick(out, "gpu_launches", "clocks")
+    return line
+
+
 # ---------------------------------------------------------------------------
 def aggregate_gbs(step_bytes: int, steps: int, world: int, ms_max: float) -> float:
     """Whole-job throughput: every rank processed `steps` steps of `step_bytes`
@@ -1376,9 +1397,9 @@ def main(argv=None):
     ap.add_argument("--sweep", action="store_true")
     ap.add_argument("--all-configs", action="store_true")
     ap.add_argument("--no-sweep", action="store_true",
-                    help="leave the per-configuration sweep out of the default line")
+                    help="leave the per-configuration sweep out of the default record")
     ap.add_argument("--no-read-ref", action="store_true",
-                    help="leave the read-bandwidth reference out of the default line")
+                    help="leave the read-bandwidth reference out of the default record")
     ap.add_argument("--only", choices=["copy", "rowsum", "copy_rowsum", "colsum", "read"])
     ap.add_argument("--config", choices=sorted(RAGGED),
                     help="--only: one of the ragged workloads (pitched rows) instead of "
@@ -1421,7 +1442,8 @@ def main(argv=None):
             backend="nccl" if torch.cuda.is_available() else "gloo")
     out = bench_gpu(args, rank, world)
     if rank == 0:
-        print(json.dumps(out), flush=True)
+        print(json.dumps(out), file=sys.stderr, flush=True)
+        print(json.dumps(headline(out)), flush=True)
     if world > 1:
         torch.distributed.destroy_process_group()
     return 0

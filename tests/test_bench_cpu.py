@@ -55,3 +55,36 @@ def test_link_bound_closed_forms():
     # 1.7 GB in, 0.85 GB out: 5 ms both ways, then 0.85 GB in alone at 210 GB/s
     t = 0.005 + 0.85e9 / 210e9
     assert abs(bench.link_bound_gbs(17 * 10**8, 85 * 10**7, 10**9, shared) - 1.0 / t) < 1e-6
+
+
+def test_default_line_is_short_and_whole():
+    """Everything a reader of the line needs, in 1500 characters, whatever the record holds."""
+    import bench
+
+    kernel = {"ms": 0.1585, "bytes": 1 << 30, "gbs": 6776.4, "ms_host_launched": 0.1591, "stages": 3, "tile": [128, 64]}
+    full = {"metric": "achieved HBM GB/s (read+write) for pipelined tile copy + rowsum", "value": 6811.2, "unit": "GB/s",
+            "n_gpus": 8, "steps": 2000, "warmup": 5, "ms_per_step": 0.3153, "higher_is_better": True, "scaling": "weak",
+            "vs_baseline": None, "dtype": "f16 copy + bf16->f32 rowsum", "data": "synthetic (seeded, drawn on device)",
+            "config": {"workload": "tile_copy fp16 16384x16384 tile 128x64 + tile_rowsum bf16 8192x65536 tile 64x256",
+                       "copy_stages": 3, "rowsum_stages": 2, "streams": "x" * 200, "launch": "x" * 200,
+                       "l2": "inputs (512 MiB, 1 GiB) larger than L2; no flush",
+                       "parallelism": "independent replica per GPU x8"},
+            "frac_of_peak": 1.003, "value_one_stream": 6726.1, "value_host_launched": 6825.3,
+            "kernels": {"copy": kernel, "rowsum": kernel},
+            "roofline": {"bound": "hbm", "kernel": "mbt_rowsum_kernel", "achieved": 6776.4, "peak": 6790.3, "unit": "GB/s",
+                         "frac": 0.998, "traffic": 1076517120, "timing": "x" * 800},
+            "e2e": {"value": 251.2, "unit": "GB/s", "h2d_bytes_per_step": 1610612736, "d2h_bytes_per_step": 536903680,
+                    "link": {"h2d_gbs": 210.0}, "link_bound": 258.9, "link_note": "x" * 400},
+            "gpu_launches": 4000, "sweep": [{"x": "y" * 400}] * 30, "flat_points": [{"x": "y" * 400}] * 5,
+            "clocks": {"sm_mhz": 2070.0, "sm_max_mhz": 2070.0, "power_w_max": 906.06, "samples": 120,
+                       "reasons": ["sw_power_cap"]},
+            "cpu_baseline": {"value": 19.5651, "unit": "GB/s", "cores": 16, "kind": "oracle", "sample": "x" * 400}}
+    line = bench.headline(full)
+    text = json.dumps(line)
+    assert len(text) <= 1500, len(text)
+    for key in ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling",
+                "vs_baseline", "dtype", "data", "config", "e2e", "gpu_launches", "clocks", "roofline", "cpu_baseline"):
+        assert key in line, key
+    assert line["value"] == 6811.2 and line["clocks"]["reasons"] == ["sw_power_cap"]
+    assert line["e2e"] == {"value": 251.2, "unit": "GB/s", "h2d_bytes_per_step": 1610612736,
+                           "d2h_bytes_per_step": 536903680, "link_bound": 258.9}
