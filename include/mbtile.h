@@ -574,6 +574,8 @@ enum { MBT_QUANT_NONE = -1, MBT_QUANT_ROW = 0 };
  *                 weight_offset)| * rstd; out = y / scale in fp32, rounded to
  *                 nearest even.  A group with a NaN has a NaN scale.
  *   rstd          fp32[M], always written (tile_rmsnorm_backward reads it).
+ * Equal calls give equal bits; a row's last bits may differ between calls of
+ * other sizes or places in memory, whose kernels add in other orders.
  * M = 0 does nothing; N = 0 writes rstd = 1 / sqrt(eps) only (and, with
  * MBT_QUANT_ROW, the smallest scale).
  */
@@ -625,10 +627,14 @@ int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd, cons
  * the slices' sums from the library's workspace for (device, stream), see
  * tile_rowsum: make the first call on a stream, with the largest shape, before a
  * capture on it (MBT_ERR_WORKSPACE where it would have to grow in one).  Sums are
- * added in a fixed order: equal calls give equal bits.  A NaN or infinity in
- * row t of x makes values of row t of out NaN or
- * infinite and leaves the other rows alone.  T = 0 or N = 0 does nothing,
- * K = 0 writes zeros.
+ * added in a fixed order: equal calls give equal bits, calls that take another
+ * kernel or other slices may differ in the last ones.  The kernel for few rows
+ * multiplies in fp32 and adds 32 columns before their scale, which asks |x| below
+ * 2^118.  The tensor instructions' form holds x in fp16, with a power of two for
+ * each row and group of columns: of a value below 2^-29 of its group's largest
+ * it drops bits (less than fp32 sums do), and of results below 2^-100.  A NaN or
+ * infinity in row t of x makes values of row t of out NaN or infinite and leaves
+ * the other rows alone.  T = 0 or N = 0 does nothing, K = 0 writes zeros.
  */
 int tile_w4_matvec(const void *x, const float *x_scales, const uint8_t *q, const void *scales,
                    const uint8_t *zeros, void *out, int64_t T, int64_t N, int64_t K, int64_t ld_x,
@@ -641,7 +647,8 @@ int tile_w4_matvec(const void *x, const float *x_scales, const uint8_t *q, const
  *   m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in fp32, updating param, exp_avg and exp_avg_sq in place.
+ * in fp32, updating param, exp_avg and exp_avg_sq in place (the square root and
+ * the quotient that only param sees are approximations to 1 and 2 ulp).
  *   tensors       HOST array of count descriptors, read during the call.  All
  *                 params have param_dtype, all grads grad_dtype (fp16, bf16 or
  *                 fp32).  master: for 16-bit params, optional fp32 weights that

@@ -5,13 +5,13 @@
 //
 // with bc = 1 - b^step, all in fp32.  Every element is read and written once,
 // so the bound with fp32 states is device memory (28 bytes an element in fp32:
-// 100 M elements 399 us, 7.0 TB/s; bf16 with an fp32 master copy, 40 M: 168 us,
+// 100 M elements 398 us, 7.0 TB/s; bf16 with an fp32 master copy, 40 M: 168 us,
 // 6.7 TB/s).  A launch takes a table of tensors as a kernel parameter (no upload,
 // nothing kept between calls); a CTA finds its chunk's tensor in the table's
 // running chunk counts.  A chunk is two 8-element accesses of each thread, all
 // of whose loads are under way before the first is used: with one, each CTA's
-// search and start are paid twice as often (8-bit states, 300 M bf16: 1038 us
-// against 649), and a loop over more chunks in a CTA leaves the memory idle
+// search and start are paid twice as often (8-bit states, 300 M bf16: 1.6
+// times the time), and a loop over more chunks in a CTA leaves the memory idle
 // between them (819).
 //
 // 8-bit states: blocks of 256 elements share an fp32 scale; one warp holds a
@@ -182,8 +182,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // not depend on how products and sums are fused.  Packed pairs halve the
 // arithmetic, which is what bounds this form: about 68 instructions an element
 // with the loads, hash and conversions, against 10 bytes of bf16 parameters,
-// gradients and states (300 M elements: 635 us, 4.8 TB/s, with 79 % of the issue
-// slots taken; with fp32 parameters and gradients, 16 bytes, 100 M: 259 us, 6.2 TB/s).
+// gradients and states (300 M elements: 657 us, 4.6 TB/s, with 79 % of the issue
+// slots taken, some of them by values kept in local memory, see below; with fp32
+// parameters and gradients, 16 bytes, 100 M: 254 us, 6.3 TB/s).
 __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, float (&p)[8], const float (&g)[8],
                                         float (&m)[8], float (&v)[8], float (&root)[8], const uint32_t (&r)[8],
                                         float *ms, float *vs) {
@@ -252,7 +253,7 @@ __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, floa
     }
     // below the normal codes (2^-6: 1 / 28672 of the block's largest) the rounding
     // takes twice the instructions; blocks without such an element go without (300 M
-    // bf16 elements: 645 us against 679)
+    // bf16 elements: 5 % less time)
     if (__any_sync(0xffffffffu, least < 0.015625f)) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) root[k] = round_at_random(root[k], r[k]);
@@ -264,8 +265,8 @@ __device__ __forceinline__ void update8(const AdamScalars &s, float gscale, floa
 }
 
 // Four CTAs an SM: held to 64 registers the 8-bit forms keep a third more warps
-// to cover each other's chains (fp32 100 M: 298 -> 259 us, bf16 300 M: 649 -> 644)
-// for some 100 bytes a thread kept in local memory; five CTAs keep more there (697).
+// to cover each other's chains (fp32 100 M 15 % faster, bf16 300 M 1 %) for 92 to 136
+// bytes a thread kept in local memory; five CTAs keep more there (8 % slower).
 template <bool PWIDE, bool GWIDE, bool MASTER, bool STATE8, int TABLE>
 __global__ void __launch_bounds__(kAdamThreads, 4)
     mbt_adamw_kernel(const __grid_constant__ AdamTable<TABLE> a) {

@@ -55,7 +55,7 @@ __device__ __forceinline__ float pair_sum(float (&v)[V]) {
 
 // Any strides and lengths: a CTA per row, two passes over it (the second one's
 // reads hit the caches), one element per access, which bounds it by instructions
-// and latency (bf16 1024 x 65536, residual: 396 us, 1.4 TB/s).
+// and latency (bf16 1024 x 65536, residual: 402 us, 1.3 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads) mbt_rmsnorm_rows_kernel(const NormArgs a) {
     using T = typename Elem<DT>::type;
@@ -272,9 +272,10 @@ struct NormVecArgs {
 // `tpr` threads hold a row in registers, C chunks each: one pass over memory.
 // Bound by device memory; rows in flight on an SM (CTAs that fit) hide the
 // latency between a row's loads and its stores (bf16, residual: 131072 x 512
-// 81 us, 6.6 TB/s; 256 x 8192 3.6 us, 4.6 TB/s from L2; one row of 8192 to e4m3 3.4
+// 80 us, 6.7 TB/s; 256 x 8192 3.6 us, 4.7 TB/s from L2; one row of 8192 to e4m3 3.5
 // us, the latency of a launch and a row).  To e4m3 the short rows are bound by
-// instructions (131072 x 512 by groups of 128: 97 us, 2.1 TB/s).
+// instructions (131072 x 512 by groups of 128, no residual: 99 us, 2.0 TB/s).
+// (Times here and below are of the kernels alone, replayed from graphs.)
 template <int DT, int C, bool RES, bool Q>
 __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant__ NormVecArgs va) {
     using T = typename Elem<DT>::type;
@@ -400,18 +401,18 @@ __global__ void __launch_bounds__(1024) mbt_rmsnorm_kernel(const __grid_constant
 // gradient of the weight, in registers for the whole kernel, and loads under way
 // while rows are reduced and written.  A unit's first warp refills a stage once
 // the unit has read it; one ring for the whole CTA made every unit wait for the
-// slowest (gradient of bf16 65536 x 128: 42.9 us, 20.9 with units; 16384 x 2048 55.5
-// and 51.8), and a warp of its own for refilling would be the 17th and cost each
+// slowest (gradient of bf16 65536 x 128: twice the time; 16384 x 2048 7 % more), and a warp of its own for refilling would be the 17th and cost each
 // thread 32 of its 128 registers.  A row costs a thread 200 to 300 instructions
 // whatever its length (barrier, shuffles, addresses), so threads take up to 32
 // elements each rather than rows fewer threads.  (32 warps of half the registers
-// were slower in the forward: bf16 4096 x 4096 28.3 us against 24.4.)
+// were slower in the forward: bf16 4096 x 4096 by 16 %.)
 //
 // Long rows are bound by device memory (fp16 16384 x 16384, residual: gradient
-// 316 us, 6.8 TB/s; forward 365 us, 5.9 TB/s); calls of a few turns by the start, the
-// last turn's latency and that overhead (bf16 4096 x 4096, residual: 23.2 us, 5.8
-// TB/s; gradient 32.2, 4.2; bf16 2047 x 8192 to e4m3 by groups of 128: 29.0, 4.0, with
-// 46 % of the issue slots taken; fp32 4097 x 8191 at an odd pitch: 63.3, 4.2).
+// 319 us, 6.7 TB/s; forward 364 us, 5.9 TB/s, 357 to 366 from run to run); calls of a
+// few turns by the start, the last turn's latency and that overhead (bf16 4096 x 4096,
+// residual: 22.4 us, 6.0 TB/s; gradient 32.1, 4.2; bf16 2047 x 8192 to e4m3 by groups of
+// 128: 29.7, 4.0, with 48 % of the issue slots taken; fp32 4097 x 8191 at an odd pitch:
+// 63.5, 4.2, its warps waiting for one another at the row's barrier).
 constexpr int kRingThreads = 512;
 constexpr int kRingStages = 8;
 constexpr int kRingBars = kRingThreads / 32 * kRingStages;   // of all units
@@ -1200,14 +1201,16 @@ cudaError_t launch_forward(const NormVecArgs &va, dim3 grid, int threads, cudaSt
              : launch_grid(mbt_rmsnorm_kernel<DT, C, false, false>, grid, threads, s, va);
 }
 
-// Where the ring is faster than a row in registers (us, ring / registers, bf16):
+// Where the ring is faster than a row in registers (us, ring / registers, bf16 with a
+// residual, both built and timed in turn):
 //  - its start (weights, barriers, the first rows' latency) is paid once per call:
-//    512 x 8192 9.4 / 8.3, 1024 x 8192 13.8 / 16.2, fp16 16384 x 16384 351 / 429;
+//    512 x 8192 7.95 / 7.87, 1024 x 8192 12.4 / 13.6, fp16 16384 x 16384 358 / 426;
 //  - rows of up to 1 KB are a warp's at most in registers, with no barrier:
-//    131072 x 256 81 / 41, 131072 x 512 101 / 81; fp32 65536 x 512 46 / 61;
+//    131072 x 256 46.5 / 41.0, 131072 x 512 91 / 80; fp32 65536 x 512 45 / 61;
 //  - two matrices read keep enough bytes on their way with short rows as well:
-//    65536 x 2048 185 / 161, 4096 x 4096 24.2 / 26.1; rows that start inside a
-//    chunk do not: 65537 x 1001 112 / 128; nor does the arithmetic of an 8-bit output.
+//    65536 x 2048 183 / 160, 4096 x 4096 22.5 / 25.8; rows that start inside a
+//    chunk do not: 65537 x 1001 105 / 127; nor does the arithmetic of an 8-bit
+//    output, by groups of 128 65536 x 2048 202 / 238, 131072 x 1024 191 / 241.
 bool ring_forward_pays(const NormArgs &a, int64_t es, int sms, int phase) {
     const int64_t row = a.N * es;
     if (a.M * row < (16ll << 20) || a.M < 4 * sms || row <= 1024) return false;

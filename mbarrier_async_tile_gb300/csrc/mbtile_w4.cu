@@ -4,8 +4,9 @@
 // The matrix is read once and each of its elements used at most eight times:
 // device memory bounds the large products, latency the small ones.  One to four
 // rows of x and few elements have a kernel of their own, mbtile_w4_few.cuh.  Here
-// fp16 16384 x 16384 by groups of 64 with zero points and 8 rows of x takes 42 us, 3.5
-// TB/s, and e4m3 8191 x 8192 by groups of 32 and 3 rows 16.3 us, 2.3 TB/s: the ring
+// fp16 16384 x 16384 by groups of 64 with zero points and 8 rows of x takes 42.1 us,
+// 3.5 TB/s, and e4m3 8191 x 8192 by groups of 32 and 3 rows 17.0 us, 2.2 TB/s (replayed
+// from graphs, q from device memory): the ring
 // alone streams the former in 25 us, the consumers' conversions and scales take
 // 53 % of the issue slots beside it, and the kernels before and after it and the
 // start some 7 us.
@@ -35,7 +36,9 @@
 // of the instruction, for which a nibble is a code as it stands, is carried out as
 // two fp16 ones with conversions here: measured, 1.4 times the instructions.)
 //
-// An A element is q - z as fp16, exactly: a 4-bit value put into the mantissa of
+// An A element is q - z as fp16, exactly, by the known addition to a power of two whose
+// last place is one (for 4-bit weights in fp16: Kim, Henry, Fahim, Awadalla, "Who Says
+// Elephants Can't Run", SustaiNLP 2022): a 4-bit value put into the mantissa of
 // 1024 (bits 0..3) is 1024 + q, from which 1024 + z is subtracted; in bits 4..7
 // it is 1024 + 16 q, which a multiplication by 1/16 and a subtraction of 64 + z
 // take to the same.  Eight values cost four ANDs with ORs, a shift and four
@@ -799,8 +802,8 @@ extern "C" int tile_w4_matvec(const void *x, const float *x_scales, const uint8_
     // the counts up to four times that (or one per step, or a unit for each CTA),
     // the one with the least time for the busiest CTA, counted in steps, a unit
     // costing 0.3 of a step beside its own (8 rows of x: with nothing for a unit
-    // 16384 x 16384 takes 57.8 us instead of 41.9 and 8192 x 8192 17.4 instead of 15.3;
-    // with two steps 4096 x 14336 takes 16.1 instead of 15.3).
+    // 16384 x 16384 takes 51.9 us instead of 38.2 and 8192 x 8192 17.6 instead of 16.2;
+    // with two steps 4096 x 14336 takes 16.7 instead of 15.4).
     int64_t longest = 1;
     while (longest < steps && x_bytes(longest + 1, a.x_rows, group) <= kW4XBytes)
         ++longest;

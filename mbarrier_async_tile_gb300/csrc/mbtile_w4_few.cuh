@@ -2,8 +2,8 @@
 // that reads q once and multiplies in fp32.  The tensor form (mbtile_w4.cu) needs x
 // converted by a kernel before it and, with K sliced, its sums added by one after
 // it, which it takes 3 to 4 us to make up for; with more elements or more rows of x
-// its instructions win (few_pays has both sides).  1 row, 4096 x 4096: 4.9 us, of
-// which half is the start of the kernel and the latency of its reads, half
+// its instructions win (few_pays has both sides).  1 row, 4096 x 4096: 5.9 us with q
+// from device memory, 5.2 from L2, of which half is the start of the kernel and the latency of its reads, half
 // instructions (4.6 an element, half of which are not arithmetic: addresses, x
 // through shared memory, sums over lanes).
 #pragma once
@@ -188,13 +188,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, T == 1 ? 6 : T == 2 && XDT != 
     store_any(a.out, a.odt, t * a.ld_out + n, y);
 }
 
-// Where the fp32 form takes less time than the tensor form; us, bf16 x, fp32 / tensor:
+// Where the fp32 form takes less time than the tensor form; us, bf16 x, groups of 128,
+// q from device memory, fp32 / tensor:
 //                 4096 x 4096   8192 x 8192   16384 x 16384
-//   1 row of x    4.9 /  7.8    14.0 / 16.1    46.6 / 40.0
-//   2 rows        6.5 /  7.9    19.0 / 16.8    66.2 / 40.5
-//   3 rows        7.7 /  8.0    22.3 / 16.8    79.3 / 40.7
-//   4 rows        9.2 /  8.1    28.2 / 18.4   103.9 / 40.9
-// and at 1024 x 1024 from 2.0 / 5.5 (1 row) to 2.6 / 5.7 (4 rows).
+//   1 row of x    5.9 /  8.7    14.4 / 14.8    45.1 / 37.4
+//   2 rows        7.4 /  8.8    19.3 / 15.0    63.9 / 37.4
+//   3 rows        8.5 /  9.0    23.2 / 15.1    77.3 / 37.6
+//   4 rows       11.2 /  9.0    29.6 / 15.1   100.9 / 37.7
+// and at 1024 x 1024 from 2.0 / 5.2 (1 row) to 2.6 / 5.5 (4 rows).
 bool few_pays(int64_t T, int64_t N, int64_t K) {
     return T <= kFewTokens && N * K <= (T == 1 ? 96ll << 20 : (48ll << 20) / T);
 }
