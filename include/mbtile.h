@@ -682,6 +682,56 @@ int tile_adamw(const mbt_adamw_tensor *tensors, int64_t count, int param_dtype, 
                int state_dtype, int64_t step, double lr, double beta1, double beta2, double eps,
                double weight_decay, const float *grad_scale, uint32_t seed, void *stream);
 
+/*
+ * Matrices in microscaled 4-bit floats: M x K codes of four bits (e2m1: sign, two bits
+ * of exponent, one of mantissa; 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, column k in
+ * the low half of byte k / 2 for even k, in the high half for odd; 16-byte aligned, the
+ * pitch (bytes; 0 => K / 2) a multiple of 16.  K a multiple of 32
+ * (MBT_ERR_UNSUPPORTED).  Each `block` columns of a row share a byte of scale:
+ *   block 16      e4m3 (at least 0), times *tensor_scale (DEVICE pointer to one fp32, above
+ *                 0; NULL: 1);
+ *   block 32      2^(byte - 127), 255: NaN; no tensor_scale (MBT_ERR_ARG).
+ * The scales lie in tiles of 128 rows x 4 blocks, 512 bytes each, tile (i, j) of
+ * ceil(M / 128) x ceil(K / block / 4) at 512 (i ceil(K / block / 4) + j): row r and
+ * block k of a tile at 16 (r % 32) + 4 (r / 32) + k.  Bytes of rows and blocks past the
+ * matrix's have to be there; those of blocks past it must not be NaN (tile_mx4_quantize
+ * writes zeros).  16-byte aligned, tile_mx4_scale_bytes bytes (or a negative mbt_status).
+ */
+int64_t tile_mx4_scale_bytes(int64_t M, int64_t K, int block);
+
+/*
+ * tile_mx4_quantize -- x (M x K of type dtype, pitch ld_x) in 4-bit floats.  With a the
+ * largest magnitude of a block, t = *tensor_scale:
+ *   block 16      s = a / (6 t) rounded to e4m3 (nearest even, at most 448), d = s t;
+ *   block 32      s = 2^(floor(log2 a) - 2), at least 2^-127, d = s;
+ *   code          x / d rounded to e2m1 (nearest even, at most 6 in magnitude).
+ * 6 t, s t and the quotients are rounded to fp32 first.  Where d is 0 or all of a block
+ * is, its codes are 0; a block with a NaN or infinity has a NaN scale and codes of 0.
+ * t is asked to lie between 2^-60 and 2^60.
+ */
+int tile_mx4_quantize(const void *x, const float *tensor_scale, uint8_t *q, uint8_t *scales,
+                      int64_t M, int64_t K, int64_t ld_x, int64_t ld_q, int block, int dtype,
+                      void *stream);
+
+/* tile_mx4_dequantize -- out (M x K of out_dtype, pitch ld_out) = code * scale *
+ * *tensor_scale, each product rounded to fp32, then to out_dtype. */
+int tile_mx4_dequantize(const uint8_t *q, const uint8_t *scales, const float *tensor_scale,
+                        void *out, int64_t M, int64_t K, int64_t ld_q, int64_t ld_out, int block,
+                        int out_dtype, void *stream);
+
+/*
+ * tile_mx4_matmul -- product of two such matrices, a (M x K) and b (N x K):
+ *   out[m][n] = *a_tensor_scale * *b_tensor_scale * sum_k a[m][k] b[n][k]
+ * summed in fp32 by the tensor instructions (out M x N, rounded once to out_dtype).
+ * Up to 128 rows of a are taken in one pass over b.  Equal calls give equal bits.  A NaN
+ * scale makes the values of out that it reaches NaN.  No workspace.  M = 0 or N = 0 does
+ * nothing, K = 0 writes zeros.
+ */
+int tile_mx4_matmul(const uint8_t *a, const uint8_t *a_scales, const float *a_tensor_scale,
+                    const uint8_t *b, const uint8_t *b_scales, const float *b_tensor_scale,
+                    void *out, int64_t M, int64_t N, int64_t K, int64_t ld_a, int64_t ld_b,
+                    int64_t ld_out, int block, int out_dtype, void *stream);
+
 /* Synchronises `stream`, then reads and clears the current device's status
  * word.  info (may be NULL) receives {code, block, stage, role * 2 + parity}
  * of the first wait that timed out (role 0 = producer, 1 = consumer).

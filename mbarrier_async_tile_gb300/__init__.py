@@ -28,7 +28,7 @@ __all__ = [
     "tile_workspace_release", "tile_read_checksum",
     "tile_status", "tile_plan", "tile_plan_device", "tile_device_info", "tile_strerror",
     "tile_stage_image",
-    "E4M3", "RmsNorm", "AdamwTensors",
+    "E4M3", "RmsNorm", "AdamwTensors", "Mx4", "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul",
     "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw",
 ]
 
@@ -158,6 +158,11 @@ def _load():
         lib.tile_rmsnorm.argtypes = [vp] * 7 + [i64] * 6 + [i32] * 3 + [f32, f32, vp]
         lib.tile_rmsnorm_backward.argtypes = [vp] * 7 + [i64] * 6 + [i32] * 2 + [f32, vp]
         lib.tile_w4_matvec.argtypes = [vp] * 6 + [i64] * 6 + [i32] * 5 + [vp]
+        lib.tile_mx4_quantize.argtypes = [vp] * 4 + [i64] * 4 + [i32] * 2 + [vp]
+        lib.tile_mx4_dequantize.argtypes = [vp] * 4 + [i64] * 4 + [i32] * 2 + [vp]
+        lib.tile_mx4_matmul.argtypes = [vp] * 7 + [i64] * 6 + [i32] * 2 + [vp]
+        lib.tile_mx4_scale_bytes.argtypes = [i64, i64, i32]
+        lib.tile_mx4_scale_bytes.restype = i64
         lib.tile_adamw.argtypes = ([vp, i64, i32, i32, i32, i64] + [f64] * 5 +
                                    [vp, ctypes.c_uint32, vp])
         for name in ("tile_copy", "tile_copy_ex", "tile_rowsum", "tile_rowsum_ex",
@@ -167,7 +172,8 @@ def _load():
                      "tile_copy_host", "tile_rowsum_host", "tile_colsum_host",
                      "tile_host_release", "tile_workspace_release", "tile_read_checksum",
                      "tile_colsum", "tile_colsum_ex", "tile_colsum_workspace_bytes",
-                     "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw"):
+                     "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw",
+                     "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul"):
             getattr(lib, name).restype = ctypes.c_int
         _C = lib
         return lib
@@ -562,5 +568,5 @@ def tile_read_checksum(buf: torch.Tensor, out: torch.Tensor | None = None,
     return out
 
 
-from .layer import (E4M3, AdamwTensors, RmsNorm, tile_adamw, tile_rmsnorm,  # noqa: E402
-                    tile_rmsnorm_backward, tile_w4_matvec)
+from .layer import (E4M3, AdamwTensors, Mx4, RmsNorm, tile_adamw, tile_mx4_dequantize,  # noqa: E402
+                    tile_mx4_matmul, tile_mx4_quantize, tile_rmsnorm, tile_rmsnorm_backward, tile_w4_matvec)

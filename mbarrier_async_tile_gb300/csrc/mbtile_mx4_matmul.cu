@@ -1,0 +1,414 @@
+// tile_mx4_matmul: out[m][n] = t_a t_b sum_k a[m][k] b[n][k] of two matrices in
+// microscaled 4-bit floats, by the tensor instructions that apply the blocks' scales
+// themselves and accumulate in fp32.
+//
+// A CTA computes tiles of 128 rows of one operand by BN rows of the other, over all of
+// K or a slice of it.  Warp roles:
+//   a producer thread: stages of 256 columns (128 bytes of codes a row) of both
+//   operands by bulk tensor copies with the 128-byte swizzle, and the scale tiles that
+//   go with them by 1-D bulk copies;
+//   a tensor thread: copies a stage's scales into tensor memory, issues the stage's
+//   products (64 columns each), and hands the stage back when they are done;
+//   four epilogue warps: a finished tile from tensor memory, scaled by t_a t_b.
+// Each stage has scale columns of its own in tensor memory, so that new scales never
+// meet products still under way.
+//
+// Few rows of a (up to 128): the rows of b are the instructions' 128 rows and those of a
+// their columns (SWAP), so that no product is spent on rows that are not there but up to
+// the next of 16, 32, 64 and 128; K is cut over the CTAs of a cluster until the device is
+// full, and the CTAs add their parts through each other's shared memory, in the order of
+// the slices.
+#include <algorithm>
+#include <atomic>
+
+#include "mbtile_elem.cuh"
+#include "mbtile_layer.h"
+#include "mbtile_mx4.cuh"
+#include "mbtile_ptx.cuh"
+#include "mbtile_tcgen05.cuh"
+
+namespace mbt {
+namespace {
+
+constexpr int kMmThreads = 256;
+constexpr int kMmRows = 128;              // of the instructions' first operand
+constexpr int kMmStep = 256;              // columns of K per stage
+constexpr int kMmMostStages = 8;
+constexpr int kMmTmem = 512;              // columns
+
+struct Mx4MatArgs {
+    const uint8_t *sr, *sc;    // scales of the rows' and of the columns' operand
+    const float *ta, *tb;
+    void *out;
+    int64_t R, C, K, ld_out;   // rows and columns of the tiles' matrix
+    int64_t scale_tiles;       // across K
+    int32_t steps;
+    int32_t tiles_r, tiles_c;
+    int32_t split;             // CTAs of a cluster, each a slice of K
+    int32_t odt;
+    int32_t vec;               // rows of out are whole aligned 16-byte chunks
+    int32_t *status;
+};
+
+template <int BN, int BLOCK>
+struct MmShape {
+    static constexpr int kTiles = kMmStep / BLOCK / 4;        // scale tiles of 128 rows per stage
+    static constexpr int kColTiles = (BN + 127) / 128;        // of the columns' operand
+    static constexpr int kRowBytes = kMmRows * kBoxRowBytes;
+    static constexpr int kColBytes = BN * kBoxRowBytes;
+    static constexpr int kScaleBytes = kTiles * 512;
+    static constexpr int kStage = kRowBytes + kColBytes + kScaleBytes * (1 + kColTiles);
+    static constexpr int kScaleCols = kTiles * 4 * (1 + kColTiles);   // tensor memory of a stage's scales
+    static constexpr int kAcc = BN < 32 ? 32 : BN;
+    static constexpr int kAccs = 2 * kAcc + kScaleCols * 4 <= kMmTmem ? 2 : 1;
+    static constexpr int kFit = 220 * 1024 / kStage;
+    static constexpr int kTmemFit = (kMmTmem - kAccs * kAcc) / kScaleCols;
+    static constexpr int kStages = kFit < kTmemFit ? (kFit < kMmMostStages ? kFit : kMmMostStages)
+                                                   : (kTmemFit < kMmMostStages ? kTmemFit : kMmMostStages);
+    static constexpr int kSmem = kStages * kStage + kSwizzleAtomBytes;
+    static_assert(kStage % kSwizzleAtomBytes == 0 && kStages >= 2);
+};
+
+// Tiles in groups of up to 16 down the rows, so that CTAs side by side share both operands.
+__device__ __forceinline__ void tile_at(const Mx4MatArgs &a, int t, int *r, int *c) {
+    const int per = 16 * a.tiles_c, g = t / per, first = g * 16, rows = min(16, a.tiles_r - first), left = t - g * per;
+    *c = left / rows;
+    *r = first + left - *c * rows;
+}
+
+// 16 neighbouring elements of a row of out.
+__device__ __forceinline__ void store16(const Mx4MatArgs &a, int64_t row, int64_t col, const float (&f)[16], int count) {
+    const int64_t at = row * a.ld_out + col;
+    if (a.vec && count >= 16) {
+        if (a.odt == MBT_F32) {
+            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+        } else {
+            uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float g[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] = f[8 * k + e];
+                p[k] = a.odt == MBT_BF16 ? pack<MBT_BF16>(g) : pack<MBT_F16>(g);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (e < count) store_any(a.out, a.odt, at + e, f[e]);
+}
+
+struct MmShared {
+    uint64_t full[kMmMostStages], empty[kMmMostStages], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+template <int BN, int BLOCK, bool SWAP>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    mbt_mx4_matmul_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap cols_map,
+                          const __grid_constant__ Mx4MatArgs a) {
+    using S = MmShape<BN, BLOCK>;
+    extern __shared__ unsigned char dyn_smem[];
+    __shared__ __align__(8) MmShared sh;
+    const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 2) tmem_alloc(smem_u32(&sh.tmem), kMmTmem);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sh.acc_full[b]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[b]), 4);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort_flag = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
+    const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int first_tile = a.split > 1 ? static_cast<int>(blockIdx.x) / a.split : static_cast<int>(blockIdx.x);
+    const int stride = a.split > 1 ? 0x40000000 : static_cast<int>(gridDim.x);   // (a cluster has one tile)
+    const int tiles = a.tiles_r * a.tiles_c;
+    const int k0 = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.split);
+    const int k1 = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / a.split);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    auto fail = [&](int role, uint32_t stage, uint32_t parity) {
+        report_timeout(w, role, stage, parity);
+        *w.abort = 1;
+    };
+    if (warp == 0 && lane == 0) {
+        uint32_t stage = 0, phase = 1;
+        bool alive = true;
+        for (int t = first_tile; t < tiles && alive; t += stride) {
+            int tr, tc;
+            tile_at(a, t, &tr, &tc);
+            for (int k = k0; k < k1; ++k) {
+                const uint32_t full = smem_u32(&sh.full[stage]);
+                if (!wait_bounded(smem_u32(&sh.empty[stage]), phase, w, true)) {
+                    fail(0, stage, phase);
+                    alive = false;
+                    break;
+                }
+                const uint32_t at = base + stage * S::kStage, sr = at + S::kRowBytes + S::kColBytes;
+                const int64_t tile = static_cast<int64_t>(k) * S::kTiles;
+                const uint32_t bytes = 512u * static_cast<uint32_t>(min(static_cast<int64_t>(S::kTiles), a.scale_tiles - tile));
+                // the columns' last tile of 128 rows may have no scales
+                const int col_tiles = S::kColTiles == 1 || (2 * tc + 1) * 128 < a.C ? S::kColTiles : 1;
+                mbar_arrive_expect_tx(full, S::kRowBytes + S::kColBytes + bytes * (1 + col_tiles));
+                tma_load_2d(at, &rows_map, k * kBoxRowBytes, tr * kMmRows, full);
+                tma_load_2d(at + S::kRowBytes, &cols_map, k * kBoxRowBytes, tc * BN, full);
+                bulk_load_1d(sr, a.sr + (tr * a.scale_tiles + tile) * 512, bytes, full);
+                for (int c = 0; c < col_tiles; ++c)
+                    bulk_load_1d(sr + (1 + c) * S::kScaleBytes,
+                                 a.sc + ((static_cast<int64_t>(tc) * S::kColTiles + c) * a.scale_tiles + tile) * 512,
+                                 bytes, full);
+                if (++stage == S::kStages) stage = 0, phase ^= 1;
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        constexpr uint32_t idesc = mx4_idesc<BLOCK>(kMmRows, BN);
+        uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 1;
+        bool alive = true;
+        for (int t = first_tile; t < tiles && alive; t += stride) {
+            if (!wait_bounded(smem_u32(&sh.acc_empty[acc]), acc_phase, w, true)) {
+                fail(2, acc, acc_phase);
+                alive = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + acc * S::kAcc;
+            for (int k = k0; k < k1; ++k) {
+                if (!wait_bounded(smem_u32(&sh.full[stage]), phase, w, true)) {
+                    fail(1, stage, phase);
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = base + stage * S::kStage, sr = at + S::kRowBytes + S::kColBytes;
+                const uint32_t scols = tmem + S::kAccs * S::kAcc + stage * S::kScaleCols;
+                const uint32_t ccols = scols + S::kTiles * 4;
+                const int left = static_cast<int>(min(static_cast<int64_t>(4), (a.K - static_cast<int64_t>(k) * kMmStep + 63) / 64));
+                const uint64_t da = desc_swizzled(at), db = desc_swizzled(at + S::kRowBytes);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    if (m >= left) break;
+                    const int s = m * S::kTiles / 4;             // the product's scale tile
+                    if (m * S::kTiles % 4 == 0) {
+                        tmem_copy_scales(scols + 4 * s, desc_rows16(sr + 512 * s));
+#pragma unroll
+                        for (int c = 0; c < S::kColTiles; ++c)
+                            tmem_copy_scales(ccols + 4 * (s * S::kColTiles + c),
+                                             desc_rows16(sr + (1 + c) * S::kScaleBytes + 512 * s));
+                    }
+                    const uint32_t id = BLOCK == 32 ? (m & 1) * 2 : 0;   // the first of the bytes in a scale column
+                    mma_mx4<BLOCK>(d, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s,
+                                   ccols + 4 * s * S::kColTiles, k > k0 || m > 0);
+                }
+                tc_commit(smem_u32(&sh.empty[stage]));
+                if (++stage == S::kStages) stage = 0, phase ^= 1;
+            }
+            if (!alive) break;
+            tc_commit(smem_u32(&sh.acc_full[acc]));
+            if (++acc == S::kAccs) acc = 0, acc_phase ^= 1;
+        }
+        if (!alive) {                        // what has been issued ends before tensor memory is freed
+            tc_commit(smem_u32(&sh.drain));
+            wait_bounded(smem_u32(&sh.drain), 0, w, false);
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3;
+        float alpha = a.ta ? *a.ta : 1.f;
+        if (a.tb) alpha *= *a.tb;
+        uint32_t acc = 0, phase = 0;
+        for (int t = first_tile; t < tiles; t += stride) {
+            int tr, tc;
+            tile_at(a, t, &tr, &tc);
+            if (!__all_sync(0xffffffffu, wait_bounded(smem_u32(&sh.acc_full[acc]), phase, w, true))) {
+                if (lane == 0) fail(3, acc, phase);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t from = tmem + acc * S::kAcc + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int r = quarter * 32 + lane;
+            const int64_t row = static_cast<int64_t>(tr) * kMmRows + r, col0 = static_cast<int64_t>(tc) * BN;
+            const int cols = static_cast<int>(min(static_cast<int64_t>(BN), a.C - col0));
+#pragma unroll 2
+            for (int c = 0; c < BN; c += 16) {
+                if (c >= cols) break;
+                float f[16];
+                __syncwarp();
+                tmem_load16(from + c, f);
+                if (SWAP && a.split > 1) {   // the slice's sums, for the cluster
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c + e) * kMmRows + r) * 4), "f"(f[e]) : "memory");
+                } else if (row < a.R) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] *= alpha;
+                    if constexpr (SWAP) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c + e < cols) store_any(a.out, a.odt, (col0 + c + e) * a.ld_out + row, f[e]);
+                    } else {
+                        store16(a, row, col0 + c, f, cols - c);
+                    }
+                }
+            }
+            __syncwarp();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[acc]));
+            if (++acc == S::kAccs) acc = 0, phase ^= 1;
+        }
+    }
+    __syncwarp();
+    if constexpr (SWAP) {
+        if (a.split > 1) {
+            cluster_sync();
+            float alpha = a.ta ? *a.ta : 1.f;
+            if (a.tb) alpha *= *a.tb;
+            const int rows = kMmRows / a.split, tr = first_tile;
+            const int cols = static_cast<int>(min(static_cast<int64_t>(BN), a.C));
+            for (int e = threadIdx.x; e < rows * cols; e += kMmThreads) {
+                const int c = e / rows, r = rank * rows + e - c * rows;
+                const int64_t n = static_cast<int64_t>(tr) * kMmRows + r;
+                if (n >= a.R) continue;
+                float sum = 0.f;
+                for (int q = 0; q < a.split; ++q) sum += cluster_load(base + (c * kMmRows + r) * 4, q);
+                store_any(a.out, a.odt, c * a.ld_out + n, sum * alpha);
+            }
+            cluster_sync();                  // no CTA leaves while another reads its sums
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.abort_flag)   // copies under way land before the CTA leaves
+        for (int s = 0; s < S::kStages; ++s)
+            for (uint32_t p = 0; p < 2; ++p) wait_bounded(smem_u32(&sh.full[s]), p, w, false);
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_free(tmem, kMmTmem);
+}
+
+__global__ void mbt_mx4_zero_kernel(void *out, int dtype, int64_t M, int64_t N, int64_t ld) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < M * N;
+         e += static_cast<int64_t>(gridDim.x) * blockDim.x)
+        store_any(out, dtype, e / N * ld + e % N, 0.f);
+}
+
+bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+template <int BN, int BLOCK, bool SWAP>
+int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_cols, Mx4MatArgs a, int sms,
+                  cudaStream_t stream) {
+    using S = MmShape<BN, BLOCK>;
+    static std::atomic<bool> raised[64];   // per device: the kernel's shared-memory limit is set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MBT_ERR_CUDA;
+    if (dev >= 64 || !raised[dev].load(std::memory_order_relaxed)) {
+        if (cudaFuncSetAttribute(mbt_mx4_matmul_kernel<BN, BLOCK, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S::kSmem) != cudaSuccess)
+            return MBT_ERR_CUDA;
+        if (dev < 64) raised[dev].store(true, std::memory_order_relaxed);
+    }
+    alignas(64) CUtensorMap rows_map, cols_map;
+    int rc = encode_bytes_map(&rows_map, rows, a.R, a.K / 2, ld_rows, kMmRows);
+    if (rc == MBT_OK) rc = encode_bytes_map(&cols_map, cols, a.C, a.K / 2, ld_cols, BN);
+    if (rc != MBT_OK) return rc;
+    a.tiles_r = static_cast<int32_t>((a.R + kMmRows - 1) / kMmRows);
+    a.tiles_c = static_cast<int32_t>((a.C + BN - 1) / BN);
+    const int64_t tiles = static_cast<int64_t>(a.tiles_r) * a.tiles_c;
+    if (tiles > 0x3fffffff) return MBT_ERR_UNSUPPORTED;
+    a.split = 1;
+    if (SWAP)
+        while (a.split < 8 && tiles * a.split * 2 <= sms && a.split * 2 <= a.steps) a.split *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.split > 1 ? tiles * a.split : std::min<int64_t>(tiles, sms)));
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, mbt_mx4_matmul_kernel<BN, BLOCK, SWAP>, rows_map, cols_map, a) == cudaSuccess
+               ? MBT_OK
+               : MBT_ERR_CUDA;
+}
+
+template <int BLOCK>
+int matmul(const uint8_t *a_q, int64_t ld_a, const uint8_t *b_q, int64_t ld_b, const uint8_t *as, const uint8_t *bs,
+           int64_t M, int64_t N, Mx4MatArgs a, int sms, cudaStream_t s) {
+    if (M <= 128) {
+        a.R = N, a.C = M, a.sr = bs, a.sc = as;
+        return M <= 16   ? launch_matmul<16, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s)
+               : M <= 32 ? launch_matmul<32, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s)
+               : M <= 64 ? launch_matmul<64, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s)
+                         : launch_matmul<128, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s);
+    }
+    a.R = M, a.C = N, a.sr = as, a.sc = bs;
+    return launch_matmul<128, BLOCK, false>(a_q, ld_a, b_q, ld_b, a, sms, s);
+}
+
+}  // namespace
+}  // namespace mbt
+
+extern "C" int tile_mx4_matmul(const uint8_t *a, const uint8_t *a_scales, const float *a_tensor_scale, const uint8_t *b,
+                               const uint8_t *b_scales, const float *b_tensor_scale, void *out, int64_t M, int64_t N,
+                               int64_t K, int64_t ld_a, int64_t ld_b, int64_t ld_out, int block, int out_dtype,
+                               void *stream) {
+    using namespace mbt;
+    if (M < 0 || N < 0 || K < 0 || M > 0x7fffffff || N > 0x7fffffff || K > 0x7fffffff || out_dtype < MBT_F16 ||
+        out_dtype > MBT_F32)
+        return MBT_ERR_ARG;
+    if ((block != 16 && block != 32) || K % 32 != 0) return MBT_ERR_UNSUPPORTED;
+    if (block != 16 && (a_tensor_scale || b_tensor_scale)) return MBT_ERR_ARG;
+    if (ld_a == 0) ld_a = K / 2;
+    if (ld_b == 0) ld_b = K / 2;
+    if (ld_out == 0) ld_out = N;
+    if (ld_a < K / 2 || ld_b < K / 2 || ld_out < N || ld_a >= (1ll << 40) || ld_b >= (1ll << 40) || ld_out > (1ll << 40))
+        return MBT_ERR_ARG;
+    if (M == 0 || N == 0) return MBT_OK;
+    if (!out || (K > 0 && (!a || !a_scales || !b || !b_scales))) return MBT_ERR_ARG;
+    const uintptr_t es = out_dtype == MBT_F32 ? 4 : 2;
+    if (!aligned(out, es) || !aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 16) || !aligned(b_scales, 16) ||
+        ld_a % 16 != 0 || ld_b % 16 != 0 || !aligned(a_tensor_scale, 4) || !aligned(b_tensor_scale, 4))
+        return MBT_ERR_ALIGN;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0) {
+        mbt_mx4_zero_kernel<<<1024, 256, 0, s>>>(out, out_dtype, M, N, ld_out);
+        return cudaGetLastError() == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
+    }
+    int sms = 0, optin = 0;
+    int rc = device_limits(&sms, &optin);
+    if (rc != MBT_OK) return rc;
+    Mx4MatArgs g{};
+    rc = device_status_word(&g.status);
+    if (rc != MBT_OK) return rc;
+    g.ta = a_tensor_scale;
+    g.tb = b_tensor_scale;
+    g.out = out;
+    g.K = K;
+    g.ld_out = ld_out;
+    g.scale_tiles = mx4_tiles(K, block);
+    g.steps = static_cast<int32_t>((K + kMmStep - 1) / kMmStep);
+    g.odt = out_dtype;
+    g.vec = aligned(out, 16) && ld_out * static_cast<int64_t>(es) % 16 == 0;
+    return block == 16 ? matmul<16>(a, ld_a, b, ld_b, a_scales, b_scales, M, N, g, sms, s)
+                       : matmul<32>(a, ld_a, b, ld_b, a_scales, b_scales, M, N, g, sms, s);
+}

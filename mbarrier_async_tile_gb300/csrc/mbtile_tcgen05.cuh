@@ -1,0 +1,102 @@
+// PTX wrappers of the fifth-generation tensor instructions and their memory.
+#pragma once
+
+#include <stdint.h>
+
+namespace mbt {
+namespace {
+
+// `columns` (a power of two from 32 on) of tensor memory; a whole warp calls it.  The
+// address is written to shared memory at `to`.
+__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// An arrival on the mbarrier once every tensor instruction of this thread so far is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Shared-memory matrices as the tensor instructions' descriptors.  K-major rows of 128
+// bytes with the 128-byte swizzle, eight rows 1024 bytes after the last eight:
+__device__ __forceinline__ uint64_t desc_swizzled(uint32_t addr) {
+    return (2ull << 61) | (1ull << 46) | (64ull << 32) | (1ull << 16) | ((addr & 0x3ffffu) >> 4);
+}
+// and rows of 16 bytes one after the other, without a swizzle (scale tiles):
+__device__ __forceinline__ uint64_t desc_rows16(uint32_t addr) {
+    return (1ull << 46) | (8ull << 32) | ((addr & 0x3ffffu) >> 4);
+}
+
+// 32 rows of 16 bytes into four columns of tensor memory, the same in each 32 lanes.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t to, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
+}
+
+// d (+)= (a sa) (b sb)^T, 64 elements of K in 4 bits; a scale for 16 or 32 of them.
+template <int BLOCK>
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        bool add) {
+    if constexpr (BLOCK == 16)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))
+            : "memory");
+}
+
+// The instruction descriptor: e2m1 operands, both K-major, rows x columns of d, scales in
+// e4m3 (BLOCK 16) or as powers of two; without the scales' byte (bits 4 and 29).
+template <int BLOCK>
+__host__ __device__ constexpr uint32_t mx4_idesc(int rows, int columns) {
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(columns >> 3) << 17) | ((BLOCK == 32 ? 1u : 0u) << 23) |
+           (static_cast<uint32_t>(rows >> 7) << 27);
+}
+
+// 32 lanes x 16 columns, a lane's in its 16 registers; a whole warp calls it.  (With the
+// wait in the same statement: nothing may use the registers before it.)
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&f)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+#pragma unroll
+    for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(r[k]);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster's CTAs; what they wrote before is seen after.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 t;\n\tmapa.shared::cluster.u32 t, %1, %2;\n\tld.shared::cluster.f32 %0, [t];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+}  // namespace
+}  // namespace mbt

@@ -13,6 +13,7 @@
 
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "mbtile.h"
 
@@ -386,6 +387,139 @@ PyObject *adamw(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return r;
 }
 
+// Scales of an M x K matrix in 4-bit floats, tiled.
+std::vector<int64_t> mx4_scales_shape(int64_t M, int64_t K, long block) {
+    return {(M + 127) / 128, (K / block + 3) / 4, 512};
+}
+
+const float *tensor_scale(PyObject *o, at::Device device) {
+    if (!given(o)) return nullptr;
+    const at::Tensor &t = tensor(o, "tensor_scale");
+    if (t.numel() != 1) bad("tensor_scale", "must hold one element");
+    return static_cast<const float *>(dense_f32(t, "tensor_scale", t.sizes(), device));
+}
+
+// An Mx4 from its parts: q, scales, tensor scale.
+struct Mx4Parts {
+    at::Device device;
+    int64_t rows, K, ld;
+    const uint8_t *q, *scales;
+    const float *ts;
+    Mx4Parts(PyObject *const *a, long block, const char *name) : device(at::kCPU) {
+        const at::Tensor &t = input(a[0], name);
+        if (t.scalar_type() != at::kByte) bad(name, "must hold uint8 codes");
+        device = t.device();
+        rows = t.size(0);
+        K = 2 * t.size(1);
+        if (K % 32 != 0 || (block != 16 && block != 32)) bad(name, "must have a multiple of 32 columns and blocks of 16 or 32");
+        ld = ::rows(t, name, rows, K / 2, at::kByte, device);
+        q = static_cast<const uint8_t *>(t.data_ptr());
+        const at::Tensor &s = tensor(a[1], "scales");
+        if (s.scalar_type() != at::kByte) bad("scales", "must be uint8");
+        scales = static_cast<const uint8_t *>(dense(s, "scales", mx4_scales_shape(rows, K, block), device));
+        ts = tensor_scale(a[2], device);
+        if (ts && block != 16) bad("tensor_scale", "goes with blocks of 16");
+    }
+};
+
+at::ScalarType type_of(long code) {
+    return code == MBT_F16 ? at::kHalf : code == MBT_F32 ? at::kFloat : at::kBFloat16;
+}
+
+// (x, tensor_scale, block, q, scales) -> (q, scales)
+PyObject *mx4_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arity(n, 5)) return nullptr;
+    const long block = PyLong_AsLong(a[2]);
+    if (PyErr_Occurred()) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const at::Tensor &x = input(a[0], "x");
+        const at::ScalarType type = x.scalar_type();
+        if (!is_wide(type)) bad("x", "has an unsupported dtype");
+        const at::Device device = x.device();
+        const int64_t M = x.size(0), K = x.size(1);
+        if (K % 32 != 0) bad("x", "must have a multiple of 32 columns");
+        void *stream = stream_of(device);
+        const int64_t ld_x = rows(x, "x", M, K, type, device);
+        const float *ts = tensor_scale(a[1], device);
+        if (ts && block != 16) bad("tensor_scale", "goes with blocks of 16");
+        const auto shape = mx4_scales_shape(M, K, block);
+        at::Tensor q, s;
+        int64_t ld_q = 0;
+        if (given(a[3])) {
+            q = tensor(a[3], "q");
+            ld_q = rows(q, "q", M, K / 2, at::kByte, device);
+        } else {
+            q = empty({M, K / 2}, at::kByte, device);
+        }
+        if (given(a[4])) {
+            s = tensor(a[4], "scales");
+            if (s.scalar_type() != at::kByte) bad("scales", "must be uint8");
+            dense(s, "scales", shape, device);
+        } else {
+            s = empty(shape, at::kByte, device);
+        }
+        if (!check(tile_mx4_quantize(x.data_ptr(), ts, static_cast<uint8_t *>(q.data_ptr()),
+                                     static_cast<uint8_t *>(s.data_ptr()), M, K, ld_x, ld_q, static_cast<int>(block),
+                                     code_of(type), stream),
+                   "tile_mx4_quantize"))
+            return nullptr;
+        written(q);
+        written(s);
+        return Py_BuildValue("(NN)", wrap(q), wrap(s));
+    });
+}
+
+// (q, scales, tensor_scale, block, out, out_code) -> out
+PyObject *mx4_dequantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arity(n, 6)) return nullptr;
+    const long block = PyLong_AsLong(a[3]), code = PyLong_AsLong(a[5]);
+    if (PyErr_Occurred()) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Mx4Parts m(a, block, "q");
+        void *stream = stream_of(m.device);
+        at::Tensor out;
+        int64_t ld_out = 0;
+        if (given(a[4])) {
+            out = tensor(a[4], "out");
+            ld_out = rows(out, "out", m.rows, m.K, type_of(code), m.device);
+        } else {
+            out = empty({m.rows, m.K}, type_of(code), m.device);
+        }
+        if (!check(tile_mx4_dequantize(m.q, m.scales, m.ts, out.data_ptr(), m.rows, m.K, m.ld, ld_out,
+                                       static_cast<int>(block), static_cast<int>(code), stream),
+                   "tile_mx4_dequantize"))
+            return nullptr;
+        written(out);
+        return THPVariable_Wrap(out);
+    });
+}
+
+// (a's q, scales, tensor_scale, b's q, scales, tensor_scale, block, out, out_code) -> out
+PyObject *mx4_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arity(n, 9)) return nullptr;
+    const long block = PyLong_AsLong(a[6]), code = PyLong_AsLong(a[8]);
+    if (PyErr_Occurred()) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Mx4Parts l(a, block, "a"), r(a + 3, block, "b");
+        if (l.K != r.K || l.device != r.device) throw BadArgument("a and b must have the same number of columns and device");
+        void *stream = stream_of(l.device);
+        at::Tensor out;
+        int64_t ld_out = 0;
+        if (given(a[7])) {
+            out = tensor(a[7], "out");
+            ld_out = rows(out, "out", l.rows, r.rows, type_of(code), l.device);
+        } else {
+            out = empty({l.rows, r.rows}, type_of(code), l.device);
+        }
+        if (!check(tile_mx4_matmul(l.q, l.scales, l.ts, r.q, r.scales, r.ts, out.data_ptr(), l.rows, r.rows, l.K, l.ld,
+                                   r.ld, ld_out, static_cast<int>(block), static_cast<int>(code), stream),
+                   "tile_mx4_matmul"))
+            return nullptr;
+        written(out);
+        return THPVariable_Wrap(out);
+    });
+}
+
 PyObject *set_error(PyObject *, PyObject *type) {
     Py_XSETREF(g_mbt_error, Py_NewRef(type));
     return Py_NewRef(Py_None);
@@ -396,6 +530,9 @@ PyMethodDef methods[] = {
     {"rmsnorm_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rmsnorm_backward)), METH_FASTCALL, nullptr},
     {"w4_matvec", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(w4_matvec)), METH_FASTCALL, nullptr},
     {"adamw", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adamw)), METH_FASTCALL, nullptr},
+    {"mx4_quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx4_quantize)), METH_FASTCALL, nullptr},
+    {"mx4_dequantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx4_dequantize)), METH_FASTCALL, nullptr},
+    {"mx4_matmul", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx4_matmul)), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

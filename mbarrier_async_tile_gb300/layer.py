@@ -124,6 +124,70 @@ def tile_w4_matvec(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor,
                  -1 if out_dtype is None else DTYPE_CODE[out_dtype])
 
 
+class Mx4(NamedTuple):
+    """A matrix in microscaled 4-bit floats (see include/mbtile.h for the formats).
+
+    ``q``: uint8, M x K / 2, two e2m1 codes a byte, even columns in the low halves.
+    ``scales``: uint8, one for each ``block`` columns of a row, in tiles of 128 rows
+    by four blocks (ceil(M / 128) x ceil(K / block / 4) x 512): e4m3 with blocks of
+    16, exponents of two plus 127 with blocks of 32.  ``tensor_scale``: with blocks of
+    16, an fp32 device scalar that multiplies every value (None: 1)."""
+    q: torch.Tensor
+    scales: torch.Tensor
+    tensor_scale: torch.Tensor | None = None
+    block: int = 16
+
+
+def tile_mx4_quantize(x: torch.Tensor, *, block: int = 16, tensor_scale: torch.Tensor | None = None,
+                      q: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None) -> Mx4:
+    """``x`` (M x K, fp16, bf16 or fp32, K a multiple of 32) in 4-bit floats: a block's
+    scale from its largest magnitude, each element rounded to the nearest code.
+
+    ``tensor_scale``: with blocks of 16, what the scales are relative to; the largest
+    magnitude of x divided by 448 * 6 uses their whole range.  ``q``, ``scales``:
+    tensors to write.  The result holds ``tensor_scale`` itself, not a copy."""
+    if block not in (16, 32):
+        raise ValueError("block must be 16 or 32")
+    q, scales = _call("mx4_quantize", stream, x, tensor_scale, block, q, scales)
+    return Mx4(q, scales, tensor_scale, block)
+
+
+def _mx4(m, name: str) -> Mx4:
+    if not isinstance(m, Mx4) or m.block not in (16, 32):
+        raise ValueError(f"{name} must be an Mx4 with blocks of 16 or 32")
+    return m
+
+
+def _out_code(out, dtype, default) -> int:
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dtype not in DTYPE_CODE or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out must be an fp16, bf16 or fp32 tensor, of the type asked for")
+        return DTYPE_CODE[out.dtype]
+    dtype = default if dtype is None else dtype
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported output type {dtype}")
+    return DTYPE_CODE[dtype]
+
+
+def tile_mx4_dequantize(m: Mx4, *, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """The values that ``m`` stands for, M x K of ``dtype`` (fp16, bf16 or fp32; default bf16)."""
+    m = _mx4(m, "m")
+    return _call("mx4_dequantize", stream, m.q, m.scales, m.tensor_scale, m.block, out,
+                 _out_code(out, dtype, torch.bfloat16))
+
+
+def tile_mx4_matmul(a: Mx4, b: Mx4, *, out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                    stream=None) -> torch.Tensor:
+    """out[m, n] = sum_k a[m, k] b[n, k], summed in fp32: M x N of ``out_dtype`` (fp16,
+    bf16 or fp32; default bf16) from an M x K and an N x K matrix with blocks of one size."""
+    a, b = _mx4(a, "a"), _mx4(b, "b")
+    if a.block != b.block:
+        raise ValueError("a and b must have blocks of one size")
+    return _call("mx4_matmul", stream, a.q, a.scales, a.tensor_scale, b.q, b.scales, b.tensor_scale, a.block, out,
+                 _out_code(out, out_dtype, torch.bfloat16))
+
+
 class _AdamwTensor(ctypes.Structure):
     """Mirror of ``mbt_adamw_tensor`` in include/mbtile.h."""
     _fields_ = [(name, ctypes.c_void_p) for name in ("param", "grad", "exp_avg", "exp_avg_sq",
