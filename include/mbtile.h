@@ -33,7 +33,8 @@
  *     allocates device memory in two places only: the host-buffer forms'
  *     staging pool, and the workspace it keeps per (device, stream) for row
  *     and column sums called without a workspace of the caller's, for
- *     tile_rmsnorm_backward with dweight and for tile_w4_matvec (see
+ *     tile_rmsnorm_backward with dweight, for tile_w4_matvec and for
+ *     tile_grad_norm (see
  *     tile_rowsum; allocated in stream order with cudaMallocAsync on the
  *     first such call on a stream, freed by tile_workspace_release).  Besides
  *     those it keeps per-device caches (SM count, shared-memory limit, the
@@ -681,6 +682,36 @@ typedef struct mbt_adamw_tensor {
 int tile_adamw(const mbt_adamw_tensor *tensors, int64_t count, int param_dtype, int grad_dtype,
                int state_dtype, int64_t step, double lr, double beta1, double beta2, double eps,
                double weight_decay, const float *grad_scale, uint32_t seed, void *stream);
+
+/*
+ * tile_grad_norm -- the 2-norm of all elements of many tensors together, and the factor
+ * that clips it:
+ *   *norm  = |gs| sqrt(sum g^2)          gs = *grad_scale (DEVICE pointer; NULL: 1)
+ *   *scale = gs min(1, max_norm / (*norm + eps))
+ *   grads         HOST array of count descriptors, read during the call; fp16, bf16 and
+ *                 fp32 tensors in any mixture, each dense, aligned to its elements.
+ *                 Empty ones are allowed.
+ *   norm, scale   DEVICE pointers to one fp32 each; scale optional.  *scale is what
+ *                 tile_adamw and tile_grad_scale take: gs, the inverse of a loss scale for
+ *                 example, and the clipping in one.  max_norm INFINITY: gs alone.
+ * Squares are added in fp32 and, from thread to thread, in 64 bits, in a fixed order; the
+ * norm is right wherever fp32 holds it.  An infinity among the elements gives a norm of
+ * infinity and a factor of 0, a NaN makes both NaN.  Takes tickets and scratch of the
+ * library's workspace for (device, stream), see tile_rowsum (MBT_ERR_WORKSPACE where it
+ * would have to grow in a capture).
+ */
+typedef struct mbt_grad {
+    void *grad;
+    int64_t n;                 /* elements */
+    int32_t dtype;
+    int32_t reserved;          /* 0 */
+} mbt_grad;
+int tile_grad_norm(const mbt_grad *grads, int64_t count, const float *grad_scale, float max_norm,
+                   float eps, float *norm, float *scale, void *stream);
+
+/* tile_grad_scale -- g = g * *scale in place over such tensors (scale: DEVICE pointer),
+ * in fp32, rounded to the tensor's type.  No two of them may overlap (MBT_ERR_ARG). */
+int tile_grad_scale(const mbt_grad *grads, int64_t count, const float *scale, void *stream);
 
 /*
  * Matrices in microscaled 4-bit floats: M x K codes of four bits (e2m1: sign, two bits

@@ -28,7 +28,8 @@ __all__ = [
     "tile_workspace_release", "tile_read_checksum",
     "tile_status", "tile_plan", "tile_plan_device", "tile_device_info", "tile_strerror",
     "tile_stage_image",
-    "E4M3", "RmsNorm", "AdamwTensors", "Mx4", "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul",
+    "E4M3", "RmsNorm", "AdamwTensors", "GradNorm", "Mx4", "tile_clip_grads", "tile_grad_norm",
+    "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul",
     "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw",
 ]
 
@@ -163,6 +164,8 @@ def _load():
         lib.tile_mx4_matmul.argtypes = [vp] * 7 + [i64] * 6 + [i32] * 2 + [vp]
         lib.tile_mx4_scale_bytes.argtypes = [i64, i64, i32]
         lib.tile_mx4_scale_bytes.restype = i64
+        lib.tile_grad_norm.argtypes = [vp, i64, vp, f32, f32, vp, vp, vp]
+        lib.tile_grad_scale.argtypes = [vp, i64, vp, vp]
         lib.tile_adamw.argtypes = ([vp, i64, i32, i32, i32, i64] + [f64] * 5 +
                                    [vp, ctypes.c_uint32, vp])
         for name in ("tile_copy", "tile_copy_ex", "tile_rowsum", "tile_rowsum_ex",
@@ -173,7 +176,8 @@ def _load():
                      "tile_host_release", "tile_workspace_release", "tile_read_checksum",
                      "tile_colsum", "tile_colsum_ex", "tile_colsum_workspace_bytes",
                      "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw",
-                     "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul"):
+                     "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul",
+                     "tile_grad_norm", "tile_grad_scale"):
             getattr(lib, name).restype = ctypes.c_int
         _C = lib
         return lib
@@ -568,5 +572,5 @@ def tile_read_checksum(buf: torch.Tensor, out: torch.Tensor | None = None,
     return out
 
 
-from .layer import (E4M3, AdamwTensors, Mx4, RmsNorm, tile_adamw, tile_mx4_dequantize,  # noqa: E402
-                    tile_mx4_matmul, tile_mx4_quantize, tile_rmsnorm, tile_rmsnorm_backward, tile_w4_matvec)
+from .layer import (E4M3, AdamwTensors, GradNorm, Mx4, RmsNorm, tile_adamw, tile_clip_grads,  # noqa: E402
+                    tile_grad_norm, tile_mx4_dequantize, tile_mx4_matmul, tile_mx4_quantize, tile_rmsnorm, tile_rmsnorm_backward, tile_w4_matvec)

@@ -1,0 +1,404 @@
+// tile_grad_norm and tile_grad_scale: the norm of all elements of many tensors, the
+// factor that clips it, and the product with a factor in place.
+//
+//   norm = |gs| (sum g^2)^(1/2)      scale = gs min(1, max_norm / (norm + eps))
+//
+// The norm reads every byte once, the product reads and writes it: device memory bounds
+// both.  A launch takes a table of tensors as a kernel parameter.  The tensors' 16-byte
+// vectors are cut into chunks of kGradVecs a thread, the chunks dealt to a grid of whole
+// CTAs per SM in spans, so that a CTA finds its first tensor once and steps to the next;
+// what lies before a tensor's first aligned vector and behind its last (at most 7 elements
+// each) goes with its first chunk.
+//
+// A thread sums squares in fp32.  Where a chunk's sum leaves 2^-100 .. 2^100, in which
+// squares neither overflow nor lose their last bits, it takes the chunk again in 64
+// bits, so that the norm is right wherever fp32 holds it.  CTAs and threads are added in
+// 64 bits in a fixed order, by the CTA that finishes last.
+#include <algorithm>
+#include <memory>
+#include <new>
+
+#include "mbtile_elem.cuh"
+#include "mbtile_layer.h"
+#include "mbtile_ptx.cuh"
+
+namespace mbt {
+namespace {
+
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;                          // 16-byte vectors of a thread and chunk
+constexpr int kGradChunk = kGradThreads * kGradVecs;  // vectors
+constexpr int kGradCtas = 6;                          // per SM
+// A launch's parameters hold at most 32764 bytes; few tensors take the small table,
+// whose launch has less to send.
+constexpr int kGradSmallTable = 32;
+constexpr int kGradLargeTable = 1500;
+
+struct GradTensor {
+    char *p;
+    int64_t n;
+};
+
+struct GradArgs {
+    int32_t count;
+    int32_t last;              // the call's last launch: sums all partials
+    int64_t per;               // chunks a CTA
+    double *partial;           // of this launch's CTAs; the call's first are `before` earlier
+    int64_t before;
+    int32_t *ticket, *clear;
+    int64_t clear_n;
+    const float *grad_scale;
+    float *norm, *scale;
+    float max_norm, eps;
+};
+
+template <int TABLE>
+struct GradTable {
+    GradArgs a;
+    GradTensor t[TABLE];
+    uint32_t end[TABLE];       // chunks up to and with tensor k
+    uint8_t type[TABLE];
+};
+
+// A tensor's aligned vectors, and the elements before and behind them.
+struct GradSpan {
+    char *vec;
+    int64_t vecs;
+    int head, tail;            // elements
+};
+
+__host__ __device__ inline GradSpan grad_span(char *p, int64_t n, int es) {
+    GradSpan s;
+    const int64_t off = static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / es;
+    s.head = static_cast<int>(off < n ? off : n);
+    s.vec = p + s.head * es;
+    s.vecs = (n - s.head) * es / 16;
+    s.tail = static_cast<int>((n - s.head) - s.vecs * (16 / es));
+    return s;
+}
+
+inline int64_t grad_chunks(const void *p, int64_t n, int es) {
+    const GradSpan s = grad_span(static_cast<char *>(const_cast<void *>(p)), n, es);
+    return s.vecs > kGradChunk ? (s.vecs + kGradChunk - 1) / kGradChunk : 1;
+}
+
+template <int DT>
+__device__ __forceinline__ float squares(const uint4 &v) {
+    constexpr int V = Elem<DT>::kVec;
+    float f[V];
+    unpack<DT>(v, f);
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < V; e += 2) s[0] += f[e] * f[e], s[1] += f[e + 1] * f[e + 1];
+    return s[0] + s[1];
+}
+
+// The sum of a chunk's squares by this thread, in 64 bits (read once more: hardly ever done).
+__device__ __noinline__ double wide_squares(const char *vec, int64_t first, int64_t vecs, int type) {
+    const int n = type == MBT_F32 ? 4 : 8;
+    double sum = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < kGradVecs; ++i) {
+        const int64_t at = first + i * kGradThreads;
+#pragma unroll 1
+        for (int e = 0; e < n && at < vecs; ++e) {
+            const double f = load_any(vec, type, at * n + e);
+            sum += f * f;
+        }
+    }
+    return sum;
+}
+
+// The sum of a chunk's squares by this thread, and whether any element is not zero.
+template <int DT>
+__device__ __forceinline__ float chunk_squares(const uint4 (&v)[kGradVecs], bool &any) {
+    float s = 0.f;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < kGradVecs; ++k) {
+        s += squares<DT>(v[k]);
+        bits |= v[k].x | v[k].y | v[k].z | v[k].w;
+    }
+    any = (bits & (DT == MBT_F32 ? 0x7fffffffu : 0x7fff7fffu)) != 0;
+    return s;
+}
+
+// The tensor of chunk c, from tensor k on (end[k - 1] <= c).
+template <int TABLE>
+__device__ __forceinline__ int grad_find(const GradTable<TABLE> &g, uint32_t c, int k) {
+    int lo = k, hi = g.a.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (g.end[mid] > c)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+// The sum over the CTA, in thread 0.
+__device__ __forceinline__ double block_sum(double v, double *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kGradThreads / 32; ++k) v += red[k];
+    return v;
+}
+
+template <int TABLE>
+__global__ void __launch_bounds__(kGradThreads, kGradCtas)
+    mbt_grad_norm_kernel(const __grid_constant__ GradTable<TABLE> g) {
+    __shared__ double red[kGradThreads / 32];
+    __shared__ int is_last;
+    const GradArgs &a = g.a;
+    const uint32_t chunks = a.count ? g.end[a.count - 1] : 0;
+    const int64_t c0 = blockIdx.x * a.per, c1 = min(c0 + a.per, static_cast<int64_t>(chunks));
+    float sum = 0.f;
+    double wide = 0.0;
+    int k = c0 < c1 ? grad_find<TABLE>(g, static_cast<uint32_t>(c0), 0) : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t c = c0; c < c1; ++c) {
+        while (g.end[k] <= c) ++k;
+        const int type = g.type[k], es = type == MBT_F32 ? 4 : 2;
+        const GradSpan s = grad_span(g.t[k].p, g.t[k].n, es);
+        const int64_t chunk = c - (k ? g.end[k - 1] : 0u), first = chunk * kGradChunk + threadIdx.x;
+        uint4 v[kGradVecs];
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int64_t at = first + i * kGradThreads;
+            v[i] = at < s.vecs ? __ldg(reinterpret_cast<const uint4 *>(s.vec) + at) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        bool any;
+        const float sq = type == MBT_F32    ? chunk_squares<MBT_F32>(v, any)
+                         : type == MBT_BF16 ? chunk_squares<MBT_BF16>(v, any)
+                                            : chunk_squares<MBT_F16>(v, any);
+        if (sq > 0x1p-100f && sq < 0x1p100f)
+            sum += sq;
+        else if (any)
+            wide += wide_squares(s.vec, first, s.vecs, type);
+        if (chunk == 0 && static_cast<int>(threadIdx.x) < s.head + s.tail) {
+            const int i = threadIdx.x;
+            const float f = load_any(g.t[k].p, type, i < s.head ? i : g.t[k].n - s.tail + i - s.head);
+            wide += static_cast<double>(f) * f;
+        }
+    }
+    const double mine = block_sum(wide + static_cast<double>(sum), red);
+    if (threadIdx.x == 0) a.partial[blockIdx.x] = mine;
+    if (!a.last) return;
+    // the library's other set of tickets is cleared for the next call
+    if (blockIdx.x == 0)
+        for (int64_t i = threadIdx.x; i < a.clear_n; i += kGradThreads) a.clear[i] = 0;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        is_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!is_last) return;
+    double all = 0.0;
+    const double *from = a.partial - a.before;
+    for (int64_t i = threadIdx.x; i < a.before + gridDim.x; i += kGradThreads) all += __ldcg(from + i);
+    all = block_sum(all, red);
+    if (threadIdx.x != 0) return;
+    *a.ticket = 0;             // for a replay of this launch
+    const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+    const float norm = static_cast<float>(sqrt(all) * fabs(static_cast<double>(gs)));
+    *a.norm = norm;
+    if (a.scale) {
+        const float clip = isinf(a.max_norm) ? 1.f : __fdiv_rn(a.max_norm, norm + a.eps);
+        *a.scale = clip >= 1.f ? gs : gs * clip;       // (a NaN norm gives a NaN factor)
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 times(const uint4 &v, float by) {
+    float f[Elem<DT>::kVec];
+    unpack<DT>(v, f);
+#pragma unroll
+    for (int e = 0; e < Elem<DT>::kVec; ++e) f[e] *= by;
+    return pack<DT>(f);
+}
+
+template <int TABLE>
+__global__ void __launch_bounds__(kGradThreads, kGradCtas)
+    mbt_grad_scale_kernel(const __grid_constant__ GradTable<TABLE> g) {
+    const GradArgs &a = g.a;
+    const uint32_t chunks = a.count ? g.end[a.count - 1] : 0;
+    const int64_t c0 = blockIdx.x * a.per, c1 = min(c0 + a.per, static_cast<int64_t>(chunks));
+    int k = c0 < c1 ? grad_find<TABLE>(g, static_cast<uint32_t>(c1 - 1), 0) : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float by = *a.scale;
+    // from the span's end: what the norm's kernel has read last is still in L2
+    for (int64_t c = c1 - 1; c >= c0; --c) {
+        while (k > 0 && g.end[k - 1] > c) --k;
+        const int type = g.type[k], es = type == MBT_F32 ? 4 : 2;
+        const GradSpan s = grad_span(g.t[k].p, g.t[k].n, es);
+        const int64_t chunk = c - (k ? g.end[k - 1] : 0u), first = chunk * kGradChunk + threadIdx.x;
+        uint4 *p = reinterpret_cast<uint4 *>(s.vec);
+        uint4 v[kGradVecs];
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int64_t at = first + i * kGradThreads;
+            if (at < s.vecs) v[i] = p[at];
+        }
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int64_t at = first + i * kGradThreads;
+            if (at >= s.vecs) continue;
+            p[at] = type == MBT_F32 ? times<MBT_F32>(v[i], by) : type == MBT_BF16 ? times<MBT_BF16>(v[i], by)
+                                                                                  : times<MBT_F16>(v[i], by);
+        }
+        if (chunk == 0 && static_cast<int>(threadIdx.x) < s.head + s.tail) {
+            const int i = threadIdx.x;
+            const int64_t at = i < s.head ? i : g.t[k].n - s.tail + i - s.head;
+            store_any(g.t[k].p, type, at, load_any(g.t[k].p, type, at) * by);
+        }
+    }
+}
+
+int es_of(int dtype) { return dtype == MBT_F32 ? 4 : 2; }
+
+int check_grads(const mbt_grad *grads, int64_t count) {
+    if (count < 0 || (count > 0 && grads == nullptr)) return MBT_ERR_ARG;
+    for (int64_t k = 0; k < count; ++k) {
+        const mbt_grad &t = grads[k];
+        if (t.n < 0 || t.n > (int64_t{1} << 40) || t.dtype < MBT_F16 || t.dtype > MBT_F32) return MBT_ERR_ARG;
+        if (t.n == 0) continue;
+        if (!t.grad) return MBT_ERR_ARG;
+        if (reinterpret_cast<uintptr_t>(t.grad) % static_cast<uintptr_t>(es_of(t.dtype)) != 0) return MBT_ERR_ALIGN;
+    }
+    return MBT_OK;
+}
+
+// Whether no two tensors share a byte.
+bool apart(const mbt_grad *grads, int64_t count, bool *known) {
+    struct Range {
+        uintptr_t from, to;
+    };
+    const std::unique_ptr<Range[]> r(new (std::nothrow) Range[static_cast<size_t>(count)]);
+    *known = r != nullptr;
+    if (!r) return false;
+    int64_t n = 0;
+    for (int64_t k = 0; k < count; ++k) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(grads[k].grad);
+        if (grads[k].n > 0) r[n++] = {p, p + static_cast<uintptr_t>(grads[k].n * es_of(grads[k].dtype))};
+    }
+    std::sort(r.get(), r.get() + n, [](const Range &x, const Range &y) { return x.from < y.from; });
+    for (int64_t k = 1; k < n; ++k)
+        if (r[k].from < r[k - 1].to) return false;
+    return true;
+}
+
+// Fills the table with tensors from *k on; chunks in it.
+template <int TABLE>
+int64_t fill_table(const mbt_grad *grads, int64_t count, int64_t *k, GradTable<TABLE> *g) {
+    int64_t chunks = 0;
+    int n = 0;
+    for (; *k < count && n < TABLE; ++*k) {
+        const mbt_grad &t = grads[*k];
+        if (t.n == 0) continue;
+        const int64_t c = grad_chunks(t.grad, t.n, es_of(t.dtype));
+        if (chunks + c > 0x7fffffff) break;
+        chunks += c;
+        g->t[n] = {static_cast<char *>(t.grad), t.n};
+        g->end[n] = static_cast<uint32_t>(chunks);
+        g->type[n] = static_cast<uint8_t>(t.dtype);
+        ++n;
+    }
+    g->a.count = n;
+    return chunks;
+}
+
+// CTAs and chunks of each.
+int grid_of(int64_t chunks, int sms, int64_t *per) {
+    *per = std::max<int64_t>(1, (chunks + static_cast<int64_t>(kGradCtas) * sms - 1) / (static_cast<int64_t>(kGradCtas) * sms));
+    return static_cast<int>(std::max<int64_t>(1, (chunks + *per - 1) / *per));
+}
+
+template <int TABLE>
+int run_norm(const mbt_grad *grads, int64_t count, GradArgs a, int sms, cudaStream_t s) {
+    // launches of the call, and its CTAs in all
+    GradTable<TABLE> g;
+    int64_t launches = 0, ctas = 0;
+    for (int64_t k = 0; k < count || launches == 0; ++launches) ctas += grid_of(fill_table(grads, count, &k, &g), sms, &a.per);
+    WorkspaceHold hold;
+    int rc = hold.take(s, 1, static_cast<size_t>(ctas) * 8);
+    if (rc != MBT_OK) return rc;
+    float *partial = nullptr;
+    hold.sums(&a.ticket, &a.clear, &a.clear_n, &partial);
+    double *const all = reinterpret_cast<double *>(partial);
+    int64_t k = 0;
+    for (int64_t l = 0; l < launches; ++l) {
+        g.a = a;
+        g.a.partial = all + a.before;
+        g.a.last = l + 1 == launches;
+        const int grid = grid_of(fill_table(grads, count, &k, &g), sms, &g.a.per);
+        if (launch_grid(mbt_grad_norm_kernel<TABLE>, dim3(static_cast<unsigned>(grid)), kGradThreads, s, g) != cudaSuccess)
+            return MBT_ERR_CUDA;
+        a.before += grid;
+    }
+    return MBT_OK;
+}
+
+template <int TABLE>
+int run_scale(const mbt_grad *grads, int64_t count, const GradArgs &a, int sms, cudaStream_t s) {
+    GradTable<TABLE> g;
+    g.a = a;
+    for (int64_t k = 0; k < count;) {
+        const int64_t chunks = fill_table(grads, count, &k, &g);
+        if (chunks == 0) break;
+        const int grid = grid_of(chunks, sms, &g.a.per);
+        if (launch_grid(mbt_grad_scale_kernel<TABLE>, dim3(static_cast<unsigned>(grid)), kGradThreads, s, g) != cudaSuccess)
+            return MBT_ERR_CUDA;
+    }
+    return MBT_OK;
+}
+
+}  // namespace
+}  // namespace mbt
+
+extern "C" int tile_grad_norm(const mbt_grad *grads, int64_t count, const float *grad_scale, float max_norm, float eps,
+                              float *norm, float *scale, void *stream) {
+    using namespace mbt;
+    int rc = check_grads(grads, count);
+    if (rc != MBT_OK) return rc;
+    if (!norm || !(max_norm >= 0.f) || !(eps >= 0.f)) return MBT_ERR_ARG;
+    for (const void *p : {static_cast<const void *>(grad_scale), static_cast<const void *>(norm), static_cast<const void *>(scale)})
+        if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return MBT_ERR_ALIGN;
+    int sms = 0, optin = 0;
+    rc = device_limits(&sms, &optin);
+    if (rc != MBT_OK) return rc;
+    GradArgs a{};
+    a.grad_scale = grad_scale;
+    a.norm = norm;
+    a.scale = scale;
+    a.max_norm = max_norm;
+    a.eps = eps;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return count <= kGradSmallTable ? run_norm<kGradSmallTable>(grads, count, a, sms, s)
+                                    : run_norm<kGradLargeTable>(grads, count, a, sms, s);
+}
+
+extern "C" int tile_grad_scale(const mbt_grad *grads, int64_t count, const float *scale, void *stream) {
+    using namespace mbt;
+    int rc = check_grads(grads, count);
+    if (rc != MBT_OK) return rc;
+    if (count == 0) return MBT_OK;
+    if (!scale) return MBT_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(scale) % 4 != 0) return MBT_ERR_ALIGN;
+    bool known = false;
+    if (!apart(grads, count, &known)) return known ? MBT_ERR_ARG : MBT_ERR_CUDA;
+    int sms = 0, optin = 0;
+    rc = device_limits(&sms, &optin);
+    if (rc != MBT_OK) return rc;
+    GradArgs a{};
+    a.scale = const_cast<float *>(scale);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return count <= kGradSmallTable ? run_scale<kGradSmallTable>(grads, count, a, sms, s)
+                                    : run_scale<kGradLargeTable>(grads, count, a, sms, s);
+}

@@ -520,6 +520,65 @@ PyObject *mx4_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// One fp32 element: the caller's tensor, or a new one.
+at::Tensor scalar(PyObject *o, const char *name, at::Device device) {
+    if (!given(o)) return empty({}, at::kFloat, device);
+    const at::Tensor &t = tensor(o, name);
+    if (t.numel() != 1) bad(name, "must hold one element");
+    dense_f32(t, name, t.sizes(), device);
+    return t;
+}
+
+// (grads, grad_scale, max_norm, eps, norm, scale, in_place) -> (norm, scale)
+PyObject *grad_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    double most, eps;
+    if (!arity(n, 7) || !number(a[2], &most) || !number(a[3], &eps)) return nullptr;
+    const int in_place = PyObject_IsTrue(a[6]);
+    if (in_place < 0) return nullptr;
+    PyObject *grads = PySequence_Fast(a[0], "grads must be a sequence of tensors");
+    if (!grads) return nullptr;
+    PyObject *r = guarded([&]() -> PyObject * {
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(grads);
+        at::Device device(at::kCUDA, 0);
+        if (count) {
+            device = tensor(PySequence_Fast_GET_ITEM(grads, 0), "grads").device();
+            if (!device.is_cuda()) bad("grads", "must be CUDA tensors");
+        } else {
+            device.set_index(c10::cuda::current_device());
+        }
+        std::vector<mbt_grad> list(static_cast<size_t>(count));
+        for (Py_ssize_t k = 0; k < count; ++k) {
+            const at::Tensor &g = tensor(PySequence_Fast_GET_ITEM(grads, k), "grads");
+            if (!is_wide(g.scalar_type()) || g.device() != device || g.layout() != at::kStrided ||
+                !(g.is_contiguous() || g.is_non_overlapping_and_dense()))
+                throw BadArgument("grads[" + std::to_string(k) + "] must be a dense fp16, bf16 or fp32 tensor on the first one's device");
+            list[static_cast<size_t>(k)] = {g.data_ptr(), g.numel(), code_of(g.scalar_type()), 0};
+        }
+        void *stream = stream_of(device);
+        const float *gs = nullptr;
+        at::Tensor factor;
+        if (given(a[1])) {
+            factor = scalar(a[1], "grad_scale", device);
+            gs = static_cast<const float *>(factor.data_ptr());
+        }
+        const at::Tensor norm = scalar(a[4], "norm", device), scale = scalar(a[5], "scale", device);
+        float *to = static_cast<float *>(scale.data_ptr());
+        if (!check(tile_grad_norm(list.data(), count, gs, static_cast<float>(most), static_cast<float>(eps),
+                                  static_cast<float *>(norm.data_ptr()), to, stream),
+                   "tile_grad_norm"))
+            return nullptr;
+        written(norm);
+        written(scale);
+        if (in_place) {
+            if (!check(tile_grad_scale(list.data(), count, to, stream), "tile_grad_scale")) return nullptr;
+            for (Py_ssize_t k = 0; k < count; ++k) written(tensor(PySequence_Fast_GET_ITEM(grads, k), "grads"));
+        }
+        return Py_BuildValue("(NN)", wrap(norm), wrap(scale));
+    });
+    Py_DECREF(grads);
+    return r;
+}
+
 PyObject *set_error(PyObject *, PyObject *type) {
     Py_XSETREF(g_mbt_error, Py_NewRef(type));
     return Py_NewRef(Py_None);
@@ -533,6 +592,7 @@ PyMethodDef methods[] = {
     {"mx4_quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx4_quantize)), METH_FASTCALL, nullptr},
     {"mx4_dequantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx4_dequantize)), METH_FASTCALL, nullptr},
     {"mx4_matmul", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx4_matmul)), METH_FASTCALL, nullptr},
+    {"grad_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grad_norm)), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

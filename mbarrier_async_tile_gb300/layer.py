@@ -262,3 +262,28 @@ def tile_adamw(tensors: AdamwTensors, grads, *, step: int, lr: float, beta1: flo
     _call("adamw", stream, tensors._address, tensors.sizes, tensors.device.index or 0, DTYPE_CODE[tensors.dtype],
           _CODE[tensors.state_dtype], grads, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed,
           tensors._written, ctypes.addressof(tensors._addresses))
+
+
+class GradNorm(NamedTuple):
+    """Results of :func:`tile_grad_norm` and :func:`tile_clip_grads`, fp32 device scalars."""
+    norm: torch.Tensor
+    scale: torch.Tensor
+
+
+def tile_grad_norm(grads, *, max_norm: float | None = None, eps: float = 1e-6, grad_scale: torch.Tensor | None = None,
+                   norm: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None) -> GradNorm:
+    """norm = |grad_scale| sqrt(sum of all squares); scale = grad_scale min(1, max_norm / (norm + eps)).
+
+    ``grads``: dense CUDA tensors on one device, fp16, bf16 and fp32 in any mixture.
+    ``grad_scale``: optional fp32 device scalar that the gradients are yet to be
+    multiplied by (None: 1).  ``scale`` is the factor for :func:`tile_adamw`'s
+    ``grad_scale``; without ``max_norm`` it is this call's ``grad_scale``."""
+    return GradNorm(*_call("grad_norm", stream, grads, grad_scale, float("inf") if max_norm is None else max_norm, eps,
+                           norm, scale, False))
+
+
+def tile_clip_grads(grads, max_norm: float, *, eps: float = 1e-6, grad_scale: torch.Tensor | None = None,
+                    norm: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None) -> GradNorm:
+    """:func:`tile_grad_norm`, and every gradient multiplied by ``scale`` in place.  No
+    two of the tensors may overlap."""
+    return GradNorm(*_call("grad_norm", stream, grads, grad_scale, max_norm, eps, norm, scale, True))
