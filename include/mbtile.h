@@ -33,8 +33,8 @@
  *     allocates device memory in two places only: the host-buffer forms'
  *     staging pool, and the workspace it keeps per (device, stream) for row
  *     and column sums called without a workspace of the caller's, for
- *     tile_rmsnorm_backward with dweight, for tile_w4_matvec and for
- *     tile_grad_norm (see
+ *     tile_rmsnorm_backward and tile_layernorm_backward with dweight (or
+ *     dbias), for tile_w4_matvec and for tile_grad_norm (see
  *     tile_rowsum; allocated in stream order with cudaMallocAsync on the
  *     first such call on a stream, freed by tile_workspace_release).  Besides
  *     those it keeps per-device caches (SM count, shared-memory limit, the
@@ -604,6 +604,39 @@ int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd, cons
                           const void *dresidual, void *dx, float *dweight, int64_t M, int64_t N,
                           int64_t ld_dy, int64_t ld_h, int64_t ld_dres, int64_t ld_dx, int dtype,
                           int weight_dtype, float weight_offset, void *stream);
+
+/*
+ * tile_layernorm -- layer norm of each row, with the residual's addition:
+ *   h[i][j] = x[i][j] + residual[i][j]
+ *   mean[i] = mean_j h[i][j]
+ *   rstd[i] = 1 / sqrt(mean_j (h[i][j] - mean[i])^2 + eps)
+ *   out[i][j] = (h[i][j] - mean[i]) * rstd[i] * (weight[j] + weight_offset) + bias[j]
+ * in fp32, each output rounded once (out does not see residual_out's rounding).  As
+ * tile_rmsnorm, with these additions:
+ *   bias          optional, N elements of weight_dtype; goes with a weight (MBT_ERR_ARG).
+ *   quant         as there; with MBT_QUANT_ROW the scale is of the row's largest |y|.
+ *   mean, rstd    fp32[M] each, always written (tile_layernorm_backward reads them).
+ * N = 0 writes mean = 0 and rstd = 1 / sqrt(eps) only (and the smallest scale of a row).
+ */
+int tile_layernorm(const void *x, const void *residual, const void *weight, const void *bias,
+                   void *out, void *residual_out, float *scales, float *mean, float *rstd,
+                   int64_t M, int64_t N, int64_t ld_x, int64_t ld_res, int64_t ld_out,
+                   int64_t ld_res_out, int dtype, int weight_dtype, int quant, float eps,
+                   float weight_offset, void *stream);
+
+/*
+ * tile_layernorm_backward -- gradient of tile_layernorm at h, from dy and the forward
+ * call's mean and rstd.  With xh = (h - mean) rstd and g = dy (weight + weight_offset):
+ *   dx[i][j] = rstd[i] (g[i][j] - mean_j(g) - xh[i][j] mean_j(g xh)) + dresidual[i][j]
+ *   dweight[j] = sum_i dy[i][j] xh[i][j]        dbias[j] = sum_i dy[i][j]
+ * Arguments, order of sums and workspace as in tile_rmsnorm_backward; dweight and dbias
+ * are optional each, fp32[N], overwritten.  M = 0 zeroes both; N = 0 does nothing.
+ */
+int tile_layernorm_backward(const void *dy, const void *h, const float *mean, const float *rstd,
+                            const void *weight, const void *dresidual, void *dx, float *dweight,
+                            float *dbias, int64_t M, int64_t N, int64_t ld_dy, int64_t ld_h,
+                            int64_t ld_dres, int64_t ld_dx, int dtype, int weight_dtype,
+                            float weight_offset, void *stream);
 
 /*
  * tile_w4_matvec -- products of a few rows with a matrix in 4 bits:

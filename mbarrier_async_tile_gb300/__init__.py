@@ -28,7 +28,8 @@ __all__ = [
     "tile_workspace_release", "tile_read_checksum",
     "tile_status", "tile_plan", "tile_plan_device", "tile_device_info", "tile_strerror",
     "tile_stage_image",
-    "E4M3", "RmsNorm", "AdamwTensors", "GradNorm", "Mx4", "tile_clip_grads", "tile_grad_norm",
+    "E4M3", "RmsNorm", "AdamwTensors", "GradNorm", "LayerNorm", "Mx4", "tile_clip_grads", "tile_grad_norm",
+    "tile_layernorm", "tile_layernorm_backward",
     "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul",
     "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw",
 ]
@@ -164,6 +165,8 @@ def _load():
         lib.tile_mx4_matmul.argtypes = [vp] * 7 + [i64] * 6 + [i32] * 2 + [vp]
         lib.tile_mx4_scale_bytes.argtypes = [i64, i64, i32]
         lib.tile_mx4_scale_bytes.restype = i64
+        lib.tile_layernorm.argtypes = [vp] * 9 + [i64] * 6 + [i32] * 3 + [f32, f32, vp]
+        lib.tile_layernorm_backward.argtypes = [vp] * 9 + [i64] * 6 + [i32] * 2 + [f32, vp]
         lib.tile_grad_norm.argtypes = [vp, i64, vp, f32, f32, vp, vp, vp]
         lib.tile_grad_scale.argtypes = [vp, i64, vp, vp]
         lib.tile_adamw.argtypes = ([vp, i64, i32, i32, i32, i64] + [f64] * 5 +
@@ -177,7 +180,7 @@ def _load():
                      "tile_colsum", "tile_colsum_ex", "tile_colsum_workspace_bytes",
                      "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw",
                      "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul",
-                     "tile_grad_norm", "tile_grad_scale"):
+                     "tile_grad_norm", "tile_grad_scale", "tile_layernorm", "tile_layernorm_backward"):
             getattr(lib, name).restype = ctypes.c_int
         _C = lib
         return lib
@@ -572,5 +575,6 @@ def tile_read_checksum(buf: torch.Tensor, out: torch.Tensor | None = None,
     return out
 
 
-from .layer import (E4M3, AdamwTensors, GradNorm, Mx4, RmsNorm, tile_adamw, tile_clip_grads,  # noqa: E402
-                    tile_grad_norm, tile_mx4_dequantize, tile_mx4_matmul, tile_mx4_quantize, tile_rmsnorm, tile_rmsnorm_backward, tile_w4_matvec)
+from .layer import (E4M3, AdamwTensors, GradNorm, LayerNorm, Mx4, RmsNorm, tile_adamw, tile_clip_grads,  # noqa: E402
+                    tile_grad_norm, tile_layernorm, tile_layernorm_backward, tile_mx4_dequantize, tile_mx4_matmul,
+                    tile_mx4_quantize, tile_rmsnorm, tile_rmsnorm_backward, tile_w4_matvec)

@@ -25,7 +25,8 @@ LIB_PATH = os.path.join(PKG_DIR, "libmbtile.so")
 SOURCES = ["mbtile_kernels.cu", "mbtile_host.cpp", "mbtile_noalloc.cu", "mbtile_hostio.cpp",
            "mbtile_probe.cu", "mbtile_norm.cu", "mbtile_norm_f16.cu", "mbtile_norm_bf16.cu",
            "mbtile_norm_f32.cu", "mbtile_w4.cu", "mbtile_adamw.cu", "mbtile_mx4.cu",
-           "mbtile_mx4_matmul.cu", "mbtile_grad.cu"]
+           "mbtile_mx4_matmul.cu", "mbtile_grad.cu", "mbtile_layernorm.cu", "mbtile_layernorm_f16.cu",
+           "mbtile_layernorm_bf16.cu", "mbtile_layernorm_f32.cu"]
 BINDING = "mbtile_torch.cpp"
 BINDING_PATH = os.path.join(PKG_DIR, "_mbtile_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_STAMP = os.path.join(BUILD_DIR, "binding.stamp")   # which torch the binding was built for

@@ -26,6 +26,34 @@ struct NormGradArgs {
     float woff;
 };
 
+// Layer norm: as above, with a mean, a bias and its gradient.
+struct LayerNormArgs {
+    const void *x, *res, *w, *b;
+    void *out, *res_out;
+    float *scales, *mean, *rstd;
+    int64_t M, N, ld_x, ld_res, ld_out, ld_res_out;
+    int64_t groups;
+    int32_t wdt, quant;      // wdt: of weight and bias
+    float eps, woff;
+};
+
+struct LayerNormGradArgs {
+    const void *dy, *h, *w, *dres;
+    const float *mean, *rstd;
+    void *dx;
+    float *dw, *db, *partial;   // partial: [2][splits][N], dw's and then db's
+    int64_t M, N, ld_dy, ld_h, ld_dres, ld_dx;
+    int64_t splits;
+    int32_t wdt;
+    float woff;
+};
+
+// (mbtile_layernorm_f16.cu, _bf16.cu, _f32.cu)  The calls after their checks, M > 0 (the gradient: N > 0 too).
+template <int DT>
+cudaError_t layernorm_forward(const LayerNormArgs &a, cudaStream_t s);
+template <int DT>
+int layernorm_backward(const LayerNormGradArgs &a, cudaStream_t s);
+
 // (mbtile_norm_f16.cu, _bf16.cu, _f32.cu)  The calls after their checks, M > 0 (the gradient: N > 0 too).
 template <int DT>
 cudaError_t norm_forward(const NormArgs &a, cudaStream_t s);

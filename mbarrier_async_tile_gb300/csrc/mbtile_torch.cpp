@@ -269,6 +269,155 @@ PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (x, weight, bias, residual, eps, weight_offset, quant, out, scales, residual_out, mean, rstd)
+// -> (out, scales, residual_out, mean, rstd); quant as in mbtile.h
+PyObject *layernorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    double eps, offset;
+    if (!arity(n, 12) || !number(a[4], &eps) || !number(a[5], &offset)) return nullptr;
+    const long quant = PyLong_AsLong(a[6]);
+    if (quant == -1 && PyErr_Occurred()) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const at::Tensor &x = input(a[0], "x");
+        const at::ScalarType type = x.scalar_type();
+        if (!is_wide(type)) bad("x", "has an unsupported dtype");
+        const at::Device device = x.device();
+        const int64_t M = x.size(0), N = x.size(1);
+        void *stream = stream_of(device);
+        const int64_t ld_x = rows(x, "x", M, N, type, device);
+        int64_t ld_res = 0, ld_ro = 0, ld_out = 0;
+        void *w = nullptr, *b = nullptr, *res = nullptr, *ro = nullptr, *sc = nullptr;
+        int wcode = 0;
+        at::Tensor out, scales, residual_out;
+        if (given(a[1])) {
+            const at::Tensor &t = tensor(a[1], "weight");
+            if (!is_wide(t.scalar_type())) bad("weight", "has an unsupported dtype");
+            w = dense(t, "weight", {N}, device);
+            wcode = code_of(t.scalar_type());
+        }
+        if (given(a[2])) {
+            const at::Tensor &t = tensor(a[2], "bias");
+            if (!given(a[1])) bad("bias", "needs a weight");
+            if (code_of(t.scalar_type()) != wcode) bad("bias", "must have weight's type");
+            b = dense(t, "bias", {N}, device);
+        }
+        if (given(a[3])) {
+            const at::Tensor &t = tensor(a[3], "residual");
+            ld_res = rows(t, "residual", M, N, type, device);
+            res = t.data_ptr();
+            if (given(a[9])) {
+                residual_out = tensor(a[9], "residual_out");
+                ld_ro = rows(residual_out, "residual_out", M, N, type, device);
+            } else {
+                residual_out = empty({M, N}, type, device);
+            }
+            ro = residual_out.data_ptr();
+        } else if (given(a[9])) {
+            bad("residual_out", "needs a residual");
+        }
+        const bool quantised = quant != MBT_QUANT_NONE;
+        const at::ScalarType out_type = quantised ? at::kFloat8_e4m3fn : type;
+        if (given(a[7])) {
+            out = tensor(a[7], "out");
+            ld_out = rows(out, "out", M, N, out_type, device);
+        } else {
+            out = empty({M, N}, out_type, device);
+        }
+        if (quantised) {
+            const int64_t groups = quant ? (N + quant - 1) / quant : 1;
+            if (given(a[8])) {
+                scales = tensor(a[8], "scales");
+                sc = dense_f32(scales, "scales", {M, groups}, device);
+            } else {
+                scales = empty({M, groups}, at::kFloat, device);
+                sc = scales.data_ptr();
+            }
+        } else if (given(a[8])) {
+            bad("scales", "need quant");
+        }
+        at::Tensor stats[2];
+        for (int k = 0; k < 2; ++k) {
+            const char *name = k ? "rstd" : "mean";
+            if (given(a[10 + k])) {
+                stats[k] = tensor(a[10 + k], name);
+                dense_f32(stats[k], name, {M}, device);
+            } else {
+                stats[k] = empty({M}, at::kFloat, device);
+            }
+        }
+        if (!check(tile_layernorm(x.data_ptr(), res, w, b, out.data_ptr(), ro, static_cast<float *>(sc),
+                                  static_cast<float *>(stats[0].data_ptr()), static_cast<float *>(stats[1].data_ptr()),
+                                  M, N, ld_x, ld_res, ld_out, ld_ro, code_of(type), wcode, static_cast<int>(quant),
+                                  static_cast<float>(eps), static_cast<float>(offset), stream),
+                   "tile_layernorm"))
+            return nullptr;
+        for (const at::Tensor *t : {&out, &scales, &residual_out, &stats[0], &stats[1]}) written(*t);
+        return Py_BuildValue("(NNNNN)", wrap(out), wrap(scales), wrap(residual_out), wrap(stats[0]), wrap(stats[1]));
+    });
+}
+
+// (dy, h, mean, rstd, weight, dresidual, weight_offset, bias, dx, dweight, dbias) -> (dx, dweight, dbias)
+PyObject *layernorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    double offset;
+    if (!arity(n, 11) || !number(a[6], &offset)) return nullptr;
+    const int bias = PyObject_IsTrue(a[7]);
+    if (bias < 0) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const at::Tensor &h = input(a[1], "h");
+        const at::ScalarType type = h.scalar_type();
+        if (!is_wide(type)) bad("h", "has an unsupported dtype");
+        const at::Device device = h.device();
+        const int64_t M = h.size(0), N = h.size(1);
+        void *stream = stream_of(device);
+        const int64_t ld_h = rows(h, "h", M, N, type, device);
+        const at::Tensor &dy = tensor(a[0], "dy");
+        const int64_t ld_dy = rows(dy, "dy", M, N, type, device);
+        const void *mean = dense_f32(tensor(a[2], "mean"), "mean", {M}, device);
+        const void *rstd = dense_f32(tensor(a[3], "rstd"), "rstd", {M}, device);
+        void *w = nullptr, *res = nullptr;
+        int64_t ld_res = 0, ld_dx = 0;
+        int wcode = 0;
+        at::Tensor dx, dw, db;
+        if (given(a[4])) {
+            const at::Tensor &t = tensor(a[4], "weight");
+            if (!is_wide(t.scalar_type())) bad("weight", "has an unsupported dtype");
+            w = dense(t, "weight", {N}, device);
+            wcode = code_of(t.scalar_type());
+        }
+        if (given(a[9])) {
+            dw = tensor(a[9], "dweight");
+            dense_f32(dw, "dweight", {N}, device);
+        } else if (given(a[4])) {
+            dw = empty({N}, at::kFloat, device);
+        }
+        if (given(a[10])) {
+            db = tensor(a[10], "dbias");
+            dense_f32(db, "dbias", {N}, device);
+        } else if (given(a[4]) && bias) {
+            db = empty({N}, at::kFloat, device);
+        }
+        if (given(a[5])) {
+            const at::Tensor &t = tensor(a[5], "dresidual");
+            ld_res = rows(t, "dresidual", M, N, type, device);
+            res = t.data_ptr();
+        }
+        if (given(a[8])) {
+            dx = tensor(a[8], "dx");
+            ld_dx = rows(dx, "dx", M, N, type, device);
+        } else {
+            dx = empty({M, N}, type, device);
+        }
+        if (!check(tile_layernorm_backward(dy.data_ptr(), h.data_ptr(), static_cast<const float *>(mean),
+                                           static_cast<const float *>(rstd), w, res, dx.data_ptr(),
+                                           dw.defined() ? static_cast<float *>(dw.data_ptr()) : nullptr,
+                                           db.defined() ? static_cast<float *>(db.data_ptr()) : nullptr, M, N, ld_dy,
+                                           ld_h, ld_res, ld_dx, code_of(type), wcode, static_cast<float>(offset), stream),
+                   "tile_layernorm_backward"))
+            return nullptr;
+        for (const at::Tensor *t : {&dx, &dw, &db}) written(*t);
+        return Py_BuildValue("(NNN)", wrap(dx), wrap(dw), wrap(db));
+    });
+}
+
 // (x, q, scales, zeros, group, x_scales, out, out_code) -> out; out_code: of a new
 // out's type, -1 for x's (bf16 for e4m3)
 PyObject *w4_matvec(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -593,6 +742,8 @@ PyMethodDef methods[] = {
     {"mx4_dequantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx4_dequantize)), METH_FASTCALL, nullptr},
     {"mx4_matmul", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx4_matmul)), METH_FASTCALL, nullptr},
     {"grad_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grad_norm)), METH_FASTCALL, nullptr},
+    {"layernorm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(layernorm)), METH_FASTCALL, nullptr},
+    {"layernorm_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(layernorm_backward)), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -107,6 +107,44 @@ def tile_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     return _call("rmsnorm_backward", stream, dy, h, rstd, weight, dresidual, weight_offset, dx, dweight)
 
 
+class LayerNorm(NamedTuple):
+    """Results of :func:`tile_layernorm`; ``scales`` and ``residual`` may be None."""
+    out: torch.Tensor
+    scales: torch.Tensor | None
+    residual: torch.Tensor | None
+    mean: torch.Tensor
+    rstd: torch.Tensor
+
+
+def tile_layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                   residual: torch.Tensor | None = None, *, eps: float = 1e-5, weight_offset: float = 0.0,
+                   quant: int | None = None, out: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                   residual_out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                   rstd: torch.Tensor | None = None, stream=None) -> LayerNorm:
+    """h = x + residual; out = (h - mean(h)) / sqrt(var(h) + eps) * (weight + weight_offset) + bias, row by row.
+
+    Arguments as in :func:`tile_rmsnorm`.  ``bias``: N elements of weight's type (only
+    with a weight).  ``mean``, ``rstd``: fp32[M] for :func:`tile_layernorm_backward`."""
+    if quant not in _QUANT:
+        raise ValueError("quant must be None, 0, 32, 64 or 128")
+    return LayerNorm(*_call("layernorm", stream, x, weight, bias, residual, eps, weight_offset, _QUANT[quant], out,
+                            scales, residual_out, mean, rstd))
+
+
+def tile_layernorm_backward(dy: torch.Tensor, h: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                            weight: torch.Tensor | None = None, *, dresidual: torch.Tensor | None = None,
+                            weight_offset: float = 0.0, bias: bool = True, dx: torch.Tensor | None = None,
+                            dweight: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                            stream=None) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor | None]:
+    """Gradient of :func:`tile_layernorm` at ``h`` (its ``residual``, or x without one):
+    ``(dx, dweight, dbias)``, dx in h's type and the gradient of x and residual alike,
+    dweight and dbias fp32[N] (None without a weight, dbias also with ``bias`` false,
+    unless one to write is given).  ``dresidual`` and ``dx`` as in
+    :func:`tile_rmsnorm_backward`."""
+    return _call("layernorm_backward", stream, dy, h, mean, rstd, weight, dresidual, weight_offset, bias, dx, dweight,
+                 dbias)
+
+
 def tile_w4_matvec(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor,
                    zeros: torch.Tensor | None = None, *, group: int = 128,
                    x_scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
