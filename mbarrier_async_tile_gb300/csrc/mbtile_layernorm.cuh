@@ -345,6 +345,482 @@ __global__ void __launch_bounds__(32 * kFinishRows) mbt_layernorm_finish_kernel(
     out[j] = pair_sum(all);
 }
 
+cudaError_t launch_ln_finish(const LayerNormGradArgs &a, cudaStream_t s) {
+    return launch_grid(mbt_layernorm_finish_kernel, dim3(static_cast<unsigned>((a.N + 31) / 32), 2), 32 * kFinishRows, s, a);
+}
+
+// ---------------------------------------------------------------------------
+// Rows through the ring in shared memory
+// ---------------------------------------------------------------------------
+// As in mbtile_norm.cuh, with a bias beside the weight, or gradients of both, in each
+// thread's registers.  What they do not hold is read where it is used: weights of another
+// type than 16-bit rows', and those of long fp32 rows, from global memory (FLY); in the
+// gradient's second pass rows of more than two (fp32: four) chunks a thread from their
+// stage once more.
+
+// Sums of a and b over a row's tpr threads, in all of them; red and turn as in row_reduce.
+__device__ __forceinline__ void row_reduce_two(float &a, float &b, int tpr, float *red, int turn) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o >= tpr) continue;
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (tpr <= 32) return;
+    const int warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp & ~(warps - 1), lane = threadIdx.x & 31;
+    float *s = red + turn * 64;
+    if (lane == 0) s[warp] = a, s[32 + warp] = b;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + first / warps), "r"(tpr) : "memory");
+    a = lane < warps ? s[first + lane] : 0.f;
+    b = lane < warps ? s[32 + first + lane] : 0.f;
+    a = warp_sum(a);
+    b = warp_sum(b);
+}
+
+// A thread's weights or biases (`none` where there are none), C chunks of them, 0 past
+// the row: packed in x's type, or read each time.
+template <int DT, int C, bool PART, bool FLY>
+struct RowVector {
+    static constexpr int V = Elem<DT>::kVec;
+    uint4 raw[FLY ? 1 : C];
+    const void *from;
+    int64_t N;
+    int mode, type, t, tpr, off;
+    float none, add;
+    __device__ __forceinline__ void fetch(int c, float offset, float (&v)[V]) const {
+        const int64_t p = static_cast<int64_t>(t + c * tpr) * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = p < N + off ? none : 0.f;
+        if (from && p < N + off) load_weight<DT>(from, mode, type, offset, p, off, N, v);
+    }
+    __device__ __forceinline__ RowVector(const void *src, int how, int wdt, float absent, float offset, int thread,
+                                         int threads, int lead, int64_t columns)
+        : from(src), N(columns), mode(how), type(wdt), t(thread), tpr(threads), off(lead), none(absent),
+          add(src ? offset : 0.f) {
+        if constexpr (!FLY)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (!PART && from) {
+                    const int p = (t + c * tpr) * V;
+                    raw[c] = make_uint4(0, 0, 0, 0);
+                    if (p < N) raw[c] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const typename Elem<DT>::type *>(from) + p));
+                } else {
+                    float v[V];
+                    fetch(c, 0.f, v);
+                    raw[c] = pack<DT>(v);
+                }
+            }
+    }
+    __device__ __forceinline__ void get(int c, uint32_t zero, float (&v)[V]) const {
+        if constexpr (FLY) {
+            fetch(c, add, v);
+        } else {
+            unpack<DT>(again(raw[c], zero), v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += add;
+        }
+    }
+};
+
+struct LayerNormRing {
+    RingArgs r;
+    int32_t bmode;           // the bias's access (the weight's: r.wmode)
+};
+
+template <int DT, int C, bool RES, bool PART, bool FLY>
+__global__ void __launch_bounds__(kRingThreads, 1)
+    mbt_layernorm_backward_kernel(const __grid_constant__ LayerNormGradArgs a, const __grid_constant__ LayerNormRing l) {
+    using T = typename Elem<DT>::type;
+    constexpr int V = Elem<DT>::kVec;
+    constexpr bool HOLD = C * V <= 16;
+    const RingArgs &r = l.r;
+    extern __shared__ __align__(128) unsigned char dyn_smem[];
+    __shared__ __align__(8) RingShared sh;
+    ring_init(sh, r);
+    RingState q(r, smem_u32(dyn_smem), smem_u32(&sh.bars[0]), WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status});
+    q.start(r, a.M);
+    const RingThread<DT, C, PART> th(r, a.M, a.N, q.ring);
+    const RowVector<DT, C, PART, FLY> wt(a.w, r.wmode, a.wdt, 1.f, a.woff, th.t, r.tpr, th.off, a.N);
+    float dw[C][V], db[C][V];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[c][e] = db[c][e] = 0.f;
+    const float inv_n = 1.f / static_cast<float>(a.N);
+    const int64_t rows = static_cast<int64_t>(gridDim.x) * r.rows;   // from one row of a slot to the next
+    T *dx = static_cast<T *>(a.dx) + th.first * a.ld_dx - th.off + th.t * V;
+    const int chunk = r.tpr * V;
+    int turn = 0;
+    float next_mean = 0.f, next_rstd = 0.f;
+    if (th.first < a.M) next_mean = __ldg(a.mean + th.first), next_rstd = __ldg(a.rstd + th.first);
+    const int turns = row_turns(a.M, th.first - th.k % r.unit_rows, rows);
+    const int mine = row_turns(a.M, th.first, rows);
+    for (int n = 0; n < turns; ++n, dx += rows * a.ld_dx) {
+        const uint32_t z1 = r.zero & n, z2 = r.zero & ~n;
+        const float mean = n < mine ? next_mean : 0.f, rstd = n < mine ? next_rstd : 0.f;
+        const int64_t i = th.first + n * rows;
+        if (n + 1 < mine) next_mean = __ldg(a.mean + i + rows), next_rstd = __ldg(a.rstd + i + rows);
+        q.wait();
+        const int have = n < mine && q.alive ? th.count : 0;
+        // chunk c of dy and h, 0 where it is not the row's
+        auto take = [&](int c, uint4 &vy, uint4 &vh) {
+            vy = vh = make_uint4(0, 0, 0, 0);
+            if (c >= have) return;
+            vy = th.chunk(q.stage, 0, c);
+            vh = th.chunk(q.stage, 1, c);
+            if (PART && !th.whole(c)) {
+                th.last_chunk(r, 0, c, i, vy);
+                th.last_chunk(r, 1, c, i, vh);
+                float f[V];
+                unpack<DT>(vy, f);
+                th.mask(c, f);
+                vy = pack<DT>(f);
+                unpack<DT>(vh, f);
+                th.mask(c, f);
+                vh = pack<DT>(f);
+            }
+        };
+        uint4 vy[HOLD ? C : 1], vh[HOLD ? C : 1];
+        if constexpr (HOLD)
+#pragma unroll
+            for (int c = 0; c < C; ++c) take(c, vy[c], vh[c]);
+        float level = 0.f, along = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float dy[V], h[V], w[V];
+            if constexpr (!HOLD) take(c, vy[0], vh[0]);
+            unpack<DT>(vy[HOLD ? c : 0], dy);
+            unpack<DT>(vh[HOLD ? c : 0], h);
+            wt.get(c, z1, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float xh = (h[e] - mean) * rstd, g = dy[e] * w[e];
+                level += g;
+                along += g * xh;
+                dw[c][e] += dy[e] * xh;
+                db[c][e] += dy[e];
+            }
+        }
+        row_reduce_two(level, along, r.tpr, sh.red[0], turn);
+        turn ^= 1;
+        level *= inv_n;
+        along *= inv_n;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (c >= have) continue;
+            uint4 vr = make_uint4(0, 0, 0, 0);
+            if constexpr (RES) {
+                vr = th.chunk(q.stage, 2, c);
+                if (PART && th.tail) th.last_chunk(r, 2, c, i, vr);
+            }
+            float dy[V], h[V], d[V], f[V], w[V];
+            if constexpr (!HOLD) take(c, vy[0], vh[0]);
+            unpack<DT>(again(vy[HOLD ? c : 0], z2), dy);
+            unpack<DT>(again(vh[HOLD ? c : 0], z2), h);
+            wt.get(c, z2, w);
+            if constexpr (RES) unpack<DT>(vr, f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                d[e] = rstd * (dy[e] * w[e] - level - (h[e] - mean) * rstd * along);
+                if constexpr (RES) d[e] += f[e];
+            }
+            th.put(dx + c * chunk, c, d);
+        }
+        q.release(r, a.M);
+    }
+    q.drain(r.stages);
+    if (!a.dw && !a.db) return;
+    // every stage has been read: its memory takes the row slots' sums, dw's and then db's
+    float *slots = reinterpret_cast<float *>(dyn_smem);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        asm volatile("bar.sync 15, %0;" ::"n"(kRingThreads) : "memory");
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int j = (th.t + c * r.tpr) * V + e - th.off;
+                if (j >= 0 && j < a.N) slots[th.k * a.N + j] = which ? db[c][e] : dw[c][e];
+            }
+        asm volatile("bar.sync 15, %0;" ::"n"(kRingThreads) : "memory");
+        for (int j = threadIdx.x; j < a.N; j += kRingThreads) {
+            float sum = slots[j];
+            if (r.rows < 8) {
+                for (int s = 1; s < r.rows; ++s) sum += slots[s * a.N + j];
+            } else {
+                float eight[8] = {};
+                for (int s = 0; s < r.rows; s += 8)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) eight[k] += slots[(s + k) * a.N + j];
+                sum = pair_sum(eight);
+            }
+            a.partial[(static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.N + j] = sum;
+        }
+    }
+}
+
+template <int DT, int C, bool RES, bool Q, bool PART, bool FLY>
+__global__ void __launch_bounds__(kRingThreads, 1)
+    mbt_layernorm_ring_kernel(const __grid_constant__ LayerNormArgs a, const __grid_constant__ LayerNormRing l) {
+    using T = typename Elem<DT>::type;
+    using O = typename std::conditional<Q, uint8_t, T>::type;
+    constexpr int V = Elem<DT>::kVec;
+    const RingArgs &r = l.r;
+    extern __shared__ __align__(128) unsigned char dyn_smem[];
+    __shared__ __align__(8) RingShared sh;
+    ring_init(sh, r);
+    RingState q(r, smem_u32(dyn_smem), smem_u32(&sh.bars[0]), WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status});
+    q.start(r, a.M);
+    const RingThread<DT, C, PART> th(r, a.M, a.N, q.ring);
+    const RowVector<DT, C, PART, FLY> wt(a.w, r.wmode, a.wdt, 1.f, a.woff, th.t, r.tpr, th.off, a.N);
+    const RowVector<DT, C, PART, FLY> bt(a.b, l.bmode, a.wdt, 0.f, 0.f, th.t, r.tpr, th.off, a.N);
+    const float inv_n = 1.f / static_cast<float>(a.N);
+    const int64_t rows = static_cast<int64_t>(gridDim.x) * r.rows;   // from one row of a slot to the next
+    const int64_t out_step = rows * a.ld_out, res_step = rows * a.ld_res_out;
+    O *out = static_cast<O *>(a.out) + th.first * a.ld_out - th.off + th.t * V;
+    T *res = static_cast<T *>(a.res_out) + th.first * a.ld_res_out - th.off + th.t * V;
+    const bool write_res = RES && a.res_out != nullptr;
+    const int chunk = r.tpr * V;
+    int turn = 0;
+    const int turns = row_turns(a.M, th.first - th.k % r.unit_rows, rows);
+    const int mine = row_turns(a.M, th.first, rows);
+    for (int n = 0; n < turns; ++n, out += out_step, res += res_step) {
+        const uint32_t z1 = r.zero & n, z2 = r.zero & ~n;
+        q.wait();
+        const int have = n < mine && q.alive ? th.count : 0;
+        const int64_t i = th.first + n * rows;
+        float h[C][V];
+        {
+            uint4 vx[C], vr[RES ? C : 1];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                vx[c] = make_uint4(0, 0, 0, 0);
+                if constexpr (RES) vr[c] = make_uint4(0, 0, 0, 0);
+                if (c >= have) continue;
+                vx[c] = th.chunk(q.stage, 0, c);
+                if constexpr (RES) vr[c] = th.chunk(q.stage, 1, c);
+            }
+            if (PART && have && th.tail)
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    th.last_chunk(r, 0, c, i, vx[c]);
+                    if constexpr (RES) th.last_chunk(r, 1, c, i, vr[c]);
+                }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                unpack<DT>(vx[c], h[c]);
+                if constexpr (RES) {
+                    float f[V];
+                    unpack<DT>(vr[c], f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) h[c][e] += f[e];
+                }
+            }
+        }
+        q.release(r, a.M);   // the row is in registers now
+        if (PART && have && (th.head || th.tail))
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (!th.whole(c)) th.mask(c, h[c]);
+        float sum = 0.f, ss = 0.f;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum += h[c][e];
+        row_reduce<false>(sum, amax, r.tpr, sh.red[0], turn);
+        turn ^= 1;
+        const float mean = sum * inv_n;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (c < have && write_res) th.put(res + c * chunk, c, h[c]);
+            float part = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                h[c][e] -= mean;                       // from here on the deviation
+                const bool in = !PART || th.whole(c) || (e >= th.lo(c) && e < th.hi(c));
+                part += in ? h[c][e] * h[c][e] : 0.f;
+            }
+            if (c < have) ss += part;
+        }
+        row_reduce<false>(ss, amax, r.tpr, sh.red[0], turn);
+        turn ^= 1;
+        const float rstd = rsqrtf(ss * inv_n + a.eps);
+        if (th.t == 0 && n < mine) {
+            a.mean[i] = mean;
+            a.rstd[i] = rstd;
+        }
+        uint32_t gmax[C];                    // largest magnitude of each chunk's group
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float w[V], b[V];
+            wt.get(c, z1, w);
+            bt.get(c, z2, b);
+            const Pair rr(rstd);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+                const float2 y = fma2(Pair(h[c][e], h[c][e + 1]) * rr, Pair(w[e], w[e + 1]), Pair(b[e], b[e + 1])).get();
+                h[c][e] = y.x, h[c][e + 1] = y.y;
+            }
+            if constexpr (!Q) {
+                if (c < have) th.put(out + c * chunk, c, h[c]);
+            } else {
+                if (PART && !th.whole(c)) th.mask(c, h[c]);
+                gmax[c] = c < have ? magnitude_max(0u, h[c]) : 0u;
+            }
+        }
+        if constexpr (Q) {
+            float scale = 0.f;
+            Divisor by;
+            if (a.quant == 0) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) amax = max(amax, gmax[c]);
+                float none = 0.f;
+                row_reduce<true>(none, amax, r.tpr, sh.red[0], turn);
+                turn ^= 1;
+                scale = group_scale(amax);
+                by = Divisor(scale);
+                if (th.t == 0 && n < mine) a.scales[i] = scale;
+            } else {                         // (rows start at a chunk)
+#pragma unroll
+                for (int o = 1; o < 128 / V; o <<= 1) {
+                    if (o >= a.quant / V) break;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) gmax[c] = max(gmax[c], __shfl_xor_sync(0xffffffffu, gmax[c], o));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (c >= have) continue;
+                if (a.quant > 0) {
+                    scale = group_scale(gmax[c]);
+                    by = Divisor(scale);
+                    const int p = th.t * V + c * chunk;
+                    if (p % a.quant == 0) a.scales[i * a.groups + p / a.quant] = scale;
+                }
+                store_e4m3<V>(out + c * chunk, h[c], by, th.lo(c), th.hi(c));
+            }
+        }
+    }
+    q.drain(r.stages);
+}
+
+template <class K, class A>
+cudaError_t launch_ln_ring(K kernel, const RingPlan &p, int bmode, cudaStream_t s, const A &a) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pipeline(kernel, p.grid, kRingThreads, p.smem, s, a, LayerNormRing{p.r, bmode});
+}
+
+template <int DT, int C, bool PART, bool FLY>
+cudaError_t launch_ln_ring_forward(const RingPlan &p, int bmode, const LayerNormArgs &a, cudaStream_t s) {
+    const bool q = a.quant != MBT_QUANT_NONE;
+    if (a.res)
+        return q ? launch_ln_ring(mbt_layernorm_ring_kernel<DT, C, true, true, PART, FLY>, p, bmode, s, a)
+                 : launch_ln_ring(mbt_layernorm_ring_kernel<DT, C, true, false, PART, FLY>, p, bmode, s, a);
+    return q ? launch_ln_ring(mbt_layernorm_ring_kernel<DT, C, false, true, PART, FLY>, p, bmode, s, a)
+             : launch_ln_ring(mbt_layernorm_ring_kernel<DT, C, false, false, PART, FLY>, p, bmode, s, a);
+}
+
+template <int DT, int C, bool PART, bool FLY>
+cudaError_t launch_ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cudaStream_t s) {
+    return a.dres ? launch_ln_ring(mbt_layernorm_backward_kernel<DT, C, true, PART, FLY>, p, 0, s, a)
+                  : launch_ln_ring(mbt_layernorm_backward_kernel<DT, C, false, PART, FLY>, p, 0, s, a);
+}
+
+// A vector that whole chunks of the rows' type can be read from, or none.
+bool plain_vector(int mode) { return mode == kSameWeight || mode == kNoWeight; }
+
+template <int DT>
+cudaError_t ln_ring_forward(const RingPlan &p, int bmode, const LayerNormArgs &a, cudaStream_t s) {
+    const int c = p.chunks;
+    const bool part = p.part || !plain_vector(p.r.wmode) || !plain_vector(bmode);
+    if constexpr (DT == MBT_F32) {
+        if (c > 5) return launch_ln_ring_forward<DT, 8, true, true>(p, bmode, a, s);
+        if (part)
+            return c <= 4 ? launch_ln_ring_forward<DT, 4, true, false>(p, bmode, a, s)
+                          : launch_ln_ring_forward<DT, 5, true, false>(p, bmode, a, s);
+        return c <= 2   ? launch_ln_ring_forward<DT, 2, false, false>(p, bmode, a, s)
+               : c <= 4 ? launch_ln_ring_forward<DT, 4, false, false>(p, bmode, a, s)
+                        : launch_ln_ring_forward<DT, 5, false, false>(p, bmode, a, s);
+    } else {
+        if (a.w && a.wdt != DT) return launch_ln_ring_forward<DT, 4, true, true>(p, bmode, a, s);
+        if (part)
+            return c <= 2 ? launch_ln_ring_forward<DT, 2, true, false>(p, bmode, a, s)
+                          : launch_ln_ring_forward<DT, 4, true, false>(p, bmode, a, s);
+        return c <= 1   ? launch_ln_ring_forward<DT, 1, false, false>(p, bmode, a, s)
+               : c <= 2 ? launch_ln_ring_forward<DT, 2, false, false>(p, bmode, a, s)
+                        : launch_ln_ring_forward<DT, 4, false, false>(p, bmode, a, s);
+    }
+}
+
+template <int DT>
+cudaError_t ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cudaStream_t s) {
+    const int c = p.chunks;
+    const bool part = p.part || !plain_vector(p.r.wmode);
+    if constexpr (DT == MBT_F32) {
+        if (c > 5) return launch_ln_ring_backward<DT, 8, true, true>(p, a, s);
+        if (part)
+            return c <= 4 ? launch_ln_ring_backward<DT, 4, true, false>(p, a, s)
+                          : launch_ln_ring_backward<DT, 5, true, false>(p, a, s);
+        return c <= 2   ? launch_ln_ring_backward<DT, 2, false, false>(p, a, s)
+               : c <= 4 ? launch_ln_ring_backward<DT, 4, false, false>(p, a, s)
+                        : launch_ln_ring_backward<DT, 5, false, false>(p, a, s);
+    } else {
+        if (a.w && a.wdt != DT) return launch_ln_ring_backward<DT, 4, true, true>(p, a, s);
+        if (part)
+            return c <= 2 ? launch_ln_ring_backward<DT, 2, true, false>(p, a, s)
+                          : launch_ln_ring_backward<DT, 4, true, false>(p, a, s);
+        return c <= 1   ? launch_ln_ring_backward<DT, 1, false, false>(p, a, s)
+               : c <= 2 ? launch_ln_ring_backward<DT, 2, false, false>(p, a, s)
+                        : launch_ln_ring_backward<DT, 4, false, false>(p, a, s);
+    }
+}
+
+// The ring's plan: up to four chunks a thread of 16-bit rows; of fp32 rows up to five, and
+// eight of those too long for that.
+bool ln_ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, int64_t N, int es, int ph, int min_tpr,
+                  int sms, RingPlan *p) {
+    if (es == 2) return ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p);
+    return ring_plan(in, ld, inputs, M, N, es, ph, 5, min_tpr, sms, p) ||
+           ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p);
+}
+
+// The gradient through the ring; *done says whether it applied.
+template <int DT>
+int ln_backward_by_ring(LayerNormGradArgs a, cudaStream_t s, int sms, bool *done) {
+    constexpr int V = Elem<DT>::kVec, es = 16 / V;
+    const int ph = phase_of(a.h, a.ld_h, es);
+    bool same = ph >= 0 && phase_of(a.dy, a.ld_dy, es) == ph && phase_of(a.dx, a.ld_dx, es) == ph;
+    if (a.dres) same = same && phase_of(a.dres, a.ld_dres, es) == ph;
+    const void *in[3] = {a.dy, a.h, a.dres};
+    const int64_t ld[3] = {a.ld_dy, a.ld_h, a.ld_dres};
+    RingPlan p;
+    *done = same && ln_ring_plan(in, ld, a.dres ? 3 : 2, a.M, a.N, es, ph, 8, sms, &p);
+    if (!*done) return MBT_OK;
+    int rc = device_status_word(&p.r.status);
+    if (rc != MBT_OK) return rc;
+    p.r.wmode = weight_mode(a.w, a.wdt, DT);
+    a.splits = p.grid;
+    WorkspaceHold hold;
+    if (a.dw || a.db) {
+        void *scratch = nullptr;
+        rc = hold.scratch(s, static_cast<size_t>(a.splits) * a.N * 8, &scratch);
+        if (rc != MBT_OK) return rc;
+        a.partial = static_cast<float *>(scratch);
+    }
+    cudaError_t e = ln_ring_backward<DT>(p, a, s);
+    if (e == cudaSuccess && (a.dw || a.db)) e = launch_ln_finish(a, s);
+    return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
+}
+
+// Where the ring is faster than a row in registers: as in the root-mean-square norm.
+bool ln_ring_pays(const LayerNormArgs &a, int64_t es, int sms, int phase) {
+    const int64_t row = a.N * es;
+    if (a.M * row < (16ll << 20) || a.M < 4 * sms || row <= 1024) return false;
+    return row > 4096 || !a.res || phase != 0 || a.quant != MBT_QUANT_NONE;
+}
+
 template <int DT, int C>
 cudaError_t launch_ln_forward(const LayerNormVecArgs &va, dim3 grid, int threads, cudaStream_t s) {
     const bool q = va.a.quant != MBT_QUANT_NONE;
@@ -370,6 +846,15 @@ cudaError_t ln_forward_any(const LayerNormArgs &a, cudaStream_t s) {
                (a.quant != MBT_QUANT_NONE || phase_of(a.out, 0, es) == 0) && a.N > 0;
     int sms = 0, optin = 0;
     if (device_limits(&sms, &optin) != MBT_OK) return cudaErrorUnknown;
+    const void *in[2] = {a.x, a.res};
+    const int64_t ld[2] = {a.ld_x, a.ld_res};
+    RingPlan p;
+    if (same && ln_ring_pays(a, es, sms, ph) &&
+        ln_ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, a.quant > 0 ? 32 : 8, sms, &p)) {
+        if (device_status_word(&p.r.status) != MBT_OK) return cudaErrorUnknown;
+        p.r.wmode = weight_mode(a.w, a.wdt, DT);
+        return ln_ring_forward<DT>(p, weight_mode(a.b, a.wdt, DT), a, s);
+    }
     LayerNormVecArgs va{a, 0, 0, 0, a.M > 1 && ph > 0};
     const int64_t chunks = (a.N + (va.phased ? V - 1 : 0) + V - 1) / V;
     if (!same || chunks > 4 * 1024) {
@@ -398,6 +883,9 @@ int ln_backward_any(LayerNormGradArgs a, cudaStream_t s) {
     int sms = 0, smem = 0;
     int rc = device_limits(&sms, &smem);
     if (rc != MBT_OK) return rc;
+    bool done = false;
+    rc = ln_backward_by_ring<DT>(a, s, sms, &done);
+    if (rc != MBT_OK || done) return rc;
     const int64_t cols = (a.N + kColThreads - 1) / kColThreads;
     if (a.dw || a.db) {
         // enough CTAs of 128 columns to fill the device, at least 32 rows each
@@ -410,8 +898,7 @@ int ln_backward_any(LayerNormGradArgs a, cudaStream_t s) {
         a.partial = static_cast<float *>(scratch);
         const dim3 grid(static_cast<unsigned>(cols), static_cast<unsigned>(a.splits));
         cudaError_t e = launch_grid(mbt_layernorm_dw_rows_kernel<DT>, grid, kColThreads, s, a);
-        if (e == cudaSuccess)
-            e = launch_grid(mbt_layernorm_finish_kernel, dim3(static_cast<unsigned>((a.N + 31) / 32), 2), 32 * kFinishRows, s, a);
+        if (e == cudaSuccess) e = launch_ln_finish(a, s);
         if (e != cudaSuccess) return MBT_ERR_CUDA;
     }
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.M, 1 << 20)));
