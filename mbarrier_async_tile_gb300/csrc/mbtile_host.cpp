@@ -1018,6 +1018,20 @@ int encode_bytes_map(CUtensorMap *map, const void *src, int64_t rows, int64_t ro
     return r == CUDA_SUCCESS ? MBT_OK : MBT_ERR_DRIVER;
 }
 
+int encode_scales_map(CUtensorMap *map, const void *src, int64_t row_tiles, int64_t tiles, int box) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    const int rc = encoder(&fn);
+    if (rc != MBT_OK) return rc;
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(tiles), static_cast<cuuint64_t>(row_tiles)};
+    const cuuint64_t strides[2] = {512, static_cast<cuuint64_t>(tiles) * 512};
+    const cuuint32_t boxes[3] = {128, static_cast<cuuint32_t>(box), 1};
+    const cuuint32_t elem_strides[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(src), dims, strides, boxes,
+                          elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MBT_OK : MBT_ERR_DRIVER;
+}
+
 int device_status_word(int32_t **word) {
     static int32_t *words[kMaxDevices];
     int dev = 0;

@@ -64,6 +64,9 @@ int norm_backward(const NormGradArgs &a, cudaStream_t s);
 // bytes apart: box = 128 bytes x box_rows rows, 128-byte swizzle, zero fill.
 int encode_bytes_map(CUtensorMap *map, const void *src, int64_t rows, int64_t row_bytes, int64_t ld,
                      int box_rows);
+// (mbtile_host.cpp)  3-D tiled map over `row_tiles` x `tiles` tiles of 512 bytes, one after
+// the other: box = `box` tiles of a row of tiles, zero fill.
+int encode_scales_map(CUtensorMap *map, const void *src, int64_t row_tiles, int64_t tiles, int box);
 // (mbtile_host.cpp)  Address of the current device's status word, looked up once per device.
 int device_status_word(int32_t **word);
 

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     __shared__ __align__(8) MmShared sh;
     const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 2) tmem_alloc(smem_u32(&sh.tmem), kMmTmem);
+    if (warp == 2) tmem_alloc<1>(smem_u32(&sh.tmem), kMmTmem);
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
@@ -204,14 +204,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     if (m >= left) break;
                     const int s = m * S::kTiles / 4;             // the product's scale tile
                     if (m * S::kTiles % 4 == 0) {
-                        tmem_copy_scales(scols + 4 * s, desc_rows16(sr + 512 * s));
+                        tmem_copy_scales<1>(scols + 4 * s, desc_rows16(sr + 512 * s));
 #pragma unroll
                         for (int c = 0; c < S::kColTiles; ++c)
-                            tmem_copy_scales(ccols + 4 * (s * S::kColTiles + c),
+                            tmem_copy_scales<1>(ccols + 4 * (s * S::kColTiles + c),
                                              desc_rows16(sr + (1 + c) * S::kScaleBytes + 512 * s));
                     }
                     const uint32_t id = BLOCK == 32 ? (m & 1) * 2 : 0;   // the first of the bytes in a scale column
-                    mma_mx4<BLOCK>(d, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s,
+                    mma_mx4<1, BLOCK>(d, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s,
                                    ccols + 4 * s * S::kColTiles, k > k0 || m > 0);
                 }
                 tc_commit(smem_u32(&sh.empty[stage]));
@@ -297,7 +297,267 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             for (uint32_t p = 0; p < 2; ++p) wait_bounded(smem_u32(&sh.full[s]), p, w, false);
     __syncthreads();
     tc_fence_after();
-    if (warp == 2) tmem_free(tmem, kMmTmem);
+    if (warp == 2) tmem_free<1>(tmem, kMmTmem);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: a pair of CTAs on 256 x 256
+// ---------------------------------------------------------------------------
+// The two CTAs of a cluster hold 128 rows each of both operands, and the pair's tensor
+// instructions read both: a byte of shared memory filled from L2 serves twice the products
+// of a 128 x 128 tile, whose rate the L2's was.  Each CTA accumulates its 128 rows by 256
+// columns and needs the scales of its rows and of all columns.  The first CTA's tensor
+// thread issues for both; copies of either CTA count on its barriers.
+//
+// Two accumulators of 256 columns would leave no tensor memory for scales: there is one,
+// and eight epilogue warps take 16-bit results out of it into registers before they
+// store them, so that the next tile's products wait for that alone.
+constexpr int kPairThreads = 384;
+constexpr int kPairCols = 256;
+
+template <int BLOCK>
+struct PairShape {
+    static constexpr int kTiles = kMmStep / BLOCK / 4;        // scale tiles of 128 rows per stage
+    static constexpr int kOperand = kMmRows * kBoxRowBytes;   // of a CTA's part of either operand
+    static constexpr int kScaleBytes = kTiles * 512;
+    static constexpr int kStage = 2 * kOperand + 3 * kScaleBytes;
+    static constexpr int kStageStride = (kStage + kSwizzleAtomBytes - 1) / kSwizzleAtomBytes * kSwizzleAtomBytes;
+    static constexpr int kScaleCols = kTiles * 4 * 3;
+    static constexpr int kStages = 5;
+    static constexpr int kSmem = kStages * kStageStride + kSwizzleAtomBytes;
+    static_assert(kPairCols + kStages * kScaleCols <= kMmTmem && kSmem <= 226 * 1024);
+};
+
+struct PairShared {
+    uint64_t full[kMmMostStages], empty[kMmMostStages], acc_full, acc_empty, drain;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+template <int BLOCK>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    mbt_mx4_pair_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap cols_map,
+                        const __grid_constant__ CUtensorMap row_scales, const __grid_constant__ CUtensorMap col_scales,
+                        const __grid_constant__ Mx4MatArgs a) {
+    using S = PairShape<BLOCK>;
+    extern __shared__ unsigned char dyn_smem[];
+    __shared__ __align__(8) PairShared sh;
+    const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (warp == 2) tmem_alloc<2>(smem_u32(&sh.tmem), kMmTmem);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sh.acc_full), 1);
+        mbar_init(smem_u32(&sh.acc_empty), 16);
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort_flag = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                          // both CTAs' barriers are there
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
+    const int first_tile = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
+    const int tiles = a.tiles_r * a.tiles_c;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    auto fail = [&](int role, uint32_t stage, uint32_t parity) {
+        report_timeout(w, role, stage, parity);
+        *w.abort = 1;
+    };
+    if (warp == 0 && lane == 0) {
+        uint32_t stage = 0, phase = 1;
+        bool alive = true;
+        for (int t = first_tile; t < tiles && alive; t += stride) {
+            int tr, tc;
+            tile_at(a, t, &tr, &tc);
+            for (int k = 0; k < a.steps; ++k) {
+                if (!wait_bounded(smem_u32(&sh.empty[stage]), phase, w, true)) {
+                    fail(0, stage, phase);
+                    alive = false;
+                    break;
+                }
+                const uint32_t full = cluster_address(smem_u32(&sh.full[stage]), 0);
+                const uint32_t at = base + stage * S::kStageStride, sc = at + 2 * S::kOperand;
+                // (boxes past the matrix's end are filled with zeros and count in full)
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[stage]), 2 * S::kStage);
+                tma_load_2d_pair(at, &rows_map, k * kBoxRowBytes, (2 * tr + static_cast<int>(rank)) * kMmRows, full);
+                tma_load_2d_pair(at + S::kOperand, &cols_map, k * kBoxRowBytes, (2 * tc + static_cast<int>(rank)) * kMmRows,
+                                 full);
+                tma_load_3d_pair(sc, &row_scales, 0, k * S::kTiles, 2 * tr + static_cast<int>(rank), full);
+                tma_load_3d_pair(sc + S::kScaleBytes, &col_scales, 0, k * S::kTiles, 2 * tc, full);
+                tma_load_3d_pair(sc + 2 * S::kScaleBytes, &col_scales, 0, k * S::kTiles, 2 * tc + 1, full);
+                if (++stage == S::kStages) stage = 0, phase ^= 1;
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        constexpr uint32_t idesc = mx4_idesc<BLOCK>(2 * kMmRows, kPairCols);
+        uint32_t stage = 0, phase = 0, acc_phase = 1;
+        bool alive = true;
+        for (int t = first_tile; t < tiles && alive; t += stride) {
+            if (!wait_bounded(smem_u32(&sh.acc_empty), acc_phase, w, true)) {
+                fail(2, 0, acc_phase);
+                alive = false;
+                break;
+            }
+            acc_phase ^= 1;
+            tc_fence_after();
+            for (int k = 0; k < a.steps; ++k) {
+                if (!wait_bounded(smem_u32(&sh.full[stage]), phase, w, true)) {
+                    fail(1, stage, phase);
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = base + stage * S::kStageStride, sc = at + 2 * S::kOperand;
+                const uint32_t scols = tmem + kPairCols + stage * S::kScaleCols, ccols = scols + S::kTiles * 4;
+                const int left = static_cast<int>(min(static_cast<int64_t>(4), (a.K - static_cast<int64_t>(k) * kMmStep + 63) / 64));
+                const uint64_t da = desc_swizzled(at), db = desc_swizzled(at + S::kOperand);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    if (m >= left) break;
+                    const int s = m * S::kTiles / 4;             // the product's scale tile
+                    if (m * S::kTiles % 4 == 0) {
+                        tmem_copy_scales<2>(scols + 4 * s, desc_rows16(sc + 512 * s));
+                        tmem_copy_scales<2>(ccols + 8 * s, desc_rows16(sc + S::kScaleBytes + 512 * s));
+                        tmem_copy_scales<2>(ccols + 8 * s + 4, desc_rows16(sc + 2 * S::kScaleBytes + 512 * s));
+                    }
+                    const uint32_t id = BLOCK == 32 ? (m & 1) * 2 : 0;   // the first of the bytes in a scale column
+                    mma_mx4<2, BLOCK>(tmem, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s, ccols + 8 * s,
+                                      k > 0 || m > 0);
+                }
+                tc_commit_pair(smem_u32(&sh.empty[stage]), 3);
+                if (++stage == S::kStages) stage = 0, phase ^= 1;
+            }
+            if (!alive) break;
+            tc_commit_pair(smem_u32(&sh.acc_full), 3);
+        }
+        if (!alive) {                        // what has been issued ends before tensor memory is freed
+            tc_commit_pair(smem_u32(&sh.drain), 1);
+            wait_bounded(smem_u32(&sh.drain), 0, w, false);
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        float alpha = a.ta ? *a.ta : 1.f;
+        if (a.tb) alpha *= *a.tb;
+        const uint32_t acc_empty = cluster_address(smem_u32(&sh.acc_empty), 0);
+        constexpr int kCols = kPairCols / 2;                     // of a warp
+        uint32_t phase = 0;
+        for (int t = first_tile; t < tiles; t += stride) {
+            int tr, tc;
+            tile_at(a, t, &tr, &tc);
+            if (!__all_sync(0xffffffffu, wait_bounded(smem_u32(&sh.acc_full), phase, w, true))) {
+                if (lane == 0) fail(3, 0, phase);
+                break;
+            }
+            phase ^= 1;
+            tc_fence_after();
+            const uint32_t from = tmem + half * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int64_t row = (static_cast<int64_t>(tr) * 2 + rank) * kMmRows + quarter * 32 + lane;
+            const int64_t col0 = static_cast<int64_t>(tc) * kPairCols + half * kCols;
+            const int cols = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(kCols), a.C - col0)));
+            if (a.odt == MBT_F32) {
+#pragma unroll 2
+                for (int c = 0; c < kCols; c += 16) {
+                    float f[16];
+                    __syncwarp();
+                    tmem_load16(from + c, f);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] *= alpha;
+                    if (row < a.R) store16(a, row, col0 + c, f, cols - c);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) cluster_arrive_at(acc_empty);
+            } else {
+                uint4 v[kCols / 8];
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    float f[16], g[2][8];
+                    tmem_load16(from + c, f);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) g[e >> 3][e & 7] = f[e] * alpha;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) v[c / 8 + k] = a.odt == MBT_BF16 ? pack<MBT_BF16>(g[k]) : pack<MBT_F16>(g[k]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) cluster_arrive_at(acc_empty);
+                if (row < a.R) {
+                    uint16_t *p = static_cast<uint16_t *>(a.out) + row * a.ld_out + col0;
+#pragma unroll
+                    for (int c = 0; c < kCols / 8; ++c) {
+                        if (a.vec && 8 * c + 8 <= cols) {
+                            reinterpret_cast<uint4 *>(p)[c] = v[c];
+                        } else {
+                            const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (8 * c + e < cols) p[8 * c + e] = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && rank == 0 && sh.abort_flag)   // copies under way land before the CTAs leave
+        for (int s = 0; s < S::kStages; ++s)
+            for (uint32_t p = 0; p < 2; ++p) wait_bounded(smem_u32(&sh.full[s]), p, w, false);
+    __syncthreads();
+    cluster_sync();                          // nor does a CTA leave while the other may still signal it
+    tc_fence_after();
+    if (warp == 2) tmem_free<2>(tmem, kMmTmem);
+}
+
+template <int BLOCK>
+int launch_pair(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_cols, Mx4MatArgs a, int sms,
+                cudaStream_t stream) {
+    using S = PairShape<BLOCK>;
+    static std::atomic<bool> raised[64];   // per device: the kernel's shared-memory limit is set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MBT_ERR_CUDA;
+    if (dev >= 64 || !raised[dev].load(std::memory_order_relaxed)) {
+        if (cudaFuncSetAttribute(mbt_mx4_pair_kernel<BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
+            cudaSuccess)
+            return MBT_ERR_CUDA;
+        if (dev < 64) raised[dev].store(true, std::memory_order_relaxed);
+    }
+    alignas(64) CUtensorMap maps[4];
+    int rc = encode_bytes_map(&maps[0], rows, a.R, a.K / 2, ld_rows, kMmRows);
+    if (rc == MBT_OK) rc = encode_bytes_map(&maps[1], cols, a.C, a.K / 2, ld_cols, kMmRows);
+    if (rc == MBT_OK) rc = encode_scales_map(&maps[2], a.sr, (a.R + 127) / 128, a.scale_tiles, S::kTiles);
+    if (rc == MBT_OK) rc = encode_scales_map(&maps[3], a.sc, (a.C + 127) / 128, a.scale_tiles, S::kTiles);
+    if (rc != MBT_OK) return rc;
+    a.tiles_r = static_cast<int32_t>((a.R + 2 * kMmRows - 1) / (2 * kMmRows));
+    a.tiles_c = static_cast<int32_t>((a.C + kPairCols - 1) / kPairCols);
+    a.split = 1;
+    const int64_t tiles = static_cast<int64_t>(a.tiles_r) * a.tiles_c;
+    if (tiles > 0x3fffffff) return MBT_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, sms / 2)));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, mbt_mx4_pair_kernel<BLOCK>, maps[0], maps[1], maps[2], maps[3], a) == cudaSuccess
+               ? MBT_OK
+               : MBT_ERR_CUDA;
 }
 
 __global__ void mbt_mx4_zero_kernel(void *out, int dtype, int64_t M, int64_t N, int64_t ld) {
@@ -351,6 +611,9 @@ int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int
                : MBT_ERR_CUDA;
 }
 
+// Whether there are tiles of 256 x 256 for every pair of SMs.
+bool pair_pays(int64_t M, int64_t N, int sms) { return (M + 255) / 256 * ((N + 255) / 256) >= sms / 2; }
+
 template <int BLOCK>
 int matmul(const uint8_t *a_q, int64_t ld_a, const uint8_t *b_q, int64_t ld_b, const uint8_t *as, const uint8_t *bs,
            int64_t M, int64_t N, Mx4MatArgs a, int sms, cudaStream_t s) {
@@ -362,6 +625,7 @@ int matmul(const uint8_t *a_q, int64_t ld_a, const uint8_t *b_q, int64_t ld_b, c
                          : launch_matmul<128, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s);
     }
     a.R = M, a.C = N, a.sr = as, a.sc = bs;
+    if (pair_pays(M, N, sms)) return launch_pair<BLOCK>(a_q, ld_a, b_q, ld_b, a, sms, s);
     return launch_matmul<128, BLOCK, false>(a_q, ld_a, b_q, ld_b, a, sms, s);
 }
 

@@ -1,19 +1,33 @@
 // PTX wrappers of the fifth-generation tensor instructions and their memory.
 #pragma once
 
+#include <cuda.h>
 #include <stdint.h>
 
 namespace mbt {
 namespace {
 
-// `columns` (a power of two from 32 on) of tensor memory; a whole warp calls it.  The
-// address is written to shared memory at `to`.
+// CTAS: 1, or 2 where the CTAs of a pair (cluster ranks 2 k and 2 k + 1) work on one tile.
+// A kernel uses one of the two throughout.
+
+// `columns` (a power of two from 32 on) of tensor memory; a whole warp (of each of the
+// CTAs) calls it.  The address is written to shared memory at `to`.
+template <int CTAS>
 __device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (CTAS == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
 }
+template <int CTAS>
 __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+    if constexpr (CTAS == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -22,6 +36,13 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // An arrival on the mbarrier once every tensor instruction of this thread so far is done.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// The same for a pair's instructions, on the mbarriers at this address in the CTAs of `mask`.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(mask)
+        : "memory");
 }
 
 // Shared-memory matrices as the tensor instructions' descriptors.  K-major rows of 128
@@ -34,28 +55,35 @@ __device__ __forceinline__ uint64_t desc_rows16(uint32_t addr) {
     return (1ull << 46) | (8ull << 32) | ((addr & 0x3ffffu) >> 4);
 }
 
-// 32 rows of 16 bytes into four columns of tensor memory, the same in each 32 lanes.
+// 32 rows of 16 bytes into four columns of tensor memory, the same in each 32 lanes; of a
+// pair, in each CTA from its own shared memory.
+template <int CTAS>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t to, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
+    if constexpr (CTAS == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
 }
 
 // d (+)= (a sa) (b sb)^T, 64 elements of K in 4 bits; a scale for 16 or 32 of them.
-template <int BLOCK>
+#define MBT_MMA_MX4(GROUP, KIND, VEC)                                                                          \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::" GROUP ".kind::" KIND  \
+                 ".block_scale.scale_vec::" VEC " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),              \
+                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))                 \
+                 : "memory")
+template <int CTAS, int BLOCK>
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                         bool add) {
-    if constexpr (BLOCK == 16)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))
-            : "memory");
+    if constexpr (CTAS == 1 && BLOCK == 16)
+        MBT_MMA_MX4("1", "mxf4nvf4", "4X");
+    else if constexpr (CTAS == 1)
+        MBT_MMA_MX4("1", "mxf4", "2X");
+    else if constexpr (BLOCK == 16)
+        MBT_MMA_MX4("2", "mxf4nvf4", "4X");
     else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))
-            : "memory");
+        MBT_MMA_MX4("2", "mxf4", "2X");
 }
+#undef MBT_MMA_MX4
 
 // The instruction descriptor: e2m1 operands, both K-major, rows x columns of d, scales in
 // e4m3 (BLOCK 16) or as powers of two; without the scales' byte (bits 4 and 29).
@@ -88,6 +116,31 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // All threads of the cluster's CTAs; what they wrote before is seen after.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address in CTA `rank` of the cluster that `addr` is in this one.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Bulk tensor copies into this CTA, counted on a barrier of either CTA of its pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
     float v;

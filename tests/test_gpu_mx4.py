@@ -234,3 +234,49 @@ def test_written_tensors_raise_their_version():
     mbt.tile_mx4_quantize(x, q=m.q, scales=m.scales)
     assert out._version > before[0] and m.q._version > before[1]
     assert scale64(m.scales[0, 0, :1], 16).isfinite().all()
+
+
+# 256 x 256 tiles for every pair of SMs, with edges of every kind
+PAIRS = [(2560, 2560), (2500, 2601), (257, 20001), (20001, 300), (2305, 2432), (4097, 2433)]
+
+
+@pytest.mark.parametrize("M,N", PAIRS)
+@pytest.mark.parametrize("K", [32, 96, 1024, 4128])
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_product_by_pairs(M, N, K, block, out):
+    t = 0.03 if block == 16 else None
+    a, va = operand(M, K, block, 40, t, pitch=16)
+    b, vb = operand(N, K, block, 41, t, fill=0x7F if block == 16 and K % 64 == 0 else 0)
+    got = mbt.tile_mx4_matmul(a, b, out_dtype=TYPES[out])
+    check_product(a, va, b, vb, got, K)
+    assert torch.equal(got, mbt.tile_mx4_matmul(a, b, out_dtype=TYPES[out]))
+    assert mbt.tile_status()[0] == 0
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_pairs_are_exact_where_sums_are(block):
+    M, N, K = 2600, 2561, 1120
+    a, va = operand(M, K, block, 42)
+    b, vb = operand(N, K, block, 43)
+    one, two = ((0x38, 0x40) if block == 16 else (127, 128))
+    sa = torch.where(torch.rand(M, K // block, generator=gen(44), device="cuda") < 0.5, one, two).to(torch.uint8)
+    sb = torch.where(torch.rand(N, K // block, generator=gen(45), device="cuda") < 0.5, one, two).to(torch.uint8)
+    a, b = a._replace(scales=tile_scales(sa)), b._replace(scales=tile_scales(sb))
+    want = values64(a.q, sa, block) @ values64(b.q, sb, block).t()
+    assert torch.equal(mbt.tile_mx4_matmul(a, b, out_dtype=torch.float32).double(), want)
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (8, 0), (1, 0), (0, 1), (3, 5)])
+@pytest.mark.parametrize("out", ["f16", "f32"])
+def test_pairs_pitches(pad, offset, out):
+    M, N, K = 2570, 2443, 320
+    a, va = operand(M, K, 16, 46, 1e-3)
+    b, vb = operand(N, K, 16, 47, 1e-2)
+    store = torch.full((M * (N + pad) + offset + 8,), 7.0, device="cuda", dtype=TYPES[out])
+    view = store[offset:offset + M * (N + pad)].view(M, N + pad)[:, :N]
+    mbt.tile_mx4_matmul(a, b, out=view)
+    check_product(a, va, b, vb, view, K)
+    kept = torch.ones_like(store, dtype=torch.bool)
+    kept[offset:offset + M * (N + pad)].view(M, N + pad)[:, :N] = False
+    assert bool((store[kept] == 7).all())
