@@ -101,6 +101,11 @@ __device__ __forceinline__ void store16(const Mx4MatArgs &a, int64_t row, int64_
         if (e < count) store_any(a.out, a.odt, at + e, f[e]);
 }
 
+// wait_bounded() by a whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_bounded(bar, parity, w, true));
+}
+
 struct MmShared {
     uint64_t full[kMmMostStages], empty[kMmMostStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     extern __shared__ unsigned char dyn_smem[];
     __shared__ __align__(8) MmShared sh;
     const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = static_cast<int>(warp_value(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (warp == 2) tmem_alloc<1>(smem_u32(&sh.tmem), kMmTmem);
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = warp_value(sh.tmem);
     const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int first_tile = a.split > 1 ? static_cast<int>(blockIdx.x) / a.split : static_cast<int>(blockIdx.x);
@@ -175,21 +180,21 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 if (++stage == S::kStages) stage = 0, phase ^= 1;
             }
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         constexpr uint32_t idesc = mx4_idesc<BLOCK>(kMmRows, BN);
         uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 1;
         bool alive = true;
         for (int t = first_tile; t < tiles && alive; t += stride) {
-            if (!wait_bounded(smem_u32(&sh.acc_empty[acc]), acc_phase, w, true)) {
-                fail(2, acc, acc_phase);
+            if (!warp_wait(smem_u32(&sh.acc_empty[acc]), acc_phase, w)) {
+                if (lane == 0) fail(2, acc, acc_phase);
                 alive = false;
                 break;
             }
             tc_fence_after();
             const uint32_t d = tmem + acc * S::kAcc;
             for (int k = k0; k < k1; ++k) {
-                if (!wait_bounded(smem_u32(&sh.full[stage]), phase, w, true)) {
-                    fail(1, stage, phase);
+                if (!warp_wait(smem_u32(&sh.full[stage]), phase, w)) {
+                    if (lane == 0) fail(1, stage, phase);
                     alive = false;
                     break;
                 }
@@ -199,30 +204,37 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 const uint32_t ccols = scols + S::kTiles * 4;
                 const int left = static_cast<int>(min(static_cast<int64_t>(4), (a.K - static_cast<int64_t>(k) * kMmStep + 63) / 64));
                 const uint64_t da = desc_swizzled(at), db = desc_swizzled(at + S::kRowBytes);
+                if (elect_one()) {
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    if (m >= left) break;
-                    const int s = m * S::kTiles / 4;             // the product's scale tile
-                    if (m * S::kTiles % 4 == 0) {
+                    for (int s = 0; s < S::kTiles; ++s) {
+                        if (4 * s >= left * S::kTiles) break;            // (no scales there)
                         tmem_copy_scales<1>(scols + 4 * s, desc_rows16(sr + 512 * s));
 #pragma unroll
                         for (int c = 0; c < S::kColTiles; ++c)
                             tmem_copy_scales<1>(ccols + 4 * (s * S::kColTiles + c),
-                                             desc_rows16(sr + (1 + c) * S::kScaleBytes + 512 * s));
+                                                desc_rows16(sr + (1 + c) * S::kScaleBytes + 512 * s));
                     }
-                    const uint32_t id = BLOCK == 32 ? (m & 1) * 2 : 0;   // the first of the bytes in a scale column
-                    mma_mx4<1, BLOCK>(d, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s,
-                                   ccols + 4 * s * S::kColTiles, k > k0 || m > 0);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        if (m >= left) break;
+                        const int s = m * S::kTiles / 4;                     // the product's scale tile
+                        const uint32_t id = BLOCK == 32 ? (m & 1) * 2 : 0;   // the first of the bytes in a scale column
+                        mma_mx4<1, BLOCK>(d, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s,
+                                          ccols + 4 * s * S::kColTiles, k > k0 || m > 0);
+                    }
+                    tc_commit(smem_u32(&sh.empty[stage]));
                 }
-                tc_commit(smem_u32(&sh.empty[stage]));
+                __syncwarp();
                 if (++stage == S::kStages) stage = 0, phase ^= 1;
             }
             if (!alive) break;
-            tc_commit(smem_u32(&sh.acc_full[acc]));
+            if (elect_one()) tc_commit(smem_u32(&sh.acc_full[acc]));
+            __syncwarp();
             if (++acc == S::kAccs) acc = 0, acc_phase ^= 1;
         }
         if (!alive) {                        // what has been issued ends before tensor memory is freed
-            tc_commit(smem_u32(&sh.drain));
+            if (elect_one()) tc_commit(smem_u32(&sh.drain));
+            __syncwarp();
             wait_bounded(smem_u32(&sh.drain), 0, w, false);
         }
     } else if (warp >= 4) {
@@ -233,7 +245,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         for (int t = first_tile; t < tiles; t += stride) {
             int tr, tc;
             tile_at(a, t, &tr, &tc);
-            if (!__all_sync(0xffffffffu, wait_bounded(smem_u32(&sh.acc_full[acc]), phase, w, true))) {
+            if (!warp_wait(smem_u32(&sh.acc_full[acc]), phase, w)) {
                 if (lane == 0) fail(3, acc, phase);
                 break;
             }
@@ -343,7 +355,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     extern __shared__ unsigned char dyn_smem[];
     __shared__ __align__(8) PairShared sh;
     const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = static_cast<int>(warp_value(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     if (warp == 2) tmem_alloc<2>(smem_u32(&sh.tmem), kMmTmem);
     if (threadIdx.x == 0) {
@@ -361,7 +373,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();                          // both CTAs' barriers are there
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = warp_value(sh.tmem);
     const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
     const int first_tile = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
     const int tiles = a.tiles_r * a.tiles_c;
@@ -395,21 +407,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (++stage == S::kStages) stage = 0, phase ^= 1;
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         constexpr uint32_t idesc = mx4_idesc<BLOCK>(2 * kMmRows, kPairCols);
         uint32_t stage = 0, phase = 0, acc_phase = 1;
         bool alive = true;
         for (int t = first_tile; t < tiles && alive; t += stride) {
-            if (!wait_bounded(smem_u32(&sh.acc_empty), acc_phase, w, true)) {
-                fail(2, 0, acc_phase);
+            if (!warp_wait(smem_u32(&sh.acc_empty), acc_phase, w)) {
+                if (lane == 0) fail(2, 0, acc_phase);
                 alive = false;
                 break;
             }
             acc_phase ^= 1;
             tc_fence_after();
             for (int k = 0; k < a.steps; ++k) {
-                if (!wait_bounded(smem_u32(&sh.full[stage]), phase, w, true)) {
-                    fail(1, stage, phase);
+                if (!warp_wait(smem_u32(&sh.full[stage]), phase, w)) {
+                    if (lane == 0) fail(1, stage, phase);
                     alive = false;
                     break;
                 }
@@ -418,27 +430,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const uint32_t scols = tmem + kPairCols + stage * S::kScaleCols, ccols = scols + S::kTiles * 4;
                 const int left = static_cast<int>(min(static_cast<int64_t>(4), (a.K - static_cast<int64_t>(k) * kMmStep + 63) / 64));
                 const uint64_t da = desc_swizzled(at), db = desc_swizzled(at + S::kOperand);
+                if (elect_one()) {
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    if (m >= left) break;
-                    const int s = m * S::kTiles / 4;             // the product's scale tile
-                    if (m * S::kTiles % 4 == 0) {
+                    for (int s = 0; s < S::kTiles; ++s) {
                         tmem_copy_scales<2>(scols + 4 * s, desc_rows16(sc + 512 * s));
                         tmem_copy_scales<2>(ccols + 8 * s, desc_rows16(sc + S::kScaleBytes + 512 * s));
                         tmem_copy_scales<2>(ccols + 8 * s + 4, desc_rows16(sc + 2 * S::kScaleBytes + 512 * s));
                     }
-                    const uint32_t id = BLOCK == 32 ? (m & 1) * 2 : 0;   // the first of the bytes in a scale column
-                    mma_mx4<2, BLOCK>(tmem, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s, ccols + 8 * s,
-                                      k > 0 || m > 0);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        if (m >= left) break;
+                        const int s = m * S::kTiles / 4;                     // the product's scale tile
+                        const uint32_t id = BLOCK == 32 ? (m & 1) * 2 : 0;   // the first of the bytes in a scale column
+                        mma_mx4<2, BLOCK>(tmem, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s,
+                                          ccols + 8 * s, k > 0 || m > 0);
+                    }
+                    tc_commit_pair(smem_u32(&sh.empty[stage]), 3);
                 }
-                tc_commit_pair(smem_u32(&sh.empty[stage]), 3);
+                __syncwarp();
                 if (++stage == S::kStages) stage = 0, phase ^= 1;
             }
             if (!alive) break;
-            tc_commit_pair(smem_u32(&sh.acc_full), 3);
+            if (elect_one()) tc_commit_pair(smem_u32(&sh.acc_full), 3);
+            __syncwarp();
         }
         if (!alive) {                        // what has been issued ends before tensor memory is freed
-            tc_commit_pair(smem_u32(&sh.drain), 1);
+            if (elect_one()) tc_commit_pair(smem_u32(&sh.drain), 1);
+            __syncwarp();
             wait_bounded(smem_u32(&sh.drain), 0, w, false);
         }
     } else if (warp >= 4) {
@@ -451,7 +469,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int t = first_tile; t < tiles; t += stride) {
             int tr, tc;
             tile_at(a, t, &tr, &tc);
-            if (!__all_sync(0xffffffffu, wait_bounded(smem_u32(&sh.acc_full), phase, w, true))) {
+            if (!warp_wait(smem_u32(&sh.acc_full), phase, w)) {
                 if (lane == 0) fail(3, 0, phase);
                 break;
             }

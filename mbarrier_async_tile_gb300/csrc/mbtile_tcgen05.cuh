@@ -7,6 +7,17 @@
 namespace mbt {
 namespace {
 
+// True in one lane of the warp, the whole of which calls it.  The tensor instructions take
+// their operands from registers that a warp shares: in a branch on this the compiler knows
+// that there is one value of each, in one on the lane's number it has to look for them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// v, which is the same in the whole warp, as such a value.
+__device__ __forceinline__ uint32_t warp_value(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // CTAS: 1, or 2 where the CTAs of a pair (cluster ranks 2 k and 2 k + 1) work on one tile.
 // A kernel uses one of the two throughout.
 
