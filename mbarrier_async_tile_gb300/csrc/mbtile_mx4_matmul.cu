@@ -347,6 +347,20 @@ struct PairShared {
     int abort_flag;
 };
 
+// An element of 2 or 4 bytes from shared to global memory.
+template <int ES>
+__device__ __forceinline__ void copy_staged(void *to, uint32_t from) {
+    if constexpr (ES == 2) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(from) : "memory");
+        *static_cast<uint16_t *>(to) = v;
+    } else {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
+        *static_cast<uint32_t *>(to) = v;
+    }
+}
+
 // A warp's 32 rows x 128 columns of results to out, a box of 128 bytes of each row at a time.
 template <int DT>
 __device__ __forceinline__ void put_box(const uint32_t (&acc)[kPairCols / 2], float alpha, uint32_t staged,
@@ -356,14 +370,6 @@ __device__ __forceinline__ void put_box(const uint32_t (&acc)[kPairCols / 2], fl
 #pragma unroll
     for (int b = 0; b < kPairCols / 2; b += kBox) {
         if (row0 >= R || col0 + b >= C) break;
-        if (col0 + b + kBox > C) {           // (such a copy writes whole 16 bytes at a row's end)
-            if (row0 + lane < R)
-#pragma unroll
-                for (int e = 0; e < kBox; ++e)
-                    if (col0 + b + e < C)
-                        store_any(out, DT, (row0 + lane) * ld_out + col0 + b + e, __uint_as_float(acc[b + e]) * alpha);
-            break;
-        }
         if (lane == 0) bulk_wait_read_all();                     // the box before this one
         __syncwarp();
 #pragma unroll
@@ -375,6 +381,15 @@ __device__ __forceinline__ void put_box(const uint32_t (&acc)[kPairCols / 2], fl
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(staged + lane * kBoxRowBytes + ((j ^ (lane & 7)) << 4)),
                          "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                          : "memory");
+        }
+        if (col0 + b + kBox > C) {           // (a bulk copy would write whole 16 bytes at the rows' end)
+            if (row0 + lane < R)
+#pragma unroll 1
+                for (int e = 0; e < static_cast<int>(C - col0 - b); ++e)
+                    copy_staged<es>(static_cast<char *>(out) + ((row0 + lane) * ld_out + col0 + b + e) * es,
+                                    staged + lane * kBoxRowBytes + (((e / V) ^ (lane & 7)) << 4) + e % V * es);
+            __syncwarp();
+            break;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
