@@ -45,6 +45,8 @@ struct Mx4MatArgs {
     int32_t steps;
     int32_t tiles_r, tiles_c;
     int32_t split;             // CTAs of a cluster, each a slice of K
+    int32_t stages, accs;      // in shared memory, in tensor memory
+    int32_t tmem;              // columns of tensor memory
     int32_t odt;
     int32_t vec;               // rows of out are whole aligned 16-byte chunks
     int32_t *status;
@@ -60,13 +62,12 @@ struct MmShape {
     static constexpr int kStage = kRowBytes + kColBytes + kScaleBytes * (1 + kColTiles);
     static constexpr int kScaleCols = kTiles * 4 * (1 + kColTiles);   // tensor memory of a stage's scales
     static constexpr int kAcc = BN < 32 ? 32 : BN;
-    static constexpr int kAccs = 2 * kAcc + kScaleCols * 4 <= kMmTmem ? 2 : 1;
-    static constexpr int kFit = 220 * 1024 / kStage;
-    static constexpr int kTmemFit = (kMmTmem - kAccs * kAcc) / kScaleCols;
-    static constexpr int kStages = kFit < kTmemFit ? (kFit < kMmMostStages ? kFit : kMmMostStages)
-                                                   : (kTmemFit < kMmMostStages ? kTmemFit : kMmMostStages);
-    static constexpr int kSmem = kStages * kStage + kSwizzleAtomBytes;
-    static_assert(kStage % kSwizzleAtomBytes == 0 && kStages >= 2);
+    static constexpr int kRecv = BN * kMmRows * 4;            // a cluster's parts of this CTA's rows
+    static_assert(kStage % kSwizzleAtomBytes == 0);
+    // Stages within `bytes` of shared memory, beside accs accumulators in tensor memory.
+    static int stages(int bytes, int accs) {
+        return std::min({bytes / kStage, (kMmTmem - accs * kAcc) / kScaleCols, kMmMostStages});
+    }
 };
 
 // Tiles in groups of up to 16 down the rows, so that CTAs side by side share both operands.
@@ -121,9 +122,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     __shared__ __align__(8) MmShared sh;
     const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
     const int warp = static_cast<int>(warp_value(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    if (warp == 2) tmem_alloc<1>(smem_u32(&sh.tmem), kMmTmem);
+    // the next kernel of the stream may be set up meanwhile; it waits for this one's end itself
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (warp == 2) tmem_alloc<1>(smem_u32(&sh.tmem), a.tmem);
+    if (warp == 1 && elect_one()) {
+        prefetch_map(&rows_map);
+        prefetch_map(&cols_map);
+    }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S::kStages; ++s) {
+        for (int s = 0; s < a.stages; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
@@ -141,12 +148,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const uint32_t tmem = warp_value(sh.tmem);
     const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    if (SWAP && a.split > 1) cluster_arrive();               // this CTA is there: see the epilogue
     const int first_tile = a.split > 1 ? static_cast<int>(blockIdx.x) / a.split : static_cast<int>(blockIdx.x);
     const int stride = a.split > 1 ? 0x40000000 : static_cast<int>(gridDim.x);   // (a cluster has one tile)
     const int tiles = a.tiles_r * a.tiles_c;
     const int k0 = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.split);
     const int k1 = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / a.split);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool in_epilogue = false;                // this thread has waited for the cluster's beginning
     auto fail = [&](int role, uint32_t stage, uint32_t parity) {
         report_timeout(w, role, stage, parity);
         *w.abort = 1;
@@ -177,7 +186,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     bulk_load_1d(sr + (1 + c) * S::kScaleBytes,
                                  a.sc + ((static_cast<int64_t>(tc) * S::kColTiles + c) * a.scale_tiles + tile) * 512,
                                  bytes, full);
-                if (++stage == S::kStages) stage = 0, phase ^= 1;
+                if (++stage == static_cast<uint32_t>(a.stages)) stage = 0, phase ^= 1;
             }
         }
     } else if (warp == 1) {
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t at = base + stage * S::kStage, sr = at + S::kRowBytes + S::kColBytes;
-                const uint32_t scols = tmem + S::kAccs * S::kAcc + stage * S::kScaleCols;
+                const uint32_t scols = tmem + a.accs * S::kAcc + stage * S::kScaleCols;
                 const uint32_t ccols = scols + S::kTiles * 4;
                 const int left = static_cast<int>(min(static_cast<int64_t>(4), (a.K - static_cast<int64_t>(k) * kMmStep + 63) / 64));
                 const uint64_t da = desc_swizzled(at), db = desc_swizzled(at + S::kRowBytes);
@@ -225,12 +234,12 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     tc_commit(smem_u32(&sh.empty[stage]));
                 }
                 __syncwarp();
-                if (++stage == S::kStages) stage = 0, phase ^= 1;
+                if (++stage == static_cast<uint32_t>(a.stages)) stage = 0, phase ^= 1;
             }
             if (!alive) break;
             if (elect_one()) tc_commit(smem_u32(&sh.acc_full[acc]));
             __syncwarp();
-            if (++acc == S::kAccs) acc = 0, acc_phase ^= 1;
+            if (++acc == static_cast<uint32_t>(a.accs)) acc = 0, acc_phase ^= 1;
         }
         if (!alive) {                        // what has been issued ends before tensor memory is freed
             if (elect_one()) tc_commit(smem_u32(&sh.drain));
@@ -254,16 +263,22 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             const int r = quarter * 32 + lane;
             const int64_t row = static_cast<int64_t>(tr) * kMmRows + r, col0 = static_cast<int64_t>(tc) * BN;
             const int cols = static_cast<int>(min(static_cast<int64_t>(BN), a.C - col0));
+            const int owned = kMmRows / a.split;
+            uint32_t owner = 0;
+            if (SWAP && a.split > 1) {
+                cluster_wait();              // every CTA of the cluster has begun
+                in_epilogue = true;
+                owner = cluster_address(base + a.stages * S::kStage + (rank * BN * owned + r % owned) * 4, r / owned);
+            }
 #pragma unroll 2
             for (int c = 0; c < BN; c += 16) {
                 if (c >= cols) break;
                 float f[16];
                 __syncwarp();
                 tmem_load16(from + c, f);
-                if (SWAP && a.split > 1) {   // the slice's sums, for the cluster
+                if (SWAP && a.split > 1) {   // the slice's sums, to the CTA that adds the row's
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c + e) * kMmRows + r) * 4), "f"(f[e]) : "memory");
+                    for (int e = 0; e < 16; ++e) cluster_store(owner + (c + e) * owned * 4, f[e]);
                 } else if (row < a.R) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) f[e] *= alpha;
@@ -280,36 +295,45 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[acc]));
-            if (++acc == S::kAccs) acc = 0, phase ^= 1;
+            if (++acc == static_cast<uint32_t>(a.accs)) acc = 0, phase ^= 1;
         }
     }
     __syncwarp();
     if constexpr (SWAP) {
         if (a.split > 1) {
-            cluster_sync();
+            // A CTA adds rows of its own from every CTA's part, in the slices' order.  (Parts
+            // are stored into the memory of the CTA that adds them, apart from its stages, which
+            // it may still use: one barrier, after which no CTA needs another's memory.)
+            if (!in_epilogue) cluster_wait();
+            cluster_arrive();
+            cluster_wait();
             float alpha = a.ta ? *a.ta : 1.f;
             if (a.tb) alpha *= *a.tb;
-            const int rows = kMmRows / a.split, tr = first_tile;
+            const int owned = kMmRows / a.split;
             const int cols = static_cast<int>(min(static_cast<int64_t>(BN), a.C));
-            for (int e = threadIdx.x; e < rows * cols; e += kMmThreads) {
-                const int c = e / rows, r = rank * rows + e - c * rows;
-                const int64_t n = static_cast<int64_t>(tr) * kMmRows + r;
+            const uint32_t recv = base + a.stages * S::kStage;
+            for (int e = threadIdx.x; e < owned * cols; e += kMmThreads) {
+                const int c = e / owned, r = e - c * owned;
+                const int64_t n = static_cast<int64_t>(first_tile) * kMmRows + rank * owned + r;
                 if (n >= a.R) continue;
                 float sum = 0.f;
-                for (int q = 0; q < a.split; ++q) sum += cluster_load(base + (c * kMmRows + r) * 4, q);
+                for (int q = 0; q < a.split; ++q) {
+                    float v;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(recv + (q * BN * owned + c * owned + r) * 4) : "memory");
+                    sum += v;
+                }
                 store_any(a.out, a.odt, c * a.ld_out + n, sum * alpha);
             }
-            cluster_sync();                  // no CTA leaves while another reads its sums
         }
     }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && sh.abort_flag)   // copies under way land before the CTA leaves
-        for (int s = 0; s < S::kStages; ++s)
+        for (int s = 0; s < a.stages; ++s)
             for (uint32_t p = 0; p < 2; ++p) wait_bounded(smem_u32(&sh.full[s]), p, w, false);
     __syncthreads();
     tc_fence_after();
-    if (warp == 2) tmem_free<1>(tmem, kMmTmem);
+    if (warp == 2) tmem_free<1>(tmem, a.tmem);
 }
 
 // ---------------------------------------------------------------------------
@@ -411,7 +435,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
     const int warp = static_cast<int>(warp_value(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
+    asm volatile("griddepcontrol.launch_dependents;");       // (see above)
     if (warp == 2) tmem_alloc<2>(smem_u32(&sh.tmem), kMmTmem);
+    if (warp == 1 && elect_one()) {
+        prefetch_map(&rows_map);
+        prefetch_map(&cols_map);
+        prefetch_map(&row_scales);
+        prefetch_map(&col_scales);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
@@ -629,6 +660,8 @@ __global__ void mbt_mx4_zero_kernel(void *out, int dtype, int64_t M, int64_t N, 
 
 bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+constexpr int kMmSmem = 226 * 1024 - 1024;   // for stages and what a cluster's CTAs leave each other
+
 template <int BN, int BLOCK, bool SWAP>
 int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_cols, Mx4MatArgs a, int sms,
                   cudaStream_t stream) {
@@ -638,7 +671,7 @@ int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int
     if (cudaGetDevice(&dev) != cudaSuccess) return MBT_ERR_CUDA;
     if (dev >= 64 || !raised[dev].load(std::memory_order_relaxed)) {
         if (cudaFuncSetAttribute(mbt_mx4_matmul_kernel<BN, BLOCK, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 S::kSmem) != cudaSuccess)
+                                 kMmSmem + kSwizzleAtomBytes) != cudaSuccess)
             return MBT_ERR_CUDA;
         if (dev < 64) raised[dev].store(true, std::memory_order_relaxed);
     }
@@ -653,10 +686,19 @@ int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int
     a.split = 1;
     if (SWAP)
         while (a.split < 8 && tiles * a.split * 2 <= sms && a.split * 2 <= a.steps) a.split *= 2;
+    // As many stages, accumulators and columns of tensor memory as a CTA has use for: what
+    // is left lets the next kernel's CTAs set up while this one's finish.
+    const int64_t ctas = a.split > 1 ? tiles * a.split : std::min<int64_t>(tiles, sms);
+    const int64_t turns = a.split > 1 ? 1 : (tiles + ctas - 1) / ctas;
+    const int recv = a.split > 1 ? S::kRecv : 0;
+    a.accs = turns > 1 ? 2 : 1;
+    a.stages = static_cast<int32_t>(std::min<int64_t>(S::stages(kMmSmem - recv, a.accs), turns * ((a.steps + a.split - 1) / a.split)));
+    a.tmem = 32;
+    while (a.tmem < a.accs * S::kAcc + a.stages * S::kScaleCols) a.tmem *= 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.split > 1 ? tiles * a.split : std::min<int64_t>(tiles, sms)));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.stages) * S::kStage + recv + kSwizzleAtomBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
