@@ -13,11 +13,11 @@
 // Each stage has scale columns of its own in tensor memory, so that new scales never
 // meet products still under way.
 //
-// Few rows of a (up to 128): the rows of b are the instructions' 128 rows and those of a
-// their columns (SWAP), so that no product is spent on rows that are not there but up to
-// the next of 16, 32, 64 and 128; K is cut over the CTAs of a cluster until the device is
-// full, and the CTAs add their parts through each other's shared memory, in the order of
-// the slices.
+// The rows of b are the instructions' 128 rows and those of a their columns, so that with few
+// rows of a no product is spent on rows that are not there but up to the next of 16, 32, 64
+// and 128, and the lanes of a warp store neighbours.  K is cut over the CTAs of a cluster
+// until the device is full, and the CTAs add their parts through each other's shared
+// memory, in the order of the slices.
 #include <algorithm>
 #include <atomic>
 
@@ -62,7 +62,10 @@ struct MmShape {
     static constexpr int kStage = kRowBytes + kColBytes + kScaleBytes * (1 + kColTiles);
     static constexpr int kScaleCols = kTiles * 4 * (1 + kColTiles);   // tensor memory of a stage's scales
     static constexpr int kAcc = BN < 32 ? 32 : BN;
-    static constexpr int kRecv = BN * kMmRows * 4;            // a cluster's parts of this CTA's rows
+    // A cluster's parts of this CTA's rows; a row's columns, and 16 bytes that spread the rows
+    // over the banks.
+    static constexpr int kRecvRow = BN * 4 + 16;
+    static constexpr int kRecv = kRecvRow * kMmRows;
     static_assert(kStage % kSwizzleAtomBytes == 0);
     // Stages within `bytes` of shared memory, beside accs accumulators in tensor memory.
     static int stages(int bytes, int accs) {
@@ -113,7 +116,7 @@ struct MmShared {
     int abort_flag;
 };
 
-template <int BN, int BLOCK, bool SWAP>
+template <int BN, int BLOCK>
 __global__ void __launch_bounds__(kMmThreads, 1)
     mbt_mx4_matmul_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap cols_map,
                           const __grid_constant__ Mx4MatArgs a) {
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const uint32_t tmem = warp_value(sh.tmem);
     const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-    if (SWAP && a.split > 1) cluster_arrive();               // this CTA is there: see the epilogue
+    if (a.split > 1) cluster_arrive();               // this CTA is there: see the epilogue
     const int first_tile = a.split > 1 ? static_cast<int>(blockIdx.x) / a.split : static_cast<int>(blockIdx.x);
     const int stride = a.split > 1 ? 0x40000000 : static_cast<int>(gridDim.x);   // (a cluster has one tile)
     const int tiles = a.tiles_r * a.tiles_c;
@@ -265,10 +268,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             const int cols = static_cast<int>(min(static_cast<int64_t>(BN), a.C - col0));
             const int owned = kMmRows / a.split;
             uint32_t owner = 0;
-            if (SWAP && a.split > 1) {
+            if (a.split > 1) {
                 cluster_wait();              // every CTA of the cluster has begun
                 in_epilogue = true;
-                owner = cluster_address(base + a.stages * S::kStage + (rank * BN * owned + r % owned) * 4, r / owned);
+                owner = cluster_address(base + a.stages * S::kStage + (rank * owned + r % owned) * S::kRecvRow, r / owned);
             }
 #pragma unroll 2
             for (int c = 0; c < BN; c += 16) {
@@ -276,19 +279,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 float f[16];
                 __syncwarp();
                 tmem_load16(from + c, f);
-                if (SWAP && a.split > 1) {   // the slice's sums, to the CTA that adds the row's
+                if (a.split > 1) {   // the slice's sums, to the CTA that adds the row's
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) cluster_store(owner + (c + e) * owned * 4, f[e]);
+                    for (int e = 0; e < 16; e += 4)
+                        if (c + e < cols) cluster_store(owner + (c + e) * 4, make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
                 } else if (row < a.R) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) f[e] *= alpha;
-                    if constexpr (SWAP) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c + e < cols) store_any(a.out, a.odt, (col0 + c + e) * a.ld_out + row, f[e]);
-                    } else {
-                        store16(a, row, col0 + c, f, cols - c);
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        if (c + e < cols) store_any(a.out, a.odt, (col0 + c + e) * a.ld_out + row, f[e]);
                 }
             }
             __syncwarp();
@@ -299,31 +299,39 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
     }
     __syncwarp();
-    if constexpr (SWAP) {
-        if (a.split > 1) {
-            // A CTA adds rows of its own from every CTA's part, in the slices' order.  (Parts
-            // are stored into the memory of the CTA that adds them, apart from its stages, which
-            // it may still use: one barrier, after which no CTA needs another's memory.)
-            if (!in_epilogue) cluster_wait();
-            cluster_arrive();
-            cluster_wait();
-            float alpha = a.ta ? *a.ta : 1.f;
-            if (a.tb) alpha *= *a.tb;
-            const int owned = kMmRows / a.split;
-            const int cols = static_cast<int>(min(static_cast<int64_t>(BN), a.C));
-            const uint32_t recv = base + a.stages * S::kStage;
-            for (int e = threadIdx.x; e < owned * cols; e += kMmThreads) {
-                const int c = e / owned, r = e - c * owned;
-                const int64_t n = static_cast<int64_t>(first_tile) * kMmRows + rank * owned + r;
-                if (n >= a.R) continue;
-                float sum = 0.f;
-                for (int q = 0; q < a.split; ++q) {
-                    float v;
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(recv + (q * BN * owned + c * owned + r) * 4) : "memory");
-                    sum += v;
+    if (a.split > 1) {
+        // A CTA adds rows of its own from every CTA's part, in the slices' order.  (Parts are
+        // stored into the memory of the CTA that adds them, apart from its stages, which it may
+        // still use: one barrier, after which no CTA needs another's memory.)
+        if (!in_epilogue) cluster_wait();
+        cluster_arrive();
+        cluster_wait();
+        float alpha = a.ta ? *a.ta : 1.f;
+        if (a.tb) alpha *= *a.tb;
+        int tr, tc;
+        tile_at(a, first_tile, &tr, &tc);
+        const int owned = kMmRows / a.split;
+        const int64_t row0 = static_cast<int64_t>(tr) * kMmRows + rank * owned, col0 = static_cast<int64_t>(tc) * BN;
+        const int cols = static_cast<int>(min(static_cast<int64_t>(BN), a.C - col0));
+        const int r = threadIdx.x & (owned - 1), at_once = kMmThreads / owned * 4;   // (owned: a power of two)
+        const uint32_t recv = base + a.stages * S::kStage + r * S::kRecvRow;
+        for (int c = threadIdx.x / owned * 4; c < cols; c += at_once) {
+            float4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < a.split) {
+                    const uint4 u = lds128(recv + q * owned * S::kRecvRow + c * 4);
+                    v[q] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
                 }
-                store_any(a.out, a.odt, c * a.ld_out + n, sum * alpha);
-            }
+            float4 sum = v[0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q)
+                if (q < a.split) sum.x += v[q].x, sum.y += v[q].y, sum.z += v[q].z, sum.w += v[q].w;
+            const float f[4] = {sum.x * alpha, sum.y * alpha, sum.z * alpha, sum.w * alpha};
+            if (row0 + r < a.R)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < cols) store_any(a.out, a.odt, (col0 + c + e) * a.ld_out + row0 + r, f[e]);
         }
     }
     tc_fence_before();
@@ -662,7 +670,7 @@ bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 
 constexpr int kMmSmem = 226 * 1024 - 1024;   // for stages and what a cluster's CTAs leave each other
 
-template <int BN, int BLOCK, bool SWAP>
+template <int BN, int BLOCK>
 int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_cols, Mx4MatArgs a, int sms,
                   cudaStream_t stream) {
     using S = MmShape<BN, BLOCK>;
@@ -670,7 +678,7 @@ int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MBT_ERR_CUDA;
     if (dev >= 64 || !raised[dev].load(std::memory_order_relaxed)) {
-        if (cudaFuncSetAttribute(mbt_mx4_matmul_kernel<BN, BLOCK, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(mbt_mx4_matmul_kernel<BN, BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kMmSmem + kSwizzleAtomBytes) != cudaSuccess)
             return MBT_ERR_CUDA;
         if (dev < 64) raised[dev].store(true, std::memory_order_relaxed);
@@ -684,8 +692,7 @@ int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int
     const int64_t tiles = static_cast<int64_t>(a.tiles_r) * a.tiles_c;
     if (tiles > 0x3fffffff) return MBT_ERR_UNSUPPORTED;
     a.split = 1;
-    if (SWAP)
-        while (a.split < 8 && tiles * a.split * 2 <= sms && a.split * 2 <= a.steps) a.split *= 2;
+    while (a.split < 8 && tiles * a.split * 2 <= sms && a.split * 2 <= a.steps) a.split *= 2;
     // As many stages, accumulators and columns of tensor memory as a CTA has use for: what
     // is left lets the next kernel's CTAs set up while this one's finish.
     const int64_t ctas = a.split > 1 ? tiles * a.split : std::min<int64_t>(tiles, sms);
@@ -708,27 +715,28 @@ int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mbt_mx4_matmul_kernel<BN, BLOCK, SWAP>, rows_map, cols_map, a) == cudaSuccess
+    return cudaLaunchKernelEx(&cfg, mbt_mx4_matmul_kernel<BN, BLOCK>, rows_map, cols_map, a) == cudaSuccess
                ? MBT_OK
                : MBT_ERR_CUDA;
 }
 
-// Whether there are tiles of 256 x 256 for every pair of SMs.
-bool pair_pays(int64_t M, int64_t N, int sms) { return (M + 255) / 256 * ((N + 255) / 256) >= sms / 2; }
+// A wave of 128 x 128 tiles has the device's SMs to itself, cut along K if need be; more of
+// them than that are slower than pairs (us, alone / by pairs): 256 x 4096 x 4096 9.8 / 10.7,
+// 512 x 8192 x 8192 26.9 / 17.0, 1024 x 8192 x 512 10.1 / 8.5, 2048 x 8192 x 2048 25.8 / 22.1.
+bool pair_pays(int64_t M, int64_t N, int sms) { return (M + 127) / 128 * ((N + 127) / 128) > sms; }
 
 template <int BLOCK>
 int matmul(const uint8_t *a_q, int64_t ld_a, const uint8_t *b_q, int64_t ld_b, const uint8_t *as, const uint8_t *bs,
            int64_t M, int64_t N, Mx4MatArgs a, int sms, cudaStream_t s) {
-    if (M <= 128) {
-        a.R = N, a.C = M, a.sr = bs, a.sc = as;
-        return M <= 16   ? launch_matmul<16, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s)
-               : M <= 32 ? launch_matmul<32, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s)
-               : M <= 64 ? launch_matmul<64, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s)
-                         : launch_matmul<128, BLOCK, true>(b_q, ld_b, a_q, ld_a, a, sms, s);
+    if (M > 128 && pair_pays(M, N, sms)) {
+        a.R = M, a.C = N, a.sr = as, a.sc = bs;
+        return launch_pair<BLOCK>(a_q, ld_a, b_q, ld_b, a, sms, s);
     }
-    a.R = M, a.C = N, a.sr = as, a.sc = bs;
-    if (pair_pays(M, N, sms)) return launch_pair<BLOCK>(a_q, ld_a, b_q, ld_b, a, sms, s);
-    return launch_matmul<128, BLOCK, false>(a_q, ld_a, b_q, ld_b, a, sms, s);
+    a.R = N, a.C = M, a.sr = bs, a.sc = as;
+    return M <= 16   ? launch_matmul<16, BLOCK>(b_q, ld_b, a_q, ld_a, a, sms, s)
+           : M <= 32 ? launch_matmul<32, BLOCK>(b_q, ld_b, a_q, ld_a, a, sms, s)
+           : M <= 64 ? launch_matmul<64, BLOCK>(b_q, ld_b, a_q, ld_a, a, sms, s)
+                     : launch_matmul<128, BLOCK>(b_q, ld_b, a_q, ld_a, a, sms, s);
 }
 
 }  // namespace
