@@ -8,10 +8,12 @@
 // rounded to fp32 before it is rounded to a code, as the formulas read in fp32, so
 // that codes do not depend on how a kernel divides.
 //
-// Both read and write every byte once: device memory bounds them.  The scales lie in
-// tiles of 128 rows x 4 blocks, the order in which the product's tensor instructions
-// take them; a warp therefore works on rows r, r + 32, r + 64, r + 96 of a tile, for two
-// neighbouring r, by 4 blocks: its 32 scale bytes are one aligned sector.
+// Both read and write every byte once: device memory bounds them.  A warp takes 32
+// pieces of 16 or 32 bytes, side by side, of each of two or four rows.  (A lane with a
+// block of its own reads lines that 32 lanes each touch eight times over: fp32 16384 x
+// 16384 by 32 260 us, 4.7 TB/s.)  The scales lie in tiles of 128 rows x 4 blocks, the
+// order in which the product's tensor instructions take them; the rows are 32 apart, so that
+// their scales lie side by side.
 #include <algorithm>
 
 #include "mbtile_elem.cuh"
@@ -22,169 +24,194 @@ namespace mbt {
 namespace {
 
 constexpr int kMx4Warps = 8;
+// Rows of a warp.  Fewer to quantise, whose arithmetic wants the registers that more warps
+// then share (fp32 16384 x 16384 by 32, us, with 2 / 4: 167 / 202; back 110 / 97).
+constexpr int kQuantizeRows = 2;
+constexpr int kDequantizeRows = 4;
 
 struct Mx4Args {
     const void *x;           // quantise: in; dequantise: out
     uint8_t *q, *s;
     const float *ts;
     int64_t M, K, ld_x, ld_q;
-    int64_t tiles, groups;   // scale tiles of a row of tiles, eights of rows
-    int32_t dtype;
-    int32_t vec;             // rows of x are whole aligned 16-byte chunks
+    int64_t tiles;           // scale tiles of a row of tiles
+    uint32_t chunks;         // of a warp's columns across a row
+    uint32_t warps;          // chunks x their rows
+    int32_t vec;             // rows of x are aligned to 16 bytes, 2: to 32
 };
 
-// The place of a lane: its row, and its block of the warp's four.
+// A lane's place: the first of its V columns, and its warp's rows.
+template <int V, int BLOCK, int ROWS>
 struct Mx4Place {
-    int64_t row, block, scale;   // scale: byte offset
-    bool in;                     // one of the scales'
+    int64_t col, first;      // first: row
+    int64_t tile;            // the lane's block's scale tile
+    int r, band, byte;       // row in its band of 32, the first row's band; the block's byte of a row's four
+    bool in, lane_in_scales; // one of the matrix's warps; its block has a byte of scale
     __device__ __forceinline__ Mx4Place(const Mx4Args &a) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int64_t tile = static_cast<int64_t>(blockIdx.x) * kMx4Warps + warp;   // of the row's tiles
-        const int64_t group = blockIdx.y + static_cast<int64_t>(gridDim.y) * blockIdx.z;   // of 8 rows
-        const int r = static_cast<int>(group & 15) * 2 + (lane >> 4), band = lane >> 2 & 3;
-        row = (group >> 4) * 128 + band * 32 + r;
-        block = tile * 4 + (lane & 3);
-        scale = ((group >> 4) * a.tiles + tile) * 512 + r * 16 + band * 4 + (lane & 3);
-        in = tile < a.tiles && group < a.groups;
+        const uint32_t id = blockIdx.x * kMx4Warps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+        in = id < a.warps;
+        const uint32_t group = id / a.chunks, chunk = id - group * a.chunks;
+        col = (static_cast<int64_t>(chunk) * 32 + lane) * V;
+        constexpr uint32_t kGroups = 128 / ROWS;   // of a row of tiles
+        const uint32_t row_tile = group / kGroups;
+        r = static_cast<int>(group & 31);
+        band = static_cast<int>(group % kGroups >> 5) * ROWS;
+        first = static_cast<int64_t>(row_tile) * 128 + band * 32 + r;
+        const int64_t block = col / BLOCK;
+        tile = row_tile * a.tiles + (block >> 2);
+        byte = static_cast<int>(block & 3);
+        lane_in_scales = (block >> 2) < a.tiles;
     }
+    __device__ __forceinline__ int64_t row(int i) const { return first + i * 32; }
+    __device__ __forceinline__ int64_t scale(int i) const { return tile * 512 + r * 16 + (band + i) * 4 + byte; }
 };
 
-// 16 elements of a row from column j on, two to a register pair.
+// 32 bytes of a row: at once, as two vectors, or by elements, as its alignment allows.
 template <int DT>
-__device__ __forceinline__ void load16(const Mx4Args &a, int64_t row, int64_t j, float (&f)[16]) {
+__device__ __forceinline__ void load_pair(const Mx4Args &a, int64_t row, int64_t col, uint4 (&v)[2]) {
     using T = typename Elem<DT>::type;
     constexpr int V = Elem<DT>::kVec;
-    const T *p = static_cast<const T *>(a.x) + row * a.ld_x + j;
-    if (a.vec) {
-        uint4 v[16 / V];
+    const T *p = static_cast<const T *>(a.x) + row * a.ld_x + col;
+    if (a.vec == 2) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z),
+                       "=r"(v[1].w)
+                     : "l"(p));
+    } else if (a.vec) {
+        v[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+        v[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    } else {
 #pragma unroll
-        for (int k = 0; k < 16 / V; ++k) v[k] = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+        for (int h = 0; h < 2; ++h) {
+            float f[V];
 #pragma unroll
-        for (int k = 0; k < 16 / V; ++k) {
-            float g[V];
-            unpack<DT>(v[k], g);
-#pragma unroll
-            for (int e = 0; e < V; ++e) f[k * V + e] = g[e];
+            for (int e = 0; e < V; ++e) f[e] = Elem<DT>::widen(p[h * V + e]);
+            v[h] = pack<DT>(f);
         }
-        return;
     }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = Elem<DT>::widen(p[e]);
 }
 
-// The 16 codes of f / d; plain: with the division itself, for quotients that the
-// corrected product below would not take within fp32's range.
-__device__ __forceinline__ uint2 codes16(const float (&f)[16], float d, bool plain) {
-    uint32_t w[2];
+// The codes of E elements f by d, eight to a word.
+template <int E, int BLOCK>
+__device__ __forceinline__ void codes_of(float (&f)[E], float d, float most, uint32_t (&w)[E / 8]) {
+    if (BLOCK == 16 && !(most < 64.f * d)) {
+        // a scale at its largest: quotients far past 6, which might leave fp32's range
+        const float high = 32.f * d;
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = fminf(fmaxf(f[e], -high), high);
+    }
+    // (of a power of two the inverse is exact, 2^127 for 2^-127)
+    const Pair inv(__uint_as_float(0x7f000000u - (__float_as_uint(d) & 0x7f800000u)));
     const Divisor by(d);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < E / 8; ++h) {
         float y[8];
-        if (plain) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = -__fdiv_rn(f[8 * h + e], d);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float2 m = by.minus(f[8 * h + e], f[8 * h + e + 1]);
-                y[e] = m.x, y[e + 1] = m.y;
-            }
+        for (int e = 0; e < 8; e += 2) {
+            const float2 v = BLOCK == 32 ? (Pair(f[8 * h + e], f[8 * h + e + 1]) * inv).get()
+                                         : by.minus(f[8 * h + e], f[8 * h + e + 1]);
+            y[e] = v.x, y[e + 1] = v.y;
         }
-        w[h] = to_e2m1x8(y) ^ 0x88888888u;
+        w[h] = to_e2m1x8(y) ^ (BLOCK == 32 ? 0u : 0x88888888u);
     }
-    return make_uint2(w[0], w[1]);
 }
 
-// A lane holds a block: 16 elements, or 32 in two halves.
+// A lane takes 32 bytes of a row: of 16-bit elements a whole block of 16, so that the
+// scale's arithmetic is done once a block (with 16 bytes, bf16 2047 x 8192 by 16: 15.6 us).
 template <int DT, int BLOCK>
-__global__ void __launch_bounds__(32 * kMx4Warps) mbt_mx4_quantize_kernel(const Mx4Args a) {
-    const Mx4Place at(a);
+__global__ void __launch_bounds__(32 * kMx4Warps, 5) mbt_mx4_quantize_kernel(const Mx4Args a) {
+    constexpr int V = Elem<DT>::kVec, E = 2 * V;
+    const Mx4Place<E, BLOCK, kQuantizeRows> at(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!at.in) return;
-    const int64_t j = at.block * BLOCK;
-    uint32_t code = 0;
-    if (at.row < a.M && j < a.K) {
-        float f[BLOCK / 16][16];
-        uint32_t amax = 0;
+    const float ts = BLOCK == 16 && a.ts ? *a.ts : 1.f;
+    const float t = 6.f * ts, it = __frcp_rn(t);
+    uint4 v[kQuantizeRows][2];
 #pragma unroll
-        for (int h = 0; h < BLOCK / 16; ++h) load16<DT>(a, at.row, j + 16 * h, f[h]);
+    for (int i = 0; i < kQuantizeRows; ++i) {
+        v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (at.row(i) < a.M && at.col < a.K) load_pair<DT>(a, at.row(i), at.col, v[i]);
+    }
 #pragma unroll
-        for (int h = 0; h < BLOCK / 16; ++h) amax = magnitude_max(amax, f[h]);
+    for (int i = 0; i < kQuantizeRows; ++i) {
+        float f[E];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float g[V];
+            unpack<DT>(v[i][h], g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[h * V + e] = g[e];
+        }
+        uint32_t amax = magnitude_max(0u, f);
+#pragma unroll
+        for (int o = 1; o < BLOCK / E; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const float most = __uint_as_float(amax);
+        const bool finite = amax < 0x7f800000u;
+        uint32_t code;
         float d;
         if constexpr (BLOCK == 16) {
-            const float ts = a.ts ? *a.ts : 1.f;
-            // (infinity and NaN: a NaN scale)
-            code = amax < 0x7f800000u ? to_e4m3x2(__fdiv_rn(most, a.ts ? 6.f * ts : 6.f), 0.f) & 0xffu : 0x7fu;
+            // a / t; past 448 by its size alone, which also keeps the quotient in range
+            const float q = most < 1024.f * t ? divide(Pair(most), Pair(-t), Pair(it)).get().x : kE4m3Max;
+            code = !finite ? 0x7fu : amax ? to_e4m3x2(q, 0.f) & 0xffu : 0u;
             d = Elem<MBT_F16>::widen2(e4m3x2_to_half2(code)).x * ts;
         } else {
             // the exponent of a power of two is its code; below 2^-125 that of the scale is 0
-            code = amax < 0x7f800000u ? static_cast<uint32_t>(max(static_cast<int>(amax >> 23) - 2, 0)) : 0xffu;
+            code = finite ? static_cast<uint32_t>(max(static_cast<int>(amax >> 23) - 2, 0)) : 0xffu;
             d = code ? __uint_as_float(code << 23) : 5.87747175e-39f;   // 2^-127
         }
-        const bool none = !(d > 0.f) || amax == 0 || amax >= 0x7f800000u;   // codes 0
-        const bool plain = !(most < 64.f * d) || d < 1e-30f || d > 1e30f;
-        uint2 w[BLOCK / 16];
-#pragma unroll
-        for (int h = 0; h < BLOCK / 16; ++h) w[h] = none ? make_uint2(0u, 0u) : codes16(f[h], d, plain);
-        uint8_t *q = a.q + at.row * a.ld_q + j / 2;
-        if constexpr (BLOCK == 16)
-            *reinterpret_cast<uint2 *>(q) = w[0];
-        else
-            *reinterpret_cast<uint4 *>(q) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+        uint32_t w[E / 8] = {};
+        if (d > 0.f && amax != 0 && finite) codes_of<E, BLOCK>(f, d, most, w);
+        if (at.row(i) < a.M && at.col < a.K) {
+            uint8_t *q = a.q + at.row(i) * a.ld_q + at.col / 2;
+            if constexpr (E == 16)
+                *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint32_t *>(q) = w[0];
+        }
+        if (at.lane_in_scales && at.col % BLOCK == 0) a.s[at.scale(i)] = static_cast<uint8_t>(code);
     }
-    a.s[at.scale] = static_cast<uint8_t>(code);
 }
 
 template <int DT, int BLOCK>
 __global__ void __launch_bounds__(32 * kMx4Warps) mbt_mx4_dequantize_kernel(const Mx4Args a) {
     using T = typename Elem<DT>::type;
     constexpr int V = Elem<DT>::kVec;
-    const Mx4Place at(a);
+    const Mx4Place<V, BLOCK, kDequantizeRows> at(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t j = at.block * BLOCK;
-    if (!at.in || at.row >= a.M || j >= a.K) return;
-    const uint32_t code = a.s[at.scale];
-    float s, ts = 1.f;
-    if constexpr (BLOCK == 16) {
-        s = Elem<MBT_F16>::widen2(e4m3x2_to_half2(code)).x;
-        if (a.ts) ts = *a.ts;
-    } else {
-        s = code == 0xffu ? __uint_as_float(0x7fc00000u) : code ? __uint_as_float(code << 23) : 5.87747175e-39f;
-    }
-    const uint8_t *q = a.q + at.row * a.ld_q + j / 2;
-    uint32_t w[BLOCK / 8];
-    if constexpr (BLOCK == 16) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(q);
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(q);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    }
-    T *p = static_cast<T *>(const_cast<void *>(a.x)) + at.row * a.ld_x + j;
+    if (!at.in || at.col >= a.K) return;
+    const float ts = BLOCK == 16 && a.ts ? *a.ts : 1.f;
+    uint32_t w[kDequantizeRows], code[kDequantizeRows];
 #pragma unroll
-    for (int h = 0; h < BLOCK / 8; ++h) {
-        float f[8];
+    for (int i = 0; i < kDequantizeRows; ++i) {
+        w[i] = code[i] = 0;
+        if (at.row(i) >= a.M) continue;
+        const uint8_t *q = a.q + at.row(i) * a.ld_q + at.col / 2;
+        w[i] = V == 8 ? __ldg(reinterpret_cast<const uint32_t *>(q)) : __ldg(reinterpret_cast<const uint16_t *>(q));
+        code[i] = __ldg(a.s + at.scale(i));
+    }
+#pragma unroll
+    for (int i = 0; i < kDequantizeRows; ++i) {
+        if (at.row(i) >= a.M) continue;
+        float s;
+        if constexpr (BLOCK == 16)
+            s = Elem<MBT_F16>::widen2(e4m3x2_to_half2(code[i])).x;
+        else
+            s = code[i] == 0xffu ? __uint_as_float(0x7fc00000u) : code[i] ? __uint_as_float(code[i] << 23) : 5.87747175e-39f;
         uint32_t pair[4];
-        e2m1x8_to_half2(w[h], pair);
+        e2m1x8_to_half2(w[i], pair);
+        float f[V];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
+        for (int e = 0; e < V; e += 2) {
             const float2 v = Elem<MBT_F16>::widen2(pair[e / 2]);
             f[e] = v.x * s * ts;
             f[e + 1] = v.y * s * ts;
         }
-        if (a.vec) {
+        T *p = static_cast<T *>(const_cast<void *>(a.x)) + at.row(i) * a.ld_x + at.col;
+        if (a.vec)
+            *reinterpret_cast<uint4 *>(p) = pack<DT>(f);
+        else
 #pragma unroll
-            for (int k = 0; k < 8 / V; ++k) {
-                float g[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) g[e] = f[k * V + e];
-                reinterpret_cast<uint4 *>(p + 8 * h)[k] = pack<DT>(g);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[8 * h + e] = Elem<DT>::round(f[e]);
-        }
+            for (int e = 0; e < V; ++e) p[e] = Elem<DT>::round(f[e]);
     }
 }
 
@@ -213,12 +240,13 @@ int mx4_convert(const void *x, const float *ts, uint8_t *q, uint8_t *scales, int
     const uintptr_t es = dtype == MBT_F32 ? 4 : 2;
     if (!aligned(x, es) || !aligned(q, 16) || ld_q % 16 != 0 || !aligned(scales, 16) || !aligned(ts, 4))
         return MBT_ERR_ALIGN;
-    // 16 groups of 8 rows to a row of tiles; a grid's second dimension holds 65535
-    const int64_t groups = (M + 127) / 128 * 16, deep = (groups + 32767) / 32768;
-    Mx4Args a{x, q, scales, ts, M, K, ld_x, ld_q, mx4_tiles(K, block), groups, dtype, 0};
-    a.vec = aligned(x, 16) && ld_x * static_cast<int64_t>(es) % 16 == 0;
-    const dim3 grid(static_cast<unsigned>((a.tiles + kMx4Warps - 1) / kMx4Warps),
-                    static_cast<unsigned>(deep > 1 ? 32768 : groups), static_cast<unsigned>(deep));
+    const int64_t wide = BACK ? 512 : 1024;   // bytes of a warp and row of x
+    const int64_t chunks = (K * static_cast<int64_t>(es) + wide - 1) / wide, warps = (M + 127) / 128 * (128 / (BACK ? kDequantizeRows : kQuantizeRows)) * chunks;
+    if (warps > 0xffffffffll - kMx4Warps) return MBT_ERR_UNSUPPORTED;
+    Mx4Args a{x, q, scales, ts, M, K, ld_x, ld_q, mx4_tiles(K, block), static_cast<uint32_t>(chunks), static_cast<uint32_t>(warps), 0};
+    const uintptr_t pitch = static_cast<uintptr_t>(ld_x) * es;
+    a.vec = aligned(x, 32) && pitch % 32 == 0 ? 2 : aligned(x, 16) && pitch % 16 == 0;
+    const dim3 grid(static_cast<unsigned>((warps + kMx4Warps - 1) / kMx4Warps));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == MBT_F16    ? launch_mx4<BACK, MBT_F16>(a, block, grid, s)
                           : dtype == MBT_BF16 ? launch_mx4<BACK, MBT_BF16>(a, block, grid, s)
