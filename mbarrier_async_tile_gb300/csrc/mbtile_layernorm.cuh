@@ -359,29 +359,42 @@ cudaError_t launch_ln_finish(const LayerNormGradArgs &a, cudaStream_t s) {
 // stage once more.
 
 // Sums of a and b over a row's tpr threads, in all of them; red and turn as in row_reduce.
+// Of a whole warp's values, the lower lanes add up a and the upper ones b.
 __device__ __forceinline__ void row_reduce_two(float &a, float &b, int tpr, float *red, int turn) {
+    const int lane = threadIdx.x & 31;
+    if (tpr < 32) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (o >= tpr) continue;
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
+        for (int o = 8; o > 0; o >>= 1) {
+            if (o >= tpr) continue;
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        return;
     }
-    if (tpr <= 32) return;
-    const int warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp & ~(warps - 1), lane = threadIdx.x & 31;
-    float *s = red + turn * 64;
-    if (lane == 0) s[warp] = a, s[32 + warp] = b;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + first / warps), "r"(tpr) : "memory");
-    a = lane < warps ? s[first + lane] : 0.f;
-    b = lane < warps ? s[32 + first + lane] : 0.f;
-    a = warp_sum(a);
-    b = warp_sum(b);
+    const bool upper = (lane & 16) != 0;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tpr > 32) {
+        const int warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp & ~(warps - 1);
+        float *s = red + turn * 64 + (upper ? 32 : 0);
+        if ((lane & 15) == 0) s[warp] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + first / warps), "r"(tpr) : "memory");
+        v = (lane & 15) < warps ? s[first + (lane & 15)] : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    a = __shfl_sync(0xffffffffu, v, 0);
+    b = __shfl_sync(0xffffffffu, v, 16);
 }
 
 // A thread's weights or biases (`none` where there are none), C chunks of them, 0 past
-// the row: packed in x's type, or read each time.
+// the row: packed in x's type, or read each time (FLY, which an offset to 16-bit weights asks
+// for too: weight and offset do not fit their type together).
 template <int DT, int C, bool PART, bool FLY>
 struct RowVector {
     static constexpr int V = Elem<DT>::kVec;
+    static constexpr bool kAgain = DT != MBT_F32 && C * V > 16;   // too many to keep unpacked
     uint4 raw[FLY ? 1 : C];
     const void *from;
     int64_t N;
@@ -400,13 +413,13 @@ struct RowVector {
         if constexpr (!FLY)
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                if (!PART && from) {
+                if (!PART && from && add == 0.f) {
                     const int p = (t + c * tpr) * V;
                     raw[c] = make_uint4(0, 0, 0, 0);
                     if (p < N) raw[c] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const typename Elem<DT>::type *>(from) + p));
                 } else {
                     float v[V];
-                    fetch(c, 0.f, v);
+                    fetch(c, add, v);
                     raw[c] = pack<DT>(v);
                 }
             }
@@ -415,9 +428,7 @@ struct RowVector {
         if constexpr (FLY) {
             fetch(c, add, v);
         } else {
-            unpack<DT>(again(raw[c], zero), v);
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[e] += add;
+            unpack<DT>(kAgain ? again(raw[c], zero) : raw[c], v);
         }
     }
 };
@@ -432,7 +443,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_layernorm_backward_kernel(const __grid_constant__ LayerNormGradArgs a, const __grid_constant__ LayerNormRing l) {
     using T = typename Elem<DT>::type;
     constexpr int V = Elem<DT>::kVec;
-    constexpr bool HOLD = C * V <= 16;
+    constexpr bool HOLD = C * V <= 16;                       // deviations and gradients in registers from pass to pass
     const RingArgs &r = l.r;
     extern __shared__ __align__(128) unsigned char dyn_smem[];
     __shared__ __align__(8) RingShared sh;
@@ -480,17 +491,15 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 vh = pack<DT>(f);
             }
         };
-        uint4 vy[HOLD ? C : 1], vh[HOLD ? C : 1];
-        if constexpr (HOLD)
-#pragma unroll
-            for (int c = 0; c < C; ++c) take(c, vy[c], vh[c]);
+        float xs[HOLD ? C : 1][V], gs[HOLD ? C : 1][V];
         float level = 0.f, along = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float dy[V], h[V], w[V];
-            if constexpr (!HOLD) take(c, vy[0], vh[0]);
-            unpack<DT>(vy[HOLD ? c : 0], dy);
-            unpack<DT>(vh[HOLD ? c : 0], h);
+            uint4 vy, vh;
+            take(c, vy, vh);
+            unpack<DT>(vy, dy);
+            unpack<DT>(vh, h);
             wt.get(c, z1, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -499,6 +508,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 along += g * xh;
                 dw[c][e] += dy[e] * xh;
                 db[c][e] += dy[e];
+                if (HOLD) xs[c][e] = xh, gs[c][e] = g;
             }
         }
         row_reduce_two(level, along, r.tpr, sh.red[0], turn);
@@ -513,16 +523,21 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 vr = th.chunk(q.stage, 2, c);
                 if (PART && th.tail) th.last_chunk(r, 2, c, i, vr);
             }
-            float dy[V], h[V], d[V], f[V], w[V];
-            if constexpr (!HOLD) take(c, vy[0], vh[0]);
-            unpack<DT>(again(vy[HOLD ? c : 0], z2), dy);
-            unpack<DT>(again(vh[HOLD ? c : 0], z2), h);
-            wt.get(c, z2, w);
+            float d[V], f[V];
             if constexpr (RES) unpack<DT>(vr, f);
+            if constexpr (HOLD) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                d[e] = rstd * (dy[e] * w[e] - level - (h[e] - mean) * rstd * along);
-                if constexpr (RES) d[e] += f[e];
+                for (int e = 0; e < V; ++e) d[e] = rstd * (gs[c][e] - level - xs[c][e] * along) + (RES ? f[e] : 0.f);
+            } else {
+                float dy[V], h[V], w[V];
+                uint4 vy, vh;
+                take(c, vy, vh);
+                unpack<DT>(vy, dy);
+                unpack<DT>(vh, h);
+                wt.get(c, z2, w);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    d[e] = rstd * (dy[e] * w[e] - level - (h[e] - mean) * rstd * along) + (RES ? f[e] : 0.f);
             }
             th.put(dx + c * chunk, c, d);
         }
@@ -744,7 +759,7 @@ cudaError_t ln_ring_forward(const RingPlan &p, int bmode, const LayerNormArgs &a
                : c <= 4 ? launch_ln_ring_forward<DT, 4, false, false>(p, bmode, a, s)
                         : launch_ln_ring_forward<DT, 5, false, false>(p, bmode, a, s);
     } else {
-        if (a.w && a.wdt != DT) return launch_ln_ring_forward<DT, 4, true, true>(p, bmode, a, s);
+        if (a.w && (a.wdt != DT || a.woff != 0.f)) return launch_ln_ring_forward<DT, 4, true, true>(p, bmode, a, s);
         if (part)
             return c <= 2 ? launch_ln_ring_forward<DT, 2, true, false>(p, bmode, a, s)
                           : launch_ln_ring_forward<DT, 4, true, false>(p, bmode, a, s);
@@ -767,7 +782,7 @@ cudaError_t ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cuda
                : c <= 4 ? launch_ln_ring_backward<DT, 4, false, false>(p, a, s)
                         : launch_ln_ring_backward<DT, 5, false, false>(p, a, s);
     } else {
-        if (a.w && a.wdt != DT) return launch_ln_ring_backward<DT, 4, true, true>(p, a, s);
+        if (a.w && (a.wdt != DT || a.woff != 0.f)) return launch_ln_ring_backward<DT, 4, true, true>(p, a, s);
         if (part)
             return c <= 2 ? launch_ln_ring_backward<DT, 2, true, false>(p, a, s)
                           : launch_ln_ring_backward<DT, 4, true, false>(p, a, s);
@@ -778,12 +793,20 @@ cudaError_t ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cuda
 }
 
 // The ring's plan: up to four chunks a thread of 16-bit rows; of fp32 rows up to five, and
-// eight of those too long for that.
+// eight of those too long for that.  Rows side by side hide each other's reductions, so few
+// threads take a row (us, four chunks / two, forward 8192 x 8192 bf16 with a residual 87 /
+// 121; gradient 16384 x 8192 187 / 215, 65536 x 1024 95 / 118; fp32 2047 x 5001, five / four
+// 37 / 52), but for a gradient of few turns, where the last one's length and the more
+// instructions of rows that registers do not hold count (3001 x 4001 48 / 38, 1024 x 4096
+// 20.4 / 17.5, 8192 x 4096 of 13 turns 61 / 64, 9001 x 1032 of 7 36 / 39).
 bool ln_ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, int64_t N, int es, int ph, int min_tpr,
-                  int sms, RingPlan *p) {
-    if (es == 2) return ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p);
-    return ring_plan(in, ld, inputs, M, N, es, ph, 5, min_tpr, sms, p) ||
-           ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p);
+                  int sms, bool gradient, RingPlan *p) {
+    if (es == 4)
+        return ring_plan(in, ld, inputs, M, N, es, ph, 5, min_tpr, sms, p, 5) ||
+               ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p);
+    if (!ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p, 4)) return false;
+    if (!gradient || M >= 6ll * p->grid * p->r.rows) return true;
+    return ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p, 2);
 }
 
 // The gradient through the ring; *done says whether it applied.
@@ -796,7 +819,7 @@ int ln_backward_by_ring(LayerNormGradArgs a, cudaStream_t s, int sms, bool *done
     const void *in[3] = {a.dy, a.h, a.dres};
     const int64_t ld[3] = {a.ld_dy, a.ld_h, a.ld_dres};
     RingPlan p;
-    *done = same && ln_ring_plan(in, ld, a.dres ? 3 : 2, a.M, a.N, es, ph, 8, sms, &p);
+    *done = same && ln_ring_plan(in, ld, a.dres ? 3 : 2, a.M, a.N, es, ph, 8, sms, true, &p);
     if (!*done) return MBT_OK;
     int rc = device_status_word(&p.r.status);
     if (rc != MBT_OK) return rc;
@@ -850,7 +873,7 @@ cudaError_t ln_forward_any(const LayerNormArgs &a, cudaStream_t s) {
     const int64_t ld[2] = {a.ld_x, a.ld_res};
     RingPlan p;
     if (same && ln_ring_pays(a, es, sms, ph) &&
-        ln_ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, a.quant > 0 ? 32 : 8, sms, &p)) {
+        ln_ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, a.quant > 0 ? 32 : 8, sms, false, &p)) {
         if (device_status_word(&p.r.status) != MBT_OK) return cudaErrorUnknown;
         p.r.wmode = weight_mode(a.w, a.wdt, DT);
         return ln_ring_forward<DT>(p, weight_mode(a.b, a.wdt, DT), a, s);

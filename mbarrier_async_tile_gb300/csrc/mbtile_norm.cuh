@@ -1030,7 +1030,8 @@ int weight_mode(const void *w, int wdt, int dtype) {
 
 // Rows, threads, stages of a ring over these matrices.  False where it does not
 // apply: rows too long for a CTA's registers or two stages, matrices whose rows
-// start at different places in a chunk.
+// start at different places in a chunk.  prefer: chunks a thread where the rows allow
+// them (0: what was measured for this norm).
 struct RingPlan {
     RingArgs r;
     int chunks;              // of 16 bytes per thread
@@ -1039,7 +1040,7 @@ struct RingPlan {
 };
 
 bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, int64_t N, int es, int ph,
-               int most, int min_tpr, int sms, RingPlan *plan) {
+               int most, int min_tpr, int sms, RingPlan *plan, int prefer = 0) {
     const int V = 16 / es;
     RingArgs &r = plan->r;
     r = RingArgs{};
@@ -1054,7 +1055,7 @@ bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, 
     // As many chunks a thread as its registers hold: rows side by side cost fewer
     // barriers than rows one after the other (bf16 4096 x 4096 gradient: 34.6 us
     // with 4 chunks, 50.3 with 1) ...
-    const int usual = most == 5 ? 4 : 32 / V;
+    const int usual = prefer ? prefer : most == 5 ? 4 : 32 / V;
     int tpr = min_tpr;
     while (tpr < kRingThreads && static_cast<int64_t>(tpr) * usual < chunks) tpr *= 2;
     if (static_cast<int64_t>(tpr) * most < chunks) return false;
