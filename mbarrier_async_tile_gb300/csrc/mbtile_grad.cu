@@ -21,6 +21,7 @@
 #include "mbtile_elem.cuh"
 #include "mbtile_layer.h"
 #include "mbtile_ptx.cuh"
+#include "mbtile_tcgen05.cuh"
 
 namespace mbt {
 namespace {
@@ -29,6 +30,11 @@ constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;                          // 16-byte vectors of a thread and chunk
 constexpr int kGradChunk = kGradThreads * kGradVecs;  // vectors
 constexpr int kGradCtas = 6;                          // per SM
+constexpr int kScaleCtas = 8;
+constexpr int kGradCluster = 8;                       // CTAs that few chunks are dealt to
+// Chunks that one cluster takes (us, cluster / grid, fp32: 100 elements 3.0 / 4.1, 50,000 4.0 /
+// 5.1, 100,000 4.9 / 5.2, 200,000 6.1 / 4.7).
+constexpr int64_t kGradFewChunks = 24;
 // A launch's parameters hold at most 32764 bytes; few tensors take the small table,
 // whose launch has less to send.
 constexpr int kGradSmallTable = 32;
@@ -137,24 +143,40 @@ __device__ __forceinline__ int grad_find(const GradTable<TABLE> &g, uint32_t c, 
     return lo;
 }
 
-// The sum over the CTA, in thread 0.
+// The sum over the CTA, in its first warp.
 __device__ __forceinline__ double block_sum(double v, double *red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
-    if (threadIdx.x == 0)
-        for (int k = 0; k < kGradThreads / 32; ++k) v += red[k];
+    if (threadIdx.x >= 32) return 0.0;
+    v = red[threadIdx.x & (kGradThreads / 32 - 1)];
+#pragma unroll
+    for (int o = kGradThreads / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-template <int TABLE>
+// The norm and the factor from the sum of all squares.
+__device__ __forceinline__ void grad_finish(const GradArgs &a, double sum) {
+    const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+    const float norm = static_cast<float>(sqrt(sum) * fabs(static_cast<double>(gs)));
+    *a.norm = norm;
+    if (a.scale) {
+        const float clip = isinf(a.max_norm) ? 1.f : __fdiv_rn(a.max_norm, norm + a.eps);
+        *a.scale = clip >= 1.f ? gs : gs * clip;       // (a NaN norm gives a NaN factor)
+    }
+}
+
+// CLUSTER: a grid of one cluster, whose first CTA adds up the others' sums: a call of few
+// chunks waits for no tickets and no memory but its gradients'.
+template <int TABLE, bool CLUSTER>
 __global__ void __launch_bounds__(kGradThreads, kGradCtas)
     mbt_grad_norm_kernel(const __grid_constant__ GradTable<TABLE> g) {
     __shared__ double red[kGradThreads / 32];
+    __shared__ double parts[kGradCluster];
     __shared__ int is_last;
+    if constexpr (CLUSTER) cluster_arrive();           // this CTA is there
     const GradArgs &a = g.a;
     const uint32_t chunks = a.count ? g.end[a.count - 1] : 0;
     const int64_t c0 = blockIdx.x * a.per, c1 = min(c0 + a.per, static_cast<int64_t>(chunks));
@@ -188,6 +210,19 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas)
         }
     }
     const double mine = block_sum(wide + static_cast<double>(sum), red);
+    if constexpr (CLUSTER) {
+        cluster_wait();
+        if (threadIdx.x == 0)
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(cluster_address(smem_u32(&parts[blockIdx.x]), 0)), "d"(mine)
+                         : "memory");
+        cluster_sync();
+        if (blockIdx.x != 0 || threadIdx.x >= 32) return;
+        double all = parts[threadIdx.x & (kGradCluster - 1)];
+#pragma unroll
+        for (int o = kGradCluster / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        if (threadIdx.x == 0) grad_finish(a, all);
+        return;
+    }
     if (threadIdx.x == 0) a.partial[blockIdx.x] = mine;
     if (!a.last) return;
     // the library's other set of tickets is cleared for the next call
@@ -206,13 +241,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas)
     all = block_sum(all, red);
     if (threadIdx.x != 0) return;
     *a.ticket = 0;             // for a replay of this launch
-    const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-    const float norm = static_cast<float>(sqrt(all) * fabs(static_cast<double>(gs)));
-    *a.norm = norm;
-    if (a.scale) {
-        const float clip = isinf(a.max_norm) ? 1.f : __fdiv_rn(a.max_norm, norm + a.eps);
-        *a.scale = clip >= 1.f ? gs : gs * clip;       // (a NaN norm gives a NaN factor)
-    }
+    grad_finish(a, all);
 }
 
 template <int DT>
@@ -225,7 +254,7 @@ __device__ __forceinline__ uint4 times(const uint4 &v, float by) {
 }
 
 template <int TABLE>
-__global__ void __launch_bounds__(kGradThreads, kGradCtas)
+__global__ void __launch_bounds__(kGradThreads, kScaleCtas)
     mbt_grad_scale_kernel(const __grid_constant__ GradTable<TABLE> g) {
     const GradArgs &a = g.a;
     const uint32_t chunks = a.count ? g.end[a.count - 1] : 0;
@@ -315,17 +344,40 @@ int64_t fill_table(const mbt_grad *grads, int64_t count, int64_t *k, GradTable<T
 }
 
 // CTAs and chunks of each.
-int grid_of(int64_t chunks, int sms, int64_t *per) {
-    *per = std::max<int64_t>(1, (chunks + static_cast<int64_t>(kGradCtas) * sms - 1) / (static_cast<int64_t>(kGradCtas) * sms));
+int grid_of(int64_t chunks, int64_t ctas, int64_t *per) {
+    *per = std::max<int64_t>(1, (chunks + ctas - 1) / ctas);
     return static_cast<int>(std::max<int64_t>(1, (chunks + *per - 1) / *per));
 }
 
 template <int TABLE>
 int run_norm(const mbt_grad *grads, int64_t count, GradArgs a, int sms, cudaStream_t s) {
-    // launches of the call, and its CTAs in all
     GradTable<TABLE> g;
+    if (TABLE == kGradSmallTable) {
+        int64_t k = 0;
+        const int64_t chunks = fill_table(grads, count, &k, &g);
+        if (chunks <= kGradFewChunks) {
+            a.per = (chunks + kGradCluster - 1) / kGradCluster;
+            const int32_t filled = g.a.count;
+            g.a = a;
+            g.a.count = filled;
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(kGradCluster);
+            cfg.blockDim = dim3(kGradThreads);
+            cfg.stream = s;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = kGradCluster;
+            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            return cudaLaunchKernelEx(&cfg, mbt_grad_norm_kernel<TABLE, true>, g) == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
+        }
+    }
+    // launches of the call, and its CTAs in all
     int64_t launches = 0, ctas = 0;
-    for (int64_t k = 0; k < count || launches == 0; ++launches) ctas += grid_of(fill_table(grads, count, &k, &g), sms, &a.per);
+    for (int64_t k = 0; k < count || launches == 0; ++launches) ctas += grid_of(fill_table(grads, count, &k, &g), kGradCtas * sms, &a.per);
     WorkspaceHold hold;
     int rc = hold.take(s, 1, static_cast<size_t>(ctas) * 8);
     if (rc != MBT_OK) return rc;
@@ -337,8 +389,8 @@ int run_norm(const mbt_grad *grads, int64_t count, GradArgs a, int sms, cudaStre
         g.a = a;
         g.a.partial = all + a.before;
         g.a.last = l + 1 == launches;
-        const int grid = grid_of(fill_table(grads, count, &k, &g), sms, &g.a.per);
-        if (launch_grid(mbt_grad_norm_kernel<TABLE>, dim3(static_cast<unsigned>(grid)), kGradThreads, s, g) != cudaSuccess)
+        const int grid = grid_of(fill_table(grads, count, &k, &g), kGradCtas * sms, &g.a.per);
+        if (launch_grid(mbt_grad_norm_kernel<TABLE, false>, dim3(static_cast<unsigned>(grid)), kGradThreads, s, g) != cudaSuccess)
             return MBT_ERR_CUDA;
         a.before += grid;
     }
@@ -352,7 +404,7 @@ int run_scale(const mbt_grad *grads, int64_t count, const GradArgs &a, int sms, 
     for (int64_t k = 0; k < count;) {
         const int64_t chunks = fill_table(grads, count, &k, &g);
         if (chunks == 0) break;
-        const int grid = grid_of(chunks, sms, &g.a.per);
+        const int grid = grid_of(chunks, kScaleCtas * sms, &g.a.per);
         if (launch_grid(mbt_grad_scale_kernel<TABLE>, dim3(static_cast<unsigned>(grid)), kGradThreads, s, g) != cudaSuccess)
             return MBT_ERR_CUDA;
     }

@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             for (int e = 0; e < V; ++e) sum += h[c][e];
         row_reduce<false>(sum, amax, r.tpr, sh.red[0], turn);
         turn ^= 1;
-        const float mean = sum * inv_n;
+        const float mean = __fdiv_rn(sum, static_cast<float>(a.N));   // (rows of one value: that value)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if (c < have && write_res) th.put(res + c * chunk, c, h[c]);
@@ -837,11 +837,15 @@ int ln_backward_by_ring(LayerNormGradArgs a, cudaStream_t s, int sms, bool *done
     return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
 }
 
-// Where the ring is faster than a row in registers: as in the root-mean-square norm.
-bool ln_ring_pays(const LayerNormArgs &a, int64_t es, int sms, int phase) {
-    const int64_t row = a.N * es;
-    if (a.M * row < (16ll << 20) || a.M < 4 * sms || row <= 1024) return false;
-    return row > 4096 || !a.res || phase != 0 || a.quant != MBT_QUANT_NONE;
+// Where the ring is faster than a row in registers (us, ring / registers): its start is paid
+// once a call, so with enough rows, of whatever length: bf16 with a residual 131072 x 512 96
+// / 113, 8192 x 8192 85 / 128, 512 x 8192 10.2 / 12.5, 256 x 8192 7.1 / 7.0, 2000 x 512 6.6 /
+// 4.4; without, 131072 x 256 31 / 48, 65537 x 1001 110 / 141, 304 x 8192 by groups of 128 to
+// e4m3 7.0 / 7.7, 1000 x 1001 8.9 / 4.0.  Long fp32 rows, whose weights it reads each time, ask
+// for several turns (152 x 16384 12.7 / 9.8).
+bool ln_ring_pays(const LayerNormArgs &a, int64_t es, int sms) {
+    const bool long_rows = es == 4 && a.N > 5 * 4 * kRingThreads;
+    return a.M * a.N * es >= (5ll << 20) && (!long_rows || a.M >= 4 * sms);
 }
 
 template <int DT, int C>
@@ -872,7 +876,7 @@ cudaError_t ln_forward_any(const LayerNormArgs &a, cudaStream_t s) {
     const void *in[2] = {a.x, a.res};
     const int64_t ld[2] = {a.ld_x, a.ld_res};
     RingPlan p;
-    if (same && ln_ring_pays(a, es, sms, ph) &&
+    if (same && ln_ring_pays(a, es, sms) &&
         ln_ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, a.quant > 0 ? 32 : 8, sms, false, &p)) {
         if (device_status_word(&p.r.status) != MBT_OK) return cudaErrorUnknown;
         p.r.wmode = weight_mode(a.w, a.wdt, DT);
