@@ -168,6 +168,7 @@ def _load():
         lib.tile_layernorm.argtypes = [vp] * 9 + [i64] * 6 + [i32] * 3 + [f32, f32, vp]
         lib.tile_layernorm_backward.argtypes = [vp] * 9 + [i64] * 6 + [i32] * 2 + [f32, vp]
         lib.tile_grad_norm.argtypes = [vp, i64, vp, f32, f32, vp, vp, vp]
+        lib.tile_grad_clip.argtypes = lib.tile_grad_norm.argtypes
         lib.tile_grad_scale.argtypes = [vp, i64, vp, vp]
         lib.tile_adamw.argtypes = ([vp, i64, i32, i32, i32, i64] + [f64] * 5 +
                                    [vp, ctypes.c_uint32, vp])
@@ -180,7 +181,7 @@ def _load():
                      "tile_colsum", "tile_colsum_ex", "tile_colsum_workspace_bytes",
                      "tile_rmsnorm", "tile_rmsnorm_backward", "tile_w4_matvec", "tile_adamw",
                      "tile_mx4_quantize", "tile_mx4_dequantize", "tile_mx4_matmul",
-                     "tile_grad_norm", "tile_grad_scale", "tile_layernorm", "tile_layernorm_backward"):
+                     "tile_grad_norm", "tile_grad_clip", "tile_grad_scale", "tile_layernorm", "tile_layernorm_backward"):
             getattr(lib, name).restype = ctypes.c_int
         _C = lib
         return lib

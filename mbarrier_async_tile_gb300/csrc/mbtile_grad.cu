@@ -5,10 +5,11 @@
 //
 // The norm reads every byte once, the product reads and writes it: device memory bounds
 // both.  A launch takes a table of tensors as a kernel parameter.  The tensors' 16-byte
-// vectors are cut into chunks of kGradVecs a thread, the chunks dealt to a grid of whole
-// CTAs per SM in spans, so that a CTA finds its first tensor once and steps to the next;
-// what lies before a tensor's first aligned vector and behind its last (at most 7 elements
-// each) goes with its first chunk.
+// vectors are cut into chunks of kGradVecs a thread; the norm's are dealt to a grid of whole
+// CTAs per SM in spans, so that a CTA finds its first tensor once and steps to the next, and
+// few sums are left to add up.  What lies before a tensor's first aligned vector and behind
+// its last (at most 7 elements each) goes with its first chunk.  Calls of few chunks are
+// one cluster, which also multiplies by the factor that it has found.
 //
 // A thread sums squares in fp32.  Where a chunk's sum leaves 2^-100 .. 2^100, in which
 // squares neither overflow nor lose their last bits, it takes the chunk again in 64
@@ -27,14 +28,13 @@ namespace mbt {
 namespace {
 
 constexpr int kGradThreads = 256;
-constexpr int kGradVecs = 4;                          // 16-byte vectors of a thread and chunk
+constexpr int kGradVecs = 8;                          // 16-byte vectors of a thread and chunk
 constexpr int kGradChunk = kGradThreads * kGradVecs;  // vectors
-constexpr int kGradCtas = 6;                          // per SM
-constexpr int kScaleCtas = 8;
+constexpr int kGradCtas = 4;                          // per SM
 constexpr int kGradCluster = 8;                       // CTAs that few chunks are dealt to
 // Chunks that one cluster takes (us, cluster / grid, fp32: 100 elements 3.0 / 4.1, 50,000 4.0 /
 // 5.1, 100,000 4.9 / 5.2, 200,000 6.1 / 4.7).
-constexpr int64_t kGradFewChunks = 24;
+constexpr int64_t kGradFewChunks = 16;
 // A launch's parameters hold at most 32764 bytes; few tensors take the small table,
 // whose launch has less to send.
 constexpr int kGradSmallTable = 32;
@@ -48,6 +48,7 @@ struct GradTensor {
 struct GradArgs {
     int32_t count;
     int32_t last;              // the call's last launch: sums all partials
+    int32_t clip;              // a cluster's launch: multiply, too
     int64_t per;               // chunks a CTA
     double *partial;           // of this launch's CTAs; the call's first are `before` earlier
     int64_t before;
@@ -157,16 +158,67 @@ __device__ __forceinline__ double block_sum(double v, double *red) {
     return v;
 }
 
-// The norm and the factor from the sum of all squares.
-__device__ __forceinline__ void grad_finish(const GradArgs &a, double sum) {
-    const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+// The norm and the factor from the sum of all squares; write: to memory, too.
+__device__ __forceinline__ float grad_finish(const GradArgs &a, double sum, float gs, bool write) {
     const float norm = static_cast<float>(sqrt(sum) * fabs(static_cast<double>(gs)));
-    *a.norm = norm;
-    if (a.scale) {
-        const float clip = isinf(a.max_norm) ? 1.f : __fdiv_rn(a.max_norm, norm + a.eps);
-        *a.scale = clip >= 1.f ? gs : gs * clip;       // (a NaN norm gives a NaN factor)
+    const float clip = isinf(a.max_norm) ? 1.f : __fdiv_rn(a.max_norm, norm + a.eps);
+    const float by = clip >= 1.f ? gs : gs * clip;     // (a NaN norm gives a NaN factor)
+    if (write) {
+        *a.norm = norm;
+        if (a.scale) *a.scale = by;
     }
+    return by;
 }
+
+template <int DT>
+__device__ __forceinline__ uint4 times(const uint4 &v, float by) {
+    float f[Elem<DT>::kVec];
+    unpack<DT>(v, f);
+#pragma unroll
+    for (int e = 0; e < Elem<DT>::kVec; ++e) f[e] *= by;
+    return pack<DT>(f);
+}
+
+// A chunk times a factor.
+struct GradChunk {
+    GradSpan s;
+    char *p;
+    int64_t n, chunk, first;
+    int type;
+    template <int TABLE>
+    __device__ __forceinline__ GradChunk(const GradTable<TABLE> &g, int k, int64_t c) {
+        type = g.type[k], p = g.t[k].p, n = g.t[k].n;
+        s = grad_span(p, n, type == MBT_F32 ? 4 : 2);
+        chunk = c - (k ? g.end[k - 1] : 0u);
+        first = chunk * kGradChunk + threadIdx.x;
+    }
+    // (not a read-only load: the vectors are written later)
+    __device__ __forceinline__ void load(uint4 (&v)[kGradVecs]) const {
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int64_t at = first + i * kGradThreads;
+            v[i] = at < s.vecs ? reinterpret_cast<const uint4 *>(s.vec)[at] : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    // This thread's element before or behind the vectors, with the first chunk; -1: none.
+    __device__ __forceinline__ int64_t edge() const {
+        const int i = threadIdx.x;
+        if (chunk != 0 || i >= s.head + s.tail) return -1;
+        return i < s.head ? i : n - s.tail + i - s.head;
+    }
+    __device__ __forceinline__ void scale(const uint4 (&v)[kGradVecs], float by) const {
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int64_t at = first + i * kGradThreads;
+            if (at >= s.vecs) continue;
+            reinterpret_cast<uint4 *>(s.vec)[at] = type == MBT_F32    ? times<MBT_F32>(v[i], by)
+                                                   : type == MBT_BF16 ? times<MBT_BF16>(v[i], by)
+                                                                      : times<MBT_F16>(v[i], by);
+        }
+        const int64_t at = edge();
+        if (at >= 0) store_any(p, type, at, load_any(p, type, at) * by);
+    }
+};
 
 // CLUSTER: a grid of one cluster, whose first CTA adds up the others' sums: a call of few
 // chunks waits for no tickets and no memory but its gradients'.
@@ -186,15 +238,10 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int64_t c = c0; c < c1; ++c) {
         while (g.end[k] <= c) ++k;
-        const int type = g.type[k], es = type == MBT_F32 ? 4 : 2;
-        const GradSpan s = grad_span(g.t[k].p, g.t[k].n, es);
-        const int64_t chunk = c - (k ? g.end[k - 1] : 0u), first = chunk * kGradChunk + threadIdx.x;
+        const GradChunk at(g, k, c);
         uint4 v[kGradVecs];
-#pragma unroll
-        for (int i = 0; i < kGradVecs; ++i) {
-            const int64_t at = first + i * kGradThreads;
-            v[i] = at < s.vecs ? __ldg(reinterpret_cast<const uint4 *>(s.vec) + at) : make_uint4(0u, 0u, 0u, 0u);
-        }
+        at.load(v);
+        const int type = at.type;
         bool any;
         const float sq = type == MBT_F32    ? chunk_squares<MBT_F32>(v, any)
                          : type == MBT_BF16 ? chunk_squares<MBT_BF16>(v, any)
@@ -202,25 +249,38 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas)
         if (sq > 0x1p-100f && sq < 0x1p100f)
             sum += sq;
         else if (any)
-            wide += wide_squares(s.vec, first, s.vecs, type);
-        if (chunk == 0 && static_cast<int>(threadIdx.x) < s.head + s.tail) {
-            const int i = threadIdx.x;
-            const float f = load_any(g.t[k].p, type, i < s.head ? i : g.t[k].n - s.tail + i - s.head);
+            wide += wide_squares(at.s.vec, at.first, at.s.vecs, type);
+        const int64_t edge = at.edge();
+        if (edge >= 0) {
+            const float f = load_any(at.p, type, edge);
             wide += static_cast<double>(f) * f;
         }
     }
     const double mine = block_sum(wide + static_cast<double>(sum), red);
+    const float gs = a.grad_scale ? *a.grad_scale : 1.f;
     if constexpr (CLUSTER) {
+        // every CTA gets all sums (the factor may be written where grad_scale was read)
         cluster_wait();
-        if (threadIdx.x == 0)
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(cluster_address(smem_u32(&parts[blockIdx.x]), 0)), "d"(mine)
+        if (threadIdx.x < kGradCluster) {
+            const double sent = __shfl_sync((1u << kGradCluster) - 1, mine, 0);
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(cluster_address(smem_u32(&parts[blockIdx.x]), threadIdx.x)),
+                         "d"(sent)
                          : "memory");
+        }
+        __syncwarp();
         cluster_sync();
-        if (blockIdx.x != 0 || threadIdx.x >= 32) return;
         double all = parts[threadIdx.x & (kGradCluster - 1)];
 #pragma unroll
         for (int o = kGradCluster / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        if (threadIdx.x == 0) grad_finish(a, all);
+        const float by = grad_finish(a, all, gs, blockIdx.x == 0 && threadIdx.x == 0);
+        if (!a.clip) return;
+        for (int64_t c = c1 - 1; c >= c0; --c) {
+            while (k > 0 && g.end[k - 1] > c) --k;
+            const GradChunk at(g, k, c);
+            uint4 v[kGradVecs];
+            at.load(v);
+            at.scale(v, by);
+        }
         return;
     }
     if (threadIdx.x == 0) a.partial[blockIdx.x] = mine;
@@ -241,53 +301,22 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas)
     all = block_sum(all, red);
     if (threadIdx.x != 0) return;
     *a.ticket = 0;             // for a replay of this launch
-    grad_finish(a, all);
+    grad_finish(a, all, gs, true);
 }
 
-template <int DT>
-__device__ __forceinline__ uint4 times(const uint4 &v, float by) {
-    float f[Elem<DT>::kVec];
-    unpack<DT>(v, f);
-#pragma unroll
-    for (int e = 0; e < Elem<DT>::kVec; ++e) f[e] *= by;
-    return pack<DT>(f);
-}
-
+// A chunk a CTA, whose loads are all under way before the first is used.  (By a grid of
+// whole CTAs per SM, as the norm's: bf16 300 M elements 198 us, 6.1 TB/s.)  From the end on:
+// what the norm's kernel has read last is still in L2.
 template <int TABLE>
-__global__ void __launch_bounds__(kGradThreads, kScaleCtas)
-    mbt_grad_scale_kernel(const __grid_constant__ GradTable<TABLE> g) {
+__global__ void __launch_bounds__(kGradThreads) mbt_grad_scale_kernel(const __grid_constant__ GradTable<TABLE> g) {
     const GradArgs &a = g.a;
-    const uint32_t chunks = a.count ? g.end[a.count - 1] : 0;
-    const int64_t c0 = blockIdx.x * a.per, c1 = min(c0 + a.per, static_cast<int64_t>(chunks));
-    int k = c0 < c1 ? grad_find<TABLE>(g, static_cast<uint32_t>(c1 - 1), 0) : 0;
+    const uint32_t c = gridDim.x - 1 - blockIdx.x;
+    const int k = grad_find<TABLE>(g, c, 0);
+    const GradChunk at(g, k, c);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float by = *a.scale;
-    // from the span's end: what the norm's kernel has read last is still in L2
-    for (int64_t c = c1 - 1; c >= c0; --c) {
-        while (k > 0 && g.end[k - 1] > c) --k;
-        const int type = g.type[k], es = type == MBT_F32 ? 4 : 2;
-        const GradSpan s = grad_span(g.t[k].p, g.t[k].n, es);
-        const int64_t chunk = c - (k ? g.end[k - 1] : 0u), first = chunk * kGradChunk + threadIdx.x;
-        uint4 *p = reinterpret_cast<uint4 *>(s.vec);
-        uint4 v[kGradVecs];
-#pragma unroll
-        for (int i = 0; i < kGradVecs; ++i) {
-            const int64_t at = first + i * kGradThreads;
-            if (at < s.vecs) v[i] = p[at];
-        }
-#pragma unroll
-        for (int i = 0; i < kGradVecs; ++i) {
-            const int64_t at = first + i * kGradThreads;
-            if (at >= s.vecs) continue;
-            p[at] = type == MBT_F32 ? times<MBT_F32>(v[i], by) : type == MBT_BF16 ? times<MBT_BF16>(v[i], by)
-                                                                                  : times<MBT_F16>(v[i], by);
-        }
-        if (chunk == 0 && static_cast<int>(threadIdx.x) < s.head + s.tail) {
-            const int i = threadIdx.x;
-            const int64_t at = i < s.head ? i : g.t[k].n - s.tail + i - s.head;
-            store_any(g.t[k].p, type, at, load_any(g.t[k].p, type, at) * by);
-        }
-    }
+    uint4 v[kGradVecs];
+    at.load(v);
+    at.scale(v, *a.scale);
 }
 
 int es_of(int dtype) { return dtype == MBT_F32 ? 4 : 2; }
@@ -350,7 +379,7 @@ int grid_of(int64_t chunks, int64_t ctas, int64_t *per) {
 }
 
 template <int TABLE>
-int run_norm(const mbt_grad *grads, int64_t count, GradArgs a, int sms, cudaStream_t s) {
+int run_norm(const mbt_grad *grads, int64_t count, GradArgs a, int sms, cudaStream_t s, bool *clipped) {
     GradTable<TABLE> g;
     if (TABLE == kGradSmallTable) {
         int64_t k = 0;
@@ -360,6 +389,7 @@ int run_norm(const mbt_grad *grads, int64_t count, GradArgs a, int sms, cudaStre
             const int32_t filled = g.a.count;
             g.a = a;
             g.a.count = filled;
+            *clipped = a.clip != 0;
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(kGradCluster);
             cfg.blockDim = dim3(kGradThreads);
@@ -398,14 +428,13 @@ int run_norm(const mbt_grad *grads, int64_t count, GradArgs a, int sms, cudaStre
 }
 
 template <int TABLE>
-int run_scale(const mbt_grad *grads, int64_t count, const GradArgs &a, int sms, cudaStream_t s) {
+int run_scale(const mbt_grad *grads, int64_t count, const GradArgs &a, cudaStream_t s) {
     GradTable<TABLE> g;
     g.a = a;
     for (int64_t k = 0; k < count;) {
         const int64_t chunks = fill_table(grads, count, &k, &g);
         if (chunks == 0) break;
-        const int grid = grid_of(chunks, kScaleCtas * sms, &g.a.per);
-        if (launch_grid(mbt_grad_scale_kernel<TABLE>, dim3(static_cast<unsigned>(grid)), kGradThreads, s, g) != cudaSuccess)
+        if (launch_grid(mbt_grad_scale_kernel<TABLE>, dim3(static_cast<unsigned>(chunks)), kGradThreads, s, g) != cudaSuccess)
             return MBT_ERR_CUDA;
     }
     return MBT_OK;
@@ -414,14 +443,25 @@ int run_scale(const mbt_grad *grads, int64_t count, const GradArgs &a, int sms, 
 }  // namespace
 }  // namespace mbt
 
-extern "C" int tile_grad_norm(const mbt_grad *grads, int64_t count, const float *grad_scale, float max_norm, float eps,
-                              float *norm, float *scale, void *stream) {
-    using namespace mbt;
+namespace mbt {
+namespace {
+
+int scale_all(const mbt_grad *grads, int64_t count, const float *scale, cudaStream_t s) {
+    GradArgs a{};
+    a.scale = const_cast<float *>(scale);
+    return count <= kGradSmallTable ? run_scale<kGradSmallTable>(grads, count, a, s)
+                                    : run_scale<kGradLargeTable>(grads, count, a, s);
+}
+
+int norm_all(const mbt_grad *grads, int64_t count, const float *grad_scale, float max_norm, float eps, float *norm,
+             float *scale, bool clip, cudaStream_t s) {
     int rc = check_grads(grads, count);
     if (rc != MBT_OK) return rc;
-    if (!norm || !(max_norm >= 0.f) || !(eps >= 0.f)) return MBT_ERR_ARG;
+    if (!norm || (clip && !scale) || !(max_norm >= 0.f) || !(eps >= 0.f)) return MBT_ERR_ARG;
     for (const void *p : {static_cast<const void *>(grad_scale), static_cast<const void *>(norm), static_cast<const void *>(scale)})
         if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return MBT_ERR_ALIGN;
+    bool known = false;
+    if (clip && !apart(grads, count, &known)) return known ? MBT_ERR_ARG : MBT_ERR_CUDA;
     int sms = 0, optin = 0;
     rc = device_limits(&sms, &optin);
     if (rc != MBT_OK) return rc;
@@ -431,26 +471,34 @@ extern "C" int tile_grad_norm(const mbt_grad *grads, int64_t count, const float 
     a.scale = scale;
     a.max_norm = max_norm;
     a.eps = eps;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return count <= kGradSmallTable ? run_norm<kGradSmallTable>(grads, count, a, sms, s)
-                                    : run_norm<kGradLargeTable>(grads, count, a, sms, s);
+    a.clip = clip;
+    bool clipped = false;
+    rc = count <= kGradSmallTable ? run_norm<kGradSmallTable>(grads, count, a, sms, s, &clipped)
+                                  : run_norm<kGradLargeTable>(grads, count, a, sms, s, &clipped);
+    return rc == MBT_OK && clip && !clipped ? scale_all(grads, count, scale, s) : rc;
+}
+
+}  // namespace
+}  // namespace mbt
+
+extern "C" int tile_grad_norm(const mbt_grad *grads, int64_t count, const float *grad_scale, float max_norm, float eps,
+                              float *norm, float *scale, void *stream) {
+    return mbt::norm_all(grads, count, grad_scale, max_norm, eps, norm, scale, false, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int tile_grad_clip(const mbt_grad *grads, int64_t count, const float *grad_scale, float max_norm, float eps,
+                              float *norm, float *scale, void *stream) {
+    return mbt::norm_all(grads, count, grad_scale, max_norm, eps, norm, scale, true, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int tile_grad_scale(const mbt_grad *grads, int64_t count, const float *scale, void *stream) {
     using namespace mbt;
-    int rc = check_grads(grads, count);
+    const int rc = check_grads(grads, count);
     if (rc != MBT_OK) return rc;
     if (count == 0) return MBT_OK;
     if (!scale) return MBT_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(scale) % 4 != 0) return MBT_ERR_ALIGN;
     bool known = false;
     if (!apart(grads, count, &known)) return known ? MBT_ERR_ARG : MBT_ERR_CUDA;
-    int sms = 0, optin = 0;
-    rc = device_limits(&sms, &optin);
-    if (rc != MBT_OK) return rc;
-    GradArgs a{};
-    a.scale = const_cast<float *>(scale);
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return count <= kGradSmallTable ? run_scale<kGradSmallTable>(grads, count, a, sms, s)
-                                    : run_scale<kGradLargeTable>(grads, count, a, sms, s);
+    return scale_all(grads, count, scale, static_cast<cudaStream_t>(stream));
 }

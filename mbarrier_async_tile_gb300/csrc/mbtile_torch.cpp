@@ -712,16 +712,14 @@ PyObject *grad_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const at::Tensor norm = scalar(a[4], "norm", device), scale = scalar(a[5], "scale", device);
         float *to = static_cast<float *>(scale.data_ptr());
-        if (!check(tile_grad_norm(list.data(), count, gs, static_cast<float>(most), static_cast<float>(eps),
-                                  static_cast<float *>(norm.data_ptr()), to, stream),
-                   "tile_grad_norm"))
-            return nullptr;
+        const int rc = (in_place ? tile_grad_clip : tile_grad_norm)(list.data(), count, gs, static_cast<float>(most),
+                                                                    static_cast<float>(eps),
+                                                                    static_cast<float *>(norm.data_ptr()), to, stream);
+        if (!check(rc, in_place ? "tile_grad_clip" : "tile_grad_norm")) return nullptr;
         written(norm);
         written(scale);
-        if (in_place) {
-            if (!check(tile_grad_scale(list.data(), count, to, stream), "tile_grad_scale")) return nullptr;
+        if (in_place)
             for (Py_ssize_t k = 0; k < count; ++k) written(tensor(PySequence_Fast_GET_ITEM(grads, k), "grads"));
-        }
         return Py_BuildValue("(NN)", wrap(norm), wrap(scale));
     });
     Py_DECREF(grads);

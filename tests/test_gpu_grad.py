@@ -176,8 +176,25 @@ def test_given_outputs_refusals_and_versions():
         mbt.tile_grad_norm([g], max_norm=-1.0)
 
 
-def test_streams_graphs_and_threads():
-    grads = tensors([3000, 70001, 12], ("f32", "bf16"), 12)
+@pytest.mark.parametrize("factor", [0.5, -2.0])
+@pytest.mark.parametrize("sizes", [[1000, 33], [3_000_001, 17]], ids=["cluster", "grid"])
+def test_factor_written_where_it_was_read(sizes, factor):
+    """One tensor as grad_scale and as scale."""
+    grads = tensors(sizes, ("f32", "bf16"), 14)
+    before = [g.clone() for g in grads]
+    for most in (1e-3, 1e9):
+        for g, b in zip(grads, before):
+            g.copy_(b)
+        scale = torch.full((1,), factor, device="cuda")
+        got = mbt.tile_clip_grads(grads, most, grad_scale=scale, scale=scale)
+        check(before, got, most, factor)
+        for g, b in zip(grads, before):
+            assert torch.equal(g, (b.float() * scale).to(g.dtype))
+
+
+@pytest.mark.parametrize("sizes", [[3000, 70001, 12], [5_000_000, 33, 70001]], ids=["cluster", "grid"])
+def test_streams_and_graphs(sizes):
+    grads = tensors(sizes, ("f32", "bf16"), 12)
     want = mbt.tile_grad_norm(grads, max_norm=0.1)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -51,6 +51,15 @@ def test_scale_argument_errors():
     assert mbt.C.tile_grad_scale(None, 0, None, None) == 0
 
 
+def test_clip_argument_errors():
+    t = (Grad * 2)(Grad(A, 10, 1, 0), Grad(A + 10, 10, 1, 0))
+
+    def clip(count=2, gs=0, most=1.0, eps=1e-6, norm=B, to=B + 4):
+        return mbt.C.tile_grad_clip(t, count, gs, most, eps, norm, to, None)
+
+    assert clip() == -1 and clip(count=1, to=0) == -1 and clip(count=1, most=-1.0) == -1 and clip(count=1, norm=B + 2) == -2
+
+
 def test_python_refusals():
     for grads in ([torch.zeros(3)], [torch.zeros(3, dtype=torch.int32)], torch.zeros(2, 3), [None]):
         with pytest.raises(ValueError):
