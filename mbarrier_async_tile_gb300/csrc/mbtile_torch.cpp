@@ -93,6 +93,28 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device device) 
     return at::detail::empty_cuda(shape, type, device, c10::nullopt);
 }
 
+// Small fp32 results of a call, in one allocation (each costs as much as the rest of a call
+// of one token): give() for each, in turn, of at most the elements asked for in all.
+class Together {
+public:
+    Together(at::Device device) : device_(device) {}
+    void want(int64_t elements) { total_ += padded(elements); }
+    at::Tensor give(at::IntArrayRef shape) {
+        if (!flat_.defined()) flat_ = empty({total_}, at::kFloat, device_);
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(flat_.storage()), flat_.key_set(), flat_.dtype());
+        t.unsafeGetTensorImpl()->set_storage_offset(used_);
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+        used_ += padded(t.numel());
+        return t;
+    }
+
+private:
+    static int64_t padded(int64_t n) { return (n + 31) / 32 * 32; }   // (128 bytes)
+    at::Device device_;
+    at::Tensor flat_;
+    int64_t total_ = 0, used_ = 0;
+};
+
 // Autograd is told that a tensor of the caller's was written.
 void written(const at::Tensor &t) {
     if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
@@ -315,6 +337,11 @@ PyObject *layernorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             bad("residual_out", "needs a residual");
         }
         const bool quantised = quant != MBT_QUANT_NONE;
+        const int64_t groups = quant > 0 ? (N + quant - 1) / quant : 1;
+        Together small(device);
+        if (quantised && !given(a[8])) small.want(M * groups);
+        for (int k = 10; k < 12; ++k)
+            if (!given(a[k])) small.want(M);
         const at::ScalarType out_type = quantised ? at::kFloat8_e4m3fn : type;
         if (given(a[7])) {
             out = tensor(a[7], "out");
@@ -323,12 +350,11 @@ PyObject *layernorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             out = empty({M, N}, out_type, device);
         }
         if (quantised) {
-            const int64_t groups = quant ? (N + quant - 1) / quant : 1;
             if (given(a[8])) {
                 scales = tensor(a[8], "scales");
                 sc = dense_f32(scales, "scales", {M, groups}, device);
             } else {
-                scales = empty({M, groups}, at::kFloat, device);
+                scales = small.give({M, groups});
                 sc = scales.data_ptr();
             }
         } else if (given(a[8])) {
@@ -341,7 +367,7 @@ PyObject *layernorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 stats[k] = tensor(a[10 + k], name);
                 dense_f32(stats[k], name, {M}, device);
             } else {
-                stats[k] = empty({M}, at::kFloat, device);
+                stats[k] = small.give({M});
             }
         }
         if (!check(tile_layernorm(x.data_ptr(), res, w, b, out.data_ptr(), ro, static_cast<float *>(sc),
@@ -669,9 +695,8 @@ PyObject *mx4_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// One fp32 element: the caller's tensor, or a new one.
+// A tensor of one fp32 element.
 at::Tensor scalar(PyObject *o, const char *name, at::Device device) {
-    if (!given(o)) return empty({}, at::kFloat, device);
     const at::Tensor &t = tensor(o, name);
     if (t.numel() != 1) bad(name, "must hold one element");
     dense_f32(t, name, t.sizes(), device);
@@ -710,7 +735,11 @@ PyObject *grad_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             factor = scalar(a[1], "grad_scale", device);
             gs = static_cast<const float *>(factor.data_ptr());
         }
-        const at::Tensor norm = scalar(a[4], "norm", device), scale = scalar(a[5], "scale", device);
+        Together small(device);
+        for (int k = 4; k < 6; ++k)
+            if (!given(a[k])) small.want(1);
+        const at::Tensor norm = given(a[4]) ? scalar(a[4], "norm", device) : small.give({});
+        const at::Tensor scale = given(a[5]) ? scalar(a[5], "scale", device) : small.give({});
         float *to = static_cast<float *>(scale.data_ptr());
         const int rc = (in_place ? tile_grad_clip : tile_grad_norm)(list.data(), count, gs, static_cast<float>(most),
                                                                     static_cast<float>(eps),

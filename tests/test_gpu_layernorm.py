@@ -408,3 +408,28 @@ def test_given_results_raise_their_version():
     mbt.tile_layernorm(x, w, w, x, out=out, residual_out=ro, mean=mean, rstd=rstd)
     mbt.tile_layernorm_backward(x, ro, mean, rstd, w, dx=dx, dweight=dw, dbias=db)
     assert [t._version for t in written] == [b + 1 for b in before]
+
+
+@pytest.mark.parametrize("M,N,quant", [(1, 64, None), (1, 4096, 0), (5, 1000, 64), (33, 128, 32), (0, 64, 0)])
+def test_results_of_one_allocation(M, N, quant):
+    """New statistics and scales are ordinary tensors that do not overlap, whatever is given and whatever is not."""
+    x = randn((M, N), torch.bfloat16, 110)
+    got = mbt.tile_layernorm(x, quant=quant)
+    small = [t for t in (got.scales, got.mean, got.rstd) if t is not None]
+    spans = sorted((t.data_ptr(), t.data_ptr() + 4 * t.numel()) for t in small)
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:])) and all(t.is_contiguous() for t in small)
+    copies = [t.clone() for t in small]
+    for k, t in enumerate(small):
+        t.add_(1)                                     # one at a time: the others keep their values
+        for o, c in zip(small, copies):
+            assert o is t or torch.equal(o, c)
+        t.copy_(copies[k])                            # (1 added and taken away again would leave a rounding)
+    assert [t._version for t in small] == [small[0]._version] * len(small)
+    mean = torch.empty(M, device="cuda")
+    again = mbt.tile_layernorm(x, quant=quant, mean=mean)
+    assert again.mean.data_ptr() == mean.data_ptr() and torch.equal(again.rstd, mbt.tile_layernorm(x, quant=quant).rstd)
+    with torch.inference_mode():
+        assert torch.equal(mbt.tile_layernorm(x, quant=quant).rstd, again.rstd)
+    n = mbt.tile_grad_norm([x])
+    n.scale.fill_(3.0)
+    assert torch.equal(n.norm, mbt.tile_grad_norm([x]).norm) and n.norm.shape == n.scale.shape == ()
