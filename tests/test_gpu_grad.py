@@ -219,3 +219,18 @@ def test_streams_and_graphs(sizes):
         assert torch.equal(got.norm, eager.norm) and torch.equal(got.scale, eager.scale)
         for g, f in zip(grads, fresh):
             assert torch.equal(g, (f.float() * got.scale).to(g.dtype))
+
+
+def test_past_four_gib():
+    """A tensor of more than 2^32 elements, an odd count from an odd address on."""
+    n = (1 << 32) + 12345
+    store = torch.ones(1, dtype=torch.bfloat16, device="cuda").expand(n + 2).contiguous()
+    g = store[1:-1]
+    got = mbt.tile_clip_grads([g], 1.0, eps=0.0)
+    assert abs(got.norm.item() / n ** 0.5 - 1) < 1e-6
+    v = torch.ones((), device="cuda").mul(got.scale).bfloat16()
+    assert bool((g[:1000] == v).all()) and bool((g[-1000:] == v).all()) and bool((g[n // 2:n // 2 + 1000] == v).all())
+    assert store[0] == 1 and store[-1] == 1
+    assert abs(g.view(-1)[:1 << 31].sum(dtype=torch.float64).item() / (v.double().item() * (1 << 31)) - 1) < 1e-9
+    del store, g
+    torch.cuda.empty_cache()

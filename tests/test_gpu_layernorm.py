@@ -433,3 +433,36 @@ def test_results_of_one_allocation(M, N, quant):
     n = mbt.tile_grad_norm([x])
     n.scale.fill_(3.0)
     assert torch.equal(n.norm, mbt.tile_grad_norm([x]).norm) and n.norm.shape == n.scale.shape == ()
+
+
+@pytest.mark.parametrize("M,N", [(700, 16384), (2600, 4096), (3001, 1001), (600, 12000)])
+@pytest.mark.parametrize("dtype,wdt", [("bf16", "bf16"), ("f16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+def test_many_rows_with_an_offset(M, N, dtype, wdt):
+    """weight + weight_offset in fp32, whatever the weight's type (zero-centred weights)."""
+    dt = TYPES[dtype]
+    x, dy = randn((M, N), dt, 120) + 1, randn((M, N), dt, 121)
+    w, b = randn(N, TYPES[wdt], 122, 0.01), randn(N, TYPES[wdt], 123)
+    got = mbt.tile_layernorm(x, w, b, eps=1e-5, weight_offset=1.0)
+    check_forward(x, w, b, None, got, 1e-5, 1.0, None)
+    grads = mbt.tile_layernorm_backward(dy, x, got.mean, got.rstd, w, weight_offset=1.0)
+    check_backward(dy, x, got.mean, got.rstd, w, None, *grads, 1.0)
+    q = mbt.tile_layernorm(x, w, b, eps=1e-5, weight_offset=1.0, quant=0)
+    check_forward(x, w, b, None, q, 1e-5, 1.0, 0)
+    none = mbt.tile_layernorm(x, None, eps=1e-5, weight_offset=1.0)      # (no weight: no offset)
+    check_forward(x, None, None, None, none, 1e-5, 0.0, None)
+    assert mbt.tile_status()[0] == 0
+
+
+@pytest.mark.parametrize("scale,eps", [(1e12, 1e-6), (1e17, 1e-6), (1e-15, 0.0), (1e-17, 0.0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,offset", [(64, 4096, 0), (64, 4096, 1), (2000, 1000, 0), (700, 16384, 0)])
+def test_any_magnitude(scale, eps, dtype, M, N, offset):
+    """Large and small rows, with dy along h so that the projection counts."""
+    dt = TYPES[dtype]
+    n = randn((M, N), torch.float32, 124).clamp(-3, 3)
+    h, w = pitched((n * scale).to(dt), 0, offset), 1 + randn(N, torch.float32, 125, 0.2)
+    dy = (0.7 * n + randn((M, N), torch.float32, 126, 0.5)).to(dt)
+    fwd = mbt.tile_layernorm(h, w, None, eps=eps)
+    check_forward(h, w, None, None, fwd, eps, 0.0, None)
+    got = mbt.tile_layernorm_backward(dy, h, fwd.mean, fwd.rstd, w)
+    check_backward(dy, h, fwd.mean, fwd.rstd, w, None, *got)

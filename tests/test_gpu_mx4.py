@@ -280,3 +280,34 @@ def test_pairs_pitches(pad, offset, out):
     kept = torch.ones_like(store, dtype=torch.bool)
     kept[offset:offset + M * (N + pad)].view(M, N + pad)[:, :N] = False
     assert bool((store[kept] == 7).all())
+
+
+def test_past_four_gib():
+    """Rows whose offsets pass 32 bits, of elements, codes and results."""
+    M, K = 140001, 65536
+    x = torch.ones(1, 1, dtype=torch.float16, device="cuda").expand(M, K).contiguous()
+    x[-3:] = randn((3, K), torch.float16, 50)
+    m = mbt.tile_mx4_quantize(x)
+    assert m.q.numel() > 1 << 32
+    last = mbt.tile_mx4_quantize(x[-3:])
+    assert torch.equal(m.q[-3:], last.q)
+    assert torch.equal(untile_scales(m.scales, M, K // 16)[-3:], untile_scales(last.scales, 3, K // 16))
+    back = mbt.tile_mx4_dequantize(m, dtype=torch.float16, out=x)
+    # (ones: 1 / 6 is 10.67 steps of 1 / 64, the scale 11 / 64, 1 by it 5.8, code 6: 66 / 64)
+    assert torch.equal(back[-3:], mbt.tile_mx4_dequantize(last, dtype=torch.float16)) and bool((back[:5] == 66 / 64).all())
+    del x, back
+    few, many = operand(2, K, 16, 51)[0], operand(150, K, 16, 52)[0]
+    want = mbt.tile_mx4_matmul(few, last, out_dtype=torch.float32)
+    assert torch.equal(mbt.tile_mx4_matmul(few, m, out_dtype=torch.float32)[:, -3:], want) or worst(
+        mbt.tile_mx4_matmul(few, m, out_dtype=torch.float32)[:, -3:], want.double(), 1e-3 * want.double().abs().amax()) <= 1
+    y = mbt.tile_mx4_matmul(m, many, out_dtype=torch.float32)          # by pairs; results past 2^32 bytes are rows here
+    size = mbt.tile_mx4_matmul(last, many, out_dtype=torch.float32)
+    assert worst(y[-3:], size.double(), 1e-4 * size.double().abs().amax()) <= 1
+    del m, y
+    wide = mbt.tile_mx4_matmul(operand(70001, 64, 16, 53)[0], operand(65539, 64, 16, 54)[0])   # 9 GB of results
+    a, b = operand(70001, 64, 16, 53)[1], operand(65539, 64, 16, 54)[1]
+    for rows in (slice(0, 3), slice(69990, 70001)):
+        ref = a[rows] @ b.t()
+        assert worst(wide[rows], ref, 2.0 ** -7 * ref.abs() + 1e-3 * ref.abs().amax()) <= 1
+    del wide, a, b
+    torch.cuda.empty_cache()
