@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_consta
     const T *r = static_cast<const T *>(a.res) + i * a.ld_res - off;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float h[C][V];
+    float w0[C > 1 ? 1 : V], b0[C > 1 ? 1 : V];        // one chunk a thread: its weights beside it, on their way at once
     {
         uint4 xv[C], rv[RES ? C : 1];
 #pragma unroll
@@ -140,10 +141,17 @@ __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_consta
             const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
             xv[k] = make_uint4(0, 0, 0, 0);
             if (RES) rv[k] = make_uint4(0, 0, 0, 0);
+            if constexpr (C == 1)
+#pragma unroll
+                for (int e = 0; e < V; ++e) w0[e] = b0[e] = 0.f;
             if (p >= end) continue;
             const int lo = p < off ? off : 0, hi = end - p < V ? static_cast<int>(end - p) : V;
             xv[k] = load_chunk<DT>(x + p, lo, hi);
             if (RES) rv[k] = load_chunk<DT>(r + p, lo, hi);
+            if constexpr (C == 1) {
+                load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p, off, a.N, w0);
+                load_bias<DT>(a.b, va.bmode, a.wdt, p, off, a.N, b0);
+            }
         }
 #pragma unroll
         for (int k = 0; k < C; ++k) {
@@ -187,8 +195,13 @@ __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_consta
     const float rstd = 1.f / sqrtf(row_sum(ss, 1) / n + a.eps);
     auto y_of = [&](int k, int64_t p, float (&y)[V]) {
         float b[V];
-        load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p, off, a.N, y);
-        load_bias<DT>(a.b, va.bmode, a.wdt, p, off, a.N, b);
+        if constexpr (C > 1) {
+            load_weight<DT>(a.w, va.wmode, a.wdt, a.woff, p, off, a.N, y);
+            load_bias<DT>(a.b, va.bmode, a.wdt, p, off, a.N, b);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = w0[e], b[e] = b0[e];
+        }
 #pragma unroll
         for (int e = 0; e < V; ++e) y[e] = (h[k][e] - mean) * rstd * y[e] + b[e];
     };
@@ -316,6 +329,123 @@ __global__ void __launch_bounds__(kColThreads) mbt_layernorm_dw_rows_kernel(cons
     }
     a.partial[s * a.N + j] = sw;
     a.partial[(a.splits + s) * a.N + j] = sb;
+}
+
+// Rows too long for the ring, all of whose chunks are whole but the last: a CTA holds dy and h
+// of a row in registers, C chunks a thread: dx in one pass over memory.  C = 0: rows too long
+// for that, too, are read twice (the second time from the caches).
+template <int DT, int C, bool RES>
+__global__ void __launch_bounds__(1024) mbt_layernorm_dx_kernel(const __grid_constant__ LayerNormGradArgs a,
+                                                                const int wmode) {
+    using T = typename Elem<DT>::type;
+    constexpr int V = Elem<DT>::kVec;
+    __shared__ float red[2][32];
+    const int tpr = blockDim.x, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int64_t i = blockIdx.x;
+    const T *dy = static_cast<const T *>(a.dy) + i * a.ld_dy, *h = static_cast<const T *>(a.h) + i * a.ld_h;
+    const T *dr = static_cast<const T *>(a.dres) + (RES ? i * a.ld_dres : 0);
+    T *dx = static_cast<T *>(a.dx) + i * a.ld_dx;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float mean = a.mean[i], rstd = a.rstd[i];
+    const int count = C ? C : static_cast<int>((a.N + static_cast<int64_t>(tpr) * V - 1) / (static_cast<int64_t>(tpr) * V));
+    auto part = [&](int64_t p) { return a.N - p < V ? static_cast<int>(a.N - p) : V; };   // elements of a chunk
+    uint4 vy[C ? C : 1], vh[C ? C : 1];
+    auto load = [&](int64_t p, uint4 &y, uint4 &x) {
+        y = load_chunk<DT>(dy + p, 0, part(p));
+        x = load_chunk<DT>(h + p, 0, part(p));
+    };
+    if constexpr (C > 0)
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
+            if (p < a.N) load(p, vy[k], vh[k]);
+        }
+    float level = 0.f, along = 0.f;
+#pragma unroll
+    for (int k = 0; k < count; ++k) {
+        const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
+        if (p >= a.N) continue;
+        float y[V], x[V], w[V];
+        if constexpr (C == 0) load(p, vy[0], vh[0]);
+        unpack<DT>(vy[C ? k : 0], y);
+        unpack<DT>(vh[C ? k : 0], x);
+        load_weight<DT>(a.w, wmode, a.wdt, a.woff, p, 0, a.N, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {                  // (dy is 0 past the row)
+            const float g = y[e] * w[e];
+            level += g;
+            along += g * ((x[e] - mean) * rstd);
+        }
+    }
+    level = warp_sum(level);
+    along = warp_sum(along);
+    if (lane == 0) red[0][warp] = level, red[1][warp] = along;
+    __syncthreads();
+    level = warp_sum(lane < (tpr >> 5) ? red[0][lane] : 0.f) / static_cast<float>(a.N);
+    along = warp_sum(lane < (tpr >> 5) ? red[1][lane] : 0.f) / static_cast<float>(a.N);
+#pragma unroll
+    for (int k = 0; k < count; ++k) {
+        const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
+        if (p >= a.N) continue;
+        float y[V], x[V], w[V], f[V];
+        if constexpr (RES) unpack<DT>(load_chunk<DT>(dr + p, 0, part(p)), f);
+        if constexpr (C == 0) load(p, vy[0], vh[0]);
+        unpack<DT>(vy[C ? k : 0], y);
+        unpack<DT>(vh[C ? k : 0], x);
+        load_weight<DT>(a.w, wmode, a.wdt, a.woff, p, 0, a.N, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            y[e] = rstd * (y[e] * w[e] - level - (x[e] - mean) * rstd * along) + (RES ? f[e] : 0.f);
+        store_chunk<DT>(dx + p, pack<DT>(y), 0, part(p));
+    }
+}
+
+// Such rows' partial sums of dw and db: CTA (b, s) takes 128 chunks of columns of the rows of
+// split s, a chunk a thread.
+template <int DT>
+__global__ void __launch_bounds__(kColThreads) mbt_layernorm_dw_kernel(const LayerNormGradArgs a) {
+    using T = typename Elem<DT>::type;
+    constexpr int V = Elem<DT>::kVec;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t j = (static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x) * V;
+    if (j >= a.N) return;
+    const int n = a.N - j < V ? static_cast<int>(a.N - j) : V;
+    const int64_t s = blockIdx.y, lo = s * a.M / a.splits, hi = (s + 1) * a.M / a.splits;
+    float w[V] = {}, b[V] = {};
+    for (int64_t i0 = lo; i0 < hi; i0 += 4) {
+        uint4 vy[4], vh[4];
+        float mean[4], rstd[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            vy[k] = vh[k] = make_uint4(0, 0, 0, 0);
+            mean[k] = rstd[k] = 0.f;
+            const int64_t i = i0 + k;
+            if (i >= hi) continue;
+            vy[k] = load_chunk<DT>(static_cast<const T *>(a.dy) + i * a.ld_dy + j, 0, n);
+            vh[k] = load_chunk<DT>(static_cast<const T *>(a.h) + i * a.ld_h + j, 0, n);
+            mean[k] = a.mean[i], rstd[k] = a.rstd[i];
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float tw = 0.f, tb = 0.f;                  // of four rows: a term goes through a quarter of the additions
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float y[V], x[V];
+                unpack<DT>(vy[k], y);
+                unpack<DT>(vh[k], x);
+                tw += y[e] * ((x[e] - mean[k]) * rstd[k]);
+                tb += y[e];
+            }
+            w[e] += tw;
+            b[e] += tb;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (e >= n) break;
+        a.partial[s * a.N + j + e] = w[e];
+        a.partial[(a.splits + s) * a.N + j + e] = b[e];
+    }
 }
 
 // dw (blockIdx.y 0) and db (1) from their partial sums: 32 columns a CTA, 16 threads a
@@ -903,19 +1033,38 @@ cudaError_t ln_forward_any(const LayerNormArgs &a, cudaStream_t s) {
                     : launch_ln_forward<DT, 4>(va, grid, threads, s);
 }
 
+template <int DT, int C>
+cudaError_t launch_ln_dx(const LayerNormGradArgs &a, int wmode, int threads, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.M));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return a.dres ? cudaLaunchKernelEx(&cfg, mbt_layernorm_dx_kernel<DT, C, true>, a, wmode)
+                  : cudaLaunchKernelEx(&cfg, mbt_layernorm_dx_kernel<DT, C, false>, a, wmode);
+}
+
 // Any strides and lengths: column sums of dw and db in splits of rows, then dx, which may
-// overwrite dy.
+// overwrite dy.  Rows that begin at whole chunks by chunks, with dx's in registers (bf16 1000 x
+// 24000 with a residual 178 us by elements).
 template <int DT>
 int ln_backward_any(LayerNormGradArgs a, cudaStream_t s) {
+    constexpr int V = Elem<DT>::kVec, es = 16 / V;
     int sms = 0, smem = 0;
     int rc = device_limits(&sms, &smem);
     if (rc != MBT_OK) return rc;
     bool done = false;
     rc = ln_backward_by_ring<DT>(a, s, sms, &done);
     if (rc != MBT_OK || done) return rc;
-    const int64_t cols = (a.N + kColThreads - 1) / kColThreads;
+    const bool read = phase_of(a.dy, a.ld_dy, es) == 0 && phase_of(a.h, a.ld_h, es) == 0;
+    const int64_t chunks = (a.N + V - 1) / V;
     if (a.dw || a.db) {
-        // enough CTAs of 128 columns to fill the device, at least 32 rows each
+        // enough CTAs of 128 columns (or chunks) to fill the device, at least 32 rows each
+        const int64_t cols = ((read ? chunks : a.N) + kColThreads - 1) / kColThreads;
         a.splits = std::max<int64_t>(1, std::min<int64_t>((a.M + 31) / 32, 16 * sms / cols));
         a.splits = std::min<int64_t>(a.splits, 65535);
         WorkspaceHold hold;
@@ -924,9 +1073,21 @@ int ln_backward_any(LayerNormGradArgs a, cudaStream_t s) {
         if (rc != MBT_OK) return rc;
         a.partial = static_cast<float *>(scratch);
         const dim3 grid(static_cast<unsigned>(cols), static_cast<unsigned>(a.splits));
-        cudaError_t e = launch_grid(mbt_layernorm_dw_rows_kernel<DT>, grid, kColThreads, s, a);
+        cudaError_t e = read ? launch_grid(mbt_layernorm_dw_kernel<DT>, grid, kColThreads, s, a)
+                             : launch_grid(mbt_layernorm_dw_rows_kernel<DT>, grid, kColThreads, s, a);
         if (e == cudaSuccess) e = launch_ln_finish(a, s);
         if (e != cudaSuccess) return MBT_ERR_CUDA;
+    }
+    if (read && phase_of(a.dx, a.ld_dx, es) == 0 && (!a.dres || phase_of(a.dres, a.ld_dres, es) == 0) &&
+        a.M <= 0x7fffffff) {
+        const int wmode = weight_mode(a.w, a.wdt, DT);
+        const int threads = static_cast<int>(std::min<int64_t>(1024, (chunks + 31) / 32 * 32));
+        const int64_t c = (chunks + threads - 1) / threads;
+        const cudaError_t e = c <= 1   ? launch_ln_dx<DT, 1>(a, wmode, threads, s)
+                              : c <= 2 ? launch_ln_dx<DT, 2>(a, wmode, threads, s)
+                              : c <= 4 ? launch_ln_dx<DT, 4>(a, wmode, threads, s)
+                                       : launch_ln_dx<DT, 0>(a, wmode, threads, s);
+        return e == cudaSuccess ? MBT_OK : MBT_ERR_CUDA;
     }
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.M, 1 << 20)));
     return launch_grid(mbt_layernorm_dx_rows_kernel<DT>, grid, kRowThreads, s, a) == cudaSuccess ? MBT_OK

@@ -466,3 +466,24 @@ def test_any_magnitude(scale, eps, dtype, M, N, offset):
     check_forward(h, w, None, None, fwd, eps, 0.0, None)
     got = mbt.tile_layernorm_backward(dy, h, fwd.mean, fwd.rstd, w)
     check_backward(dy, h, fwd.mean, fwd.rstd, w, None, *got)
+
+
+@pytest.mark.parametrize("M,N,pad", [(300, 24576, 0), (41, 32768, 0), (300, 20001, 7), (33, 17000, 8), (2, 32760, 0), (70, 40000, 0),
+                                     (1, 20000, 0), (100, 24001, 0)])
+@pytest.mark.parametrize("dtype,wdt", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32"), ("bf16", None)])
+@pytest.mark.parametrize("dres", [False, True])
+def test_long_rows_backward(M, N, pad, dtype, wdt, dres):
+    """Rows too long for the ring: by chunks where they begin at one, and by elements."""
+    dt = TYPES[dtype]
+    h, dy = pitched(randn((M, N), dt, 130) + 1, pad), pitched(randn((M, N), dt, 131), pad)
+    w = None if wdt is None else randn(N, TYPES[wdt], 132)
+    d = pitched(randn((M, N), dt, 133), pad) if dres else None
+    fwd = mbt.tile_layernorm(h, w)
+    given = dict(dweight=torch.empty(N, device="cuda"), dbias=torch.empty(N, device="cuda"))
+    wide = torch.zeros(M, N + pad, dtype=dt, device="cuda")
+    got = mbt.tile_layernorm_backward(dy, h, fwd.mean, fwd.rstd, w, dresidual=d, dx=wide[:, :N], **given)
+    check_backward(dy, h, fwd.mean, fwd.rstd, w, d, *got)
+    assert bool((wide[:, N:] == 0).all())
+    copy = dy.contiguous().clone()
+    again = mbt.tile_layernorm_backward(copy, h, fwd.mean, fwd.rstd, w, dresidual=d, dx=copy)
+    assert pad or torch.equal(again[0], got[0])
