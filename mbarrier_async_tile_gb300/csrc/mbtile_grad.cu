@@ -35,9 +35,10 @@ constexpr int kGradCluster = 8;                       // CTAs that few chunks ar
 // Chunks that one cluster takes (us, cluster / grid, fp32: 100 elements 3.0 / 4.1, 50,000 4.0 /
 // 5.1, 100,000 4.9 / 5.2, 200,000 6.1 / 4.7).
 constexpr int64_t kGradFewChunks = 16;
-// A launch's parameters hold at most 32764 bytes; few tensors take the small table,
-// whose launch has less to send.
+// A launch's parameters hold at most 32764 bytes; fewer tensors take a smaller table, whose
+// launch has less to send.
 constexpr int kGradSmallTable = 32;
+constexpr int kGradMiddleTable = 256;
 constexpr int kGradLargeTable = 1500;
 
 struct GradTensor {
@@ -381,7 +382,7 @@ int grid_of(int64_t chunks, int64_t ctas, int64_t *per) {
 template <int TABLE>
 int run_norm(const mbt_grad *grads, int64_t count, GradArgs a, int sms, cudaStream_t s, bool *clipped) {
     GradTable<TABLE> g;
-    if (TABLE == kGradSmallTable) {
+    if constexpr (TABLE == kGradSmallTable) {
         int64_t k = 0;
         const int64_t chunks = fill_table(grads, count, &k, &g);
         if (chunks <= kGradFewChunks) {
@@ -449,8 +450,9 @@ namespace {
 int scale_all(const mbt_grad *grads, int64_t count, const float *scale, cudaStream_t s) {
     GradArgs a{};
     a.scale = const_cast<float *>(scale);
-    return count <= kGradSmallTable ? run_scale<kGradSmallTable>(grads, count, a, s)
-                                    : run_scale<kGradLargeTable>(grads, count, a, s);
+    return count <= kGradSmallTable    ? run_scale<kGradSmallTable>(grads, count, a, s)
+           : count <= kGradMiddleTable ? run_scale<kGradMiddleTable>(grads, count, a, s)
+                                       : run_scale<kGradLargeTable>(grads, count, a, s);
 }
 
 int norm_all(const mbt_grad *grads, int64_t count, const float *grad_scale, float max_norm, float eps, float *norm,
@@ -473,8 +475,9 @@ int norm_all(const mbt_grad *grads, int64_t count, const float *grad_scale, floa
     a.eps = eps;
     a.clip = clip;
     bool clipped = false;
-    rc = count <= kGradSmallTable ? run_norm<kGradSmallTable>(grads, count, a, sms, s, &clipped)
-                                  : run_norm<kGradLargeTable>(grads, count, a, sms, s, &clipped);
+    rc = count <= kGradSmallTable    ? run_norm<kGradSmallTable>(grads, count, a, sms, s, &clipped)
+         : count <= kGradMiddleTable ? run_norm<kGradMiddleTable>(grads, count, a, sms, s, &clipped)
+                                     : run_norm<kGradLargeTable>(grads, count, a, sms, s, &clipped);
     return rc == MBT_OK && clip && !clipped ? scale_all(grads, count, scale, s) : rc;
 }
 

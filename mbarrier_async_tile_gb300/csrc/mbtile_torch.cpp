@@ -93,23 +93,28 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device device) 
     return at::detail::empty_cuda(shape, type, device, c10::nullopt);
 }
 
-// Small fp32 results of a call, in one allocation (each costs as much as the rest of a call
-// of one token): give() for each, in turn, of at most the elements asked for in all.
+// The new results of a call, of which small ones share an allocation (each costs as much
+// as the rest of a call of one token): want() for all of them, then give() for each.  Results
+// over kMost bytes in all have one each, so that a large one's memory is not held by others.
 class Together {
 public:
-    Together(at::Device device) : device_(device) {}
-    void want(int64_t elements) { total_ += padded(elements); }
-    at::Tensor give(at::IntArrayRef shape) {
-        if (!flat_.defined()) flat_ = empty({total_}, at::kFloat, device_);
-        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(flat_.storage()), flat_.key_set(), flat_.dtype());
-        t.unsafeGetTensorImpl()->set_storage_offset(used_);
+    explicit Together(at::Device device) : device_(device) {}
+    void want(int64_t elements, at::ScalarType type) { total_ += padded(elements * size(type)); }
+    at::Tensor give(at::IntArrayRef shape, at::ScalarType type) {
+        if (total_ > kMost) return empty(shape, type, device_);
+        if (!flat_.defined()) flat_ = empty({total_}, at::kByte, device_);
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(flat_.storage()), flat_.key_set(),
+                                                                c10::scalarTypeToTypeMeta(type));
+        t.unsafeGetTensorImpl()->set_storage_offset(used_ / size(type));
         t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-        used_ += padded(t.numel());
+        used_ += padded(t.numel() * size(type));
         return t;
     }
 
 private:
-    static int64_t padded(int64_t n) { return (n + 31) / 32 * 32; }   // (128 bytes)
+    static constexpr int64_t kMost = 256 << 10;
+    static int64_t size(at::ScalarType type) { return static_cast<int64_t>(c10::elementSize(type)); }
+    static int64_t padded(int64_t bytes) { return (bytes + 127) / 128 * 128; }
     at::Device device_;
     at::Tensor flat_;
     int64_t total_ = 0, used_ = 0;
@@ -322,6 +327,15 @@ PyObject *layernorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (code_of(t.scalar_type()) != wcode) bad("bias", "must have weight's type");
             b = dense(t, "bias", {N}, device);
         }
+        const bool quantised = quant != MBT_QUANT_NONE;
+        const at::ScalarType out_type = quantised ? at::kFloat8_e4m3fn : type;
+        const int64_t groups = quant > 0 ? (N + quant - 1) / quant : 1;
+        Together fresh(device);
+        if (given(a[3]) && !given(a[9])) fresh.want(M * N, type);
+        if (!given(a[7])) fresh.want(M * N, out_type);
+        if (quantised && !given(a[8])) fresh.want(M * groups, at::kFloat);
+        for (int k = 10; k < 12; ++k)
+            if (!given(a[k])) fresh.want(M, at::kFloat);
         if (given(a[3])) {
             const at::Tensor &t = tensor(a[3], "residual");
             ld_res = rows(t, "residual", M, N, type, device);
@@ -330,31 +344,24 @@ PyObject *layernorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 residual_out = tensor(a[9], "residual_out");
                 ld_ro = rows(residual_out, "residual_out", M, N, type, device);
             } else {
-                residual_out = empty({M, N}, type, device);
+                residual_out = fresh.give({M, N}, type);
             }
             ro = residual_out.data_ptr();
         } else if (given(a[9])) {
             bad("residual_out", "needs a residual");
         }
-        const bool quantised = quant != MBT_QUANT_NONE;
-        const int64_t groups = quant > 0 ? (N + quant - 1) / quant : 1;
-        Together small(device);
-        if (quantised && !given(a[8])) small.want(M * groups);
-        for (int k = 10; k < 12; ++k)
-            if (!given(a[k])) small.want(M);
-        const at::ScalarType out_type = quantised ? at::kFloat8_e4m3fn : type;
         if (given(a[7])) {
             out = tensor(a[7], "out");
             ld_out = rows(out, "out", M, N, out_type, device);
         } else {
-            out = empty({M, N}, out_type, device);
+            out = fresh.give({M, N}, out_type);
         }
         if (quantised) {
             if (given(a[8])) {
                 scales = tensor(a[8], "scales");
                 sc = dense_f32(scales, "scales", {M, groups}, device);
             } else {
-                scales = small.give({M, groups});
+                scales = fresh.give({M, groups}, at::kFloat);
                 sc = scales.data_ptr();
             }
         } else if (given(a[8])) {
@@ -367,7 +374,7 @@ PyObject *layernorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 stats[k] = tensor(a[10 + k], name);
                 dense_f32(stats[k], name, {M}, device);
             } else {
-                stats[k] = small.give({M});
+                stats[k] = fresh.give({M}, at::kFloat);
             }
         }
         if (!check(tile_layernorm(x.data_ptr(), res, w, b, out.data_ptr(), ro, static_cast<float *>(sc),
@@ -618,20 +625,23 @@ PyObject *mx4_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const float *ts = tensor_scale(a[1], device);
         if (ts && block != 16) bad("tensor_scale", "goes with blocks of 16");
         const auto shape = mx4_scales_shape(M, K, block);
+        Together fresh(device);
+        if (!given(a[3])) fresh.want(M * (K / 2), at::kByte);
+        if (!given(a[4])) fresh.want(shape[0] * shape[1] * shape[2], at::kByte);
         at::Tensor q, s;
         int64_t ld_q = 0;
         if (given(a[3])) {
             q = tensor(a[3], "q");
             ld_q = rows(q, "q", M, K / 2, at::kByte, device);
         } else {
-            q = empty({M, K / 2}, at::kByte, device);
+            q = fresh.give({M, K / 2}, at::kByte);
         }
         if (given(a[4])) {
             s = tensor(a[4], "scales");
             if (s.scalar_type() != at::kByte) bad("scales", "must be uint8");
             dense(s, "scales", shape, device);
         } else {
-            s = empty(shape, at::kByte, device);
+            s = fresh.give(shape, at::kByte);
         }
         if (!check(tile_mx4_quantize(x.data_ptr(), ts, static_cast<uint8_t *>(q.data_ptr()),
                                      static_cast<uint8_t *>(s.data_ptr()), M, K, ld_x, ld_q, static_cast<int>(block),
@@ -735,11 +745,11 @@ PyObject *grad_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             factor = scalar(a[1], "grad_scale", device);
             gs = static_cast<const float *>(factor.data_ptr());
         }
-        Together small(device);
+        Together fresh(device);
         for (int k = 4; k < 6; ++k)
-            if (!given(a[k])) small.want(1);
-        const at::Tensor norm = given(a[4]) ? scalar(a[4], "norm", device) : small.give({});
-        const at::Tensor scale = given(a[5]) ? scalar(a[5], "scale", device) : small.give({});
+            if (!given(a[k])) fresh.want(1, at::kFloat);
+        const at::Tensor norm = given(a[4]) ? scalar(a[4], "norm", device) : fresh.give({}, at::kFloat);
+        const at::Tensor scale = given(a[5]) ? scalar(a[5], "scale", device) : fresh.give({}, at::kFloat);
         float *to = static_cast<float *>(scale.data_ptr());
         const int rc = (in_place ? tile_grad_clip : tile_grad_norm)(list.data(), count, gs, static_cast<float>(most),
                                                                     static_cast<float>(eps),
