@@ -23,7 +23,7 @@
 namespace mbt {
 namespace {
 
-constexpr int kMx4Warps = 8;
+constexpr int kMx4Warps = 4;
 // Rows of a warp.  Fewer to quantise, whose arithmetic wants the registers that more warps
 // then share (fp32 16384 x 16384 by 32, us, with 2 / 4: 167 / 202; back 110 / 97).
 constexpr int kQuantizeRows = 2;
@@ -119,7 +119,7 @@ __device__ __forceinline__ void codes_of(float (&f)[E], float d, float most, uin
 // A lane takes 32 bytes of a row: of 16-bit elements a whole block of 16, so that the
 // scale's arithmetic is done once a block (with 16 bytes, bf16 2047 x 8192 by 16: 15.6 us).
 template <int DT, int BLOCK>
-__global__ void __launch_bounds__(32 * kMx4Warps, 5) mbt_mx4_quantize_kernel(const Mx4Args a) {
+__global__ void __launch_bounds__(32 * kMx4Warps, 10) mbt_mx4_quantize_kernel(const Mx4Args a) {
     constexpr int V = Elem<DT>::kVec, E = 2 * V;
     const Mx4Place<E, BLOCK, kQuantizeRows> at(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
