@@ -93,26 +93,30 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device device) 
     return at::detail::empty_cuda(shape, type, device, c10::nullopt);
 }
 
-// The new results of a call, of which small ones share an allocation (each costs as much
-// as the rest of a call of one token): want() for all of them, then give() for each.  Results
-// over kMost bytes in all have one each, so that a large one's memory is not held by others.
+// The new results of a call, of which the small ones share an allocation (each costs as much
+// as the rest of a call of one token): want() for all of them, then give() for each.  A
+// result over kMost bytes has its own, so that large memory is not held by others.
 class Together {
 public:
     explicit Together(at::Device device) : device_(device) {}
-    void want(int64_t elements, at::ScalarType type) { total_ += padded(elements * size(type)); }
+    void want(int64_t elements, at::ScalarType type) {
+        if (elements * size(type) <= kMost) total_ += padded(elements * size(type));
+    }
     at::Tensor give(at::IntArrayRef shape, at::ScalarType type) {
-        if (total_ > kMost) return empty(shape, type, device_);
+        int64_t bytes = size(type);
+        for (const int64_t n : shape) bytes *= n;
+        if (bytes > kMost) return empty(shape, type, device_);
         if (!flat_.defined()) flat_ = empty({total_}, at::kByte, device_);
         at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(flat_.storage()), flat_.key_set(),
                                                                 c10::scalarTypeToTypeMeta(type));
         t.unsafeGetTensorImpl()->set_storage_offset(used_ / size(type));
         t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-        used_ += padded(t.numel() * size(type));
+        used_ += padded(bytes);
         return t;
     }
 
 private:
-    static constexpr int64_t kMost = 256 << 10;
+    static constexpr int64_t kMost = 64 << 10;
     static int64_t size(at::ScalarType type) { return static_cast<int64_t>(c10::elementSize(type)); }
     static int64_t padded(int64_t bytes) { return (bytes + 127) / 128 * 128; }
     at::Device device_;
@@ -410,6 +414,11 @@ PyObject *layernorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         int64_t ld_res = 0, ld_dx = 0;
         int wcode = 0;
         at::Tensor dx, dw, db;
+        const bool new_dw = !given(a[9]) && given(a[4]), new_db = !given(a[10]) && given(a[4]) && bias;
+        Together fresh(device);
+        if (!given(a[8])) fresh.want(M * N, type);
+        if (new_dw) fresh.want(N, at::kFloat);
+        if (new_db) fresh.want(N, at::kFloat);
         if (given(a[4])) {
             const at::Tensor &t = tensor(a[4], "weight");
             if (!is_wide(t.scalar_type())) bad("weight", "has an unsupported dtype");
@@ -419,14 +428,14 @@ PyObject *layernorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (given(a[9])) {
             dw = tensor(a[9], "dweight");
             dense_f32(dw, "dweight", {N}, device);
-        } else if (given(a[4])) {
-            dw = empty({N}, at::kFloat, device);
+        } else if (new_dw) {
+            dw = fresh.give({N}, at::kFloat);
         }
         if (given(a[10])) {
             db = tensor(a[10], "dbias");
             dense_f32(db, "dbias", {N}, device);
-        } else if (given(a[4]) && bias) {
-            db = empty({N}, at::kFloat, device);
+        } else if (new_db) {
+            db = fresh.give({N}, at::kFloat);
         }
         if (given(a[5])) {
             const at::Tensor &t = tensor(a[5], "dresidual");
@@ -437,7 +446,7 @@ PyObject *layernorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
             dx = tensor(a[8], "dx");
             ld_dx = rows(dx, "dx", M, N, type, device);
         } else {
-            dx = empty({M, N}, type, device);
+            dx = fresh.give({M, N}, type);
         }
         if (!check(tile_layernorm_backward(dy.data_ptr(), h.data_ptr(), static_cast<const float *>(mean),
                                            static_cast<const float *>(rstd), w, res, dx.data_ptr(),
