@@ -35,6 +35,13 @@ constexpr int kMmRows = 128;              // of the instructions' first operand
 constexpr int kMmStep = 256;              // columns of K per stage
 constexpr int kMmMostStages = 8;
 constexpr int kMmTmem = 512;              // columns
+// Shared memory that a CTA takes for each column of tensor memory, at least.  A CTA waits in
+// the allocation until another of its SM frees enough, and the CTAs of a cluster wait for each
+// other: two clusters (of two streams, or of two kernels, one of which set up early) that each
+// held what the other's CTA waits for would wait for ever.  CTAs that an SM's shared memory
+// holds together (228 KB) must therefore fit its tensor memory together.  Allocations are
+// multiples of 64 columns, so what does not fit is 576 of them or more: 576 x 420 > 228 KB.
+constexpr int kMmSmemPerColumn = 420;
 
 struct Mx4MatArgs {
     const uint8_t *sr, *sc;    // scales of the rows' and of the columns' operand
@@ -125,8 +132,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     __shared__ __align__(8) MmShared sh;
     const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
     const int warp = static_cast<int>(warp_value(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    // the next kernel of the stream may be set up meanwhile; it waits for this one's end itself
-    asm volatile("griddepcontrol.launch_dependents;");
     if (warp == 2) tmem_alloc<1>(smem_u32(&sh.tmem), a.tmem);
     if (warp == 1 && elect_one()) {
         prefetch_map(&rows_map);
@@ -148,6 +153,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // the next kernel of the stream may be set up from now on; it waits for this one's end itself
+    asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t tmem = warp_value(sh.tmem);
     const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -369,7 +376,8 @@ struct PairShape {
     static constexpr int kScaleCols = kTiles * 4 * 3;
     static constexpr int kStages = 5;
     static constexpr int kOutBox = 32 * kBoxRowBytes;         // 32 rows of an epilogue warp, 128 bytes of each
-    static constexpr int kSmem = kStages * kStageStride + 8 * kOutBox + kSwizzleAtomBytes;
+    static constexpr int kNeeds = kStages * kStageStride + 8 * kOutBox + kSwizzleAtomBytes;
+    static constexpr int kSmem = kNeeds > kMmTmem * kMmSmemPerColumn ? kNeeds : kMmTmem * kMmSmemPerColumn;
     static_assert(kPairCols + kStages * kScaleCols <= kMmTmem && kSmem <= 226 * 1024);
 };
 
@@ -443,7 +451,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
     const int warp = static_cast<int>(warp_value(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    asm volatile("griddepcontrol.launch_dependents;");       // (see above)
     if (warp == 2) tmem_alloc<2>(smem_u32(&sh.tmem), kMmTmem);
     if (warp == 1 && elect_one()) {
         prefetch_map(&rows_map);
@@ -466,6 +473,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();                          // both CTAs' barriers are there
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");       // (see above)
     const uint32_t tmem = warp_value(sh.tmem);
     const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
     const int first_tile = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
@@ -700,12 +708,13 @@ int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int
     const int recv = a.split > 1 ? S::kRecv : 0;
     a.accs = turns > 1 ? 2 : 1;
     a.stages = static_cast<int32_t>(std::min<int64_t>(S::stages(kMmSmem - recv, a.accs), turns * ((a.steps + a.split - 1) / a.split)));
-    a.tmem = 32;
+    a.tmem = 64;
     while (a.tmem < a.accs * S::kAcc + a.stages * S::kScaleCols) a.tmem *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.stages) * S::kStage + recv + kSwizzleAtomBytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(
+        std::max(a.stages * S::kStage + recv + kSwizzleAtomBytes, a.tmem * kMmSmemPerColumn));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -311,3 +311,24 @@ def test_past_four_gib():
         assert worst(wide[rows], ref, 2.0 ** -7 * ref.abs() + 1e-3 * ref.abs().amax()) <= 1
     del wide, a, b
     torch.cuda.empty_cache()
+
+
+def test_products_on_streams_side_by_side():
+    """Products of every variant on three streams at once, back to back: clusters whose CTAs share SMs with others'."""
+    shapes = [(1, 512, 4096), (17, 1024, 2048), (64, 640, 8192), (128, 512, 1024), (200, 256, 256), (100, 9000, 256),
+              (2500, 2600, 512), (3, 128, 256), (33, 300, 16384)]
+    cases = []
+    for k, (M, N, K) in enumerate(shapes):
+        block = 16 if k % 2 else 32
+        a, b = operand(M, K, block, 60 + 2 * k)[0], operand(N, K, block, 61 + 2 * k)[0]
+        cases.append((a, b, mbt.tile_mx4_matmul(a, b, out_dtype=torch.float32)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    results = []
+    for turn in range(40):
+        for s, stream in enumerate(streams):
+            a, b, want = cases[(turn * (s + 1) + 2 * s) % len(cases)]
+            results.append((mbt.tile_mx4_matmul(a, b, out_dtype=torch.float32, stream=stream), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(got, want) for got, want in results)
+    assert mbt.tile_status()[0] == 0
