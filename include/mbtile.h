@@ -723,7 +723,7 @@ int tile_adamw(const mbt_adamw_tensor *tensors, int64_t count, int param_dtype, 
  *   *scale = gs min(1, max_norm / (*norm + eps))
  *   grads         HOST array of count descriptors, read during the call; fp16, bf16 and
  *                 fp32 tensors in any mixture, each dense, aligned to its elements.
- *                 Empty ones are allowed.
+ *                 Empty ones are allowed; one given twice counts twice.
  *   norm, scale   DEVICE pointers to one fp32 each; scale optional.  *scale is what
  *                 tile_adamw and tile_grad_scale take: gs, the inverse of a loss scale for
  *                 example, and the clipping in one.  max_norm INFINITY: gs alone.
@@ -774,7 +774,7 @@ int64_t tile_mx4_scale_bytes(int64_t M, int64_t K, int block);
  *   code          x / d rounded to e2m1 (nearest even, at most 6 in magnitude).
  * 6 t, s t and the quotients are rounded to fp32 first.  Where d is 0 or all of a block
  * is, its codes are 0; a block with a NaN or infinity has a NaN scale and codes of 0.
- * t is asked to lie between 2^-60 and 2^60.
+ * t is asked to lie between 2^-60 and 2^60.  q and scales overlap x in no byte.
  */
 int tile_mx4_quantize(const void *x, const float *tensor_scale, uint8_t *q, uint8_t *scales,
                       int64_t M, int64_t K, int64_t ld_x, int64_t ld_q, int block, int dtype,
@@ -791,8 +791,8 @@ int tile_mx4_dequantize(const uint8_t *q, const uint8_t *scales, const float *te
  *   out[m][n] = *a_tensor_scale * *b_tensor_scale * sum_k a[m][k] b[n][k]
  * summed in fp32 by the tensor instructions (out M x N, rounded once to out_dtype).
  * Up to 128 rows of a are taken in one pass over b.  Equal calls give equal bits.  A NaN
- * scale makes the values of out that it reaches NaN.  No workspace.  M = 0 or N = 0 does
- * nothing, K = 0 writes zeros.
+ * scale makes the values of out that it reaches NaN.  out overlaps no input.  No workspace.
+ * M = 0 or N = 0 does nothing, K = 0 writes zeros.
  */
 int tile_mx4_matmul(const uint8_t *a, const uint8_t *a_scales, const float *a_tensor_scale,
                     const uint8_t *b, const uint8_t *b_scales, const float *b_tensor_scale,

