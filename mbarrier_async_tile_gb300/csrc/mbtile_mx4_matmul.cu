@@ -42,14 +42,6 @@ constexpr int kMmRows = 128;              // of the instructions' first operand
 constexpr int kMmStep = 256;              // columns of K per stage
 constexpr int kMmMostStages = 8;
 constexpr int kMmTmem = 512;              // columns
-// Shared memory that a CTA takes for each column of tensor memory, at least.  A CTA waits in
-// the allocation until another of its SM frees enough, and the CTAs of a cluster wait for each
-// other: two clusters (of two streams, or of two kernels, one of which set up early) that each
-// held what the other's CTA waits for would wait for ever.  CTAs that an SM's shared memory
-// holds together (228 KB) must therefore fit its tensor memory together.  Allocations are
-// multiples of 64 columns, so what does not fit is 576 of them or more: 576 x 420 > 228 KB.
-constexpr int kMmSmemPerColumn = 420;
-
 struct Mx4MatArgs {
     const uint8_t *sr, *sc;    // scales of the rows' and of the columns' operand
     const float *ta, *tb;
@@ -69,12 +61,11 @@ struct Mx4MatArgs {
 template <int BN, int BLOCK>
 struct MmShape {
     static constexpr int kTiles = kMmStep / BLOCK / 4;        // scale tiles of 128 rows per stage
-    static constexpr int kColTiles = (BN + 127) / 128;        // of the columns' operand
     static constexpr int kRowBytes = kMmRows * kBoxRowBytes;
     static constexpr int kColBytes = BN * kBoxRowBytes;
     static constexpr int kScaleBytes = kTiles * 512;
-    static constexpr int kStage = kRowBytes + kColBytes + kScaleBytes * (1 + kColTiles);
-    static constexpr int kScaleCols = kTiles * 4 * (1 + kColTiles);   // tensor memory of a stage's scales
+    static constexpr int kStage = kRowBytes + kColBytes + kScaleBytes * 2;
+    static constexpr int kScaleCols = kTiles * 4 * 2;   // tensor memory of a stage's scales
     static constexpr int kAcc = BN < 32 ? 32 : BN;
     // A cluster's parts of this CTA's rows; a row's columns, and 16 bytes that spread the rows
     // over the banks.
@@ -92,31 +83,6 @@ __device__ __forceinline__ void tile_at(const Mx4MatArgs &a, int t, int *r, int 
     const int per = 16 * a.tiles_c, g = t / per, first = g * 16, rows = min(16, a.tiles_r - first), left = t - g * per;
     *c = left / rows;
     *r = first + left - *c * rows;
-}
-
-// 16 neighbouring elements of a row of out.
-__device__ __forceinline__ void store16(const Mx4MatArgs &a, int64_t row, int64_t col, const float (&f)[16], int count) {
-    const int64_t at = row * a.ld_out + col;
-    if (a.vec && count >= 16) {
-        if (a.odt == MBT_F32) {
-            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-        } else {
-            uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float g[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] = f[8 * k + e];
-                p[k] = a.odt == MBT_BF16 ? pack<MBT_BF16>(g) : pack<MBT_F16>(g);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (e < count) store_any(a.out, a.odt, at + e, f[e]);
 }
 
 // wait_bounded() by a whole warp.
@@ -139,6 +105,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     __shared__ __align__(8) MmShared sh;
     const uint32_t base = (smem_u32(dyn_smem) + kSwizzleAtomBytes - 1) & ~static_cast<uint32_t>(kSwizzleAtomBytes - 1);
     const int warp = static_cast<int>(warp_value(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    // This CTA is there, and its memory may be stored to: see the epilogue.  A CTA waits in the
+    // allocation until what else its SM runs frees enough tensor memory.  No CTA waits for
+    // another of its cluster between that and its own tensor memory's release but for this arrival
+    // before it: two clusters that each held what a CTA of the other needs would wait for ever.
+    if (a.split > 1) cluster_arrive();
     if (warp == 2) tmem_alloc<1>(smem_u32(&sh.tmem), a.tmem);
     if (warp == 1 && elect_one()) {
         prefetch_map(&rows_map);
@@ -165,7 +136,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const uint32_t tmem = warp_value(sh.tmem);
     const WaitCtl w{kDefaultWaitBudgetNs, &sh.abort_flag, a.status};
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-    if (a.split > 1) cluster_arrive();               // this CTA is there: see the epilogue
     const int first_tile = a.split > 1 ? static_cast<int>(blockIdx.x) / a.split : static_cast<int>(blockIdx.x);
     const int stride = a.split > 1 ? 0x40000000 : static_cast<int>(gridDim.x);   // (a cluster has one tile)
     const int tiles = a.tiles_r * a.tiles_c;
@@ -193,16 +163,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 const uint32_t at = base + stage * S::kStage, sr = at + S::kRowBytes + S::kColBytes;
                 const int64_t tile = static_cast<int64_t>(k) * S::kTiles;
                 const uint32_t bytes = 512u * static_cast<uint32_t>(min(static_cast<int64_t>(S::kTiles), a.scale_tiles - tile));
-                // the columns' last tile of 128 rows may have no scales
-                const int col_tiles = S::kColTiles == 1 || (2 * tc + 1) * 128 < a.C ? S::kColTiles : 1;
-                mbar_arrive_expect_tx(full, S::kRowBytes + S::kColBytes + bytes * (1 + col_tiles));
+                mbar_arrive_expect_tx(full, S::kRowBytes + S::kColBytes + bytes * 2);
                 tma_load_2d(at, &rows_map, k * kBoxRowBytes, tr * kMmRows, full);
                 tma_load_2d(at + S::kRowBytes, &cols_map, k * kBoxRowBytes, tc * BN, full);
                 bulk_load_1d(sr, a.sr + (tr * a.scale_tiles + tile) * 512, bytes, full);
-                for (int c = 0; c < col_tiles; ++c)
-                    bulk_load_1d(sr + (1 + c) * S::kScaleBytes,
-                                 a.sc + ((static_cast<int64_t>(tc) * S::kColTiles + c) * a.scale_tiles + tile) * 512,
-                                 bytes, full);
+                bulk_load_1d(sr + S::kScaleBytes, a.sc + (tc * a.scale_tiles + tile) * 512, bytes, full);
                 if (++stage == static_cast<uint32_t>(a.stages)) stage = 0, phase ^= 1;
             }
         }
@@ -235,10 +200,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     for (int s = 0; s < S::kTiles; ++s) {
                         if (4 * s >= left * S::kTiles) break;            // (no scales there)
                         tmem_copy_scales<1>(scols + 4 * s, desc_rows16(sr + 512 * s));
-#pragma unroll
-                        for (int c = 0; c < S::kColTiles; ++c)
-                            tmem_copy_scales<1>(ccols + 4 * (s * S::kColTiles + c),
-                                                desc_rows16(sr + (1 + c) * S::kScaleBytes + 512 * s));
+                        tmem_copy_scales<1>(ccols + 4 * s, desc_rows16(sr + S::kScaleBytes + 512 * s));
                     }
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
@@ -246,7 +208,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         const int s = m * S::kTiles / 4;                     // the product's scale tile
                         const uint32_t id = BLOCK == 32 ? (m & 1) * 2 : 0;   // the first of the bytes in a scale column
                         mma_mx4<1, BLOCK>(d, da + 2 * m, db + 2 * m, idesc | id << 4 | id << 29, scols + 4 * s,
-                                          ccols + 4 * s * S::kColTiles, k > k0 || m > 0);
+                                          ccols + 4 * s, k > k0 || m > 0);
                     }
                     tc_commit(smem_u32(&sh.empty[stage]));
                 }
@@ -313,12 +275,18 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
     }
     __syncwarp();
+    bool freed = false;
     if (a.split > 1) {
         // A CTA adds rows of its own from every CTA's part, in the slices' order.  (Parts are
         // stored into the memory of the CTA that adds them, apart from its stages, which it may
         // still use: one barrier, after which no CTA needs another's memory.)
         if (!in_epilogue) cluster_wait();
         cluster_arrive();
+        if (warp == 2 && warp_wait(smem_u32(&sh.acc_empty[0]), 0, w)) {   // (its tile has been read)
+            tc_fence_after();
+            tmem_free<1>(tmem, a.tmem);
+            freed = true;
+        }
         cluster_wait();
         float alpha = a.ta ? *a.ta : 1.f;
         if (a.tb) alpha *= *a.tb;
@@ -355,7 +323,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             for (uint32_t p = 0; p < 2; ++p) wait_bounded(smem_u32(&sh.full[s]), p, w, false);
     __syncthreads();
     tc_fence_after();
-    if (warp == 2) tmem_free<1>(tmem, a.tmem);
+    if (warp == 2 && !freed) tmem_free<1>(tmem, a.tmem);
 }
 
 // ---------------------------------------------------------------------------
@@ -388,8 +356,11 @@ struct PairShape {
     static constexpr int kScaleCols = kTiles * 4 * 3;
     static constexpr int kStages = 5;
     static constexpr int kOutBox = 32 * kBoxRowBytes;         // 32 rows of an epilogue warp, 128 bytes of each
+    // (At least: the CTAs of a pair wait for each other with tensor memory in hand, so an SM that
+    // holds one is to hold no other CTA that might do the same.)
+    static constexpr int kLeast = 225 * 1024;
     static constexpr int kNeeds = kStages * kStageStride + 8 * kOutBox + kSwizzleAtomBytes;
-    static constexpr int kSmem = kNeeds > kMmTmem * kMmSmemPerColumn ? kNeeds : kMmTmem * kMmSmemPerColumn;
+    static constexpr int kSmem = kNeeds > kLeast ? kNeeds : kLeast;
     static_assert(kPairCols + kStages * kScaleCols <= kMmTmem && kSmem <= 226 * 1024);
 };
 
@@ -602,12 +573,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (!a.vec) {
                 if (row < a.R)
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 16) {
-                        float f[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(acc[c + e]) * alpha;
-                        store16(a, row, col0 + c, f, cols - c);
-                    }
+                    for (int c = 0; c < kCols; ++c)
+                        if (c < cols) store_any(a.out, a.odt, row * a.ld_out + col0 + c, __uint_as_float(acc[c]) * alpha);
                 continue;
             }
             // By way of shared memory, in the swizzle's order, and bulk tensor copies of 128
@@ -725,8 +692,7 @@ int launch_matmul(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(
-        std::max(a.stages * S::kStage + recv + kSwizzleAtomBytes, a.tmem * kMmSmemPerColumn));
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.stages * S::kStage + recv + kSwizzleAtomBytes);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
