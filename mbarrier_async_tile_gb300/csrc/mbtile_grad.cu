@@ -11,7 +11,7 @@
 // its last (at most 7 elements each) goes with its first chunk.  Calls of few chunks are
 // one cluster, which also multiplies by the factor that it has found.
 //
-// A thread sums squares in fp32.  Where a chunk's sum leaves 2^-100 .. 2^100, in which
+// A thread sums the squares of up to 64 chunks in fp32.  Where a chunk's sum leaves 2^-100 .. 2^100, in which
 // squares neither overflow nor lose their last bits, it takes the chunk again in 64
 // bits, so that the norm is right wherever fp32 holds it.  CTAs and threads are added in
 // 64 bits in a fixed order, by the CTA that finishes last.  (bf16 300 M elements in 160 tensors:
@@ -32,6 +32,7 @@ constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 8;                          // 16-byte vectors of a thread and chunk
 constexpr int kGradChunk = kGradThreads * kGradVecs;  // vectors
 constexpr int kGradCtas = 4;                          // per SM
+constexpr int kGradFold = 64;                         // chunks that a thread adds in fp32
 constexpr int kGradCluster = 8;                       // CTAs that few chunks are dealt to
 // Chunks that one cluster takes (us, cluster / grid, fp32: 100 elements 3.0 / 4.1, 50,000 4.0 /
 // 5.1, 100,000 4.9 / 5.2, 200,000 6.1 / 4.7).
@@ -243,6 +244,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas)
         const GradChunk at(g, k, c);
         uint4 v[kGradVecs];
         at.load(v);
+        if ((c - c0) % kGradFold == 0) wide += static_cast<double>(sum), sum = 0.f;
         const int type = at.type;
         bool any;
         const float sq = type == MBT_F32    ? chunk_squares<MBT_F32>(v, any)

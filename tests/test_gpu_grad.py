@@ -234,3 +234,16 @@ def test_past_four_gib():
     assert abs(g.view(-1)[:1 << 31].sum(dtype=torch.float64).item() / (v.double().item() * (1 << 31)) - 1) < 1e-9
     del store, g
     torch.cuda.empty_cache()
+
+
+def test_long_sums():
+    """Some 1700 chunks a thread, whose sums in fp32 alone would drift one way.
+
+    A square is one rounding, its chunk's 32 are at most 10 additions deep, and 64 chunks
+    are added before fp32 ends: 75 half steps of the sum, half as many of its root, and one."""
+    n, x = 1 << 33, 1.6491228342056274
+    g = torch.full((n,), x, device="cuda")
+    got = mbt.tile_grad_norm([g])
+    assert abs(got.norm.item() / (g[0].double().item() * n ** 0.5) - 1) <= 38.5 * U
+    del g
+    torch.cuda.empty_cache()
