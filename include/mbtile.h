@@ -743,7 +743,8 @@ int tile_grad_norm(const mbt_grad *grads, int64_t count, const float *grad_scale
                    float eps, float *norm, float *scale, void *stream);
 
 /* tile_grad_scale -- g = g * *scale in place over such tensors (scale: DEVICE pointer),
- * in fp32, rounded to the tensor's type.  No two of them may overlap (MBT_ERR_ARG).
+ * in fp32, rounded to the tensor's type.  No two of them, nor one and scale (or norm), may
+ * overlap (MBT_ERR_ARG).
  * tile_grad_clip -- tile_grad_norm (with a scale), then tile_grad_scale by *scale. */
 int tile_grad_clip(const mbt_grad *grads, int64_t count, const float *grad_scale, float max_norm,
                    float eps, float *norm, float *scale, void *stream);

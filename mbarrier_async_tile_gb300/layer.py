@@ -323,5 +323,5 @@ def tile_grad_norm(grads, *, max_norm: float | None = None, eps: float = 1e-6, g
 def tile_clip_grads(grads, max_norm: float, *, eps: float = 1e-6, grad_scale: torch.Tensor | None = None,
                     norm: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None) -> GradNorm:
     """:func:`tile_grad_norm`, and every gradient multiplied by ``scale`` in place.  No
-    two of the tensors may overlap."""
+    two of the tensors may overlap, nor one of them ``norm`` or ``scale``."""
     return GradNorm(*_call("grad_norm", stream, grads, grad_scale, max_norm, eps, norm, scale, True))

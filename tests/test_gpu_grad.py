@@ -176,6 +176,20 @@ def test_given_outputs_refusals_and_versions():
         mbt.tile_grad_norm([g], max_norm=-1.0)
 
 
+def test_scalars_within_gradients_are_refused():
+    g = randn(100, torch.float32, 15)
+    before = g.clone()
+    for bad in (dict(scale=g[7:8]), dict(norm=g[99:])):
+        with pytest.raises(mbt.MbtError):
+            mbt.tile_clip_grads([torch.ones(3, device="cuda"), g], 1e-3, **bad)
+    assert torch.equal(g, before)
+    # a factor that one of them holds is only read
+    scale = torch.ones(1, device="cuda")
+    got = mbt.tile_clip_grads([g], 1e-3, grad_scale=g[7:8], scale=scale)
+    check([before], got, 1e-3, before[7].item())
+    assert torch.equal(g, before * scale)
+
+
 @pytest.mark.parametrize("factor", [0.5, -2.0])
 @pytest.mark.parametrize("sizes", [[1000, 33], [3_000_001, 17]], ids=["cluster", "grid"])
 def test_factor_written_where_it_was_read(sizes, factor):

@@ -60,6 +60,17 @@ def test_clip_argument_errors():
     assert clip() == -1 and clip(count=1, to=0) == -1 and clip(count=1, most=-1.0) == -1 and clip(count=1, norm=B + 2) == -2
 
 
+def test_scalars_within_gradients_are_refused():
+    # (a factor that one of the tensors holds would change while others are multiplied by it)
+    assert scale([(A, 10, 2)], A + 36) == -1 and scale([(A, 10, 2), (B, 3, 1)], B + 4) == -1
+    t = Grad(A, 10, 2, 0)
+
+    def clip(norm, to):
+        return mbt.C.tile_grad_clip(ctypes.byref(t), 1, 0, 1.0, 1e-6, norm, to, None)
+
+    assert clip(A, B) == -1 and clip(B, A + 36) == -1 and clip(B, B) == -1
+
+
 def test_python_refusals():
     for grads in ([torch.zeros(3)], [torch.zeros(3, dtype=torch.int32)], torch.zeros(2, 3), [None]):
         with pytest.raises(ValueError):
