@@ -118,8 +118,8 @@ __device__ __forceinline__ void load_bias(const void *b, int mode, int wdt, int6
 
 // `tpr` threads hold a row in registers, C chunks each: one pass over memory.  For calls of few
 // rows, whose time is a launch and a row's latency with two or three sums in turn (one row of
-// 4096 to e4m3 3.5 us, 600 x 2048 3.4), and rows too long for the ring (bf16 2000 x 32000 with a
-// residual 150 us, 3.4 TB/s).
+// 4096 to e4m3 3.5 us, 600 x 2048 3.4), and rows too long for the ring (bf16 2000 x 32001 with a
+// residual 180 us, 2.8 TB/s).
 template <int DT, int C, bool RES, bool Q>
 __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_constant__ LayerNormVecArgs va) {
     using T = typename Elem<DT>::type;
@@ -709,7 +709,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     }
 }
 
-// The norm.  bf16 8192 x 16384 with a residual 161 us, 6.7 TB/s: memory.
+// The norm.  bf16 8192 x 16384 with a residual 161 us, 6.7 TB/s: memory.  6881 x 19504 199 us,
+// 5.4 TB/s: 36 instructions an element on half the issue slots.
 template <int DT, int C, bool RES, bool Q, bool PART, bool FLY>
 __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_layernorm_ring_kernel(const __grid_constant__ LayerNormArgs a, const __grid_constant__ LayerNormRing l) {
@@ -740,6 +741,126 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         q.wait();
         const int have = n < mine && q.alive ? th.count : 0;
         const int64_t i = th.first + n * rows;
+        if constexpr (C > 5) {
+            // Long rows stay in their stage and are read in each pass, which leaves registers for
+            // the weights (read from L2 by every row those take as long as the rest: bf16 6881 x
+            // 19504 with a residual 564 us).  A last chunk that is not copied is held: the
+            // residual's sum may overwrite it before the last pass.
+            uint4 end_x = make_uint4(0, 0, 0, 0), end_r = end_x;
+            if (PART && have && th.tail) {
+                end_x = th.chunk(q.stage, 0, have - 1);
+                th.last_chunk(r, 0, have - 1, i, end_x);
+                if constexpr (RES) {
+                    end_r = th.chunk(q.stage, 1, have - 1);
+                    th.last_chunk(r, 1, have - 1, i, end_r);
+                }
+            }
+            // chunk c of h, 0 where it is not the row's
+            auto row = [&](int c, float (&f)[V]) {
+                uint4 vx = make_uint4(0, 0, 0, 0), vr = vx;
+                if (c < have) {
+                    const bool last = PART && th.tail && c == have - 1;
+                    vx = last ? end_x : th.chunk(q.stage, 0, c);
+                    if constexpr (RES) vr = last ? end_r : th.chunk(q.stage, 1, c);
+                }
+                unpack<DT>(vx, f);
+                if constexpr (RES) {
+                    float g[V];
+                    unpack<DT>(vr, g);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) f[e] += g[e];
+                }
+                if (PART && !th.whole(c)) th.mask(c, f);
+            };
+            float sum = 0.f, ss = 0.f;
+            uint32_t amax = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float f[V];
+                row(c, f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum += f[e];
+            }
+            row_reduce<false>(sum, amax, r.tpr, sh.red[0], turn);
+            turn ^= 1;
+            const float mean = __fdiv_rn(sum, static_cast<float>(a.N));
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (c >= have) continue;
+                float f[V];
+                row(c, f);
+                if (write_res) th.put(res + c * chunk, c, f);
+                float part = 0.f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float d = f[e] - mean;
+                    const bool in = !PART || th.whole(c) || (e >= th.lo(c) && e < th.hi(c));
+                    part += in ? d * d : 0.f;
+                }
+                ss += part;
+            }
+            row_reduce<false>(ss, amax, r.tpr, sh.red[0], turn);
+            turn ^= 1;
+            const float rstd = rsqrtf(ss * inv_n + a.eps);
+            if (th.t == 0 && n < mine) {
+                a.mean[i] = mean;
+                a.rstd[i] = rstd;
+            }
+            auto y_of = [&](int c, uint32_t z, float (&f)[V]) {
+                float w[V], b[V];
+                row(c, f);
+                wt.get(c, z, w);
+                bt.get(c, z, b);
+                const Pair rr(rstd);
+#pragma unroll
+                for (int e = 0; e < V; e += 2) {
+                    const float2 y = fma2(Pair(f[e] - mean, f[e + 1] - mean) * rr, Pair(w[e], w[e + 1]), Pair(b[e], b[e + 1])).get();
+                    f[e] = y.x, f[e + 1] = y.y;
+                }
+                if (Q && PART && !th.whole(c)) th.mask(c, f);
+            };
+            float scale = 0.f;
+            Divisor by;
+            if (Q && a.quant == 0) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    if (c >= have) continue;
+                    float f[V];
+                    y_of(c, z1, f);
+                    amax = magnitude_max(amax, f);
+                }
+                float none = 0.f;
+                row_reduce<true>(none, amax, r.tpr, sh.red[0], turn);
+                turn ^= 1;
+                scale = group_scale(amax);
+                by = Divisor(scale);
+                if (th.t == 0 && n < mine) a.scales[i] = scale;
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float f[V];
+                y_of(c, z2, f);
+                if constexpr (!Q) {
+                    if (c < have) th.put(out + c * chunk, c, f);
+                } else {
+                    if (a.quant > 0) {       // (rows start at a chunk)
+                        uint32_t m = c < have ? magnitude_max(0u, f) : 0u;
+#pragma unroll
+                        for (int o = 1; o < 128 / V; o <<= 1) {
+                            if (o >= a.quant / V) break;
+                            m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        }
+                        scale = group_scale(m);
+                        by = Divisor(scale);
+                        const int p = th.t * V + c * chunk;
+                        if (c < have && p % a.quant == 0) a.scales[i * a.groups + p / a.quant] = scale;
+                    }
+                    if (c < have) store_e4m3<V>(out + c * chunk, f, by, th.lo(c), th.hi(c));
+                }
+            }
+            q.release(r, a.M);
+            continue;
+        }
         float h[C][V];
         {
             uint4 vx[C], vr[RES ? C : 1];
@@ -887,7 +1008,9 @@ cudaError_t ln_ring_forward(const RingPlan &p, int bmode, const LayerNormArgs &a
     const int c = p.chunks;
     const bool part = p.part || !plain_vector(p.r.wmode) || !plain_vector(bmode);
     if constexpr (DT == MBT_F32) {
-        if (c > 5) return launch_ln_ring_forward<DT, 8, true, true>(p, bmode, a, s);
+        if (c > 5)
+            return part ? launch_ln_ring_forward<DT, 8, true, false>(p, bmode, a, s)
+                        : launch_ln_ring_forward<DT, 8, false, false>(p, bmode, a, s);
         if (part)
             return c <= 4 ? launch_ln_ring_forward<DT, 4, true, false>(p, bmode, a, s)
                           : launch_ln_ring_forward<DT, 5, true, false>(p, bmode, a, s);
@@ -895,6 +1018,7 @@ cudaError_t ln_ring_forward(const RingPlan &p, int bmode, const LayerNormArgs &a
                : c <= 4 ? launch_ln_ring_forward<DT, 4, false, false>(p, bmode, a, s)
                         : launch_ln_ring_forward<DT, 5, false, false>(p, bmode, a, s);
     } else {
+        if (c > 4) return launch_ln_ring_forward<DT, 8, false, false>(p, bmode, a, s);
         if (a.w && (a.wdt != DT || a.woff != 0.f)) return launch_ln_ring_forward<DT, 4, true, true>(p, bmode, a, s);
         if (part)
             return c <= 2 ? launch_ln_ring_forward<DT, 2, true, false>(p, bmode, a, s)
@@ -928,19 +1052,24 @@ cudaError_t ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cuda
     }
 }
 
-// The ring's plan: up to four chunks a thread of 16-bit rows; of fp32 rows up to five, and
-// eight of those too long for that.  Rows side by side hide each other's reductions, so few
+// The ring's plan: up to four chunks a thread of 16-bit rows, of fp32 rows up to five; up to
+// eight of rows too long for that, forward, where 16-bit rows ask for weights of their type and
+// whole chunks (2000 x 32001 with a residual 195 us, 180 without the ring).  A single stage will
+// do for the longest: forward the next row is copied while this one's is stored, and for the
+// gradient (fp32 2000 x 10240 with a residual 71 us) the alternative reads rows twice (132).
+// Rows side by side hide each other's reductions, so few
 // threads take a row (us, four chunks / two, forward 8192 x 8192 bf16 with a residual 87 /
 // 121; gradient 16384 x 8192 187 / 215, 65536 x 1024 95 / 118; fp32 2047 x 5001, five / four
 // 37 / 52), but for a gradient of few turns, where the last one's length and the more
 // instructions of rows that registers do not hold count (3001 x 4001 48 / 38, 1024 x 4096
 // 20.4 / 17.5, 8192 x 4096 of 13 turns 61 / 64, 9001 x 1032 of 7 36 / 39).
 bool ln_ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, int64_t N, int es, int ph, int min_tpr,
-                  int sms, bool gradient, RingPlan *p) {
+                  int sms, bool gradient, bool plain, RingPlan *p) {
     if (es == 4)
-        return ring_plan(in, ld, inputs, M, N, es, ph, 5, min_tpr, sms, p, 5) ||
-               ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p);
-    if (!ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p, 4)) return false;
+        return ring_plan(in, ld, inputs, M, N, es, ph, 5, min_tpr, sms, p, 5, 1) ||
+               ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 0, gradient ? 2 : 1);
+    if (!ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p, 4))
+        return plain && !gradient && ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 0, 1) && !p->part;
     if (!gradient || M >= 6ll * p->grid * p->r.rows) return true;
     return ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p, 2);
 }
@@ -955,7 +1084,7 @@ int ln_backward_by_ring(LayerNormGradArgs a, cudaStream_t s, int sms, bool *done
     const void *in[3] = {a.dy, a.h, a.dres};
     const int64_t ld[3] = {a.ld_dy, a.ld_h, a.ld_dres};
     RingPlan p;
-    *done = same && ln_ring_plan(in, ld, a.dres ? 3 : 2, a.M, a.N, es, ph, 8, sms, true, &p);
+    *done = same && ln_ring_plan(in, ld, a.dres ? 3 : 2, a.M, a.N, es, ph, 8, sms, true, false, &p);
     if (!*done) return MBT_OK;
     int rc = device_status_word(&p.r.status);
     if (rc != MBT_OK) return rc;
@@ -976,13 +1105,9 @@ int ln_backward_by_ring(LayerNormGradArgs a, cudaStream_t s, int sms, bool *done
 // Where the ring is faster than a row in registers (us, ring / registers): its start is paid
 // once a call, so with enough rows, of whatever length: bf16 with a residual 131072 x 512 96
 // / 113, 8192 x 8192 85 / 128, 512 x 8192 10.2 / 12.5, 256 x 8192 7.1 / 7.0, 2000 x 512 6.6 /
-// 4.4; without, 131072 x 256 31 / 48, 65537 x 1001 110 / 141, 304 x 8192 by groups of 128 to
-// e4m3 7.0 / 7.7, 1000 x 1001 8.9 / 4.0.  Long fp32 rows, whose weights it reads each time, ask
-// for several turns (152 x 16384 12.7 / 9.8).
-bool ln_ring_pays(const LayerNormArgs &a, int64_t es, int sms) {
-    const bool long_rows = es == 4 && a.N > 5 * 4 * kRingThreads;
-    return a.M * a.N * es >= (5ll << 20) && (!long_rows || a.M >= 4 * sms);
-}
+// 4.4, 6881 x 19504 199 / 390, 152 x 32768 12.2 / 14.4; without, 131072 x 256 31 / 48, 65537 x
+// 1001 110 / 141, 304 x 8192 by groups of 128 to e4m3 7.0 / 7.7, 1000 x 1001 8.9 / 4.0.
+bool ln_ring_pays(const LayerNormArgs &a, int64_t es) { return a.M * a.N * es >= (5ll << 20); }
 
 template <int DT, int C>
 cudaError_t launch_ln_forward(const LayerNormVecArgs &va, dim3 grid, int threads, cudaStream_t s) {
@@ -1011,9 +1136,10 @@ cudaError_t ln_forward_any(const LayerNormArgs &a, cudaStream_t s) {
     if (device_limits(&sms, &optin) != MBT_OK) return cudaErrorUnknown;
     const void *in[2] = {a.x, a.res};
     const int64_t ld[2] = {a.ld_x, a.ld_res};
+    const bool plain = plain_vector(weight_mode(a.w, a.wdt, DT)) && plain_vector(weight_mode(a.b, a.wdt, DT)) && a.woff == 0.f;
     RingPlan p;
-    if (same && ln_ring_pays(a, es, sms) &&
-        ln_ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, a.quant > 0 ? 32 : 8, sms, false, &p)) {
+    if (same && ln_ring_pays(a, es) &&
+        ln_ring_plan(in, ld, a.res ? 2 : 1, a.M, a.N, es, ph, a.quant > 0 ? 32 : 8, sms, false, plain, &p)) {
         if (device_status_word(&p.r.status) != MBT_OK) return cudaErrorUnknown;
         p.r.wmode = weight_mode(a.w, a.wdt, DT);
         return ln_ring_forward<DT>(p, weight_mode(a.b, a.wdt, DT), a, s);

@@ -1040,7 +1040,7 @@ struct RingPlan {
 };
 
 bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, int64_t N, int es, int ph,
-               int most, int min_tpr, int sms, RingPlan *plan, int prefer = 0) {
+               int most, int min_tpr, int sms, RingPlan *plan, int prefer = 0, int least = 2) {
     const int V = 16 / es;
     RingArgs &r = plan->r;
     r = RingArgs{};
@@ -1072,7 +1072,7 @@ bool ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, 
     r.stage_bytes = static_cast<uint32_t>(r.slot) * r.unit_rows * inputs;
     const int64_t stage = static_cast<int64_t>(r.slot) * r.rows * inputs;
     r.stages = static_cast<int32_t>(std::min<int64_t>(kRingStages, kRingBytes / stage));
-    if (r.stages < 2) return false;
+    if (r.stages < least) return false;
     plan->chunks = static_cast<int>((chunks + tpr - 1) / tpr);
     plan->part = r.phased || N % V != 0;
     plan->smem = static_cast<int>(std::max<int64_t>(r.stages * stage, r.rows * N * 4));

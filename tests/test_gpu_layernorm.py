@@ -175,6 +175,43 @@ def test_many_rows_with_pitches(pad):
     assert all(bool((t[:, N:] == 0).all()) for t in wide)
 
 
+@pytest.mark.parametrize("M,N", [(700, 16392), (310, 20008), (200, 26624), (160, 26632), (157, 32768), (154, 12000), (320, 13320),
+                                 (156, 16384), (311, 12001), (155, 16381), (400, 8888), (309, 10239)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("quant", [None, 0, 32, 128])
+def test_long_rows(M, N, dtype, quant):
+    """Rows that stay in shared memory from pass to pass, in several stages or one; one turn and more."""
+    dt = TYPES[dtype]
+    w, b = randn(N, dt, 73), randn(N, dt, 74)
+    for r in (None, randn((M, N), dt, 72, 3.0)):
+        x = randn((M, N), dt, 71) + 1
+        check_forward(x, w, b, r, mbt.tile_layernorm(x, w, b, r, eps=1e-5, quant=quant), 1e-5, 0.0, quant)
+    if quant is None:
+        check_forward(x, None, None, r, mbt.tile_layernorm(x, None, None, r, eps=1e-5), 1e-5, 0.0, None)
+        check_forward(x, w, b, r, mbt.tile_layernorm(x, w, b, r, eps=1e-5, weight_offset=0.5), 1e-5, 0.5, None)
+    assert mbt.tile_status()[0] == 0
+
+
+@pytest.mark.parametrize("M,N", [(330, 20008), (160, 32768), (311, 12001), (155, 16381), (311, 9001), (200, 10240)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_rows_in_place(M, N, dtype):
+    dt = TYPES[dtype]
+    x, r, w, b = randn((M, N), dt, 75), randn((M, N), dt, 76), randn(N, dt, 77), randn(N, dt, 78)
+    want = mbt.tile_layernorm(x, w, b, r)
+    check_forward(x, w, b, r, want, 1e-5, 0.0, None)
+    x2, r2 = x.clone(), r.clone()
+    got = mbt.tile_layernorm(x2, w, b, r2, out=x2, residual_out=r2)
+    for a, c in zip((got.out, r2, got.mean, got.rstd), (want.out, want.residual, want.mean, want.rstd)):
+        assert torch.equal(a, c)
+    dy = randn((M, N), dt, 79)
+    first = mbt.tile_layernorm_backward(dy, r2, got.mean, got.rstd, w, dresidual=x)
+    check_backward(dy, r2, got.mean, got.rstd, w, x, *first)
+    again = mbt.tile_layernorm_backward(dy, r2, got.mean, got.rstd, w, dresidual=x, dx=x)
+    for a, c in zip(first, again):
+        assert torch.equal(a, c)
+    assert mbt.tile_status()[0] == 0
+
+
 @pytest.mark.parametrize("rows,N", [(65, 1024), (65, 1001), (2600, 4001), (700, 16384), (3, 70000)])
 def test_in_place(rows, N):
     x, r = randn((rows, N), torch.bfloat16, 13), randn((rows, N), torch.bfloat16, 14)
