@@ -566,6 +566,95 @@ struct RowVector {
     }
 };
 
+// Rows that end inside chunks.  The first and the last chunk of a row may hold other rows'
+// elements; the warps that have them (`edge`, the same in a warp) do what it takes in straight
+// code: as calls in a branch of a thread's own they held up the row's other warps at its sums
+// (bf16 8192 x 8191 with a residual 232 us, 8192 x 8192 84).
+struct EdgeMasks {
+    uint4 from[9];           // [k]: all bits of a chunk's elements from k on
+};
+template <int DT>
+__device__ __forceinline__ void edge_masks(EdgeMasks &m) {
+    constexpr int V = Elem<DT>::kVec, es = 16 / V;
+    if (threadIdx.x > V) return;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int bytes = static_cast<int>(threadIdx.x) * es - 4 * k;   // of this word, to be left out
+        w[k] = bytes <= 0 ? ~0u : bytes >= 4 ? 0u : ~0u << (8 * bytes);
+    }
+    m.from[threadIdx.x] = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int DT, int C, bool PART>
+struct EdgeThread : RingThread<DT, C, PART> {
+    using Base = RingThread<DT, C, PART>;
+    using T = typename Elem<DT>::type;
+    static constexpr int V = Elem<DT>::kVec;
+    int last;                // the row's last chunk is some thread's of this number
+    bool edge;
+    uint32_t masks;
+    __device__ __forceinline__ EdgeThread(const RingArgs &r, int64_t M, int64_t N, uint32_t ring, const EdgeMasks &m)
+        : Base(r, M, N, ring) {
+        last = PART ? ((Base::end + V - 1) / V - 1) / r.tpr : 0;
+        edge = PART && __any_sync(0xffffffffu, Base::head || Base::tail);
+        masks = smem_u32(&m);
+    }
+    __device__ __forceinline__ bool at_edge(int c) const { return PART && edge && (c == 0 || c == last); }
+    // v of chunk c, with 0 for other rows' elements.
+    __device__ __forceinline__ uint4 own(int c, const uint4 &v) const {
+        if (!at_edge(c)) return v;
+        const uint4 a = lds128(masks + 16 * Base::lo(c)), b = lds128(masks + 16 * Base::hi(c));
+        return make_uint4(v.x & a.x & ~b.x, v.y & a.y & ~b.y, v.z & a.z & ~b.z, v.w & a.w & ~b.w);
+    }
+    // Others' elements of chunk c to x.
+    __device__ __forceinline__ void fill(int c, float x, float (&v)[V]) const {
+        if (!at_edge(c)) return;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < Base::lo(c) || e >= Base::hi(c)) v[e] = x;
+    }
+    // The matrix's own last chunk, which is not copied: to its place in the stage, where this
+    // thread alone reads it.
+    __device__ __forceinline__ void complete(const RingArgs &r, uint32_t stage, int64_t row) const {
+        if (!PART || !Base::tail) return;
+        bool any = false;
+        for (int m = 0; m < r.inputs; ++m) {
+            if (row < r.tail[m]) continue;
+            const int c = Base::count - 1;
+            const T *from = reinterpret_cast<const T *>(r.in[m] + row * r.ld[m]) - Base::off + (Base::t + c * r.tpr) * V;
+            const uint32_t to = Base::addr + stage * Base::stage_bytes + static_cast<uint32_t>(m) * Base::input_step +
+                                static_cast<uint32_t>(c) * Base::chunk_step;
+#pragma unroll 1
+            for (int e = Base::lo(c); e < Base::hi(c); ++e) {
+                if constexpr (V == 8)
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2 * e), "h"(*reinterpret_cast<const uint16_t *>(from + e))
+                                 : "memory");
+                else
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + 4 * e), "f"(from[e]) : "memory");
+            }
+            any = true;
+        }
+        if (any) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the stage may be copied to again)
+    }
+    __device__ __forceinline__ void put(T *to, int c, const float (&v)[V]) const {
+        const uint4 p = pack<DT>(v);
+        if (!at_edge(c) || Base::whole(c)) {
+            *reinterpret_cast<uint4 *>(to) = p;
+            return;
+        }
+        const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+        const int lo = Base::lo(c), hi = Base::hi(c);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (e < lo || e >= hi) continue;
+            if constexpr (V == 8)
+                reinterpret_cast<uint16_t *>(to)[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+            else
+                reinterpret_cast<uint32_t *>(to)[e] = w[e];
+        }
+    }
+};
+
 struct LayerNormRing {
     RingArgs r;
     int32_t bmode;           // the bias's access (the weight's: r.wmode)
@@ -582,10 +671,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     const RingArgs &r = l.r;
     extern __shared__ __align__(128) unsigned char dyn_smem[];
     __shared__ __align__(8) RingShared sh;
+    __shared__ EdgeMasks masks;
+    if constexpr (PART) edge_masks<DT>(masks);
     ring_init(sh, r);
     RingState q(r, smem_u32(dyn_smem), smem_u32(&sh.bars[0]), WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status});
     q.start(r, a.M);
-    const RingThread<DT, C, PART> th(r, a.M, a.N, q.ring);
+    const EdgeThread<DT, C, PART> th(r, a.M, a.N, q.ring, masks);
     const RowVector<DT, C, PART, FLY> wt(a.w, r.wmode, a.wdt, 1.f, a.woff, th.t, r.tpr, th.off, a.N);
     float dw[C][V], db[C][V];
 #pragma unroll
@@ -608,23 +699,13 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         if (n + 1 < mine) next_mean = __ldg(a.mean + i + rows), next_rstd = __ldg(a.rstd + i + rows);
         q.wait();
         const int have = n < mine && q.alive ? th.count : 0;
+        if (PART && have) th.complete(r, q.stage, i);
         // chunk c of dy and h, 0 where it is not the row's
         auto take = [&](int c, uint4 &vy, uint4 &vh) {
             vy = vh = make_uint4(0, 0, 0, 0);
             if (c >= have) return;
-            vy = th.chunk(q.stage, 0, c);
-            vh = th.chunk(q.stage, 1, c);
-            if (PART && !th.whole(c)) {
-                th.last_chunk(r, 0, c, i, vy);
-                th.last_chunk(r, 1, c, i, vh);
-                float f[V];
-                unpack<DT>(vy, f);
-                th.mask(c, f);
-                vy = pack<DT>(f);
-                unpack<DT>(vh, f);
-                th.mask(c, f);
-                vh = pack<DT>(f);
-            }
+            vy = th.own(c, th.chunk(q.stage, 0, c));
+            vh = th.own(c, th.chunk(q.stage, 1, c));
         };
         float xs[HOLD ? C : 1][V], gs[HOLD ? C : 1][V];
         float level = 0.f, along = 0.f;
@@ -654,10 +735,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         for (int c = 0; c < C; ++c) {
             if (c >= have) continue;
             uint4 vr = make_uint4(0, 0, 0, 0);
-            if constexpr (RES) {
-                vr = th.chunk(q.stage, 2, c);
-                if (PART && th.tail) th.last_chunk(r, 2, c, i, vr);
-            }
+            if constexpr (RES) vr = th.chunk(q.stage, 2, c);
             float d[V], f[V];
             if constexpr (RES) unpack<DT>(vr, f);
             if constexpr (HOLD) {
@@ -720,10 +798,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     const RingArgs &r = l.r;
     extern __shared__ __align__(128) unsigned char dyn_smem[];
     __shared__ __align__(8) RingShared sh;
+    __shared__ EdgeMasks masks;
+    if constexpr (PART) edge_masks<DT>(masks);
     ring_init(sh, r);
     RingState q(r, smem_u32(dyn_smem), smem_u32(&sh.bars[0]), WaitCtl{kDefaultWaitBudgetNs, &sh.abort_flag, r.status});
     q.start(r, a.M);
-    const RingThread<DT, C, PART> th(r, a.M, a.N, q.ring);
+    const EdgeThread<DT, C, PART> th(r, a.M, a.N, q.ring, masks);
     const RowVector<DT, C, PART, FLY> wt(a.w, r.wmode, a.wdt, 1.f, a.woff, th.t, r.tpr, th.off, a.N);
     const RowVector<DT, C, PART, FLY> bt(a.b, l.bmode, a.wdt, 0.f, 0.f, th.t, r.tpr, th.off, a.N);
     const float inv_n = 1.f / static_cast<float>(a.N);
@@ -741,27 +821,17 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         q.wait();
         const int have = n < mine && q.alive ? th.count : 0;
         const int64_t i = th.first + n * rows;
+        if (PART && have) th.complete(r, q.stage, i);
         if constexpr (C > 5) {
             // Long rows stay in their stage and are read in each pass, which leaves registers for
             // the weights (read from L2 by every row those take as long as the rest: bf16 6881 x
-            // 19504 with a residual 564 us).  A last chunk that is not copied is held: the
-            // residual's sum may overwrite it before the last pass.
-            uint4 end_x = make_uint4(0, 0, 0, 0), end_r = end_x;
-            if (PART && have && th.tail) {
-                end_x = th.chunk(q.stage, 0, have - 1);
-                th.last_chunk(r, 0, have - 1, i, end_x);
-                if constexpr (RES) {
-                    end_r = th.chunk(q.stage, 1, have - 1);
-                    th.last_chunk(r, 1, have - 1, i, end_r);
-                }
-            }
+            // 19504 with a residual 564 us).
             // chunk c of h, 0 where it is not the row's
             auto row = [&](int c, float (&f)[V]) {
                 uint4 vx = make_uint4(0, 0, 0, 0), vr = vx;
                 if (c < have) {
-                    const bool last = PART && th.tail && c == have - 1;
-                    vx = last ? end_x : th.chunk(q.stage, 0, c);
-                    if constexpr (RES) vr = last ? end_r : th.chunk(q.stage, 1, c);
+                    vx = th.own(c, th.chunk(q.stage, 0, c));
+                    if constexpr (RES) vr = th.own(c, th.chunk(q.stage, 1, c));
                 }
                 unpack<DT>(vx, f);
                 if constexpr (RES) {
@@ -770,7 +840,6 @@ __global__ void __launch_bounds__(kRingThreads, 1)
 #pragma unroll
                     for (int e = 0; e < V; ++e) f[e] += g[e];
                 }
-                if (PART && !th.whole(c)) th.mask(c, f);
             };
             float sum = 0.f, ss = 0.f;
             uint32_t amax = 0;
@@ -790,12 +859,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 float f[V];
                 row(c, f);
                 if (write_res) th.put(res + c * chunk, c, f);
+                th.fill(c, mean, f);
                 float part = 0.f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float d = f[e] - mean;
-                    const bool in = !PART || th.whole(c) || (e >= th.lo(c) && e < th.hi(c));
-                    part += in ? d * d : 0.f;
+                    part += d * d;
                 }
                 ss += part;
             }
@@ -817,7 +886,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                     const float2 y = fma2(Pair(f[e] - mean, f[e + 1] - mean) * rr, Pair(w[e], w[e + 1]), Pair(b[e], b[e + 1])).get();
                     f[e] = y.x, f[e + 1] = y.y;
                 }
-                if (Q && PART && !th.whole(c)) th.mask(c, f);
+                if (Q) th.fill(c, 0.f, f);
             };
             float scale = 0.f;
             Divisor by;
@@ -869,15 +938,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 vx[c] = make_uint4(0, 0, 0, 0);
                 if constexpr (RES) vr[c] = make_uint4(0, 0, 0, 0);
                 if (c >= have) continue;
-                vx[c] = th.chunk(q.stage, 0, c);
-                if constexpr (RES) vr[c] = th.chunk(q.stage, 1, c);
+                vx[c] = th.own(c, th.chunk(q.stage, 0, c));
+                if constexpr (RES) vr[c] = th.own(c, th.chunk(q.stage, 1, c));
             }
-            if (PART && have && th.tail)
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    th.last_chunk(r, 0, c, i, vx[c]);
-                    if constexpr (RES) th.last_chunk(r, 1, c, i, vr[c]);
-                }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 unpack<DT>(vx[c], h[c]);
@@ -890,10 +953,6 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             }
         }
         q.release(r, a.M);   // the row is in registers now
-        if (PART && have && (th.head || th.tail))
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (!th.whole(c)) th.mask(c, h[c]);
         float sum = 0.f, ss = 0.f;
         uint32_t amax = 0;
 #pragma unroll
@@ -907,11 +966,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         for (int c = 0; c < C; ++c) {
             if (c < have && write_res) th.put(res + c * chunk, c, h[c]);
             float part = 0.f;
+            th.fill(c, mean, h[c]);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 h[c][e] -= mean;                       // from here on the deviation
-                const bool in = !PART || th.whole(c) || (e >= th.lo(c) && e < th.hi(c));
-                part += in ? h[c][e] * h[c][e] : 0.f;
+                part += h[c][e] * h[c][e];
             }
             if (c < have) ss += part;
         }
@@ -937,7 +996,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             if constexpr (!Q) {
                 if (c < have) th.put(out + c * chunk, c, h[c]);
             } else {
-                if (PART && !th.whole(c)) th.mask(c, h[c]);
+                th.fill(c, 0.f, h[c]);
                 gmax[c] = c < have ? magnitude_max(0u, h[c]) : 0u;
             }
         }
