@@ -567,9 +567,10 @@ struct RowVector {
 };
 
 // Rows that end inside chunks.  The first and the last chunk of a row may hold other rows'
-// elements; the warps that have them (`edge`, the same in a warp) do what it takes in straight
-// code: as calls in a branch of a thread's own they held up the row's other warps at its sums
-// (bf16 8192 x 8191 with a residual 232 us, 8192 x 8192 84).
+// elements; what that takes is done by the warps that have those chunks (`edge`, the same in
+// a warp) in blocks of their own: the row's other warps wait for them at its sums, and
+// branches between a thread's loads keep these from being under way together (bf16 8192 x 8191
+// with a residual 232 us with calls for each, 212 in the loops over chunks, 189).
 struct EdgeMasks {
     uint4 from[9];           // [k]: all bits of a chunk's elements from k on
 };
@@ -585,26 +586,63 @@ __device__ __forceinline__ void edge_masks(EdgeMasks &m) {
     }
     m.from[threadIdx.x] = make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void sts128(uint32_t at, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// v's elements from one on (a) and below another (b).
+__device__ __forceinline__ uint4 between(const uint4 &v, const uint4 &a, const uint4 &b) {
+    return make_uint4(v.x & a.x & ~b.x, v.y & a.y & ~b.y, v.z & a.z & ~b.z, v.w & a.w & ~b.w);
+}
 template <int DT, int C, bool PART>
 struct EdgeThread : RingThread<DT, C, PART> {
     using Base = RingThread<DT, C, PART>;
     using T = typename Elem<DT>::type;
     static constexpr int V = Elem<DT>::kVec;
     int last;                // the row's last chunk is some thread's of this number
+    int most;                // chunks of a thread of this warp, at most
     bool edge;
     uint32_t masks;
+    int64_t tail_row;        // from here on a row's last chunk may not have been copied
     __device__ __forceinline__ EdgeThread(const RingArgs &r, int64_t M, int64_t N, uint32_t ring, const EdgeMasks &m)
         : Base(r, M, N, ring) {
         last = PART ? ((Base::end + V - 1) / V - 1) / r.tpr : 0;
+        most = __reduce_max_sync(0xffffffffu, Base::count);
         edge = PART && __any_sync(0xffffffffu, Base::head || Base::tail);
         masks = smem_u32(&m);
+        tail_row = min(r.tail[0], r.tail[1]);
+        if (r.inputs > 2) tail_row = min(tail_row, r.tail[2]);
+        if (r.inputs < 2) tail_row = r.tail[0];
     }
+    // No thread of this warp has a chunk c.  Rows may fill little more than half of a class's
+    // chunks; asked of the last ones, as each branch costs full rows a little (us, from the third /
+    // fourth chunk on / never: bf16 with a residual 8192 x 10000 140 / 138 / 144, 8192 x 16384 165
+    // / 162 / 161, gradient 8192 x 10000 155 / 160 / 166, 16384 x 8192 187 / 189 / 188).
+    template <int FROM>
+    __device__ __forceinline__ bool none(int c) const { return c >= FROM && c >= most; }
     __device__ __forceinline__ bool at_edge(int c) const { return PART && edge && (c == 0 || c == last); }
-    // v of chunk c, with 0 for other rows' elements.
-    __device__ __forceinline__ uint4 own(int c, const uint4 &v) const {
-        if (!at_edge(c)) return v;
-        const uint4 a = lds128(masks + 16 * Base::lo(c)), b = lds128(masks + 16 * Base::hi(c));
-        return make_uint4(v.x & a.x & ~b.x, v.y & a.y & ~b.y, v.z & a.z & ~b.z, v.w & a.w & ~b.w);
+    // Before a row is read from its stage: other rows' elements in its first and last chunk
+    // of the first INPUTS matrices to 0, by the threads that alone read them; and the matrix's
+    // own last chunk, which is not copied, from the matrix.
+    template <int INPUTS>
+    __device__ __forceinline__ void prepare(const RingArgs &r, uint32_t stage, int64_t row) const {
+        if (!PART || !edge || !(Base::head || Base::tail) || Base::count == 0) return;
+        const int c = Base::count - 1;
+        if (row >= tail_row && Base::tail) complete(r, stage, row);
+        uint4 v[INPUTS], u[INPUTS];
+        const uint32_t at = Base::addr + stage * Base::stage_bytes, to = at + static_cast<uint32_t>(c) * Base::chunk_step;
+#pragma unroll
+        for (int m = 0; m < INPUTS; ++m) {
+            v[m] = lds128(at + m * Base::input_step);
+            u[m] = lds128(to + m * Base::input_step);
+        }
+        const uint4 a = lds128(masks + 16 * Base::lo(0)), b = lds128(masks + 16 * Base::hi(0));
+        const uint4 e = lds128(masks + 16 * Base::lo(c)), f = lds128(masks + 16 * Base::hi(c));
+#pragma unroll
+        for (int m = 0; m < INPUTS; ++m) {
+            sts128(at + m * Base::input_step, between(v[m], a, b));
+            sts128(to + m * Base::input_step, between(u[m], e, f));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the stage is copied to again)
     }
     // Others' elements of chunk c to x.
     __device__ __forceinline__ void fill(int c, float x, float (&v)[V]) const {
@@ -613,11 +651,7 @@ struct EdgeThread : RingThread<DT, C, PART> {
         for (int e = 0; e < V; ++e)
             if (e < Base::lo(c) || e >= Base::hi(c)) v[e] = x;
     }
-    // The matrix's own last chunk, which is not copied: to its place in the stage, where this
-    // thread alone reads it.
     __device__ __forceinline__ void complete(const RingArgs &r, uint32_t stage, int64_t row) const {
-        if (!PART || !Base::tail) return;
-        bool any = false;
         for (int m = 0; m < r.inputs; ++m) {
             if (row < r.tail[m]) continue;
             const int c = Base::count - 1;
@@ -632,16 +666,16 @@ struct EdgeThread : RingThread<DT, C, PART> {
                 else
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + 4 * e), "f"(from[e]) : "memory");
             }
-            any = true;
         }
-        if (any) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the stage may be copied to again)
     }
-    __device__ __forceinline__ void put(T *to, int c, const float (&v)[V]) const {
+    // Chunk c of a row, if it is the row's alone; and after all of them the parts of those that
+    // are not.
+    __device__ __forceinline__ void put_whole(T *to, int c, const float (&v)[V]) const {
+        if (!PART || (c < Base::count && Base::whole(c))) *reinterpret_cast<uint4 *>(to) = pack<DT>(v);
+    }
+    __device__ __forceinline__ void put_part(T *to, int c, const float (&v)[V]) const {
+        if (!at_edge(c) || c >= Base::count || Base::whole(c)) return;
         const uint4 p = pack<DT>(v);
-        if (!at_edge(c) || Base::whole(c)) {
-            *reinterpret_cast<uint4 *>(to) = p;
-            return;
-        }
         const uint32_t w[4] = {p.x, p.y, p.z, p.w};
         const int lo = Base::lo(c), hi = Base::hi(c);
 #pragma unroll
@@ -653,6 +687,10 @@ struct EdgeThread : RingThread<DT, C, PART> {
                 reinterpret_cast<uint32_t *>(to)[e] = w[e];
         }
     }
+    __device__ __forceinline__ void put(T *to, int c, const float (&v)[V]) const {
+        put_whole(to, c, v);
+        put_part(to, c, v);
+    }
 };
 
 struct LayerNormRing {
@@ -661,7 +699,7 @@ struct LayerNormRing {
 };
 
 // The gradient.  bf16 16384 x 8192 with a residual 187 us, 5.7 TB/s: 31 instructions an element
-// on 62 % of the issue slots; fp32 2047 x 5001 36 us, by the latency of a row's turn.
+// on 62 % of the issue slots; fp32 2047 x 5001 35.6 us, by the latency of a row's turn.
 template <int DT, int C, bool RES, bool PART, bool FLY>
 __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_layernorm_backward_kernel(const __grid_constant__ LayerNormGradArgs a, const __grid_constant__ LayerNormRing l) {
@@ -699,18 +737,19 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         if (n + 1 < mine) next_mean = __ldg(a.mean + i + rows), next_rstd = __ldg(a.rstd + i + rows);
         q.wait();
         const int have = n < mine && q.alive ? th.count : 0;
-        if (PART && have) th.complete(r, q.stage, i);
+        if (have) th.template prepare<2>(r, q.stage, i);
         // chunk c of dy and h, 0 where it is not the row's
         auto take = [&](int c, uint4 &vy, uint4 &vh) {
             vy = vh = make_uint4(0, 0, 0, 0);
             if (c >= have) return;
-            vy = th.own(c, th.chunk(q.stage, 0, c));
-            vh = th.own(c, th.chunk(q.stage, 1, c));
+            vy = th.chunk(q.stage, 0, c);
+            vh = th.chunk(q.stage, 1, c);
         };
         float xs[HOLD ? C : 1][V], gs[HOLD ? C : 1][V];
         float level = 0.f, along = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
+            if (th.template none<2>(c)) continue;
             float dy[V], h[V], w[V];
             uint4 vy, vh;
             take(c, vy, vh);
@@ -787,8 +826,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     }
 }
 
-// The norm.  bf16 8192 x 16384 with a residual 161 us, 6.7 TB/s: memory.  6881 x 19504 199 us,
-// 5.4 TB/s: 36 instructions an element on half the issue slots.
+// The norm.  bf16 8192 x 16384 with a residual 161 us, 6.7 TB/s: memory.  6881 x 19504 190 us,
+// 5.7 TB/s: 36 instructions an element on half the issue slots.
 template <int DT, int C, bool RES, bool Q, bool PART, bool FLY>
 __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_layernorm_ring_kernel(const __grid_constant__ LayerNormArgs a, const __grid_constant__ LayerNormRing l) {
@@ -821,7 +860,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         q.wait();
         const int have = n < mine && q.alive ? th.count : 0;
         const int64_t i = th.first + n * rows;
-        if (PART && have) th.complete(r, q.stage, i);
+        if (have) th.template prepare<RES ? 2 : 1>(r, q.stage, i);
         if constexpr (C > 5) {
             // Long rows stay in their stage and are read in each pass, which leaves registers for
             // the weights (read from L2 by every row those take as long as the rest: bf16 6881 x
@@ -830,8 +869,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             auto row = [&](int c, float (&f)[V]) {
                 uint4 vx = make_uint4(0, 0, 0, 0), vr = vx;
                 if (c < have) {
-                    vx = th.own(c, th.chunk(q.stage, 0, c));
-                    if constexpr (RES) vr = th.own(c, th.chunk(q.stage, 1, c));
+                    vx = th.chunk(q.stage, 0, c);
+                    if constexpr (RES) vr = th.chunk(q.stage, 1, c);
                 }
                 unpack<DT>(vx, f);
                 if constexpr (RES) {
@@ -845,6 +884,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             uint32_t amax = 0;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
+                if (th.template none<3>(c)) continue;
                 float f[V];
                 row(c, f);
 #pragma unroll
@@ -907,6 +947,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
+                if (th.template none<3>(c)) continue;
                 float f[V];
                 y_of(c, z2, f);
                 if constexpr (!Q) {
@@ -938,11 +979,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 vx[c] = make_uint4(0, 0, 0, 0);
                 if constexpr (RES) vr[c] = make_uint4(0, 0, 0, 0);
                 if (c >= have) continue;
-                vx[c] = th.own(c, th.chunk(q.stage, 0, c));
-                if constexpr (RES) vr[c] = th.own(c, th.chunk(q.stage, 1, c));
+                vx[c] = th.chunk(q.stage, 0, c);
+                if constexpr (RES) vr[c] = th.chunk(q.stage, 1, c);
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
+                if (th.template none<3>(c)) continue;
                 unpack<DT>(vx[c], h[c]);
                 if constexpr (RES) {
                     float f[V];
@@ -956,17 +998,31 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         float sum = 0.f, ss = 0.f;
         uint32_t amax = 0;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            if (th.template none<3>(c)) continue;
 #pragma unroll
             for (int e = 0; e < V; ++e) sum += h[c][e];
+        }
         row_reduce<false>(sum, amax, r.tpr, sh.red[0], turn);
         turn ^= 1;
         const float mean = __fdiv_rn(sum, static_cast<float>(a.N));   // (rows of one value: that value)
+        if constexpr (PART) {
+            if (write_res && have) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) th.put_whole(res + c * chunk, c, h[c]);
+                if (th.edge)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) th.put_part(res + c * chunk, c, h[c]);
+            }
+            if (th.edge)
+#pragma unroll
+                for (int c = 0; c < C; ++c) th.fill(c, mean, h[c]);
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (c < have && write_res) th.put(res + c * chunk, c, h[c]);
+            if (th.template none<3>(c)) continue;
+            if (!PART && c < have && write_res) th.put(res + c * chunk, c, h[c]);
             float part = 0.f;
-            th.fill(c, mean, h[c]);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 h[c][e] -= mean;                       // from here on the deviation
@@ -984,6 +1040,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         uint32_t gmax[C];                    // largest magnitude of each chunk's group
 #pragma unroll
         for (int c = 0; c < C; ++c) {
+            if constexpr (Q) gmax[c] = 0u;
+            if (th.template none<3>(c)) continue;
             float w[V], b[V];
             wt.get(c, z1, w);
             bt.get(c, z2, b);
@@ -994,12 +1052,15 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 h[c][e] = y.x, h[c][e + 1] = y.y;
             }
             if constexpr (!Q) {
-                if (c < have) th.put(out + c * chunk, c, h[c]);
+                if (c < have) th.put_whole(reinterpret_cast<T *>(out + c * chunk), c, h[c]);
             } else {
                 th.fill(c, 0.f, h[c]);
                 gmax[c] = c < have ? magnitude_max(0u, h[c]) : 0u;
             }
         }
+        if (!Q && PART && th.edge && have)
+#pragma unroll
+            for (int c = 0; c < C; ++c) th.put_part(reinterpret_cast<T *>(out + c * chunk), c, h[c]);
         if constexpr (Q) {
             float scale = 0.f;
             Divisor by;
