@@ -1138,7 +1138,9 @@ cudaError_t ln_ring_forward(const RingPlan &p, int bmode, const LayerNormArgs &a
                : c <= 4 ? launch_ln_ring_forward<DT, 4, false, false>(p, bmode, a, s)
                         : launch_ln_ring_forward<DT, 5, false, false>(p, bmode, a, s);
     } else {
-        if (c > 4) return launch_ln_ring_forward<DT, 8, false, false>(p, bmode, a, s);
+        if (c > 4)
+            return part ? launch_ln_ring_forward<DT, 8, true, false>(p, bmode, a, s)
+                        : launch_ln_ring_forward<DT, 8, false, false>(p, bmode, a, s);
         if (a.w && (a.wdt != DT || a.woff != 0.f)) return launch_ln_ring_forward<DT, 4, true, true>(p, bmode, a, s);
         if (part)
             return c <= 2 ? launch_ln_ring_forward<DT, 2, true, false>(p, bmode, a, s)
@@ -1173,23 +1175,29 @@ cudaError_t ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cuda
 }
 
 // The ring's plan: up to four chunks a thread of 16-bit rows, of fp32 rows up to five; up to
-// eight of rows too long for that, forward, where 16-bit rows ask for weights of their type and
-// whole chunks (2000 x 32001 with a residual 195 us, 180 without the ring).  A single stage will
-// do for the longest: forward the next row is copied while this one's is stored, and for the
-// gradient (fp32 2000 x 10240 with a residual 71 us) the alternative reads rows twice (132).
-// Rows side by side hide each other's reductions, so few
-// threads take a row (us, four chunks / two, forward 8192 x 8192 bf16 with a residual 87 /
-// 121; gradient 16384 x 8192 187 / 215, 65536 x 1024 95 / 118; fp32 2047 x 5001, five / four
-// 37 / 52), but for a gradient of few turns, where the last one's length and the more
-// instructions of rows that registers do not hold count (3001 x 4001 48 / 38, 1024 x 4096
-// 20.4 / 17.5, 8192 x 4096 of 13 turns 61 / 64, 9001 x 1032 of 7 36 / 39).
+// eight of rows too long for that, forward, where 16-bit rows ask for weights of their type.
+// A single stage will do for the longest: forward the next row is copied while this one's is
+// stored, and for the gradient (fp32 2000 x 10240 with a residual 71 us) the alternative reads
+// rows twice (132).  Rows side by side hide each other's reductions, so few threads take a row
+// (us, four chunks / two, forward 8192 x 8192 bf16 with a residual 87 / 121; gradient 16384 x 8192
+// 187 / 215, 65536 x 1024 95 / 118; fp32 2047 x 5001, five / four 37 / 52), but for a gradient of
+// few turns, where the last one's length and the more instructions of rows that registers do not
+// hold count (3001 x 4001 48 / 38, 1024 x 4096 20.4 / 17.5, 8192 x 4096 of 13 turns 61 / 64, 9001
+// x 1032 of 7 36 / 39).  Forward eight chunks of 16-bit rows are ahead of four, given the turns:
+// with a residual 8192 x 10000 113 / 139, 8192 x 8200 108 / 137, 16384 x 1400 of 7 turns 35 / 39,
+// 8192 x 8192 83 / 83, 700 x 8200 of 2 15.9 / 15.6; of parts of chunks 8192 x 8191 160 / 189, 8192
+// x 5001 of 13 70 / 80, 4000 x 5001 of 7 to e4m3 84 / 68.
 bool ln_ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, int64_t N, int es, int ph, int min_tpr,
                   int sms, bool gradient, bool plain, RingPlan *p) {
     if (es == 4)
         return ring_plan(in, ld, inputs, M, N, es, ph, 5, min_tpr, sms, p, 5, 1) ||
                ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 0, gradient ? 2 : 1);
+    const bool eight = plain && !gradient;
+    if (eight && ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 8) &&
+        M >= (p->part ? 10ll : 6ll) * p->grid * p->r.rows)
+        return true;
     if (!ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p, 4))
-        return plain && !gradient && ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 0, 1) && !p->part;
+        return eight && ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 8, 1);
     if (!gradient || M >= 6ll * p->grid * p->r.rows) return true;
     return ring_plan(in, ld, inputs, M, N, es, ph, 4, min_tpr, sms, p, 2);
 }

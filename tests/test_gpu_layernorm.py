@@ -175,7 +175,8 @@ def test_many_rows_with_pitches(pad):
     assert all(bool((t[:, N:] == 0).all()) for t in wide)
 
 
-@pytest.mark.parametrize("M,N", [(700, 16392), (310, 20008), (200, 26624), (160, 26632), (157, 32768), (154, 12000), (320, 13320),
+@pytest.mark.parametrize("M,N", [(6000, 4104), (7000, 4103), (13000, 2056), (40001, 520), (40000, 511), (1900, 16379), (310, 20001),
+                                 (155, 32761), (700, 16392), (310, 20008), (200, 26624), (160, 26632), (157, 32768), (154, 12000), (320, 13320),
                                  (156, 16384), (311, 12001), (155, 16381), (400, 8888), (309, 10239)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("quant", [None, 0, 32, 128])
