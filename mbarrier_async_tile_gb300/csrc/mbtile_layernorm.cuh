@@ -487,9 +487,8 @@ cudaError_t launch_ln_finish(const LayerNormGradArgs &a, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // As in mbtile_norm.cuh, with a bias beside the weight, or gradients of both, in each
 // thread's registers.  What they do not hold is read where it is used: weights of another
-// type than 16-bit rows', and those of long fp32 rows, from global memory (FLY); in the
-// gradient's second pass rows of more than two (fp32: four) chunks a thread from their
-// stage once more.
+// type than 16-bit rows' from global memory (FLY); rows of more than five chunks a thread
+// (the gradient's second pass: of more than two, fp32 four) from their stage once more.
 
 // Sums of a and b over a row's tpr threads, in all of them; red and turn as in row_reduce.
 // Of a whole warp's values, the lower lanes add up a and the upper ones b.
@@ -1156,7 +1155,6 @@ cudaError_t ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cuda
     const int c = p.chunks;
     const bool part = p.part || !plain_vector(p.r.wmode);
     if constexpr (DT == MBT_F32) {
-        if (c > 5) return launch_ln_ring_backward<DT, 8, true, true>(p, a, s);
         if (part)
             return c <= 4 ? launch_ln_ring_backward<DT, 4, true, false>(p, a, s)
                           : launch_ln_ring_backward<DT, 5, true, false>(p, a, s);
@@ -1178,7 +1176,8 @@ cudaError_t ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cuda
 // eight of rows too long for that, forward, where 16-bit rows ask for weights of their type.
 // A single stage will do for the longest: forward the next row is copied while this one's is
 // stored, and for the gradient (fp32 2000 x 10240 with a residual 71 us) the alternative reads
-// rows twice (132).  Rows side by side hide each other's reductions, so few threads take a row
+// rows twice (132; of longer fp32 rows by eight chunks, whose weights it would read each time,
+// 2000 x 12000 142 us, without the ring 119).  Rows side by side hide each other's reductions, so few threads take a row
 // (us, four chunks / two, forward 8192 x 8192 bf16 with a residual 87 / 121; gradient 16384 x 8192
 // 187 / 215, 65536 x 1024 95 / 118; fp32 2047 x 5001, five / four 37 / 52), but for a gradient of
 // few turns, where the last one's length and the more instructions of rows that registers do not
@@ -1191,7 +1190,7 @@ bool ln_ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t 
                   int sms, bool gradient, bool plain, RingPlan *p) {
     if (es == 4)
         return ring_plan(in, ld, inputs, M, N, es, ph, 5, min_tpr, sms, p, 5, 1) ||
-               ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 0, gradient ? 2 : 1);
+               (!gradient && ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 0, 1));
     const bool eight = plain && !gradient;
     if (eight && ring_plan(in, ld, inputs, M, N, es, ph, 8, min_tpr, sms, p, 8) &&
         M >= (p->part ? 10ll : 6ll) * p->grid * p->r.rows)
