@@ -5,13 +5,26 @@
 //
 // The variance is summed from deviations, in a second pass over the row's elements
 // where they are held: sums of squares would lose the variance of rows whose mean is
-// large against it (fp32, mean 1000, deviation 1: the third digit).
+// large against it (fp32, mean 1000, deviation 1: the third digit).  The deviations are from
+// the rounded sum's mean, which is some units in the last place off; of rows that vary by less
+// than that it would be seen in y (fp32, 16384 times 12345.678, eps 1e-5: 0.9 instead of 0).  So
+// their own mean, the shift, is summed in the same pass and taken into account:
+//   m = sum h / N   s = sum (h - m) / N   mean = m + s   var = sum (h - m)^2 / N - s^2
 #pragma once
 
 #include "mbtile_norm.cuh"
 
 namespace mbt {
 namespace {
+
+// The statistics of a row.  m, s, q: means of the elements, of the deviations from m and of
+// their squares.  A shift that is not finite (rows with an infinity, or whose sum is one) is
+// left out: the mean stays m then, and what the deviations make NaN is NaN without it.
+__device__ __forceinline__ float row_shift(float s) { return fabsf(s) < __uint_as_float(0x7f800000u) ? s : 0.f; }
+__device__ __forceinline__ float row_variance(float s, float q) {
+    const float v = fmaf(-s, s, q);
+    return v < 0.f ? 0.f : v;                          // (NaN stays NaN)
+}
 
 // Any strides and lengths, one element per access: a CTA per row, a pass for the mean, one
 // for the variance, with a scale for the row one for the largest magnitude, and one that
@@ -31,19 +44,23 @@ __global__ void __launch_bounds__(kRowThreads) mbt_layernorm_rows_kernel(const L
         float sum = 0.f;
         for (int64_t j = threadIdx.x; j < a.N; j += kRowThreads) sum += h_at(j);
         block_reduce<kRowThreads>(sum, amax, red);
-        const float mean = a.N ? sum / static_cast<float>(a.N) : 0.f;
+        const float n = static_cast<float>(a.N), mean = a.N ? sum / n : 0.f;
         float ss = 0.f;
+        sum = 0.f;
         for (int64_t j = threadIdx.x; j < a.N; j += kRowThreads) {
             const float d = h_at(j) - mean;
+            sum += d;
             ss += d * d;
         }
+        block_reduce<kRowThreads>(sum, amax, red);
         block_reduce<kRowThreads>(ss, amax, red);
-        const float rstd = 1.f / sqrtf((a.N ? ss / static_cast<float>(a.N) : 0.f) + a.eps);
+        const float shift = row_shift(a.N ? sum / n : 0.f);
+        const float rstd = 1.f / sqrtf((a.N ? row_variance(shift, ss / n) : 0.f) + a.eps);
         auto y_of = [&](float h, int64_t j) {
-            return (h - mean) * rstd * weight_at(a.w, a.wdt, a.woff, j) + (a.b ? load_any(a.b, a.wdt, j) : 0.f);
+            return (h - mean - shift) * rstd * weight_at(a.w, a.wdt, a.woff, j) + (a.b ? load_any(a.b, a.wdt, j) : 0.f);
         };
         if (threadIdx.x == 0) {
-            a.mean[i] = mean;
+            a.mean[i] = mean + shift;
             a.rstd[i] = rstd;
         }
         if (a.quant <= 0) {
@@ -124,7 +141,7 @@ template <int DT, int C, bool RES, bool Q>
 __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_constant__ LayerNormVecArgs va) {
     using T = typename Elem<DT>::type;
     constexpr int V = Elem<DT>::kVec;
-    __shared__ float red[2][32];
+    __shared__ float red[3][32];
     __shared__ uint32_t redm[32];
     const LayerNormArgs &a = va.a;
     const int tpr = va.tpr, t = threadIdx.x & (tpr - 1);
@@ -167,35 +184,64 @@ __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_consta
             }
         }
     }
-    // the sum over the row, in all of its threads
-    auto row_sum = [&](float v, int turn) {
+    // the sum over the row, in all of its threads; and two of them, in whole warps the first by
+    // the lower lanes and the second by the upper ones
+    auto row_sum = [&](float v) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             if (o < tpr) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (tpr > 32) {                                // one row per CTA
-            if ((t & 31) == 0) red[turn][t >> 5] = v;
+            if ((t & 31) == 0) red[0][t >> 5] = v;
             __syncthreads();
-            v = warp_sum((t & 31) < (tpr >> 5) ? red[turn][t & 31] : 0.f);
+            v = warp_sum((t & 31) < (tpr >> 5) ? red[0][t & 31] : 0.f);
         }
         return v;
+    };
+    auto row_sums = [&](float &v, float &u) {
+        if (tpr < 32) {
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                if (o < tpr) {
+                    v += __shfl_xor_sync(0xffffffffu, v, o);
+                    u += __shfl_xor_sync(0xffffffffu, u, o);
+                }
+            return;
+        }
+        const int lane = t & 31, l = t & 15, warps = tpr >> 5;
+        float f = (lane & 16 ? u : v) + __shfl_xor_sync(0xffffffffu, lane & 16 ? v : u, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+        if (tpr > 32) {
+            float *const to = red[1 + (lane >> 4)];
+            if (l == 0) to[t >> 5] = f;
+            __syncthreads();
+            f = (l < warps ? to[l] : 0.f) + (l + 16 < warps ? to[l + 16] : 0.f);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+        }
+        v = __shfl_sync(0xffffffffu, f, 0);
+        u = __shfl_sync(0xffffffffu, f, 16);
     };
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < C; ++k)
 #pragma unroll
         for (int e = 0; e < V; ++e) sum += h[k][e];
-    const float n = static_cast<float>(a.N), mean = row_sum(sum, 0) / n;
+    const float n = static_cast<float>(a.N), mean = row_sum(sum) / n;
     float ss = 0.f;
+    sum = 0.f;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
         const int64_t p = static_cast<int64_t>(t + k * tpr) * V;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float d = h[k][e] - mean;
-            if (p + e >= off && p + e < end) ss += d * d;
+            if (p + e >= off && p + e < end) sum += d, ss += d * d;
         }
     }
-    const float rstd = 1.f / sqrtf(row_sum(ss, 1) / n + a.eps);
+    row_sums(sum, ss);
+    const float shift = row_shift(sum / n);
+    const float rstd = 1.f / sqrtf(row_variance(shift, ss / n) + a.eps), lead = -shift * rstd;
     auto y_of = [&](int k, int64_t p, float (&y)[V]) {
         float b[V];
         if constexpr (C > 1) {
@@ -206,7 +252,7 @@ __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_consta
             for (int e = 0; e < V; ++e) y[e] = w0[e], b[e] = b0[e];
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) y[e] = (h[k][e] - mean) * rstd * y[e] + b[e];
+        for (int e = 0; e < V; ++e) y[e] = fmaf(h[k][e] - mean, rstd, lead) * y[e] + b[e];
     };
     float scale = 0.f;
     Divisor by;
@@ -235,7 +281,7 @@ __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_consta
         by = Divisor(scale);
     }
     if (live && t == 0) {
-        a.mean[i] = mean;
+        a.mean[i] = mean + shift;
         a.rstd[i] = rstd;
         if (Q && a.quant == 0) a.scales[i] = scale;
     }
@@ -892,6 +938,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             row_reduce<false>(sum, amax, r.tpr, sh.red[0], turn);
             turn ^= 1;
             const float mean = __fdiv_rn(sum, static_cast<float>(a.N));
+            sum = 0.f;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 if (c >= have) continue;
@@ -899,19 +946,23 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 row(c, f);
                 if (write_res) th.put(res + c * chunk, c, f);
                 th.fill(c, mean, f);
-                float part = 0.f;
+                const Pair from(-mean);
+                Pair part(0.f), dev(0.f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float d = f[e] - mean;
-                    part += d * d;
+                for (int e = 0; e < V; e += 2) {
+                    const Pair d = Pair(f[e], f[e + 1]) + from;
+                    dev = dev + d;
+                    part = fma2(d, d, part);
                 }
-                ss += part;
+                sum += dev.get().x + dev.get().y;
+                ss += part.get().x + part.get().y;
             }
-            row_reduce<false>(ss, amax, r.tpr, sh.red[0], turn);
+            row_reduce_two(sum, ss, r.tpr, sh.red[0], turn);
             turn ^= 1;
-            const float rstd = rsqrtf(ss * inv_n + a.eps);
+            const float shift = row_shift(sum * inv_n);
+            const float rstd = rsqrtf(row_variance(shift, ss * inv_n) + a.eps);
             if (th.t == 0 && n < mine) {
-                a.mean[i] = mean;
+                a.mean[i] = mean + shift;
                 a.rstd[i] = rstd;
             }
             auto y_of = [&](int c, uint32_t z, float (&f)[V]) {
@@ -919,10 +970,10 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 row(c, f);
                 wt.get(c, z, w);
                 bt.get(c, z, b);
-                const Pair rr(rstd);
+                const Pair rr(rstd), lead(-shift * rstd);
 #pragma unroll
                 for (int e = 0; e < V; e += 2) {
-                    const float2 y = fma2(Pair(f[e] - mean, f[e + 1] - mean) * rr, Pair(w[e], w[e + 1]), Pair(b[e], b[e + 1])).get();
+                    const float2 y = fma2(fma2(Pair(f[e] - mean, f[e + 1] - mean), rr, lead), Pair(w[e], w[e + 1]), Pair(b[e], b[e + 1])).get();
                     f[e] = y.x, f[e + 1] = y.y;
                 }
                 if (Q) th.fill(c, 0.f, f);
@@ -1004,7 +1055,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
         row_reduce<false>(sum, amax, r.tpr, sh.red[0], turn);
         turn ^= 1;
-        const float mean = __fdiv_rn(sum, static_cast<float>(a.N));   // (rows of one value: that value)
+        const float mean = __fdiv_rn(sum, static_cast<float>(a.N));
+        sum = 0.f;
         if constexpr (PART) {
             if (write_res && have) {
 #pragma unroll
@@ -1021,19 +1073,23 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         for (int c = 0; c < C; ++c) {
             if (th.template none<3>(c)) continue;
             if (!PART && c < have && write_res) th.put(res + c * chunk, c, h[c]);
-            float part = 0.f;
+            const Pair from(-mean);
+            Pair part(0.f), dev(0.f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                h[c][e] -= mean;                       // from here on the deviation
-                part += h[c][e] * h[c][e];
+            for (int e = 0; e < V; e += 2) {
+                const Pair d = Pair(h[c][e], h[c][e + 1]) + from;   // from here on the deviation
+                h[c][e] = d.get().x, h[c][e + 1] = d.get().y;
+                dev = dev + d;
+                part = fma2(d, d, part);
             }
-            if (c < have) ss += part;
+            if (c < have) sum += dev.get().x + dev.get().y, ss += part.get().x + part.get().y;
         }
-        row_reduce<false>(ss, amax, r.tpr, sh.red[0], turn);
+        row_reduce_two(sum, ss, r.tpr, sh.red[0], turn);
         turn ^= 1;
-        const float rstd = rsqrtf(ss * inv_n + a.eps);
+        const float shift = row_shift(sum * inv_n);
+        const float rstd = rsqrtf(row_variance(shift, ss * inv_n) + a.eps);
         if (th.t == 0 && n < mine) {
-            a.mean[i] = mean;
+            a.mean[i] = mean + shift;
             a.rstd[i] = rstd;
         }
         uint32_t gmax[C];                    // largest magnitude of each chunk's group
@@ -1044,10 +1100,10 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             float w[V], b[V];
             wt.get(c, z1, w);
             bt.get(c, z2, b);
-            const Pair rr(rstd);
+            const Pair rr(rstd), lead(-shift * rstd);
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
-                const float2 y = fma2(Pair(h[c][e], h[c][e + 1]) * rr, Pair(w[e], w[e + 1]), Pair(b[e], b[e + 1])).get();
+                const float2 y = fma2(fma2(Pair(h[c][e], h[c][e + 1]), rr, lead), Pair(w[e], w[e + 1]), Pair(b[e], b[e + 1])).get();
                 h[c][e] = y.x, h[c][e + 1] = y.y;
             }
             if constexpr (!Q) {
