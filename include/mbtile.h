@@ -611,8 +611,8 @@ int tile_rmsnorm_backward(const void *dy, const void *h, const float *rstd, cons
  *   mean[i] = mean_j h[i][j]
  *   rstd[i] = 1 / sqrt(mean_j (h[i][j] - mean[i])^2 + eps)
  *   out[i][j] = (h[i][j] - mean[i]) * rstd[i] * (weight[j] + weight_offset) + bias[j]
- * in fp32, each output rounded once (out does not see residual_out's rounding).  As
- * tile_rmsnorm, with these additions:
+ * in fp32, each output rounded once (out sees neither residual_out's rounding nor
+ * mean's).  As tile_rmsnorm, with these additions:
  *   bias          optional, N elements of weight_dtype; goes with a weight (MBT_ERR_ARG).
  *   quant         as there; with MBT_QUANT_ROW the scale is of the row's largest |y|.
  *   mean, rstd    fp32[M] each, always written (tile_layernorm_backward reads them).

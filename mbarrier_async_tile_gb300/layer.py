@@ -1,9 +1,16 @@
-"""Python binding of the layer operators: RMS norm and its gradient, the 4-bit
-matrix-vector product, the AdamW step (see include/mbtile.h).
+"""Python binding of the layer operators: RMS norm, layer norm and their gradients, the
+4-bit matrix-vector product, matrices in 4-bit floats and their product, the
+gradients' norm, the AdamW step (see include/mbtile.h).
 
 The signatures and documentation; checks, allocation of results that the caller
 does not provide, and the call are compiled (csrc/mbtile_torch.cpp).  If the
 compiled parts are missing, every call raises; there is no fallback path.
+
+New results of at most 64 KiB of one call of layer norm, its gradient, the gradients'
+norm or the quantisation to 4-bit floats are parts of one storage: values and versions
+are each tensor's own, but saving one with ``torch.save`` writes the whole storage, one
+that is kept keeps the memory of all, and a storage that is resized or freed takes the
+others with it.  Results that the caller gives have storages of their own.
 
 Autograd sees none of the operators: results carry no gradient, whatever the
 inputs require (the gradient of the norm is a call of its own).  It is told which
@@ -124,7 +131,8 @@ def tile_layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     """h = x + residual; out = (h - mean(h)) / sqrt(var(h) + eps) * (weight + weight_offset) + bias, row by row.
 
     Arguments as in :func:`tile_rmsnorm`.  ``bias``: N elements of weight's type (only
-    with a weight).  ``mean``, ``rstd``: fp32[M] for :func:`tile_layernorm_backward`."""
+    with a weight).  ``mean``, ``rstd``: fp32[M] for :func:`tile_layernorm_backward`.
+    New small results share a storage (see the module)."""
     if quant not in _QUANT:
         raise ValueError("quant must be None, 0, 32, 64 or 128")
     return LayerNorm(*_call("layernorm", stream, x, weight, bias, residual, eps, weight_offset, _QUANT[quant], out,
@@ -140,7 +148,7 @@ def tile_layernorm_backward(dy: torch.Tensor, h: torch.Tensor, mean: torch.Tenso
     ``(dx, dweight, dbias)``, dx in h's type and the gradient of x and residual alike,
     dweight and dbias fp32[N] (None without a weight, dbias also with ``bias`` false,
     unless one to write is given).  ``dresidual`` and ``dx`` as in
-    :func:`tile_rmsnorm_backward`."""
+    :func:`tile_rmsnorm_backward`.  New small results share a storage (see the module)."""
     return _call("layernorm_backward", stream, dy, h, mean, rstd, weight, dresidual, weight_offset, bias, dx, dweight,
                  dbias)
 
@@ -183,7 +191,8 @@ def tile_mx4_quantize(x: torch.Tensor, *, block: int = 16, tensor_scale: torch.T
 
     ``tensor_scale``: with blocks of 16, what the scales are relative to; the largest
     magnitude of x divided by 448 * 6 uses their whole range.  ``q``, ``scales``:
-    tensors to write.  The result holds ``tensor_scale`` itself, not a copy."""
+    tensors to write.  The result holds ``tensor_scale`` itself, not a copy; new small
+    codes and scales share a storage (see the module)."""
     if block not in (16, 32):
         raise ValueError("block must be 16 or 32")
     q, scales = _call("mx4_quantize", stream, x, tensor_scale, block, q, scales)
@@ -315,7 +324,8 @@ def tile_grad_norm(grads, *, max_norm: float | None = None, eps: float = 1e-6, g
     ``grads``: dense CUDA tensors on one device, fp16, bf16 and fp32 in any mixture.
     ``grad_scale``: optional fp32 device scalar that the gradients are yet to be
     multiplied by (None: 1).  ``scale`` is the factor for :func:`tile_adamw`'s
-    ``grad_scale``; without ``max_norm`` it is this call's ``grad_scale``."""
+    ``grad_scale``; without ``max_norm`` it is this call's ``grad_scale``.  A new norm
+    and scale share a storage (see the module)."""
     return GradNorm(*_call("grad_norm", stream, grads, grad_scale, float("inf") if max_norm is None else max_norm, eps,
                            norm, scale, False))
 
