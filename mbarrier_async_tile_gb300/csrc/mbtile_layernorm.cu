@@ -5,9 +5,10 @@
 //   xh = (h - mu) rstd    y = xh (w + o) + b    g = dy (w + o)
 //   dx = rstd (g - mean_j g - xh mean_j(g xh)) + dres    dw_j = sum_i dy xh    db_j = sum_i dy
 //
-// Both read and write every matrix once and compute a handful of operations per
-// element: device memory bounds them.  All sums are fp32.  The kernels are in
-// mbtile_layernorm.cuh; here are the entry points and their checks.
+// Both compute a handful of operations per element, and device memory bounds them.  The norm,
+// and the gradient of rows that the shared-memory ring takes, read and write every matrix once;
+// the gradient of longer rows reads dy and h for dw and db and again for dx.  All sums are
+// fp32.  The kernels are in mbtile_layernorm.cuh; here are the entry points and their checks.
 #include "mbtile_layer.h"
 
 namespace mbt {

@@ -135,8 +135,9 @@ __device__ __forceinline__ void load_bias(const void *b, int mode, int wdt, int6
 
 // `tpr` threads hold a row in registers, C chunks each: one pass over memory.  For calls of few
 // rows, whose time is a launch and a row's latency with two or three sums in turn (one row of
-// 4096 to e4m3 3.5 us, 600 x 2048 3.4), and rows too long for the ring (bf16 2000 x 32001 with a
-// residual 180 us, 2.8 TB/s).
+// 4096 to e4m3 3.6 us, 600 x 2048 3.65), and 16-bit rows of more than 16384 elements whose weight
+// or bias is of another type, not aligned or with an offset, which the ring does not take (bf16
+// 2000 x 32001 with a residual and fp32 weights 269 us; with bf16 ones by the ring 153).
 template <int DT, int C, bool RES, bool Q>
 __global__ void __launch_bounds__(1024) mbt_layernorm_kernel(const __grid_constant__ LayerNormVecArgs va) {
     using T = typename Elem<DT>::type;
@@ -871,8 +872,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     }
 }
 
-// The norm.  bf16 8192 x 16384 with a residual 161 us, 6.7 TB/s: memory.  6881 x 19504 190 us,
-// 5.7 TB/s: 36 instructions an element on half the issue slots.
+// The norm.  bf16 8192 x 16384 with a residual 163 us, 6.6 TB/s: memory.  6881 x 19504 195 us,
+// 5.5 TB/s: 32 instructions an element on 55 % of the issue slots.
 template <int DT, int C, bool RES, bool Q, bool PART, bool FLY>
 __global__ void __launch_bounds__(kRingThreads, 1)
     mbt_layernorm_ring_kernel(const __grid_constant__ LayerNormArgs a, const __grid_constant__ LayerNormRing l) {
@@ -1241,7 +1242,8 @@ cudaError_t ln_ring_backward(const RingPlan &p, const LayerNormGradArgs &a, cuda
 // x 1032 of 7 36 / 39).  Forward eight chunks of 16-bit rows are ahead of four, given the turns:
 // with a residual 8192 x 10000 113 / 139, 8192 x 8200 108 / 137, 16384 x 1400 of 7 turns 35 / 39,
 // 8192 x 8192 83 / 83, 700 x 8200 of 2 15.9 / 15.6; of parts of chunks 8192 x 8191 160 / 189, 8192
-// x 5001 of 13 70 / 80, 4000 x 5001 of 7 to e4m3 84 / 68.
+// x 5001 of 13 70 / 80, 4000 x 5001 of 7 to e4m3 84 / 68.  (Forward figures here and at
+// ln_ring_pays precede the shift, which cost up to 3 %.)
 bool ln_ring_plan(const void *const *in, const int64_t *ld, int inputs, int64_t M, int64_t N, int es, int ph, int min_tpr,
                   int sms, bool gradient, bool plain, RingPlan *p) {
     if (es == 4)

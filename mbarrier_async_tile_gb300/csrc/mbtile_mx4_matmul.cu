@@ -335,10 +335,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 // columns and needs the scales of its rows and of all columns.  The first CTA's tensor
 // thread issues for both; copies of either CTA count on its barriers.
 //
-// 8192 x 16384 x 8192 by 16 takes 346 us, 6.4 PFLOP/s (374 once the power cap holds the clock at
-// 1.8 GHz), with the tensor pipe busy for 67 % of it: the copies alone take 316 us, 55 of the 64
-// bytes a cycle that an SM takes in, the products alone 230.  1024 x 8192 x 8192 29.5 us, 4.7
-// PFLOP/s.
+// 8192 x 16384 x 8192 by 16 takes 374 us in use, 5.9 PFLOP/s, with the clock held at 1.8 GHz by
+// the power cap (346 before the cap, with the tensor pipe busy for 67 % of it: the copies alone
+// 316 us, 55 of the 64 bytes a cycle that an SM takes in, the products alone 230).  1024 x 8192 x
+// 8192 29.5 us, 4.7 PFLOP/s.
 //
 // Two accumulators of 256 columns would leave no tensor memory for scales: there is one,
 // and eight epilogue warps take all of it into registers before they convert and store,
